@@ -24,10 +24,14 @@ OP = {"quant_act_1x128": 0, "quant_w_128x128": 1, "requant_128x1": 2,
       "gemm_fp8_fwd": 3, "gemm_fp8_dgrad": 4, "gemm_fp8_wgrad": 5,
       "token_mult_prob_error": 6, "quant_dual_1x128_128x1": 7, "token_mismatch_masked": 8,
       "swiglu_quant_1x128": 9, "kv_calibrate": 10, "kv_cache_write": 11,
-      "token_mismatch_per_sequence": 12, "rmsnorm_quant_1x128": 13}
+      "token_mismatch_per_sequence": 12, "rmsnorm_quant_1x128": 13,
+      "add_rmsnorm_quant_1x128": 14, "add_rmsnorm_bwd": 15, "rope": 16,
+      "rope_kv_cache_write": 17, "kv_slot_map": 18, "sample": 19}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "wavelength": 2, "ramp": 3}
 
 # name -> argtypes (restype is int status unless listed in _RESTYPE)
-P, I, Z = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+P, I, Z, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "jet_status_str": [ctypes.c_int],
     "jet_version": [],
@@ -49,6 +53,15 @@ SIGNATURES = {
     "jet_token_mult_prob_error": [P, P, I, P, P, Z, P],
     "jet_token_mult_prob_error_noalloc": [P, P, I, P, P],
     "jet_token_mismatch_masked": [P, P, P, I, ctypes.c_float, P, P, P, P, Z, P],
+    "jet_add_rmsnorm_quant_1x128": [P, P, P, I, I, F, P, P, P, P, P],
+    "jet_add_rmsnorm_bwd": [P, P, P, P, P, P, P, I, I, P, P, P, Z, P],
+    "jet_rope_inv_freq": [I, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double,
+                          ctypes.c_double, ctypes.c_double, P, P],
+    "jet_rope": [P, I, I, P, I, I, I, I, I, P, P, ctypes.c_int, F, ctypes.c_int, P, I, P, I, P],
+    "jet_rope_kv_cache_write": [P, I, I, P, I, P, I, I, I, I, I, P, P, ctypes.c_int, F, P, P, P,
+                                P, I, P, P, I, P],
+    "jet_kv_slot_map": [P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P],
+    "jet_sample": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
     "jet_workspace_bytes": [ctypes.c_int, I, I, I],
     "jet_device_status": [P, ctypes.POINTER(ctypes.c_uint32)],
     "jet_selftest_bounded_wait": [ctypes.c_uint32, P],
@@ -583,3 +596,242 @@ def token_mismatch_masked(logp_train, logp_rollout, mask=None, cap: float = 0.0,
                      device=dev)
     jet_token_mismatch_masked(logp_train, logp_rollout, mask, cap, w, out, count, ws, stream)
     return out, count, w
+
+
+# --------------------------------------------------------------------------
+# Residual RMSNorm, rotary positions, slot maps, sampling
+# --------------------------------------------------------------------------
+
+def _arg(t, dtype, shape, name):
+    """The address of a contiguous CUDA tensor of this type and shape, or of None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, shape, name)
+    return t.data_ptr() or None
+
+
+def _raw_stream(stream):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _allocating_on(stream):
+    """Allocations inside belong to the stream the call runs on."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def jet_add_rmsnorm_quant_1x128(x, d, g, eps, h, q, s, rstd=None, stream=None):
+    """h = x + d (h may be x or d itself) and the 1x128 form (q, s) of its
+    RMSNorm; rstd [M] receives what the backward needs, if given."""
+    import torch
+    M, K = x.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    _check("jet_add_rmsnorm_quant_1x128", load().jet_add_rmsnorm_quant_1x128(
+        _arg(x, bf16, (M, K), "x"), _arg(d, bf16, (M, K), "d"), _arg(g, bf16, (K,), "g"), M, K,
+        eps, _arg(h, bf16, (M, K), "h"), _arg(q, torch.uint8, (M, K), "q"),
+        _arg(s, f32, (K // 128, M), "s"), _arg(rstd, f32, (M,), "rstd"), _raw_stream(stream)))
+
+
+def add_rmsnorm_quant_1x128(x, d, g, eps=1e-5, with_rstd=False, stream=None):
+    """(h, q, s), or (h, q, s, rstd): the new residual stream x + d and the
+    1x128 form of its RMSNorm with gain g."""
+    import torch
+    M, K = x.shape
+    with _allocating_on(stream):
+        h = torch.empty_like(x)
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
+        rstd = torch.empty((M,), dtype=torch.float32, device=x.device) if with_rstd else None
+    jet_add_rmsnorm_quant_1x128(x, d, g, eps, h, q, s, rstd, stream)
+    return (h, q, s, rstd) if with_rstd else (h, q, s)
+
+
+def jet_add_rmsnorm_bwd(h, g, rstd, dys, dres, dx, dg, ws=None, stream=None):
+    """dx [M,K] (of both summands; may be dres itself) and dg [K] from the one
+    to three gradients `dys` of the normalised activation and the gradient
+    `dres` arriving on the residual stream (or None)."""
+    import torch
+    M, K = h.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    if not 1 <= len(dys) <= 3:
+        raise ValueError(f"dys: expected one to three gradients, got {len(dys)}")
+    dy = [_arg(t, bf16, (M, K), f"dys[{i}]") for i, t in enumerate(dys)] + [None, None]
+    if ws is None:
+        need = workspace_bytes("add_rmsnorm_bwd", M, 0, K)
+        with _allocating_on(stream):
+            ws = torch.empty((need,), dtype=torch.uint8, device=h.device)
+    _check("jet_add_rmsnorm_bwd", load().jet_add_rmsnorm_bwd(
+        _arg(h, bf16, (M, K), "h"), _arg(g, bf16, (K,), "g"), _arg(rstd, f32, (M,), "rstd"),
+        dy[0], dy[1], dy[2], _arg(dres, bf16, (M, K), "dres"), M, K,
+        _arg(dx, bf16, (M, K), "dx"), _arg(dg, f32, (K,), "dg"), ws.data_ptr() or None,
+        ws.numel() * ws.element_size(), _raw_stream(stream)))
+
+
+def add_rmsnorm_bwd(h, g, rstd, dys, dres=None, stream=None):
+    """(dx, dg) of jet_add_rmsnorm_bwd."""
+    import torch
+    with _allocating_on(stream):
+        dx = torch.empty_like(h)
+        dg = torch.empty((h.shape[1],), dtype=torch.float32, device=h.device)
+    jet_add_rmsnorm_bwd(h, g, rstd, dys, dres, dx, dg, None, stream)
+    return dx, dg
+
+
+def rope_inv_freq(R, base=10000.0, scaling="none", factor=1.0, context=8192.0, low=1.0, high=4.0,
+                  device="cuda"):
+    """(inv_freq float64 [R/2], mscale): the angle per position of each channel
+    pair and the factor its result is scaled by; see the C header."""
+    import torch
+    freq = torch.empty((max(R // 2, 1),), dtype=torch.float64)
+    mscale = ctypes.c_float(0.0)
+    _check("jet_rope_inv_freq", load().jet_rope_inv_freq(
+        R, base, ROPE_SCALING[scaling], factor, context, low, high, freq.data_ptr(),
+        ctypes.addressof(mscale)))
+    return freq.to(device), mscale.value
+
+
+def _heads(t, T, D, name):
+    """(address, token stride, heads) of [T, H, D] BF16 heads, dense within a token."""
+    import torch
+    if t is None:
+        return None, 0, 0
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
+        raise ValueError(f"{name}: expected shape ({T}, heads, {D}), got {tuple(t.shape)}")
+    H = t.shape[1]
+    if t.numel() == 0:
+        return None, H * D, H
+    st = t.stride()
+    if not t.is_cuda or (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"{name}: must be a CUDA tensor whose tokens hold contiguous heads")
+    return t.data_ptr(), (st[0] if T > 1 else H * D), H
+
+
+def jet_rope(q, k, inv_freq, pos, q_out, k_out, layout="half", mscale=1.0, backward=False,
+             stream=None):
+    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (or None) into q_out
+    and k_out (which may be q and k); backward=True for the gradients."""
+    import torch
+    T, _, D = (q if q is not None else k).shape
+    R = 2 * inv_freq.numel()
+    qp, ldq, Hq = _heads(q, T, D, "q")
+    kp, ldk, Hk = _heads(k, T, D, "k")
+    qo, ldqo, Hqo = _heads(q_out, T, D, "q_out")
+    ko, ldko, Hko = _heads(k_out, T, D, "k_out")
+    if Hqo != Hq or Hko != Hk:
+        raise ValueError("q_out and k_out must have the heads of q and k")
+    _check("jet_rope", load().jet_rope(
+        qp, ldq, Hq, kp, ldk, Hk, T, D, R, _arg(inv_freq, torch.float64, (R // 2,), "inv_freq"),
+        _arg(pos, torch.int64, (T,), "pos"), ROPE_LAYOUT[layout], mscale, int(backward), qo, ldqo,
+        ko, ldko, _raw_stream(stream)))
+
+
+def rope(q, k, inv_freq, pos, layout="half", mscale=1.0, backward=False, stream=None):
+    """(q, k) rotated, as new dense tensors; k may be None."""
+    import torch
+    with _allocating_on(stream):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    jet_rope(q, k, inv_freq, pos, qo, ko, layout, mscale, backward, stream)
+    return qo, ko
+
+
+def jet_rope_kv_cache_write(q, k, v, inv_freq, pos, k_scale, v_scale, slots, q_out, k_cache,
+                            v_cache, layout="half", mscale=1.0, stream=None):
+    """q rotated into q_out; k rotated and v as E4M3 codes into rows `slots` of
+    k_cache and v_cache [S, Hk, D]."""
+    import torch
+    T, _, D = q.shape
+    R, f32, u8 = 2 * inv_freq.numel(), torch.float32, torch.uint8
+    qp, ldq, Hq = _heads(q, T, D, "q")
+    kp, ldk, Hk = _heads(k, T, D, "k")
+    vp, ldv, Hv = _heads(v, T, D, "v")
+    qo, ldqo, Hqo = _heads(q_out, T, D, "q_out")
+    S = k_cache.shape[0]
+    if Hqo != Hq or Hv != Hk:
+        raise ValueError("q_out must have the heads of q, and v those of k")
+    _check("jet_rope_kv_cache_write", load().jet_rope_kv_cache_write(
+        qp, ldq, Hq, kp, ldk, vp, ldv, Hk, T, D, R,
+        _arg(inv_freq, torch.float64, (R // 2,), "inv_freq"), _arg(pos, torch.int64, (T,), "pos"),
+        ROPE_LAYOUT[layout], mscale, _arg(k_scale, f32, (Hk,), "k_scale"),
+        _arg(v_scale, f32, (Hk,), "v_scale"), _arg(slots, torch.int64, (T,), "slots"), qo, ldqo,
+        _arg(k_cache, u8, (S, Hk, D), "k_cache"), _arg(v_cache, u8, (S, Hk, D), "v_cache"), S,
+        _raw_stream(stream)))
+
+
+def jet_kv_slot_map(cached, added, block_size, table, free_blocks, free_next, offsets, positions,
+                    slots, rows, counts, stream=None):
+    """Block table entries, positions and cache slots of a step's new tokens
+    from the requests' lengths; see the C header."""
+    import torch
+    B, width, n_free, N = cached.numel(), table.shape[1], free_blocks.numel(), slots.numel()
+    i32, i64 = torch.int32, torch.int64
+    _check("jet_kv_slot_map", load().jet_kv_slot_map(
+        _arg(cached, i32, (B,), "cached"), _arg(added, i32, (B,), "added"), B, block_size,
+        _arg(table, i32, (B, width), "table"), width,
+        _arg(free_blocks, i32, (n_free,), "free_blocks"), n_free,
+        _arg(free_next, i64, free_next.shape, "free_next"), N,
+        _arg(offsets, i64, (B + 1,), "offsets"), _arg(positions, i64, (N,), "positions"),
+        _arg(slots, i64, (N,), "slots"), _arg(rows, i32, (N,), "rows"),
+        _arg(counts, i64, (2,), "counts"), _raw_stream(stream)))
+
+
+def kv_slot_map(cached, added, block_size, table, free_blocks, free_next, capacity, stream=None):
+    """(offsets [B+1], positions, slots, rows [capacity], counts [2]); the new
+    blocks are entered in `table`.  counts[:1] is the next call's free_next."""
+    import torch
+    B, dev, i64 = cached.numel(), cached.device, torch.int64
+    with _allocating_on(stream):
+        offsets = torch.empty((B + 1,), dtype=i64, device=dev)
+        positions = torch.empty((capacity,), dtype=i64, device=dev)
+        slots = torch.empty((capacity,), dtype=i64, device=dev)
+        rows = torch.empty((capacity,), dtype=torch.int32, device=dev)
+        counts = torch.empty((2,), dtype=i64, device=dev)
+    jet_kv_slot_map(cached, added, block_size, table, free_blocks, free_next, offsets, positions,
+                    slots, rows, counts, stream)
+    return offsets, positions, slots, rows, counts
+
+
+def jet_sample(logits, u, temperature, top_k, top_p, min_p, token, logp, logp_all, kept,
+               stream=None):
+    """One token per row of logits [B, V] (BF16 or FP32, rows may be strided)
+    from the uniform numbers u [B]; the settings are per row, or None."""
+    import torch
+    B, V = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    if logits.dtype not in (torch.bfloat16, f32):
+        raise TypeError(f"logits: expected torch.bfloat16 or torch.float32, got {logits.dtype}")
+    if logits.numel() and (not logits.is_cuda or (V > 1 and logits.stride(1) != 1)):
+        raise ValueError("logits: must be a CUDA tensor with contiguous rows")
+    ld = logits.stride(0) if B > 1 else V
+    _check("jet_sample", load().jet_sample(
+        logits.data_ptr() or None, int(logits.dtype == f32), B, V, ld, _arg(u, f32, (B,), "u"),
+        _arg(temperature, f32, (B,), "temperature"), _arg(top_k, i32, (B,), "top_k"),
+        _arg(top_p, f32, (B,), "top_p"), _arg(min_p, f32, (B,), "min_p"),
+        _arg(token, torch.int64, (B,), "token"), _arg(logp, f32, (B,), "logp"),
+        _arg(logp_all, f32, (B,), "logp_all"), _arg(kept, i32, (B,), "kept"),
+        _raw_stream(stream)))
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """(token int64, logp, logp_all float32, kept int32), each [B]."""
+    import torch
+    B, dev = logits.shape[0], logits.device
+    with _allocating_on(stream):
+        token = torch.empty((B,), dtype=torch.int64, device=dev)
+        logp = torch.empty((B,), dtype=torch.float32, device=dev)
+        logp_all = torch.empty((B,), dtype=torch.float32, device=dev)
+        kept = torch.empty((B,), dtype=torch.int32, device=dev)
+    jet_sample(logits, u, temperature, top_k, top_p, min_p, token, logp, logp_all, kept, stream)
+    return token, logp, logp_all, kept

@@ -101,6 +101,8 @@ int jet_metric_blocks(int64_t n);
 size_t jet_gemm_workspace(int op, int64_t M, int64_t N, int64_t K);
 // Per-block sums and counts of the masked metric's first pass.
 size_t jet_mismatch_masked_workspace(int64_t n);
+// Partial rows of the gain's gradient.
+size_t jet_add_rmsnorm_bwd_workspace(int64_t M, int64_t K);
 
 extern "C" {
 
@@ -130,6 +132,8 @@ size_t jet_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
         return jet_gemm_workspace(op, M, N, K);
     case JET_OP_TOKEN_MISMATCH_MASKED:
         return jet_mismatch_masked_workspace(M);
+    case JET_OP_ADD_RMSNORM_BWD:
+        return jet_add_rmsnorm_bwd_workspace(M, K);
     default:
         return 0;
     }

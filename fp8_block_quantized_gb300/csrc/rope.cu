@@ -1,0 +1,432 @@
+// Rotary positions of q and k (jet_rope, forward and backward), and the same
+// rotation fused with the FP8 KV-cache write (jet_rope_kv_cache_write).
+//
+// Channel pair i of a head (the first R of its D channels; pairs (i, i + R/2)
+// in the half layout, (2 i, 2 i + 1) in the interleaved one) is turned by the
+// angle pos * f_i and scaled by mscale:
+//   y_a = a cos - b sin,  y_b = b cos + a sin;
+// channels R .. D-1 pass through.  The backward turns by the negative angle.
+//
+// Angles: pos * f_i reaches 10^6 radians and more in long contexts, where a
+// binary32 product keeps no fraction.  Here f_i / (2 pi) is held as a 64-bit
+// binary fraction of a turn, so pos * fraction modulo 2^64 is the angle modulo
+// a whole turn, in integer arithmetic with an error below |pos| 2^-54 turns (the
+// binary64 product) at any position; its top 32 bits, as a signed half-turn count,
+// go to sincospi in binary32.
+#include <cmath>
+
+#include "jet_common.cuh"
+#include "quant_rule.cuh"
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxD = 1024;
+constexpr int kRopeBatch = 4;  // heads per thread at most (one set of angles)
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two binary32 values rounded to BF16 (nearest, ties to even), a in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// The fraction of a turn per position, times 2^64.
+__device__ __forceinline__ unsigned long long turn_fraction(double f) {
+    double t = f * 0.15915494309189533577;  // 1 / (2 pi)
+    t -= floor(t);
+    return __double2ull_rn(t * 18446744073709551616.0);
+}
+
+__device__ __forceinline__ void angle(unsigned long long frac, int64_t pos, float mscale,
+                                      bool backward, float &c, float &s) {
+    const unsigned long long p = frac * (unsigned long long)pos;
+    const float half_turns = __int2float_rn((int)(p >> 32)) * 0x1p-31f;
+    sincospif(half_turns, &s, &c);
+    c *= mscale;
+    s *= backward ? -mscale : mscale;
+}
+
+struct RopeArgs {
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    int Hq, Hk, Hv, D, R;
+    int64_t T;
+    const double *freq;
+    const int64_t *pos;
+    float mscale;
+    int backward;
+    uint16_t *qo, *ko;
+    int64_t ldqo, ldko;
+    // KV-cache form
+    const float *ks, *vs;
+    const int64_t *slots;
+    uint8_t *kc, *vc;
+    int64_t S;
+    // split of the work: threads = T * groups * items, hpt heads each
+    int groups, items, hpt;
+};
+
+// One head's place: where it is read and where its result goes.
+struct Head {
+    const uint16_t *in;
+    uint16_t *out;   // BF16 output, or null
+    uint8_t *code;   // cache entry, or null
+    float scale;
+    bool rotate;
+};
+
+template <bool kCache>
+__device__ __forceinline__ Head head_of(const RopeArgs &a, int64_t t, int h, int64_t slot) {
+    Head r;
+    r.out = nullptr;
+    r.code = nullptr;
+    r.scale = 1.0f;
+    r.rotate = true;
+    if (h < a.Hq) {
+        r.in = a.q + t * a.ldq + (int64_t)h * a.D;
+        r.out = a.qo + t * a.ldqo + (int64_t)h * a.D;
+        return r;
+    }
+    h -= a.Hq;
+    const bool is_v = kCache && h >= a.Hk;
+    if (is_v) h -= a.Hk;
+    r.rotate = !is_v;
+    r.in = (is_v ? a.v + t * a.ldv : a.k + t * a.ldk) + (int64_t)h * a.D;
+    if (kCache) {
+        if (slot >= 0 && slot < a.S) {
+            r.code = (is_v ? a.vc : a.kc) + (slot * a.Hk + h) * a.D;
+            r.scale = (is_v ? a.vs : a.ks)[h];
+        }
+    } else {
+        r.out = a.ko + t * a.ldko + (int64_t)h * a.D;
+    }
+    return r;
+}
+
+// Eight BF16 values (packed) to where a head's chunk at channel d goes.
+template <bool kCache>
+__device__ __forceinline__ void store8(const Head &hd, int d, const uint4 &y) {
+    if (!kCache || hd.out) {
+        *reinterpret_cast<uint4 *>(hd.out + d) = y;
+    } else if (hd.code) {
+        const Divisor dv = make_divisor(hd.scale);
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+        float nf[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            nf[2 * i] = __uint_as_float((w[i] << 16) ^ 0x80000000u);
+            nf[2 * i + 1] = __uint_as_float((w[i] & 0xFFFF0000u) ^ 0x80000000u);
+        }
+        *reinterpret_cast<uint2 *>(hd.code + d) = make_uint2(encode4(nf, dv), encode4(nf + 4, dv));
+    }
+}
+
+// Half layout, one pair of words: x holds channels i, i+1 of the first half,
+// y those of the second.
+__device__ __forceinline__ void turn_half(uint32_t &x, uint32_t &y, const float *c, const float *s) {
+    const float a0 = bf16_lo(x), a1 = bf16_hi(x), b0 = bf16_lo(y), b1 = bf16_hi(y);
+    x = pack_bf16(__fmaf_rn(a0, c[0], -__fmul_rn(b0, s[0])), __fmaf_rn(a1, c[1], -__fmul_rn(b1, s[1])));
+    y = pack_bf16(__fmaf_rn(b0, c[0], __fmul_rn(a0, s[0])), __fmaf_rn(b1, c[1], __fmul_rn(a1, s[1])));
+}
+
+__device__ __forceinline__ uint32_t turn_pair(uint32_t x, float c, float s) {
+    const float a = bf16_lo(x), b = bf16_hi(x);
+    return pack_bf16(__fmaf_rn(a, c, -__fmul_rn(b, s)), __fmaf_rn(b, c, __fmul_rn(a, s)));
+}
+
+// A thread takes one item of up to kRopeBatch heads of one token.  Items of a
+// head: kHalf: R/16 pairs of 8-channel chunks (c, c + R/16), then the chunks
+// past R; interleaved: D/8 chunks.  Needs R % 16 == 0 (half) or R % 8 == 0.
+template <bool kHalf, bool kCache>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(const RopeArgs a) {
+    extern __shared__ unsigned long long frac[];  // [R/2]
+    jet::griddep_launch_dependents();
+    jet::griddep_wait();
+    for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) frac[i] = turn_fraction(a.freq[i]);
+    __syncthreads();
+    constexpr int kPairs = kHalf ? 8 : 4;
+    const int nrot = kHalf ? a.R / 16 : a.R / 8;
+    const int heads = a.Hq + a.Hk + a.Hv;
+    const uint32_t per_token = (uint32_t)a.groups * a.items;
+    const uint32_t total = (uint32_t)a.T * per_token;
+    const bool inplace = !kCache && a.q == a.qo && a.k == a.ko;
+    for (uint64_t idx = blockIdx.x * (uint64_t)kRopeThreads + threadIdx.x; idx < total;
+         idx += (uint64_t)gridDim.x * kRopeThreads) {
+        const uint32_t t = (uint32_t)idx / per_token, rest = (uint32_t)idx - t * per_token;
+        const uint32_t grp = rest / a.items;
+        const int item = (int)(rest - grp * a.items);
+        const bool rot = item < nrot;
+        if (!rot && inplace) continue;
+        const int h0 = (int)grp * a.hpt, h1 = min(h0 + a.hpt, heads);
+        const int64_t slot = kCache ? a.slots[t] : 0;
+        const int d0 = kHalf ? (rot ? 8 * item : a.R + 8 * (item - nrot)) : 8 * item;
+        const int d1 = kHalf ? a.R / 2 + 8 * item : 0;
+        uint4 x[kRopeBatch], y[kRopeBatch];
+#pragma unroll
+        for (int b = 0; b < kRopeBatch; ++b) {
+            if (h0 + b >= h1) break;
+            const Head hd = head_of<kCache>(a, t, h0 + b, -1);
+            x[b] = *reinterpret_cast<const uint4 *>(hd.in + d0);
+            if (kHalf && rot) y[b] = *reinterpret_cast<const uint4 *>(hd.in + d1);
+        }
+        float c[kPairs], s[kPairs];
+        if (rot) {
+            const int64_t pos = a.pos[t];
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                angle(frac[kPairs * item + i], pos, a.mscale, a.backward, c[i], s[i]);
+        }
+#pragma unroll
+        for (int b = 0; b < kRopeBatch; ++b) {
+            if (h0 + b >= h1) break;
+            const Head hd = head_of<kCache>(a, t, h0 + b, slot);
+            if (rot && hd.rotate) {
+                if (kHalf) {
+                    turn_half(x[b].x, y[b].x, c, s);
+                    turn_half(x[b].y, y[b].y, c + 2, s + 2);
+                    turn_half(x[b].z, y[b].z, c + 4, s + 4);
+                    turn_half(x[b].w, y[b].w, c + 6, s + 6);
+                } else {
+                    x[b].x = turn_pair(x[b].x, c[0], s[0]);
+                    x[b].y = turn_pair(x[b].y, c[1], s[1]);
+                    x[b].z = turn_pair(x[b].z, c[2], s[2]);
+                    x[b].w = turn_pair(x[b].w, c[3], s[3]);
+                }
+            }
+            store8<kCache>(hd, d0, x[b]);
+            if (kHalf && rot) store8<kCache>(hd, d1, y[b]);
+        }
+    }
+}
+
+template <bool kCache>
+__device__ __forceinline__ void store1(const Head &hd, int d, uint32_t bf16) {
+    if (!kCache || hd.out) {
+        hd.out[d] = (uint16_t)bf16;
+    } else if (hd.code) {
+        const float q = qdiv_neg(__uint_as_float((bf16 << 16) ^ 0x80000000u), make_divisor(hd.scale));
+        hd.code[d] = (uint8_t)f32x4_to_e4m3x4(q, q, q, q);
+    }
+}
+
+// Any even R (the pairs do not fill 16-byte chunks): items are the R/2 pairs,
+// then the single channels past R.
+template <bool kHalf, bool kCache>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_any_kernel(const RopeArgs a) {
+    extern __shared__ unsigned long long frac[];
+    jet::griddep_launch_dependents();
+    jet::griddep_wait();
+    for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) frac[i] = turn_fraction(a.freq[i]);
+    __syncthreads();
+    const int heads = a.Hq + a.Hk + a.Hv;
+    const uint32_t per_token = (uint32_t)a.groups * a.items;
+    const uint32_t total = (uint32_t)a.T * per_token;
+    for (uint64_t idx = blockIdx.x * (uint64_t)kRopeThreads + threadIdx.x; idx < total;
+         idx += (uint64_t)gridDim.x * kRopeThreads) {
+        const uint32_t t = (uint32_t)idx / per_token, rest = (uint32_t)idx - t * per_token;
+        const uint32_t grp = rest / a.items;
+        const int item = (int)(rest - grp * a.items);
+        const bool rot = item < a.R / 2;
+        const int h0 = (int)grp * a.hpt, h1 = min(h0 + a.hpt, heads);
+        const int64_t slot = kCache ? a.slots[t] : 0;
+        const int d0 = !rot ? item + a.R / 2 : kHalf ? item : 2 * item;
+        const int d1 = kHalf ? item + a.R / 2 : 2 * item + 1;
+        float c = 1.0f, s = 0.0f;
+        if (rot) angle(frac[item], a.pos[t], a.mscale, a.backward, c, s);
+        for (int h = h0; h < h1; ++h) {
+            const Head hd = head_of<kCache>(a, t, h, slot);
+            const uint32_t x = hd.in[d0];
+            if (!rot) {
+                store1<kCache>(hd, d0, x);
+                continue;
+            }
+            uint32_t w = x | ((uint32_t)hd.in[d1] << 16);
+            if (hd.rotate) w = turn_pair(w, c, s);
+            store1<kCache>(hd, d0, w & 0xFFFFu);
+            store1<kCache>(hd, d1, w >> 16);
+        }
+    }
+}
+
+jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo &dev,
+                       jet_stream_t stream) {
+    const bool half = layout == JET_ROPE_HALF;
+    const bool vec = half ? a.R % 16 == 0 : a.R % 8 == 0;
+    a.items = vec ? (half ? a.R / 16 + (a.D - a.R) / 8 : a.D / 8) : a.R / 2 + (a.D - a.R);
+    const int heads = a.Hq + a.Hk + a.Hv;
+    // More heads per thread share one set of angles; fewer keep the SMs busy
+    // when there are few tokens.
+    a.hpt = kRopeBatch;
+    while (a.hpt > 1 && a.T * ((heads + a.hpt - 1) / a.hpt) * a.items < (int64_t)dev.num_sms * 2048)
+        a.hpt /= 2;
+    a.groups = (heads + a.hpt - 1) / a.hpt;
+    const int64_t total = a.T * a.groups * a.items;
+    if (total >= ((int64_t)1 << 32)) return JET_ERR_SHAPE;
+    const int64_t want = (total + kRopeThreads - 1) / kRopeThreads;
+    const int64_t cap = (int64_t)dev.num_sms * 8;
+    void (*kernel)(RopeArgs) =
+        vec ? (half ? (cache ? rope_kernel<true, true> : rope_kernel<true, false>)
+                    : (cache ? rope_kernel<false, true> : rope_kernel<false, false>))
+            : (half ? (cache ? rope_any_kernel<true, true> : rope_any_kernel<true, false>)
+                    : (cache ? rope_any_kernel<false, true> : rope_any_kernel<false, false>));
+    return jet::launch_pdl(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kRopeThreads),
+                           (size_t)a.R / 2 * sizeof(unsigned long long), jet::as_stream(stream), a);
+}
+
+// Sizes both entry points share.
+bool rope_sizes_ok(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int layout) {
+    return T < ((int64_t)1 << 31) && Hq <= 1024 && Hk <= 1024 && D <= kRopeMaxD && D % 8 == 0 &&
+           R >= 0 && R <= D && R % 2 == 0 &&
+           (layout == JET_ROPE_HALF || layout == JET_ROPE_INTERLEAVED);
+}
+
+bool ld_ok(int64_t ld, int64_t H, int64_t D) { return ld >= H * D && ld < ((int64_t)1 << 40); }
+
+template <int kBytes>
+bool aligned_to(const void *p) { return (reinterpret_cast<uintptr_t>(p) & (kBytes - 1)) == 0; }
+
+}  // namespace
+
+jet_status jet_rope(const uint16_t *q, int64_t ldq, int64_t Hq, const uint16_t *k, int64_t ldk,
+                    int64_t Hk, int64_t T, int64_t D, int64_t R, const double *inv_freq,
+                    const int64_t *pos, int layout, float mscale, int backward, uint16_t *qo,
+                    int64_t ldqo, uint16_t *ko, int64_t ldko, jet_stream_t stream) {
+    JET_REQUIRE(T >= 0 && Hq >= 0 && Hk >= 0 && D >= 0, JET_ERR_SHAPE);
+    const bool hasq = T > 0 && D > 0 && Hq > 0, hask = T > 0 && D > 0 && Hk > 0;
+    JET_REQUIRE((!hasq || (q && qo)) && (!hask || (k && ko)), JET_ERR_NULL);
+    JET_REQUIRE((!hasq && !hask) || (pos && (R <= 0 || inv_freq)), JET_ERR_NULL);
+    JET_REQUIRE(rope_sizes_ok(T, Hq, Hk, D, R, layout), JET_ERR_SHAPE);
+    JET_REQUIRE(!hasq || (ld_ok(ldq, Hq, D) && ld_ok(ldqo, Hq, D)), JET_ERR_SHAPE);
+    JET_REQUIRE(!hask || (ld_ok(ldk, Hk, D) && ld_ok(ldko, Hk, D)), JET_ERR_SHAPE);
+    JET_REQUIRE(!hasq || (ldq % 8 == 0 && ldqo % 8 == 0 && jet::aligned16(q) && jet::aligned16(qo)),
+                JET_ERR_ALIGN);
+    JET_REQUIRE(!hask || (ldk % 8 == 0 && ldko % 8 == 0 && jet::aligned16(k) && jet::aligned16(ko)),
+                JET_ERR_ALIGN);
+    JET_REQUIRE(aligned_to<8>(pos) && aligned_to<8>(inv_freq), JET_ERR_ALIGN);
+    jet::DeviceInfo dev;
+    jet_status st = jet::current_device(&dev);
+    if (st != JET_OK) return st;
+    if (!hasq && !hask) return JET_OK;
+    RopeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.Hq = (int)Hq;
+    a.Hk = (int)Hk;
+    a.D = (int)D;
+    a.R = (int)R;
+    a.T = T;
+    a.freq = inv_freq;
+    a.pos = pos;
+    a.mscale = mscale;
+    a.backward = backward != 0;
+    a.qo = qo;
+    a.ko = ko;
+    a.ldqo = ldqo;
+    a.ldko = ldko;
+    return rope_launch(a, layout, false, dev, stream);
+}
+
+jet_status jet_rope_kv_cache_write(const uint16_t *q, int64_t ldq, int64_t Hq, const uint16_t *k,
+                                   int64_t ldk, const uint16_t *v, int64_t ldv, int64_t Hk,
+                                   int64_t T, int64_t D, int64_t R, const double *inv_freq,
+                                   const int64_t *pos, int layout, float mscale,
+                                   const float *k_scale, const float *v_scale,
+                                   const int64_t *slots, uint16_t *qo, int64_t ldqo,
+                                   uint8_t *k_cache, uint8_t *v_cache, int64_t S,
+                                   jet_stream_t stream) {
+    JET_REQUIRE(T >= 0 && Hq >= 0 && Hk >= 0 && D >= 0 && S >= 0, JET_ERR_SHAPE);
+    const bool hasq = T > 0 && D > 0 && Hq > 0, hask = T > 0 && D > 0 && Hk > 0;
+    JET_REQUIRE(!hasq || (q && qo), JET_ERR_NULL);
+    JET_REQUIRE(!hask || (k && v && k_scale && v_scale && slots && (S == 0 || (k_cache && v_cache))),
+                JET_ERR_NULL);
+    JET_REQUIRE((!hasq && !hask) || (pos && (R <= 0 || inv_freq)), JET_ERR_NULL);
+    JET_REQUIRE(rope_sizes_ok(T, Hq, Hk, D, R, layout) && D % 16 == 0 && S < ((int64_t)1 << 40),
+                JET_ERR_SHAPE);
+    JET_REQUIRE(!hasq || (ld_ok(ldq, Hq, D) && ld_ok(ldqo, Hq, D)), JET_ERR_SHAPE);
+    JET_REQUIRE(!hask || (ld_ok(ldk, Hk, D) && ld_ok(ldv, Hk, D)), JET_ERR_SHAPE);
+    JET_REQUIRE(!hasq || (ldq % 8 == 0 && ldqo % 8 == 0 && jet::aligned16(q) && jet::aligned16(qo)),
+                JET_ERR_ALIGN);
+    JET_REQUIRE(!hask || (ldk % 8 == 0 && ldv % 8 == 0 && jet::aligned16(k) && jet::aligned16(v) &&
+                          aligned_to<4>(k_scale) && aligned_to<4>(v_scale) &&
+                          aligned_to<8>(slots) && jet::aligned16(k_cache) &&
+                          jet::aligned16(v_cache)),
+                JET_ERR_ALIGN);
+    JET_REQUIRE(aligned_to<8>(pos) && aligned_to<8>(inv_freq), JET_ERR_ALIGN);
+    jet::DeviceInfo dev;
+    jet_status st = jet::current_device(&dev);
+    if (st != JET_OK) return st;
+    if (!hasq && !hask) return JET_OK;
+    RopeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.Hq = (int)Hq;
+    a.Hk = (int)Hk;
+    a.Hv = (int)Hk;
+    a.D = (int)D;
+    a.R = (int)R;
+    a.T = T;
+    a.freq = inv_freq;
+    a.pos = pos;
+    a.mscale = mscale;
+    a.qo = qo;
+    a.ldqo = ldqo;
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.slots = slots;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.S = S;
+    return rope_launch(a, layout, true, dev, stream);
+}
+
+jet_status jet_rope_inv_freq(int64_t R, double base, int scaling, double factor, double context,
+                             double low, double high, double *inv_freq, float *mscale) {
+    JET_REQUIRE(inv_freq && mscale, JET_ERR_NULL);
+    JET_REQUIRE(R >= 2 && R <= kRopeMaxD && R % 2 == 0 && base > 1.0 && base <= 1e300,
+                JET_ERR_SHAPE);
+    const bool blend = scaling == JET_ROPE_SCALE_WAVELENGTH || scaling == JET_ROPE_SCALE_RAMP;
+    JET_REQUIRE(blend || scaling == JET_ROPE_SCALE_NONE || scaling == JET_ROPE_SCALE_LINEAR,
+                JET_ERR_SHAPE);
+    JET_REQUIRE(scaling == JET_ROPE_SCALE_NONE || (factor > 0.0 && factor <= 1e300), JET_ERR_SHAPE);
+    JET_REQUIRE(!blend || (context > 0.0 && context <= 1e300 && low > 0.0 && high > low &&
+                           high <= 1e300),
+                JET_ERR_SHAPE);
+    constexpr double kTwoPi = 6.28318530717958647693;
+    double from = 0.0, to = 0.0;
+    if (scaling == JET_ROPE_SCALE_RAMP) {
+        const double last = (double)(R - 1);
+        from = std::floor((double)R * std::log(context / (kTwoPi * high)) / (2.0 * std::log(base)));
+        to = std::ceil((double)R * std::log(context / (kTwoPi * low)) / (2.0 * std::log(base)));
+        from = std::fmin(std::fmax(from, 0.0), last);
+        to = std::fmin(std::fmax(to, 0.0), last);
+        if (to <= from) to = from + 0.001;  // a step
+    }
+    for (int64_t i = 0; i < R / 2; ++i) {
+        double f = std::pow(base, -2.0 * (double)i / (double)R);
+        if (scaling == JET_ROPE_SCALE_LINEAR) {
+            f /= factor;
+        } else if (blend) {
+            const double s = scaling == JET_ROPE_SCALE_WAVELENGTH
+                                 ? (high - context * f / kTwoPi) / (high - low)
+                                 : ((double)i - from) / (to - from);
+            const double c = std::fmin(std::fmax(s, 0.0), 1.0);
+            f *= 1.0 - c + c / factor;
+        }
+        inv_freq[i] = f;
+    }
+    *mscale = scaling == JET_ROPE_SCALE_RAMP && factor > 1.0
+                  ? (float)(1.0 + 0.1 * std::log(factor)) : 1.0f;
+    return JET_OK;
+}

@@ -26,7 +26,10 @@
  *    at +-448, sign of zero kept.  The stored scale dequantizes: v ~ q * s.
  *  - Every call validates its arguments on the host, in this order, and returns
  *    the first violation without launching anything: JET_ERR_NULL,
- *    JET_ERR_SHAPE, JET_ERR_ALIGN (every pointer must be 16-byte aligned),
+ *    JET_ERR_SHAPE, JET_ERR_ALIGN (every pointer must be 16-byte aligned, but
+ *    for the arrays of one value per token, row, request or head of
+ *    jet_add_rmsnorm_*, jet_rope*, jet_kv_slot_map and jet_sample, which need
+ *    their type's alignment),
  *    JET_ERR_WORKSPACE, JET_ERR_DEVICE (current device must be sm_103).
  *    A pointer may be NULL only when its tensor is empty.
  *  - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL is the
@@ -81,8 +84,28 @@ typedef enum {
     JET_OP_KV_CALIBRATE = 10,
     JET_OP_KV_CACHE_WRITE = 11,
     JET_OP_TOKEN_MISMATCH_PER_SEQUENCE = 12,
-    JET_OP_RMSNORM_QUANT_1X128 = 13
+    JET_OP_RMSNORM_QUANT_1X128 = 13,
+    JET_OP_ADD_RMSNORM_QUANT_1X128 = 14,
+    JET_OP_ADD_RMSNORM_BWD = 15,
+    JET_OP_ROPE = 16,
+    JET_OP_ROPE_KV_CACHE_WRITE = 17,
+    JET_OP_KV_SLOT_MAP = 18,
+    JET_OP_SAMPLE = 19
 } jet_op;
+
+/* Pair layouts of jet_rope: (i, i + R/2) or (2 i, 2 i + 1). */
+typedef enum { JET_ROPE_HALF = 0, JET_ROPE_INTERLEAVED = 1 } jet_rope_layout;
+
+/* Frequency scalings of jet_rope_inv_freq. */
+typedef enum {
+    JET_ROPE_SCALE_NONE = 0,
+    JET_ROPE_SCALE_LINEAR = 1,
+    JET_ROPE_SCALE_WAVELENGTH = 2,
+    JET_ROPE_SCALE_RAMP = 3
+} jet_rope_scaling;
+
+/* Types of the logits of jet_sample. */
+typedef enum { JET_BF16 = 0, JET_FP32 = 1 } jet_dtype;
 
 /* A cudaStream_t handle passed as an opaque pointer. */
 typedef void *jet_stream_t;
@@ -439,6 +462,180 @@ JET_API jet_status jet_token_mismatch_per_sequence(const float *logp_train,
                                                    const int64_t *seq_offsets, int64_t S,
                                                    int64_t n, float cap, float *w, float *out,
                                                    int64_t *count, jet_stream_t stream);
+
+/*
+ * The residual addition, RMSNorm and the 1x128 quantization in one pass: the
+ * step between two projections of a layer.  The pages have no counterpart
+ * beyond the fused RMSNorm of jet_rmsnorm_quant_1x128, whose arithmetic this
+ * call follows:
+ *   h = BF16(x + d) (binary32 sum, one rounding), then
+ *   q, s = jet_rmsnorm_quant_1x128(h, g, eps), bit for bit, at any M.
+ *   x   [M][K] BF16 bits (in; the residual stream), d [M][K] BF16 bits (in;
+ *       the preceding projection's output), g [K] BF16 bits (in; the gain).
+ *   h   [M][K] BF16 bits (out; the new residual stream).  May be x or d
+ *       itself (in place); no other overlap is allowed.
+ *   q   [M][K] E4M3 codes, s [K/128][M] FP32 scales (out).
+ *   rstd [M] FP32 (out; 1 / sqrt(mean(h^2) + eps) of each row, 0 where that
+ *       sum is 0; what jet_add_rmsnorm_bwd needs), or NULL.
+ * M, K >= 0, K a multiple of 128 and below 2^24; eps >= 0 (finite).
+ */
+JET_API jet_status jet_add_rmsnorm_quant_1x128(const uint16_t *x, const uint16_t *d,
+                                               const uint16_t *g, int64_t M, int64_t K, float eps,
+                                               uint16_t *h, uint8_t *q, float *s, float *rstd,
+                                               jet_stream_t stream);
+
+/*
+ * Backward of the addition and the norm (the quantization passes gradients
+ * straight through).  With dy = dy0 + dy1 + dy2 (the DGrads of the products
+ * that read the normalised activation: q, k, v or gate, up) and r = rstd:
+ *   dx = dres + r (g dy - h r^2 sum_k(g dy h) / K)      (of x and of d alike)
+ *   dg = sum_m dy h r
+ * in binary32; dx rounded once to BF16, dg kept in FP32, its sum over the
+ * rows in one fixed order (deterministic).
+ *   h [M][K], g [K] BF16 bits, rstd [M] FP32: as written by the forward.
+ *   dy0, dy1, dy2 [M][K] BF16 bits (in); dy1 and dy2 may be NULL.
+ *   dres [M][K] BF16 bits (in; the gradient arriving on the residual stream),
+ *       or NULL for none.
+ *   dx [M][K] BF16 bits (out; may be dres itself), dg [K] FP32 (out; zeros
+ *       when M == 0).
+ *   ws / ws_bytes: at least jet_workspace_bytes(JET_OP_ADD_RMSNORM_BWD, M, 0,
+ *       K) bytes of device memory; scratch, not initialised.
+ * M >= 0; K a multiple of 128, 0 <= K <= 32768.
+ */
+JET_API jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float *rstd,
+                                       const uint16_t *dy0, const uint16_t *dy1,
+                                       const uint16_t *dy2, const uint16_t *dres, int64_t M,
+                                       int64_t K, uint16_t *dx, float *dg, void *ws,
+                                       size_t ws_bytes, jet_stream_t stream);
+
+/*
+ * Rotary position frequencies, a HOST function (no device, no stream): the
+ * angle per position of channel pair i, 0 <= i < R/2, in binary64,
+ *   f_i = base^(-2 i / R),
+ * scaled for contexts longer than the `context` positions of training:
+ *   NONE        f_i
+ *   LINEAR      f_i / factor
+ *   WAVELENGTH  with n_i = context f_i / (2 pi) turns over that context:
+ *               f_i (1 - s + s / factor), s = 0 for n_i >= high, 1 for
+ *               n_i <= low, (high - n_i) / (high - low) between.
+ *   RAMP        the same blend with s linear in i between the pairs that turn
+ *               `high` and `low` times over that context: i_n = R ln(context /
+ *               (2 pi n)) / (2 ln base), from floor(i_high) to ceil(i_low),
+ *               both kept within [0, R - 1]; and mscale = 1 + 0.1 ln(factor)
+ *               for factor > 1 (published as YaRN, Peng et al., 2023).
+ *   inv_freq [R/2] (out, host memory), mscale (out, host; 1 except for RAMP).
+ * R even, 2 <= R <= 1024; base > 1; factor, context > 0; WAVELENGTH and RAMP:
+ * 0 < low < high.  Unused parameters are ignored.
+ */
+JET_API jet_status jet_rope_inv_freq(int64_t R, double base, int scaling, double factor,
+                                     double context, double low, double high, double *inv_freq,
+                                     float *mscale);
+
+/*
+ * Rotary positions of q and k in one launch, forward and backward.  Channel
+ * pair (a, b) number i of the first R channels of every head is turned by the
+ * angle pos[t] f_i and scaled:
+ *   a' = mscale (a cos - b sin),  b' = mscale (b cos + a sin),
+ * pairs (i, i + R/2) in JET_ROPE_HALF, (2 i, 2 i + 1) in
+ * JET_ROPE_INTERLEAVED; channels R .. D-1 are copied.  backward != 0 turns by
+ * the negative angle: the gradients of the inputs from those of the outputs.
+ * Angles are reduced modulo a turn in 64-bit integer arithmetic, so positions
+ * may be any int64; products in binary32, one rounding to BF16.
+ *   q: token t, head h at q + t*ldq + h*D (BF16 bits), h < Hq; k likewise
+ *       with ldk, Hk.  qo, ko: outputs, strides ldqo, ldko; they may be q and
+ *       k themselves with the same strides (in place).  A tensor with no head
+ *       may be NULL.
+ *   inv_freq [R/2] FP64, pos [T] int64: DEVICE arrays.
+ * T, Hq, Hk >= 0, at most 1024 heads each; D a multiple of 8, at most 1024;
+ * R even, 0 <= R <= D; strides >= H*D and multiples of 8.
+ */
+JET_API jet_status jet_rope(const uint16_t *q, int64_t ldq, int64_t Hq, const uint16_t *k,
+                            int64_t ldk, int64_t Hk, int64_t T, int64_t D, int64_t R,
+                            const double *inv_freq, const int64_t *pos, int layout, float mscale,
+                            int backward, uint16_t *qo, int64_t ldqo, uint16_t *ko, int64_t ldko,
+                            jet_stream_t stream);
+
+/*
+ * Rotary positions fused with the FP8 KV-cache write, for serving: q is
+ * rotated into qo, k is rotated and written with v as E4M3 codes into their
+ * cache slots.  Equal bit for bit to jet_rope of q and k followed by
+ * jet_kv_cache_write of the rotated k (k_scale, k_cache) and of v (v_scale,
+ * v_cache).  Arguments as in those calls; a slot outside [0, S) is skipped
+ * (its q is still rotated); D a multiple of 16.
+ */
+JET_API jet_status jet_rope_kv_cache_write(const uint16_t *q, int64_t ldq, int64_t Hq,
+                                           const uint16_t *k, int64_t ldk, const uint16_t *v,
+                                           int64_t ldv, int64_t Hk, int64_t T, int64_t D,
+                                           int64_t R, const double *inv_freq, const int64_t *pos,
+                                           int layout, float mscale, const float *k_scale,
+                                           const float *v_scale, const int64_t *slots,
+                                           uint16_t *qo, int64_t ldqo, uint8_t *k_cache,
+                                           uint8_t *v_cache, int64_t S, jet_stream_t stream);
+
+/*
+ * Block tables and slot maps of a paged KV cache from the requests' lengths,
+ * on the GPU.  The cache's slots come in blocks of block_size; request b holds
+ * cached[b] tokens in the blocks table[b][0 ..] and adds added[b] tokens in
+ * this step.  The blocks it lacks are taken from the free list in request
+ * order, starting at free_blocks[*free_next], and entered in the table; then
+ * for every new token t, in request order,
+ *   positions[t] = its position in its request,
+ *   slots[t] = table[b][pos / block_size] * block_size + pos % block_size,
+ *   rows[t] = b.
+ * A token without a block gets slot -1 (which the cache writes skip): past the
+ * table's width, past the free list's end (its table entry becomes -1), or
+ * behind a negative table entry.  Negative lengths count as 0.
+ *   cached, added [B] int32; table [B][width] int32 (in/out); free_blocks
+ *   [n_free] int32; free_next [1] int64: the number of free blocks already
+ *   taken (in).  All DEVICE arrays.
+ *   N: capacity of the token outputs.  Tokens past N are not written;
+ *   positions, slots, rows of [total, N) get 0, -1, -1.
+ *   offsets [B+1] int64 (out): first token of each request, then the total.
+ *   positions, slots [N] int64, rows [N] int32 (out).
+ *   counts [2] int64 (out): the next free_next (at most n_free), and the
+ *   number of blocks that were lacking.  counts must not hold free_next
+ *   (JET_ERR_SHAPE); a loop alternates two of them, counts being the next
+ *   call's free_next.
+ * 0 <= B <= 8192; 1 <= block_size < 2^30; width, n_free < 2^31; N >= 0.
+ */
+JET_API jet_status jet_kv_slot_map(const int32_t *cached, const int32_t *added, int64_t B,
+                                   int64_t block_size, int32_t *table, int64_t width,
+                                   const int32_t *free_blocks, int64_t n_free,
+                                   const int64_t *free_next, int64_t N, int64_t *offsets,
+                                   int64_t *positions, int64_t *slots, int32_t *rows,
+                                   int64_t *counts, jet_stream_t stream);
+
+/*
+ * One token per row of logits, drawn with temperature, top-k, top-p and min-p
+ * from given uniform numbers, and its log-probabilities (the logp_rollout of
+ * the mismatch metric).  Per row, with m the largest logit:
+ *   z_i = fl32(fl32(x_i - m) * fl32(1 / temperature)), w_i = fl32(e^z_i);
+ * in the order of falling logit, ties by rising index, kept are the tokens of
+ * rank < top_k, of those the ones before which less than top_p of their mass
+ * lies, and of those the ones with w_i >= min_p (the largest w is 1).  Drawn
+ * is the first kept token, in index order, at which the running sum of the
+ * kept weights exceeds u times their sum.  The sums are exact, in 64-bit
+ * integers of w_i 2^45 (rounded to nearest), so the token does not depend on
+ * the batch or the launch.
+ *   logits: row b at logits + b*ld elements, BF16 or FP32 by `dtype`
+ *       (jet_dtype).  -inf and NaN are never drawn; +inf entries share the
+ *       row's whole weight.  ld >= V; rows need no alignment.
+ *   u [B] FP32 in [0, 1) (others are brought to the nearest end).
+ *   temperature, top_p, min_p [B] FP32, top_k [B] int32: one per row, or NULL:
+ *       1, 1, 0, off.  temperature <= 0: the largest logit (lowest index);
+ *       top_k <= 0, top_p >= 1, min_p <= 0 turn their filter off; top_p <= 0
+ *       keeps the first token alone; min_p > 1 counts as 1.
+ *   token [B] int64 (out): -1 for a row with nothing to draw.
+ *   logp [B] FP32 (out): log-probability under the kept, renormalised weights;
+ *   logp_all [B] FP32 (out): under all of them (a greedy row's at temperature
+ *       1); NaN for a row with nothing to draw.
+ *   kept [B] int32 (out): the number of kept tokens.
+ * 0 <= B < 2^28; 1 <= V <= 262144.
+ */
+JET_API jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64_t ld,
+                              const float *u, const float *temperature, const int32_t *top_k,
+                              const float *top_p, const float *min_p, int64_t *token, float *logp,
+                              float *logp_all, int32_t *kept, jet_stream_t stream);
 
 /*
  * Workspace bytes an operation needs for the given sizes (0 if none).
