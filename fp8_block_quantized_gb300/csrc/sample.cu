@@ -14,12 +14,22 @@
 // order of summation, number of CTAs or batch changes a token.
 //
 // A cluster of 1 to 8 CTAs holds one row in its shared memory, read from HBM
-// once; each warp owns a contiguous range of the row, so that a running sum in
-// index order needs only one total per warp.  The filters' cut (the last kept
-// token) is found without a sort of the row: a histogram of counts and masses
-// over 2048 steps of z finds the step it lies in, and the few tokens of that
-// step are ranked against each other; a step with too many of them is split
-// again on the bits of the logits, and one of equal logits by counting.
+// once (cp.async); each warp owns a contiguous range of the row, so that a
+// running sum in index order needs only one total per warp.  Without a filter
+// two passes over shared memory (maximum, weights) and two cluster barriers
+// lead to the draw.
+//
+// The filters' cut (the last kept token) is found without a sort of the row.
+// A bound z_lo is taken below which it cannot lie (top-k: a group of z up to
+// which k of the threads' own maxima lie; top-p: all tokens below w = (1 - p)
+// S / V together weigh less than (1 - p) S; min-p: its own weight).  When at
+// most kListMax tokens lie above it, they go to the first CTA, which sorts
+// them in registers, finds the cut and draws, while the others end.  Flat
+// distributions and large k take the general way: a histogram of counts and
+// masses over 2048 steps of z finds the step the cut lies in, and the few
+// tokens of that step are ranked against each other; a step with too many of
+// them is split again on the bits of the logits, and one of equal logits by
+// counting.
 #include <cooperative_groups.h>
 
 #include "jet_common.cuh"
@@ -28,14 +38,14 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSaThreads = 512;
-constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxWarps = 16;
 constexpr int kBins = 2048;           // steps of 1/64 of z; z <= -32 is bin kBins
 constexpr float kBinsPerZ = 64.0f;
-constexpr int kListCap = 512;         // tokens ranked against each other
+constexpr int kGroups = 128;          // groups of 16 steps: 1/4 of z
+constexpr float kGroupsPerZ = 4.0f;
+constexpr int kListMax = 4096;        // tokens sorted by the first CTA
 constexpr int64_t kSaMaxV = 262144;   // so that the sum of 2^45-scaled weights fits 64 bits
-constexpr float kWeightScale = 0x1p45f;
 
 typedef unsigned long long u64;
 
@@ -51,46 +61,40 @@ struct SampleArgs {
     int chunks_per_warp;
 };
 
-struct Entry {
-    unsigned key;
-    int idx;
-    u64 w;
-};
-
 // What a CTA of the cluster holds besides its slice of the row.  Arrays over
 // ranks are written by the peers and read after a cluster barrier.
 struct Shared {
-    u64 warp_mass[kSaWarps], rank_mass[kMaxCluster], seg_mass[kMaxCluster];
-    unsigned warp_cnt[kSaWarps], rank_cnt[kMaxCluster], seg_cnt[kMaxCluster];
-    float warp_max[kSaWarps], rank_max[kMaxCluster];
-    unsigned warp_lo[kSaWarps], warp_hi[kSaWarps], rank_lo[kMaxCluster], rank_hi[kMaxCluster];
-    u64 scan_mass[kSaWarps];
-    unsigned scan_cnt[kSaWarps];
-    // the selected bin
-    int sel_bin;
-    unsigned sel_before, sel_cnt;
-    u64 sel_mass;
-    unsigned list_n;
-    u64 best;
-    // the cut: the last kept token
-    unsigned cut_key;
+    u64 warp_mass[kMaxWarps], rank_mass[kMaxCluster], seg_mass[kMaxCluster];
+    u64 scan[2][kMaxWarps], sel_mass, cut_entry;
+    unsigned warp_cnt[kMaxWarps], rank_cnt[kMaxCluster];
+    float warp_max[kMaxWarps], rank_max[kMaxCluster];
+    unsigned warp_lo[kMaxWarps], warp_hi[kMaxWarps], rank_lo[kMaxCluster], rank_hi[kMaxCluster];
+    int sel_bin;  // the selected bin
     int cut_idx;
-    u64 cut_mass;
 };
 
+// The general way's histogram, or the list the first CTA sorts.
 struct FilterShared {
-    u64 mass[kBins];
-    unsigned cnt[kBins];
-    Entry list[kListCap];
+    union {
+        // counts, or masses in three 15-bit parts: shared-memory atomics on 32
+        // bits run in hardware, and 2^17 tokens of one CTA cannot overflow a part
+        unsigned hist[3][kBins];
+        u64 sorted[kListMax];  // ~key, index
+    };
+    unsigned grp[kMaxCluster][kGroups];  // threads' maxima by group of z
 };
 
-__device__ __forceinline__ unsigned key_of(float x) {  // orders as the logit does
-    const unsigned b = __float_as_uint(x);
+__device__ __forceinline__ unsigned key_of(float x) {  // orders as the logit does, zeros alike
+    const unsigned b = __float_as_uint(x + 0.0f);
     return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// A logit as the kernel holds it: NaN never drawn, one zero.
-__device__ __forceinline__ float clean(float x) { return x == x ? x + 0.0f : -INFINITY; }
+__device__ __forceinline__ float logit_of(unsigned key) {
+    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// A logit as the kernel uses it: NaN is never drawn.
+__device__ __forceinline__ float clean(float x) { return fmaxf(x, -INFINITY); }
 
 template <bool kBf16>
 struct Elems;
@@ -142,10 +146,67 @@ __device__ __forceinline__ float z_of(float x, float m, float rt) {
     return z <= 0.0f && x > -INFINITY ? z : -INFINITY;
 }
 
-__device__ __forceinline__ u64 mass_of(float w) { return __float2ull_rn(w * kWeightScale); }
+__device__ __forceinline__ u64 mass_of(float w) { return __float2ull_rn(w * 0x1p45f); }
 
-__device__ __forceinline__ int bin_of(float z) {
-    return z > -32.0f ? (int)(z * -kBinsPerZ) : kBins;
+// floor(f s) and ceil(f s) for 0 <= f < 1, exact: f = mant 2^-sh.
+__device__ __forceinline__ u64 share(float f, u64 s, bool up) {
+    const unsigned bits = __float_as_uint(f), e = bits >> 23;
+    const u64 mant = e ? (bits & 0x7FFFFFu) | 0x800000u : bits;
+    const int sh = 150 - (e ? (int)e : 1);  // 24 .. 149
+    const u64 lo = mant * s, hi = __umul64hi(mant, s);
+    u64 q, rest;
+    if (sh < 64) {
+        q = (hi << (64 - sh)) | (lo >> sh);
+        rest = lo << (64 - sh);
+    } else if (sh < 128) {
+        q = sh == 64 ? hi : hi >> (sh - 64);
+        rest = lo | (sh == 64 ? 0 : hi << (128 - sh));
+    } else {
+        q = 0;
+        rest = lo | hi;
+    }
+    return q + (up && rest != 0);
+}
+
+// Sums of round(w 2^45) of one thread, in two 32-bit halves (weights of 1 at
+// most, 512 of them at most): adding 2^23 to w 2^22 leaves its integer part
+// `hi` in the low bits; what is left, times 2^23, is rounded the same way.
+// Exact, and without the 64-bit conversion, whose rate is a quarter of the
+// multiply-adds'.
+struct MassSum {
+    unsigned hi = 0, lo = 0;
+    __device__ __forceinline__ void add2(float w0, float w1) {
+        const float2 w = make_float2(w0, w1), up = make_float2(0x1p22f, 0x1p22f);
+        const float2 big = make_float2(0x1p23f, 0x1p23f);
+        const float2 t = __ffma2_rn(w, up, big);
+        const float2 whole = __fadd2_rn(t, make_float2(-0x1p23f, -0x1p23f));
+        const float2 r = __ffma2_rn(w, up, make_float2(-whole.x, -whole.y));
+        const float2 l = __ffma2_rn(r, big, make_float2(0x1.8p23f, 0x1.8p23f));
+        hi += __float_as_uint(t.x) + __float_as_uint(t.y);
+        lo += __float_as_uint(l.x) + __float_as_uint(l.y);
+    }
+    // n: how many weights were added
+    __device__ __forceinline__ u64 total(unsigned n) const {
+        return ((u64)(hi - n * 0x4B000000u) << 23) + (u64)(int64_t)(int)(lo - n * 0x4B400000u);
+    }
+};
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (unsigned)__cvta_generic_to_shared(dst)),
+                 "l"(src)
+                 : "memory");
+}
+
+template <int kPending>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// A z below which every token weighs less than w (-inf when past the steps).
+__device__ __forceinline__ float z_below(float w) {
+    const float z = w > 0.0f ? fminf(logf(w) - 1e-3f, 0.0f) : -INFINITY;
+    return z > -32.0f ? z : -INFINITY;
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -154,33 +215,49 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
     return v;
 }
 
-template <bool kBf16, bool kFilter>
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 q = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += q;
+    }
+    return v;
+}
+
+template <bool kBf16, bool kFilter, int kThreads>
 struct Sampler {
     typedef Elems<kBf16> El;
     static constexpr int E = El::E;
+    static constexpr int kWarps = kThreads / 32;
 
     const SampleArgs &a;
     cg::cluster_group cl;
     Shared *sh;
     FilterShared *fs;
-    uint4 *row;
+    uint4 *row;   // this warp's chunk c0 is row[0]
     int C, rank, lane, warp;
-    int c0, c1;  // this warp's chunks of the row
-    int shift;   // elements before the row in its first chunk
+    int c0, c1;   // this warp's chunks of the row
+    int shift;    // elements before the row in its first chunk
     float m, rt, min_w;
-    unsigned cut_key;
+    bool regular;  // m and 1/T finite: z needs no care
+    float cut_x;
     int cut_idx;
 
     __device__ Sampler(const SampleArgs &args) : a(args), cl(cg::this_cluster()) {}
 
+    __device__ __forceinline__ float z(float x) const {
+        return regular ? __fmul_rn(__fadd_rn(x, -m), rt) : z_of(x, m, rt);
+    }
+
     // f(x, index) for every element of this warp's range.
     template <typename F>
     __device__ __forceinline__ void each(F f) {
+#pragma unroll 1
         for (int c = c0 + lane; c < c1; c += 32) {
             float v[E];
-            El::load(row[c - c0 + warp * a.chunks_per_warp], v);
+            El::load(row[c - c0], v);
 #pragma unroll
-            for (int e = 0; e < E; ++e) f(v[e], c * E + e - shift);
+            for (int e = 0; e < E; ++e) f(clean(v[e]), c * E + e - shift);
         }
     }
 
@@ -191,10 +268,8 @@ struct Sampler {
     }
 
     __device__ __forceinline__ bool kept(float x, float w, int idx) const {
-        if (x == -INFINITY) return false;
-        if (!kFilter) return true;
-        const unsigned k = key_of(x);
-        return (k > cut_key || (k == cut_key && idx <= cut_idx)) && w >= min_w;
+        if (!kFilter) return true;  // weight 0 where it could matter
+        return (x > cut_x || (x == cut_x && idx <= cut_idx)) && w >= min_w && x > -INFINITY;
     }
 
     // Warp, CTA and cluster totals of a mass and a count; ends with a cluster
@@ -210,7 +285,8 @@ struct Sampler {
         if ((int)threadIdx.x < C) {
             u64 t = 0;
             unsigned n = 0;
-            for (int i = 0; i < kSaWarps; ++i) {
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
                 t += sh->warp_mass[i];
                 n += sh->warp_cnt[i];
             }
@@ -231,126 +307,371 @@ struct Sampler {
         return t;
     }
 
-    // Histogram of this CTA's elements of an interval of keys (level > 0), or
-    // of all by the step of z (level 0).
-    __device__ void histogram(int level, unsigned lo, unsigned hi, int sft) {
-        for (int i = threadIdx.x; i < kBins; i += kSaThreads) {
-            fs->mass[i] = 0;
-            fs->cnt[i] = 0;
+    // The row into shared memory by this thread's own copies, four groups of
+    // them in flight; the maximum of what this thread copied and how many of
+    // them are logits that can be drawn.
+    __device__ float load_row(const typename El::T *x, unsigned &finite) {
+        const int V = a.V;
+        const uint4 *src = reinterpret_cast<const uint4 *>(x - shift);
+        uint4 *dst = row - c0;
+        const int quarter = (a.chunks_per_warp / 32 + 3) / 4 * 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            for (int c = c0 + i * quarter + lane; c < min(c0 + (i + 1) * quarter, c1); c += 32) {
+                if (c * E >= shift && (c + 1) * E - shift <= V) {
+                    cp_async16(dst + c, src + c);
+                } else {  // the row's ragged ends
+                    float v[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int idx = c * E + e - shift;
+                        v[e] = idx >= 0 && idx < V ? El::one(x + idx) : -INFINITY;
+                    }
+                    dst[c] = El::store(v);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        float mx = -INFINITY;
+        unsigned n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i == 0) cp_wait<3>();
+            if (i == 1) cp_wait<2>();
+            if (i == 2) cp_wait<1>();
+            if (i == 3) cp_wait<0>();
+            for (int c = c0 + i * quarter + lane; c < min(c0 + (i + 1) * quarter, c1); c += 32) {
+                float v[E];
+                El::load(dst[c], v);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    mx = fmaxf(mx, v[e]);  // a NaN leaves it as it is
+                    n += v[e] > -INFINITY;
+                }
+            }
+        }
+        finite = n;
+        return mx;
+    }
+
+    // This thread's weights.  Where m and 1/T are finite, x = -inf gives z =
+    // -inf and weight 0 by itself.
+    __device__ __forceinline__ u64 weigh() {
+        MassSum s;
+        unsigned n = 0;
+        const float2 nm = make_float2(-m, -m), r2 = make_float2(rt, rt);
+        if (regular) {
+            for (int c = c0 + lane; c < c1; c += 32) {
+                float v[E];
+                El::load(row[c - c0], v);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 zz = __fmul2_rn(__fadd2_rn(make_float2(clean(v[e]), clean(v[e + 1])), nm), r2);
+                    s.add2(expf(zz.x), expf(zz.y));
+                }
+                n += E;
+            }
+        } else {
+#pragma unroll 1
+            for (int c = c0 + lane; c < c1; c += 32) {
+                float v[E];
+                El::load(row[c - c0], v);
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    s.add2(expf(z_of(clean(v[e]), m, rt)), expf(z_of(clean(v[e + 1]), m, rt)));
+                n += E;
+            }
+        }
+        return s.total(n);
+    }
+
+    // Exclusive sum of v over the CTA's threads, the total, and the total of o.
+    __device__ u64 block_scan(u64 v, u64 &total, u64 o, u64 &total_o) {
+        const u64 inc = warp_scan(v, lane);
+        o = warp_sum(o);
+        __syncthreads();  // the arrays may still be read
+        if (lane == 31) {
+            sh->scan[0][warp] = inc;
+            sh->scan[1][warp] = o;
         }
         __syncthreads();
-        each([&](float x, int) {
-            if (x == -INFINITY) return;
-            const float z = z_of(x, m, rt);
-            int b;
-            if (level == 0) {
-                b = bin_of(z);
-            } else {
-                const unsigned k = key_of(x);
-                b = k >= lo && k <= hi ? (int)((hi - k) >> sft) : kBins;
+        u64 before = inc - v, t = 0;
+        total_o = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) before += t;
+            t += sh->scan[0][w];
+            total_o += sh->scan[1][w];
+        }
+        total = t;
+        return before;
+    }
+
+    // Bitonic sort of the first n of kThreads * N values (the others are ~0 and
+    // stay), N consecutive ones a thread, ascending: strides inside a thread in registers, inside a warp by
+    // shuffles, across warps through `buf` (value i of thread t at
+    // buf[i kThreads + t]).
+    template <int N>
+    __device__ void sort(u64 (&r)[N], unsigned n, u64 *buf) {
+        const int first = (int)threadIdx.x * N;
+#pragma unroll 1
+        for (int size = 2; size < 2 * (int)n; size *= 2) {  // up to the power of two that holds n
+#pragma unroll 1
+            for (int d = size / 2; d >= N; d /= 2) {
+                const int dt = d / N;  // partner thread distance
+                if (dt >= 32) {
+                    __syncthreads();
+#pragma unroll
+                    for (int j = 0; j < N; ++j) buf[j * kThreads + threadIdx.x] = r[j];
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const u64 o = dt >= 32 ? buf[j * kThreads + (threadIdx.x ^ dt)]
+                                           : __shfl_xor_sync(0xffffffffu, r[j], dt);
+                    const bool low = ((first + j) & d) == 0, up = ((first + j) & size) == 0;
+                    r[j] = (low == up) == (r[j] < o) ? r[j] : o;
+                }
             }
-            if (b < kBins) {
-                atomicAdd(&fs->cnt[b], 1u);
-                const u64 w = mass_of(expf(z));
-                if (w) atomicAdd(&fs->mass[b], w);
+#pragma unroll
+            for (int d = N / 2; d >= 1; d /= 2) {
+                if (d >= size) continue;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if (j & d) continue;
+                    const bool up = ((first + j) & size) == 0;
+                    if ((r[j] > r[j | d]) == up) {
+                        const u64 t = r[j];
+                        r[j] = r[j | d];
+                        r[j | d] = t;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+    // The list's entries (N a thread) sorted by falling logit, their masses,
+    // and the mass before this thread's.
+    template <int N>
+    __device__ u64 sorted_list(unsigned n, unsigned k, u64 (&r)[N], u64 (&w)[N], u64 &S_k) {
+        const unsigned first = threadIdx.x * N;
+#pragma unroll
+        for (int j = 0; j < N; ++j) r[j] = first + j < n ? fs->sorted[first + j] : ~0ull;
+        __syncthreads();
+        sort<N>(r, n, fs->sorted);
+        u64 own = 0, own_k = 0, total;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            w[j] = first + j < n ? mass_of(weight_of(~(unsigned)(r[j] >> 32))) : 0;
+            own += w[j];
+            own_k += first + j < k ? w[j] : 0;
+        }
+        return block_scan(own, total, own_k, S_k);
+    }
+
+    __device__ __forceinline__ float weight_of(unsigned key) const {
+        return expf(z_of(logit_of(key), m, rt));
+    }
+
+    // The first CTA's part of the list way: n candidates in fs->sorted, which
+    // hold the cut.  The kept prefix is sorted by index, and the draw is where
+    // its running sum crosses u S.
+    template <int N>
+    __device__ void draw_from_list(int64_t b, unsigned n, unsigned k, bool k_on, float p, u64 S_all) {
+        u64 r[N], w[N], S_k, S, nk, total;
+        const unsigned first = threadIdx.x * N;
+        u64 at = sorted_list<N>(n, k, r, w, S_k);
+        const u64 target = p < 1.0f ? share(p, k_on ? S_k : S_all, true) : ~0ull;
+        u64 own = 0, own_n = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const unsigned i = first + j;
+            const bool in = i < n && i < k && (i == 0 || at < target) &&
+                            weight_of(~(unsigned)(r[j] >> 32)) >= min_w;
+            at += w[j];
+            own += in ? w[j] : 0;
+            own_n += in;
+            r[j] = in ? (r[j] << 32) | (r[j] >> 32) : ~0ull;  // index, ~key
+        }
+        block_scan(own, S, own_n, nk);
+        sort<N>(r, (unsigned)nk, fs->sorted);
+        own = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            w[j] = first + j < (unsigned)nk ? mass_of(weight_of(~(unsigned)r[j])) : 0;
+            own += w[j];
+        }
+        at = block_scan(own, total, 0, total);
+        const u64 aim = share(uniform(b), S, false);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (at <= aim && at + w[j] > aim) put(b, (int)(r[j] >> 32), w[j], S, S_all, (unsigned)nk);
+            at += w[j];
+        }
+    }
+
+    // The first CTA's part of a filter's cut: n tokens in fs->sorted, one of
+    // which is the last whose rank is below target_cnt or the mass before
+    // which is below target_mass; it goes to every CTA.
+    template <int N>
+    __device__ void cut_from_list(unsigned n, bool by_mass, unsigned target_cnt, u64 target_mass,
+                                  unsigned base_cnt, u64 base_mass) {
+        u64 r[N], w[N], unused;
+        const unsigned first = threadIdx.x * N;
+        u64 at = base_mass + sorted_list<N>(n, 0, r, w, unused);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const unsigned rank_ = base_cnt + first + j;
+            const u64 end = at + w[j];
+            const bool in = by_mass ? at < target_mass : rank_ < target_cnt;
+            const bool next = by_mass ? end < target_mass : rank_ + 1 < target_cnt;
+            if (first + j < n && in && (!next || first + j + 1 == n)) sh->cut_entry = r[j];
+            at = end;
+        }
+        __syncthreads();
+        const u64 entry = sh->cut_entry;
+        to_all(&sh->cut_entry, entry);
+    }
+
+    // The tokens for which f(x) into the first CTA's list, if there are at most
+    // kListMax; their number.  Ends with a cluster barrier.
+    template <typename F>
+    __device__ unsigned gather(F f) {
+        u64 hit[3] = {0, 0, 0};  // of this thread's elements, 136 at most
+        unsigned mine = 0;
+        int at = 0;
+#pragma unroll 1
+        for (int c = c0 + lane; c < c1; c += 32, at += E) {
+            float v[E];
+            El::load(row[c - c0], v);
+            unsigned bits = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) bits |= f(clean(v[e])) ? 1u << e : 0u;
+            mine += __popc(bits);
+            if (at < 64) hit[0] |= (u64)bits << at;
+            else if (at < 128) hit[1] |= (u64)bits << (at - 64);
+            else hit[2] |= (u64)bits << (at - 128);
+        }
+        totals(0, mine);
+        const unsigned n = all_cnt();
+        if (n <= kListMax) {
+            unsigned to = (unsigned)warp_scan(mine, lane) - mine;
+            for (int r = 0; r < rank; ++r) to += sh->rank_cnt[r];
+            for (int w = 0; w < warp; ++w) to += sh->warp_cnt[w];
+            u64 *list = cl.map_shared_rank(fs, 0)->sorted;
+            for (int i0 = 0; i0 < 192; i0 += 64) {
+                u64 bits = i0 == 0 ? hit[0] : i0 == 64 ? hit[1] : hit[2];
+                for (; bits; bits &= bits - 1) {
+                    const int i = i0 + __ffsll((long long)bits) - 1;
+                    const int c = c0 + lane + 32 * (i / E), e = i % E;
+                    const float xv = El::one(reinterpret_cast<const typename El::T *>(row + (c - c0)) + e);
+                    list[to++] = ((u64)~key_of(xv) << 32) | (unsigned)(c * E + e - shift);
+                }
+            }
+            cl.sync();
+        }
+        return n;
+    }
+
+    __device__ __forceinline__ float uniform(int64_t b) const {
+        const float u = a.u[b];
+        return u >= 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
+    }
+
+    // log(w / s), through log1p where the share is near one.
+    static __device__ __forceinline__ float log_share(u64 w, u64 s) {
+        const float sf = __ull2float_rn(s);
+        return 2 * w > s ? log1pf(-__fdiv_rn(__ull2float_rn(s - w), sf))
+                         : logf(__fdiv_rn(__ull2float_rn(w), sf));
+    }
+
+    __device__ void put(int64_t b, int idx, u64 w, u64 S, u64 S_all, unsigned n_kept) {
+        a.token[b] = idx;
+        a.logp[b] = log_share(w, S);
+        a.logp_all[b] = log_share(w, S_all);
+        a.kept[b] = (int)n_kept;
+    }
+
+    // Histogram of this CTA's elements with z > z_lo by the step of z (level
+    // 0), or of those of an interval of keys: masses or counts.
+    __device__ void histogram(bool by_mass, int level, float z_lo, unsigned lo, unsigned hi, int sft) {
+        for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&fs->hist[0][0])[i] = 0;
+        __syncthreads();
+        const float x_lo = logit_of(lo), x_hi = logit_of(hi);
+        each([&](float x, int) {
+            const float zx = z(x);
+            if (level == 0 ? zx > z_lo : x >= x_lo && x <= x_hi && x > -INFINITY) {
+                const int b = level == 0 ? (int)(zx * -kBinsPerZ) : (int)((hi - key_of(x)) >> sft);
+                if (by_mass) {
+                    const u64 w = mass_of(expf(zx));
+                    atomicAdd(&fs->hist[0][b], (unsigned)w & 0x7FFFu);
+                    atomicAdd(&fs->hist[1][b], (unsigned)(w >> 15) & 0x7FFFu);
+                    atomicAdd(&fs->hist[2][b], (unsigned)(w >> 30));
+                } else {
+                    atomicAdd(&fs->hist[0][b], 1u);
+                }
             }
         });
         cl.sync();
     }
 
-    // The first bin whose end reaches the target (a count or a mass), given
-    // what lies before the histogram; its place goes to every CTA.
-    __device__ void select(bool by_mass, unsigned target_cnt, double target_mass, unsigned base_cnt,
-                           u64 base_mass) {
-        const int seg = kBins / C;                         // bins this CTA merges
-        const int per = seg > kSaThreads ? seg / kSaThreads : 1;
-        u64 bm[kBins / kSaThreads];
-        unsigned bc[kBins / kSaThreads];
-        u64 tm = 0;
-        unsigned tc = 0;
+    // The first bin whose end reaches the target, given what lies before the
+    // histogram, with what lies before the bin, at every CTA.
+    __device__ void select(bool by_mass, u64 target, u64 base) {
+        constexpr int kPer = kBins / kThreads;           // bins a thread at most
+        const int seg = kBins / C;                       // bins this CTA merges
+        const int per = seg > kThreads ? seg / kThreads : 1;
+        u64 bin[kPer], own = 0;
         const int first = rank * seg + (int)threadIdx.x * per;
         const bool active = (int)threadIdx.x * per < seg;
 #pragma unroll
-        for (int j = 0; j < kBins / kSaThreads; ++j) {
-            bm[j] = 0;
-            bc[j] = 0;
+        for (int j = 0; j < kPer; ++j) {
+            bin[j] = 0;
             if (active && j < per) {
-                for (int r = 0; r < C; ++r) {
-                    const FilterShared *o = cl.map_shared_rank(fs, r);
-                    bm[j] += o->mass[first + j];
-                    bc[j] += o->cnt[first + j];
+                // a peer past the cluster is read as this one and not counted, so
+                // that all the loads are in flight together
+                unsigned part[kMaxCluster];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (i > 0 && !by_mass) break;
+#pragma unroll
+                    for (int r = 0; r < kMaxCluster; ++r)
+                        part[r] = cl.map_shared_rank(fs, r < C ? r : rank)->hist[i][first + j];
+                    u64 sum = 0;
+#pragma unroll
+                    for (int r = 0; r < kMaxCluster; ++r) sum += r < C ? part[r] : 0;
+                    bin[j] += sum << (15 * i);
                 }
-                tm += bm[j];
-                tc += bc[j];
+                own += bin[j];
             }
         }
-        u64 im = tm;  // inclusive over the CTA's threads
-        unsigned ic = tc;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 q = __shfl_up_sync(0xffffffffu, im, o);
-            const unsigned n = __shfl_up_sync(0xffffffffu, ic, o);
-            if (lane >= o) {
-                im += q;
-                ic += n;
-            }
-        }
-        if (lane == 31) {
-            sh->scan_mass[warp] = im;
-            sh->scan_cnt[warp] = ic;
-        }
-        if (threadIdx.x == 0) {
-            sh->sel_bin = kBins;
-            sh->list_n = 0;
-            sh->best = 0;
-        }
-        __syncthreads();
-        u64 sm = 0;
-        unsigned sc = 0;
-        for (int w = 0; w < kSaWarps; ++w) {
-            if (w < warp) {
-                im += sh->scan_mass[w];
-                ic += sh->scan_cnt[w];
-            }
-            sm += sh->scan_mass[w];
-            sc += sh->scan_cnt[w];
-        }
-        to_all(&sh->seg_mass[rank], sm);
-        to_all(&sh->seg_cnt[rank], sc);
+        u64 total, unused;
+        u64 at = base + block_scan(own, total, 0, unused);
+        if (threadIdx.x == 0) sh->sel_bin = kBins;
+        to_all(&sh->seg_mass[rank], total);
         cl.sync();
-        u64 pm = base_mass + im - tm;
-        unsigned pc = base_cnt + ic - tc;
-        for (int r = 0; r < rank; ++r) {
-            pm += sh->seg_mass[r];
-            pc += sh->seg_cnt[r];
-        }
+        for (int r = 0; r < rank; ++r) at += sh->seg_mass[r];
 #pragma unroll
-        for (int j = 0; j < kBins / kSaThreads; ++j) {
+        for (int j = 0; j < kPer; ++j) {
             if (active && j < per) {
-                const u64 em = pm + bm[j];
-                const unsigned ec = pc + bc[j];
-                const bool before = by_mass ? (double)pm < target_mass : pc < target_cnt;
-                const bool after = by_mass ? (double)em < target_mass : ec < target_cnt;
-                if (before && !after) {
+                if (at < target && at + bin[j] >= target) {
                     for (int r = 0; r < C; ++r) {
                         Shared *o = cl.map_shared_rank(sh, r);
                         o->sel_bin = first + j;
-                        o->sel_before = pc;
-                        o->sel_mass = pm;
-                        o->sel_cnt = bc[j];
+                        o->sel_mass = at;
                     }
                 }
-                pm = em;
-                pc = ec;
+                at += bin[j];
             }
         }
         cl.sync();
     }
 
     // The cut among tokens of one logit: the first `n` of them in index order.
-    __device__ void cut_ties(unsigned key, unsigned n, u64 mass) {
+    __device__ void cut_ties(float x, unsigned n) {
         unsigned mine = 0;
-        each([&](float x, int) { mine += x > -INFINITY && key_of(x) == key; });
+        each([&](float v, int) { mine += v == x; });
         totals(0, mine);
         unsigned before = 0;
         for (int r = 0; r < rank; ++r) before += sh->rank_cnt[r];
@@ -362,115 +683,70 @@ struct Sampler {
                 float v[E];
                 unsigned t = 0;
                 if (c < c1) {
-                    El::load(row[c - c0 + warp * a.chunks_per_warp], v);
+                    El::load(row[c - c0], v);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) t += v[e] > -INFINITY && key_of(v[e]) == key;
+                    for (int e = 0; e < E; ++e) t += v[e] == x;
                 }
-                unsigned inc = t;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const unsigned q = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += q;
-                }
+                const unsigned inc = (unsigned)warp_scan(t, lane);
                 if (before + inc - t < n && n <= before + inc) {
                     unsigned at = before + inc - t;
                     int idx = 0;
 #pragma unroll
                     for (int e = 0; e < E; ++e)
-                        if (v[e] > -INFINITY && key_of(v[e]) == key && ++at == n)
-                            idx = c * E + e - shift;
-                    for (int r = 0; r < C; ++r) {
-                        Shared *o = cl.map_shared_rank(sh, r);
-                        o->cut_key = key;
-                        o->cut_idx = idx;
-                        o->cut_mass = mass;
-                    }
+                        if (v[e] == x && ++at == n) idx = c * E + e - shift;
+                    for (int r = 0; r < C; ++r) cl.map_shared_rank(sh, r)->cut_idx = idx;
                 }
                 before += __shfl_sync(0xffffffffu, inc, 31);
             }
         }
         cl.sync();
-        cut_key = sh->cut_key;
+        cut_x = x;
         cut_idx = sh->cut_idx;
     }
 
-    // The cut of a filter: the last token whose rank is below target_cnt, or
-    // the mass before which is below target_mass.  The caller has checked that
-    // the target lies inside the row.  Returns the kept mass.
-    __device__ u64 cut(bool by_mass, unsigned target_cnt, double target_mass) {
-        unsigned lo = 0, hi = 0xFFFFFFFFu, base_cnt = 0;
-        u64 base_mass = 0;
+    // The cut of a filter: the last token whose rank is below the target (a
+    // count), or the mass before which is.  The caller has checked that the
+    // target lies inside the row, at z > z_lo.
+    __device__ void cut(bool by_mass, u64 target, float z_lo) {
+        unsigned lo = 0, hi = 0xFFFFFFFFu;
+        u64 base = 0;  // mass or count before the interval
         int sft = 0;
+        // Step b is exactly -(b + 1) / 64 < z <= -b / 64 (the product with 64 is
+        // exact); whole steps are counted.
+        z_lo = ceilf(fmaxf(z_lo, -32.0f) * -kBinsPerZ) * (-1.0f / kBinsPerZ);
         for (int level = 0;; ++level) {
-            histogram(level, lo, hi, sft);
-            select(by_mass, target_cnt, target_mass, base_cnt, base_mass);
+            histogram(by_mass, level, z_lo, lo, hi, sft);
+            select(by_mass, target, base);
             const int bin = sh->sel_bin;
-            unsigned n = sh->sel_cnt;
             if (bin < kBins) {
-                base_cnt = sh->sel_before;
-                base_mass = sh->sel_mass;
+                base = sh->sel_mass;
             } else {  // level 0 only: past the steps, among weights that round to zero
-                for (int r = 0; r < C; ++r) {
-                    base_cnt += sh->seg_cnt[r];
-                    base_mass += sh->seg_mass[r];
-                }
-                n = 0xFFFFFFFFu;
+                for (int r = 0; r < C; ++r) base += sh->seg_mass[r];
             }
+            // the bin's tokens: an interval of z, or of logits
+            const float z0 = bin < kBins ? (float)(bin + 1) * (-1.0f / kBinsPerZ) : -INFINITY;
+            const float z1 = (float)bin * (-1.0f / kBinsPerZ);
+            const unsigned span = (unsigned)min((u64)(bin + 1) << sft, (u64)(hi - lo) + 1) - 1;
+            const float x0 = logit_of(hi - span), x1 = logit_of(hi - ((unsigned)bin << sft));
             auto in_bin = [&](float x) {
-                if (x == -INFINITY) return false;
-                if (level == 0) return bin_of(z_of(x, m, rt)) == bin;
-                const unsigned k = key_of(x);
-                return k >= lo && k <= hi && (int)((hi - k) >> sft) == bin;
+                if (level > 0) return x >= x0 && x <= x1 && x > -INFINITY;
+                const float zx = z(x);
+                return zx <= z1 && (zx > z0 || bin == kBins) && x > -INFINITY;
             };
-            if (n <= kListCap) {
-                Shared *s0 = cl.map_shared_rank(sh, 0);
-                FilterShared *f0 = cl.map_shared_rank(fs, 0);
-                each([&](float x, int idx) {
-                    if (in_bin(x)) {
-                        const unsigned at = atomicAdd(&s0->list_n, 1u);
-                        if (at < kListCap)
-                            f0->list[at] = {key_of(x), idx, mass_of(expf(z_of(x, m, rt)))};
-                    }
-                });
-                cl.sync();
+            const unsigned n = gather(in_bin);
+            if (n <= kListMax) {
                 if (rank == 0) {
-                    for (unsigned i = threadIdx.x; i < n; i += kSaThreads) {
-                        const Entry me = fs->list[i];
-                        unsigned ahead = 0;
-                        u64 before = 0;
-                        for (unsigned j = 0; j < n; ++j) {
-                            const Entry o = fs->list[j];
-                            if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) {
-                                ++ahead;
-                                before += o.w;
-                            }
-                        }
-                        const bool in = by_mass ? (double)(base_mass + before) < target_mass
-                                                : base_cnt + ahead < target_cnt;
-                        if (in) atomicMax(&sh->best, ((u64)(ahead + 1) << 32) | i);
-                    }
-                    __syncthreads();
-                    const Entry last = fs->list[(unsigned)sh->best];
-                    u64 part = 0;  // mass of the list up to and including the last
-                    for (unsigned i = threadIdx.x; i < n; i += kSaThreads) {
-                        const Entry o = fs->list[i];
-                        if (o.key > last.key || (o.key == last.key && o.idx <= last.idx)) part += o.w;
-                    }
-                    part = warp_sum(part);
-                    if (lane == 0) sh->scan_mass[warp] = part;
-                    __syncthreads();
-                    u64 total = base_mass;
-                    for (int w = 0; w < kSaWarps; ++w) total += sh->scan_mass[w];
-                    to_all(&sh->cut_key, last.key);
-                    to_all(&sh->cut_idx, last.idx);
-                    to_all(&sh->cut_mass, total);
+                    const unsigned bc = by_mass ? 0 : (unsigned)base, tc = by_mass ? 0 : (unsigned)target;
+                    const u64 bm = by_mass ? base : 0;
+                    if (n <= kThreads) cut_from_list<1>(n, by_mass, tc, target, bc, bm);
+                    else cut_from_list<kListMax / kThreads>(n, by_mass, tc, target, bc, bm);
                 }
                 cl.sync();
-                cut_key = sh->cut_key;
-                cut_idx = sh->cut_idx;
-                return sh->cut_mass;
+                cut_x = logit_of(~(unsigned)(sh->cut_entry >> 32));
+                cut_idx = (int)(unsigned)sh->cut_entry;
+                return;
             }
-            // too many to rank: the bin's own interval of keys
+            // too many to sort: the bin's own interval of keys
             unsigned klo = 0xFFFFFFFFu, khi = 0;
             each([&](float x, int) {
                 if (in_bin(x)) {
@@ -486,7 +762,7 @@ struct Sampler {
             }
             __syncthreads();
             if ((int)threadIdx.x < C) {
-                for (int w = 0; w < kSaWarps; ++w) {
+                for (int w = 0; w < kWarps; ++w) {
                     klo = min(klo, sh->warp_lo[w]);
                     khi = max(khi, sh->warp_hi[w]);
                 }
@@ -501,72 +777,57 @@ struct Sampler {
                 hi = max(hi, sh->rank_hi[r]);
             }
             if (lo == hi) {  // one logit: the first so many in index order
-                const float x = __uint_as_float(lo ^ ((lo >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-                const u64 w = mass_of(expf(z_of(x, m, rt)));
-                unsigned q;
-                if (!by_mass) {
-                    q = target_cnt - base_cnt;
-                } else {  // token i of them is kept when base + i w < target
-                    const double at = w ? (target_mass - (double)base_mass) / (double)w : 1.0;
-                    q = at < 1.0 ? 1u : (unsigned)at;
-                    while (q > 1 && (double)(base_mass + (q - 1) * w) >= target_mass) --q;
-                    while (w && q < n && (double)(base_mass + q * w) < target_mass) ++q;
-                }
-                const u64 mass = base_mass + q * w;
-                cut_ties(lo, q, mass);
-                return mass;
+                const u64 w = mass_of(weight_of(lo));
+                // by mass, token i of them is kept when base + i w < target
+                const u64 q = !by_mass ? target - base : w ? (target - base + w - 1) / w : 1;
+                cut_ties(logit_of(lo), (unsigned)q);
+                return;
             }
-            const unsigned range = hi - lo;
-            sft = max(0, 32 - __clz((int)range) - 11);  // range >> sft < 2048
+            sft = max(0, 32 - __clz((int)(hi - lo)) - 11);  // (hi - lo) >> sft < 2048
         }
     }
 
+    // Mass and number of the kept tokens (all of them at every CTA).
+    __device__ u64 kept_totals() {
+        MassSum s;
+        unsigned n = 0, cnt = 0;
+#pragma unroll 1
+        for (int c = c0 + lane; c < c1; c += 32, n += E) {
+            float v[E], w[E];
+            El::load(row[c - c0], v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float x = clean(v[e]);
+                w[e] = expf(z(x));
+                const bool in = kept(x, w[e], c * E + e - shift);
+                w[e] = in ? w[e] : 0.0f;
+                cnt += in;
+            }
+#pragma unroll
+            for (int e = 0; e < E; e += 2) s.add2(w[e], w[e + 1]);
+        }
+        totals(s.total(n), cnt);
+        return all_mass();
+    }
+
     __device__ void run(int64_t b) {
-        const int V = a.V;
         const typename El::T *x = static_cast<const typename El::T *>(a.x) + b * a.ld;
         shift = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(typename El::T));
-        const int chunks = (shift + V + E - 1) / E;
-        c0 = min((rank * kSaWarps + warp) * a.chunks_per_warp, chunks);
+        const int chunks = (shift + a.V + E - 1) / E;
+        c0 = min((rank * kWarps + warp) * a.chunks_per_warp, chunks);
         c1 = min(c0 + a.chunks_per_warp, chunks);
-        // the row into shared memory, and its maximum
-        const uint4 *src = reinterpret_cast<const uint4 *>(x - shift);
-        float mx = -INFINITY;
-        constexpr int kLoads = 4;
-        for (int base = c0; base < c1; base += 32 * kLoads) {
-            uint4 t[kLoads];
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int c = base + 32 * i + lane;
-                if (c < c1 && c * E >= shift && (c + 1) * E - shift <= V) t[i] = src[c];
-            }
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int c = base + 32 * i + lane;
-                if (c >= c1) break;
-                float v[E];
-                if (c * E >= shift && (c + 1) * E - shift <= V) {
-                    El::load(t[i], v);
-                } else {  // the row's ragged ends
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const int idx = c * E + e - shift;
-                        v[e] = idx >= 0 && idx < V ? El::one(x + idx) : -INFINITY;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    v[e] = clean(v[e]);
-                    mx = fmaxf(mx, v[e]);
-                }
-                row[c - c0 + warp * a.chunks_per_warp] = El::store(v);
-            }
-        }
+        unsigned cnt;
+        const float own_max = load_row(x, cnt);
+        float mx = own_max;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (lane == 0) sh->warp_max[warp] = mx;
+        if (kFilter)
+            for (int i = threadIdx.x; i < kGroups; i += kThreads) fs->grp[rank][i] = 0;
         __syncthreads();
         if ((int)threadIdx.x < C) {
-            for (int w = 0; w < kSaWarps; ++w) mx = fmaxf(mx, sh->warp_max[w]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh->warp_max[w]);
             to_all(&sh->rank_max[rank], mx);
         }
         cl.sync();
@@ -581,129 +842,155 @@ struct Sampler {
             }
             return;
         }
-        const float T = a.temperature ? a.temperature[b] : 1.0f;
+        const float T = kFilter && a.temperature ? a.temperature[b] : 1.0f;
         const bool greedy = !(T > 0.0f);
         rt = __fdiv_rn(1.0f, greedy ? 1.0f : T);
-        u64 mass = 0;
-        unsigned cnt = 0;
-        each([&](float xv, int) {
-            mass += mass_of(expf(z_of(xv, m, rt)));
-            cnt += xv > -INFINITY;
-        });
-        totals(mass, cnt);
+        regular = m < INFINITY && rt > 0.0f && rt < INFINITY;
+        int k = 0x7FFFFFFF;
+        float p = 1.0f;
+        min_w = 0.0f;
+        cut_x = -INFINITY;
+        cut_idx = 0;
+        if (kFilter) {
+            k = greedy ? 1 : a.top_k && a.top_k[b] > 0 ? a.top_k[b] : 0x7FFFFFFF;
+            if (a.top_p && a.top_p[b] < 1.0f) p = a.top_p[b];
+            if (a.min_p) min_w = fminf(fmaxf(a.min_p[b], 0.0f), 1.0f);
+        }
+        if (kFilter && k > 1 && k < 0x7FFFFFFF) {  // the threads' maxima, to every CTA
+            const float zx = z_of(own_max, m, rt);
+            if (zx > -32.0f) atomicAdd(&fs->grp[rank][(int)(zx * -kGroupsPerZ)], 1u);
+            __syncthreads();
+            for (int i = threadIdx.x; i < C * kGroups; i += kThreads)
+                if (i / kGroups != rank)
+                    cl.map_shared_rank(fs, i / kGroups)->grp[rank][i % kGroups] = fs->grp[rank][i % kGroups];
+        }
+        totals(weigh(), cnt);
         const u64 S_all = all_mass();
         u64 S = S_all;
         unsigned n_kept = all_cnt();
-        min_w = 0.0f;
-        cut_key = 0;
-        cut_idx = 0x7FFFFFFF;
-        if (kFilter) {
-            const int k = greedy ? 1 : a.top_k && a.top_k[b] > 0 ? a.top_k[b] : 0x7FFFFFFF;
-            const float p = a.top_p ? a.top_p[b] : 1.0f;
-            const float mp = a.min_p ? a.min_p[b] : 0.0f;
-            min_w = mp > 0.0f ? fminf(mp, 1.0f) : 0.0f;
+        if (kFilter && (k < 0x7FFFFFFF || p < 1.0f || min_w > 0.0f)) {
             const unsigned finite = n_kept;
+            const bool k_on = (unsigned)k < finite;
             bool cut_any = min_w > 0.0f;
-            if (k == 1) {
-                cut_ties(key_of(m), 1, mass_of(1.0f));
+            if (k == 1 || p <= 0.0f) {
+                cut_ties(m, 1);
                 cut_any = true;
-            } else {
-                u64 S_k = S_all;
-                if ((unsigned)k < finite) {
-                    S_k = cut(false, (unsigned)k, 0.0);
-                    cut_any = true;
+            } else if (k_on || p < 1.0f || cut_any) {
+                // no token at or below z_lo matters: the highest of the filters' bounds
+                float z_lo = min_w > 0.0f ? z_below(min_w) : -INFINITY;
+                float z_p = -INFINITY;
+                if (!k_on && p < 1.0f)
+                    z_p = z_below(0.999f * (1.0f - p) * (__ull2float_rn(S_all) * 0x1p-45f) / (float)a.V);
+                z_lo = fmaxf(z_lo, z_p);
+                if (k_on) {
+                    unsigned g4[kGroups / 32], sum = 0;  // every warp scans the groups itself
+#pragma unroll
+                    for (int j = 0; j < kGroups / 32; ++j) {
+                        g4[j] = 0;
+                        for (int r = 0; r < C; ++r) g4[j] += fs->grp[r][lane * (kGroups / 32) + j];
+                        sum += g4[j];
+                    }
+                    unsigned upto = (unsigned)warp_scan(sum, lane) - sum;
+                    int g = kGroups;
+#pragma unroll
+                    for (int j = kGroups / 32 - 1; j >= 0; --j) {
+                        unsigned t = upto;
+                        for (int i = 0; i <= j; ++i) t += g4[i];
+                        if (t >= (unsigned)k) g = lane * (kGroups / 32) + j;
+                    }
+                    g = __reduce_min_sync(0xffffffffu, g);
+                    const float z_k = g < kGroups ? (float)(g + 1) * (-1.0f / kGroupsPerZ) : -INFINITY;
+                    // with top-p the mass of all k counts, whatever min-p cuts
+                    z_lo = p < 1.0f ? z_k : fmaxf(z_lo, z_k);
                 }
-                if (p < 1.0f) {
-                    const double target = (double)fmaxf(p, 0.0f) * (double)S_k;
-                    if (target > 0.0) cut(true, 0, target);
-                    else cut_ties(key_of(m), 1, mass_of(1.0f));
+                const bool everything = finite <= kListMax;
+                if (everything || z_lo > -INFINITY) {
+                    auto in_list = [&](float xv) {
+                        return everything ? xv > -INFINITY : z(xv) > z_lo;
+                    };
+                    const unsigned n_c = gather(in_list);
+                    if (n_c <= kListMax) {
+                        if (rank != 0) return;
+                        const unsigned kk = k_on ? (unsigned)k : finite;
+                        if (n_c <= kThreads) draw_from_list<1>(b, n_c, kk, k_on, p, S_all);
+                        else if (n_c <= 4 * kThreads) draw_from_list<4>(b, n_c, kk, k_on, p, S_all);
+                        else draw_from_list<kListMax / kThreads>(b, n_c, kk, k_on, p, S_all);
+                        return;
+                    }
+                }
+                for (int by_mass = 0; by_mass < 2; ++by_mass) {
+                    if (by_mass ? p >= 1.0f : !k_on) continue;
+                    u64 target = (u64)(unsigned)k;
+                    if (by_mass) {
+                        const float own_min = min_w;  // min-p does not count here
+                        min_w = 0.0f;
+                        target = share(p, k_on ? kept_totals() : S_all, true);
+                        min_w = own_min;
+                    }
+                    cut(by_mass, target, by_mass ? z_p : -INFINITY);
                     cut_any = true;
                 }
             }
             if (cut_any) {
-                mass = 0;
-                cnt = 0;
-                each([&](float xv, int idx) {
-                    const float w = expf(z_of(xv, m, rt));
-                    if (kept(xv, w, idx)) {
-                        mass += mass_of(w);
-                        ++cnt;
-                    }
-                });
-                totals(mass, cnt);
-                S = all_mass();
+                S = kept_totals();
                 n_kept = all_cnt();
             }
         }
-        // the draw: the CTA, the warp, then the lane and element at which the
-        // running sum exceeds u S
-        float u = a.u[b];
-        u = u >= 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
-        const double target = (double)u * (double)S;
+        // the draw: the CTA and the warp range in which the running sum exceeds
+        // u S; then all warps sum a part of that range, then a lane its own
+        const u64 aim = share(uniform(b), S, false);
         u64 before = 0;
         for (int r = 0; r < rank; ++r) before += sh->rank_mass[r];
-        for (int w = 0; w < warp; ++w) before += sh->warp_mass[w];
-        if ((double)before > target || !((double)(before + sh->warp_mass[warp]) > target)) return;
-        for (int base = c0; base < c1; base += 32) {
-            const int c = base + lane;
-            u64 w[E], t = 0;
-            if (c < c1) {
-                float v[E];
-                El::load(row[c - c0 + warp * a.chunks_per_warp], v);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float wf = expf(z_of(v[e], m, rt));
-                    w[e] = kept(v[e], wf, c * E + e - shift) ? mass_of(wf) : 0;
-                    t += w[e];
-                }
-            }
-            u64 inc = t;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 q = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += q;
-            }
-            u64 at = before + inc - t;
-            if (!((double)at > target) && (double)(at + t) > target) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    if (!((double)at > target) && (double)(at + w[e]) > target) {
-                        a.token[b] = c * E + e - shift;
-                        a.logp[b] = log_share(w[e], S);
-                        a.logp_all[b] = log_share(w[e], S_all);
-                        a.kept[b] = (int)n_kept;
-                    }
-                    at += w[e];
-                }
-            }
-            before += __shfl_sync(0xffffffffu, inc, 31);
-            if ((double)before > target) break;
+        if (before > aim || before + sh->rank_mass[rank] <= aim) return;
+        int wi = 0;
+        while (wi < kWarps - 1 && before + sh->warp_mass[wi] <= aim) before += sh->warp_mass[wi++];
+        const typename El::T *src =
+            reinterpret_cast<const typename El::T *>(row + (wi - warp) * a.chunks_per_warp);
+        const int r0 = min((rank * kWarps + wi) * a.chunks_per_warp, chunks);
+        const int n = (min(r0 + a.chunks_per_warp, chunks) - r0) * E;  // elements of the range
+        const int per = (n + kThreads - 1) / kThreads;
+        const int l0 = min((int)threadIdx.x * per, n), l1 = min(l0 + per, n);
+        auto weight = [&](int i) -> u64 {
+            const float xv = clean(El::one(src + i)), w = expf(z(xv));
+            return kept(xv, w, r0 * E + i - shift) ? mass_of(w) : 0;
+        };
+        u64 own = 0, all;
+#pragma unroll 1
+        for (int i = l0; i < l1; ++i) own += weight(i);
+        before += block_scan(own, all, 0, all);
+        if (before > aim || before + own <= aim) return;
+#pragma unroll 1
+        for (int i = l0; i < l1; ++i) {
+            const u64 w = weight(i);
+            if (before <= aim && before + w > aim) put(b, r0 * E + i - shift, w, S, S_all, n_kept);
+            before += w;
         }
-    }
-
-    // log(w / s), through log1p where the share is near one.
-    static __device__ __forceinline__ float log_share(u64 w, u64 s) {
-        const float sf = __ull2float_rn(s);
-        return 2 * w > s ? log1pf(-__fdiv_rn(__ull2float_rn(s - w), sf))
-                         : logf(__fdiv_rn(__ull2float_rn(w), sf));
     }
 };
 
-template <bool kBf16, bool kFilter>
-__global__ void __launch_bounds__(kSaThreads) sample_kernel(const SampleArgs a) {
+template <bool kBf16, bool kFilter, int kThreads>
+__global__ void __launch_bounds__(kThreads, (kThreads == 256 ? 3 : 2) - kFilter)
+sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     jet::griddep_launch_dependents();
     jet::griddep_wait();
-    Sampler<kBf16, kFilter> s(a);
+    Sampler<kBf16, kFilter, kThreads> s(a);
     s.C = (int)s.cl.num_blocks();
     s.rank = (int)s.cl.block_rank();
     s.lane = threadIdx.x & 31;
     s.warp = threadIdx.x >> 5;
+    constexpr size_t kHead = (sizeof(Shared) + 15) / 16 * 16;
     s.sh = reinterpret_cast<Shared *>(smem);
-    s.fs = reinterpret_cast<FilterShared *>(smem + (sizeof(Shared) + 15) / 16 * 16);
-    s.row = reinterpret_cast<uint4 *>(smem + (sizeof(Shared) + 15) / 16 * 16 +
-                                      (kFilter ? sizeof(FilterShared) : 0));
+    s.fs = reinterpret_cast<FilterShared *>(smem + kHead);
+    s.row = reinterpret_cast<uint4 *>(smem + kHead + (kFilter ? sizeof(FilterShared) : 0)) +
+            s.warp * a.chunks_per_warp;
     s.run(blockIdx.x / s.C);
+}
+
+template <int kThreads>
+void (*kernel_for(bool bf16, bool filter))(SampleArgs) {
+    return bf16 ? (filter ? sample_kernel<true, true, kThreads> : sample_kernel<true, false, kThreads>)
+                : (filter ? sample_kernel<false, true, kThreads> : sample_kernel<false, false, kThreads>);
 }
 
 template <int kBytes>
@@ -734,10 +1021,12 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     const int E = bf16 ? 8 : 4;
     const int64_t chunks = (V + E - 1 + E - 1) / E;  // a row may start inside a chunk
     // CTAs per row: all eight while the rows alone cannot fill the SMs, else
-    // the fewest that keep a slice within 72 KB; a slice has 512 chunks at least.
+    // the fewest that keep a slice within 64 KB or so; a slice has 256 chunks at least.
     int C = B * kMaxCluster <= 2 * (int64_t)dev.num_sms ? kMaxCluster : 1;
-    while (C < kMaxCluster && chunks * 16 > (int64_t)C * 72 * 1024) C *= 2;
-    while (C > 1 && chunks < (int64_t)C * kSaThreads) C /= 2;
+    while (C < kMaxCluster && chunks * 16 > (int64_t)C * 64 * 1024 + 2048) C *= 2;
+    while (C > 1 && chunks < (int64_t)C * 256) C /= 2;
+    // 512 threads a CTA where the SMs are not full anyway
+    const int threads = B * C <= (int64_t)dev.num_sms ? 512 : 256;
     SampleArgs a = {};
     a.x = logits;
     a.ld = ld;
@@ -752,12 +1041,12 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     a.logp = logp;
     a.logp_all = logp_all;
     a.kept = kept;
-    const int64_t parts = (int64_t)C * kSaWarps;
+    const int64_t parts = (int64_t)C * (threads / 32);
     a.chunks_per_warp = (int)(((chunks + parts - 1) / parts + 31) / 32 * 32);
     const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + (filter ? sizeof(FilterShared) : 0) +
-                        (size_t)kSaWarps * a.chunks_per_warp * 16;
-    void (*kernel)(SampleArgs) = bf16 ? (filter ? sample_kernel<true, true> : sample_kernel<true, false>)
-                                      : (filter ? sample_kernel<false, true> : sample_kernel<false, false>);
+                        (size_t)(threads / 32) * a.chunks_per_warp * 16;
+    void (*kernel)(SampleArgs) =
+        threads == 512 ? kernel_for<512>(bf16, filter) : kernel_for<256>(bf16, filter);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess) {
         cudaGetLastError();
@@ -765,7 +1054,7 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(B * C));
-    cfg.blockDim = dim3(kSaThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = jet::as_stream(stream);
     cudaLaunchAttribute attr[2];
