@@ -65,7 +65,7 @@ struct SampleArgs {
 // ranks are written by the peers and read after a cluster barrier.
 struct Shared {
     u64 warp_mass[kMaxWarps], rank_mass[kMaxCluster], seg_mass[kMaxCluster];
-    u64 scan[2][kMaxWarps], sel_mass, cut_entry;
+    u64 scan[2][kMaxWarps], list_lo[kMaxWarps], list_hi[kMaxWarps], sel_mass, cut_entry;
     unsigned warp_cnt[kMaxWarps], rank_cnt[kMaxCluster];
     float warp_max[kMaxWarps], rank_max[kMaxCluster];
     unsigned warp_lo[kMaxWarps], warp_hi[kMaxWarps], rank_lo[kMaxCluster], rank_hi[kMaxCluster];
@@ -114,6 +114,7 @@ struct Elems<false> {
                           __float_as_uint(f[3]));
     }
     static __device__ __forceinline__ float one(const T *p) { return *p; }
+    static __device__ __forceinline__ float largest() { return 0x1.fffffep127f; }
 };
 
 template <>
@@ -138,13 +139,8 @@ struct Elems<true> {
     static __device__ __forceinline__ float one(const T *p) {
         return __uint_as_float((unsigned)*p << 16);
     }
+    static __device__ __forceinline__ float largest() { return 0x1.fep127f; }
 };
-
-// z of a logit x <= m; -inf and undefined products give -inf.
-__device__ __forceinline__ float z_of(float x, float m, float rt) {
-    const float z = x == m ? 0.0f : __fmul_rn(__fadd_rn(x, -m), rt);
-    return z <= 0.0f && x > -INFINITY ? z : -INFINITY;
-}
 
 __device__ __forceinline__ u64 mass_of(float w) { return __float2ull_rn(w * 0x1p45f); }
 
@@ -234,31 +230,114 @@ struct Sampler {
     cg::cluster_group cl;
     Shared *sh;
     FilterShared *fs;
-    uint4 *row;   // this warp's chunk c0 is row[0]
+    uint4 *row;   // with a filter: this warp's chunk c0 is row[0]
+    const typename El::T *x;  // the row in global memory
+    bool infinite;  // the row holds +inf
     int C, rank, lane, warp;
     int c0, c1;   // this warp's chunks of the row
     int shift;    // elements before the row in its first chunk
     float m, rt, min_w;
-    bool regular;  // m and 1/T finite: z needs no care
     float cut_x;
     int cut_idx;
 
-    __device__ Sampler(const SampleArgs &args) : a(args), cl(cg::this_cluster()) {}
+    __device__ Sampler(const SampleArgs &args) : a(args), cl(cg::this_cluster()), infinite(false) {}
 
-    __device__ __forceinline__ float z(float x) const {
-        return regular ? __fmul_rn(__fadd_rn(x, -m), rt) : z_of(x, m, rt);
+    // m is finite and rt a normal number, so x = -inf gives -inf and nothing else
+    // is undefined.
+    __device__ __forceinline__ float z(float x) const { return __fmul_rn(__fadd_rn(x, -m), rt); }
+
+    // A chunk of the row in shared memory.
+    __device__ __forceinline__ void chunk(int c, float (&v)[E]) const {
+        El::load(row[c - c0], v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
+    }
+
+    // Whether all of a chunk lies inside the row.
+    __device__ __forceinline__ bool whole(int c) const {
+        return c * E >= shift && (c + 1) * E - shift <= a.V;
+    }
+
+    // A chunk at the row's ends, element by element.
+    __device__ __forceinline__ void ragged(int c, float (&v)[E]) const {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int idx = c * E + e - shift;
+            v[e] = idx >= 0 && idx < a.V ? El::one(x + idx) : -INFINITY;
+        }
+    }
+
+    // +inf counts as the type's largest finite number.
+    static __device__ __forceinline__ void lower(float (&v)[E]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = v[e] == INFINITY ? El::largest() : v[e];
+    }
+
+    // A row that holds +inf: lowered, in shared memory by the threads that
+    // copied it.  Its new maximum.
+    __device__ float lower_infinities() {
+        infinite = true;
+        if (kFilter) {
+            for (int c = c0 + lane; c < c1; c += 32) {
+                float v[E];
+                El::load(row[c - c0], v);
+                lower(v);
+                row[c - c0] = El::store(v);
+            }
+        }
+        return El::largest();
+    }
+
+    // f(values, chunk) for every chunk of this warp's range, the values as they
+    // are in global memory; kAhead loads in flight a thread.
+    template <typename F>
+    __device__ __forceinline__ void global_chunks(F f) {
+        constexpr int kAhead = 4;
+        for (int base = c0 + lane; base < c1; base += 32 * kAhead) {
+            uint4 t[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int c = base + 32 * i;
+                if (c < c1 && whole(c)) t[i] = *reinterpret_cast<const uint4 *>(x + (c * E - shift));
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int c = base + 32 * i;
+                if (c >= c1) break;
+                float v[E];
+                if (whole(c)) El::load(t[i], v);
+                else ragged(c, v);
+                f(v, c);
+            }
+        }
+    }
+
+    // f(values, chunk) for every chunk of this warp's range.
+    template <typename F>
+    __device__ __forceinline__ void chunks(F f) {
+        if (kFilter) {
+            for (int c = c0 + lane; c < c1; c += 32) {
+                float v[E];
+                chunk(c, v);
+                f(v, c);
+            }
+        } else {
+            global_chunks([&](float (&v)[E], int c) {
+                if (infinite) lower(v);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
+                f(v, c);
+            });
+        }
     }
 
     // f(x, index) for every element of this warp's range.
     template <typename F>
     __device__ __forceinline__ void each(F f) {
-#pragma unroll 1
-        for (int c = c0 + lane; c < c1; c += 32) {
-            float v[E];
-            El::load(row[c - c0], v);
+        chunks([&](const float (&v)[E], int c) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) f(clean(v[e]), c * E + e - shift);
-        }
+            for (int e = 0; e < E; ++e) f(v[e], c * E + e - shift);
+        });
     }
 
     // v of every rank into arr[rank] of every CTA, by thread 0 .. C-1.
@@ -307,33 +386,40 @@ struct Sampler {
         return t;
     }
 
-    // The row into shared memory by this thread's own copies, four groups of
-    // them in flight; the maximum of what this thread copied and how many of
-    // them are logits that can be drawn.
-    __device__ float load_row(const typename El::T *x, unsigned &finite) {
-        const int V = a.V;
+    // The maximum of this thread's part of the row and the number of logits in it
+    // that can be drawn.  With a filter the part goes to shared memory by this
+    // thread's own copies, four groups of them in flight.
+    __device__ float load_row(unsigned &finite) {
+        float mx = -INFINITY;
+        unsigned n = 0;
+        auto take = [&](const float (&v)[E]) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                mx = fmaxf(mx, v[e]);  // a NaN leaves it as it is
+                n += v[e] > -INFINITY;
+            }
+        };
+        if (!kFilter) {
+            global_chunks([&](float (&v)[E], int) { take(v); });
+            finite = n;
+            return mx;
+        }
         const uint4 *src = reinterpret_cast<const uint4 *>(x - shift);
         uint4 *dst = row - c0;
         const int quarter = (a.chunks_per_warp / 32 + 3) / 4 * 32;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             for (int c = c0 + i * quarter + lane; c < min(c0 + (i + 1) * quarter, c1); c += 32) {
-                if (c * E >= shift && (c + 1) * E - shift <= V) {
+                if (whole(c)) {
                     cp_async16(dst + c, src + c);
-                } else {  // the row's ragged ends
+                } else {
                     float v[E];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const int idx = c * E + e - shift;
-                        v[e] = idx >= 0 && idx < V ? El::one(x + idx) : -INFINITY;
-                    }
+                    ragged(c, v);
                     dst[c] = El::store(v);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        float mx = -INFINITY;
-        unsigned n = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i == 0) cp_wait<3>();
@@ -343,45 +429,26 @@ struct Sampler {
             for (int c = c0 + i * quarter + lane; c < min(c0 + (i + 1) * quarter, c1); c += 32) {
                 float v[E];
                 El::load(dst[c], v);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    mx = fmaxf(mx, v[e]);  // a NaN leaves it as it is
-                    n += v[e] > -INFINITY;
-                }
+                take(v);
             }
         }
         finite = n;
         return mx;
     }
 
-    // This thread's weights.  Where m and 1/T are finite, x = -inf gives z =
-    // -inf and weight 0 by itself.
+    // This thread's weights.
     __device__ __forceinline__ u64 weigh() {
         MassSum s;
         unsigned n = 0;
         const float2 nm = make_float2(-m, -m), r2 = make_float2(rt, rt);
-        if (regular) {
-            for (int c = c0 + lane; c < c1; c += 32) {
-                float v[E];
-                El::load(row[c - c0], v);
+        chunks([&](const float (&v)[E], int) {
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 zz = __fmul2_rn(__fadd2_rn(make_float2(clean(v[e]), clean(v[e + 1])), nm), r2);
-                    s.add2(expf(zz.x), expf(zz.y));
-                }
-                n += E;
+            for (int e = 0; e < E; e += 2) {
+                const float2 zz = __fmul2_rn(__fadd2_rn(make_float2(v[e], v[e + 1]), nm), r2);
+                s.add2(expf(zz.x), expf(zz.y));
             }
-        } else {
-#pragma unroll 1
-            for (int c = c0 + lane; c < c1; c += 32) {
-                float v[E];
-                El::load(row[c - c0], v);
-#pragma unroll
-                for (int e = 0; e < E; e += 2)
-                    s.add2(expf(z_of(clean(v[e]), m, rt)), expf(z_of(clean(v[e + 1]), m, rt)));
-                n += E;
-            }
-        }
+            n += E;
+        });
         return s.total(n);
     }
 
@@ -407,131 +474,215 @@ struct Sampler {
         return before;
     }
 
-    // Bitonic sort of the first n of kThreads * N values (the others are ~0 and
-    // stay), N consecutive ones a thread, ascending: strides inside a thread in registers, inside a warp by
-    // shuffles, across warps through `buf` (value i of thread t at
-    // buf[i kThreads + t]).
-    template <int N>
-    __device__ void sort(u64 (&r)[N], unsigned n, u64 *buf) {
-        const int first = (int)threadIdx.x * N;
+    // Bitonic sort of the first n values (the others are ~0 and stay), one a
+    // thread, ascending: inside a warp by shuffles, across warps through
+    // shared memory.
+    __device__ void sort(u64 &r, unsigned n) {
+        u64 *buf = fs->sorted;
+        const int i = threadIdx.x;
 #pragma unroll 1
         for (int size = 2; size < 2 * (int)n; size *= 2) {  // up to the power of two that holds n
 #pragma unroll 1
-            for (int d = size / 2; d >= N; d /= 2) {
-                const int dt = d / N;  // partner thread distance
-                if (dt >= 32) {
+            for (int d = size / 2; d >= 1; d /= 2) {
+                u64 o;
+                if (d >= 32) {
                     __syncthreads();
-#pragma unroll
-                    for (int j = 0; j < N; ++j) buf[j * kThreads + threadIdx.x] = r[j];
+                    buf[i] = r;
                     __syncthreads();
+                    o = buf[i ^ d];
+                } else {
+                    o = __shfl_xor_sync(0xffffffffu, r, d);
                 }
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const u64 o = dt >= 32 ? buf[j * kThreads + (threadIdx.x ^ dt)]
-                                           : __shfl_xor_sync(0xffffffffu, r[j], dt);
-                    const bool low = ((first + j) & d) == 0, up = ((first + j) & size) == 0;
-                    r[j] = (low == up) == (r[j] < o) ? r[j] : o;
-                }
-            }
-#pragma unroll
-            for (int d = N / 2; d >= 1; d /= 2) {
-                if (d >= size) continue;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    if (j & d) continue;
-                    const bool up = ((first + j) & size) == 0;
-                    if ((r[j] > r[j | d]) == up) {
-                        const u64 t = r[j];
-                        r[j] = r[j | d];
-                        r[j | d] = t;
-                    }
-                }
+                const bool low = (i & d) == 0, up = (i & size) == 0;
+                r = (low == up) == (r < o) ? r : o;
             }
         }
         __syncthreads();
-    }
-
-    // The list's entries (N a thread) sorted by falling logit, their masses,
-    // and the mass before this thread's.
-    template <int N>
-    __device__ u64 sorted_list(unsigned n, unsigned k, u64 (&r)[N], u64 (&w)[N], u64 &S_k) {
-        const unsigned first = threadIdx.x * N;
-#pragma unroll
-        for (int j = 0; j < N; ++j) r[j] = first + j < n ? fs->sorted[first + j] : ~0ull;
-        __syncthreads();
-        sort<N>(r, n, fs->sorted);
-        u64 own = 0, own_k = 0, total;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            w[j] = first + j < n ? mass_of(weight_of(~(unsigned)(r[j] >> 32))) : 0;
-            own += w[j];
-            own_k += first + j < k ? w[j] : 0;
-        }
-        return block_scan(own, total, own_k, S_k);
     }
 
     __device__ __forceinline__ float weight_of(unsigned key) const {
-        return expf(z_of(logit_of(key), m, rt));
+        return expf(z(logit_of(key)));
     }
 
-    // The first CTA's part of the list way: n candidates in fs->sorted, which
-    // hold the cut.  The kept prefix is sorted by index, and the draw is where
-    // its running sum crosses u S.
-    template <int N>
-    __device__ void draw_from_list(int64_t b, unsigned n, unsigned k, bool k_on, float p, u64 S_all) {
-        u64 r[N], w[N], S_k, S, nk, total;
-        const unsigned first = threadIdx.x * N;
-        u64 at = sorted_list<N>(n, k, r, w, S_k);
+    // Mass of a list value: the key's complement is its upper half, or where the
+    // list goes by index its lower.
+    __device__ __forceinline__ u64 mass_in(u64 v, bool by_index) const {
+        return mass_of(weight_of(~(unsigned)(by_index ? v : v >> 32)));
+    }
+
+    // The first CTA's part of the list way for a short list: n candidates in
+    // fs->sorted, which hold the cut, one a thread.  Sorted by falling logit; the
+    // kept prefix is then sorted by index, and the draw is where its running
+    // sum crosses u S.
+    __device__ void draw_from_short(int64_t b, unsigned n, unsigned k, bool k_on, float p, u64 S_all) {
+        const unsigned i = threadIdx.x;
+        u64 r = i < n ? fs->sorted[i] : ~0ull, S_k, S, nk, total;
+        __syncthreads();
+        sort(r, n);
+        const float wf = i < n ? weight_of(~(unsigned)(r >> 32)) : 0.0f;
+        u64 w = mass_of(wf);
+        const u64 at = block_scan(w, total, i < k ? w : 0, S_k);
         const u64 target = p < 1.0f ? share(p, k_on ? S_k : S_all, true) : ~0ull;
-        u64 own = 0, own_n = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const unsigned i = first + j;
-            const bool in = i < n && i < k && (i == 0 || at < target) &&
-                            weight_of(~(unsigned)(r[j] >> 32)) >= min_w;
-            at += w[j];
-            own += in ? w[j] : 0;
-            own_n += in;
-            r[j] = in ? (r[j] << 32) | (r[j] >> 32) : ~0ull;  // index, ~key
-        }
-        block_scan(own, S, own_n, nk);
-        sort<N>(r, (unsigned)nk, fs->sorted);
-        own = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            w[j] = first + j < (unsigned)nk ? mass_of(weight_of(~(unsigned)r[j])) : 0;
-            own += w[j];
-        }
-        at = block_scan(own, total, 0, total);
+        const bool in = i < n && i < k && (i == 0 || at < target) && wf >= min_w;
+        r = in ? (r << 32) | (r >> 32) : ~0ull;  // index, ~key
+        block_scan(in ? w : 0, S, in, nk);
+        sort(r, (unsigned)nk);
+        w = i < (unsigned)nk ? mass_in(r, true) : 0;
+        const u64 before = block_scan(w, total, 0, total);
         const u64 aim = share(uniform(b), S, false);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (at <= aim && at + w[j] > aim) put(b, (int)(r[j] >> 32), w[j], S, S_all, (unsigned)nk);
-            at += w[j];
-        }
+        if (before <= aim && before + w > aim) put(b, (int)(r >> 32), w, S, S_all, (unsigned)nk);
     }
 
-    // The first CTA's part of a filter's cut: n tokens in fs->sorted, one of
-    // which is the last whose rank is below target_cnt or the mass before
-    // which is below target_mass; it goes to every CTA.
+    // The same for a long list, N a thread: top-k, top-p and, by index, the draw
+    // are each a cut of what is left.
+    __device__ void draw_from_long(int64_t b, unsigned n, unsigned k, bool k_on, float p, u64 S_all) {
+        constexpr int N = kListMax / kThreads;
+        u64 r[N], S = S_all, nk = n, last = 0;
+        load_list(r, n);
+        auto totals_of = [&](u64 &mass, u64 &number) {
+            u64 own = 0, own_n = 0;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                own += r[j] != ~0ull ? mass_in(r[j], false) : 0;
+                own_n += r[j] != ~0ull;
+            }
+            block_scan(own, mass, own_n, number);
+        };
+        for (int step = 0; step < 3; ++step) {
+            u64 target = k;
+            if (step == 0 && (!k_on || k >= n)) continue;
+            if (step == 1) {
+                if (p >= 1.0f) continue;
+                if (k_on) totals_of(S, nk);
+                target = share(p, S, true);
+            }
+            if (step == 2) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (r[j] != ~0ull && weight_of(~(unsigned)(r[j] >> 32)) < min_w) r[j] = ~0ull;
+                totals_of(S, nk);
+#pragma unroll
+                for (int j = 0; j < N; ++j) r[j] = (r[j] << 32) | (r[j] >> 32);  // index, ~key
+                target = share(uniform(b), S, false) + 1;
+            }
+            last = list_cut(r, step > 0, target, step == 2);
+            if (step == 2) break;
+#pragma unroll
+            for (int j = 0; j < N; ++j) r[j] = r[j] <= last ? r[j] : ~0ull;
+        }
+        if (threadIdx.x == 0) put(b, (int)(last >> 32), mass_in(last, true), S, S_all, (unsigned)nk);
+    }
+
     template <int N>
-    __device__ void cut_from_list(unsigned n, bool by_mass, unsigned target_cnt, u64 target_mass,
-                                  unsigned base_cnt, u64 base_mass) {
-        u64 r[N], w[N], unused;
-        const unsigned first = threadIdx.x * N;
-        u64 at = base_mass + sorted_list<N>(n, 0, r, w, unused);
+    __device__ __forceinline__ void load_list(u64 (&r)[N], unsigned n) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const unsigned rank_ = base_cnt + first + j;
-            const u64 end = at + w[j];
-            const bool in = by_mass ? at < target_mass : rank_ < target_cnt;
-            const bool next = by_mass ? end < target_mass : rank_ + 1 < target_cnt;
-            if (first + j < n && in && (!next || first + j + 1 == n)) sh->cut_entry = r[j];
-            at = end;
+            const unsigned i = j * kThreads + threadIdx.x;
+            r[j] = i < n ? fs->sorted[i] : ~0ull;
         }
         __syncthreads();
-        const u64 entry = sh->cut_entry;
-        to_all(&sh->cut_entry, entry);
+    }
+
+    // Among the distinct values r (N a thread, ~0 for none), in rising order, the
+    // last one before which less than `target` lies: their number, or their
+    // mass.  A histogram of the values' range, then of its bin that holds the
+    // target, until a bin's values can be sorted one a thread.
+    template <int N>
+    __device__ u64 list_cut(const u64 (&r)[N], bool by_mass, u64 target, bool by_index) {
+        u64 lo = 0, hi = ~0ull - 1;
+        unsigned n;
+        for (;;) {
+            u64 mn = ~0ull, mx = 0, cnt = 0, unused;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (r[j] < lo || r[j] > hi) continue;
+                mn = min(mn, r[j]);
+                mx = max(mx, r[j]);
+                ++cnt;
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) {
+                mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            }
+            if (lane == 0) {
+                sh->list_lo[warp] = mn;
+                sh->list_hi[warp] = mx;
+            }
+            block_scan(0, unused, cnt, cnt);
+            n = (unsigned)cnt;
+            for (int w = 0; w < kWarps; ++w) {
+                lo = w == 0 ? sh->list_lo[0] : min(lo, sh->list_lo[w]);
+                hi = w == 0 ? sh->list_hi[0] : max(hi, sh->list_hi[w]);
+            }
+            if (n <= kThreads) break;
+            const int sft = max(0, 64 - __clzll((long long)(hi - lo)) - 11);
+            clear_histogram();
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (r[j] >= lo && r[j] <= hi)
+                    count_in((int)((r[j] - lo) >> sft), by_mass, by_mass ? mass_in(r[j], by_index) : 0);
+            __syncthreads();
+            constexpr int kPer = kBins / kThreads;
+            u64 bin[kPer], own = 0, total;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int i = threadIdx.x * kPer + j;
+                bin[j] = fs->hist[0][i] + ((u64)fs->hist[1][i] << 15) + ((u64)fs->hist[2][i] << 30);
+                own += bin[j];
+            }
+            u64 at = block_scan(own, total, 0, unused);
+            if (total < target) return hi;  // all of them
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (at < target && at + bin[j] >= target) {
+                    sh->sel_bin = threadIdx.x * kPer + j;
+                    sh->sel_mass = at;
+                }
+                at += bin[j];
+            }
+            __syncthreads();
+            target -= sh->sel_mass;
+            lo += (u64)sh->sel_bin << sft;
+            hi = min(hi, lo + ((1ull << sft) - 1));
+            __syncthreads();  // before sel_bin, list_lo and the histogram are written again
+        }
+        // the values left, one a thread
+        u64 *buf = fs->sorted + kListMax - kThreads;  // past the histogram
+        unsigned own = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) own += r[j] >= lo && r[j] <= hi;
+        u64 total, unused;
+        unsigned to = (unsigned)block_scan(own, total, 0, unused);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (r[j] >= lo && r[j] <= hi) buf[to++] = r[j];
+        __syncthreads();
+        u64 v = threadIdx.x < n ? buf[threadIdx.x] : ~0ull;
+        __syncthreads();
+        sort(v, n);
+        const u64 w = threadIdx.x >= n ? 0 : by_mass ? mass_in(v, by_index) : 1;
+        const u64 at = block_scan(w, total, 0, unused);
+        if (threadIdx.x < n && at < target && (at + w >= target || threadIdx.x + 1 == n))
+            sh->cut_entry = v;
+        __syncthreads();
+        return sh->cut_entry;
+    }
+
+    __device__ void clear_histogram() {
+        for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&fs->hist[0][0])[i] = 0;
+        __syncthreads();
+    }
+
+    // One token into a bin of the histogram.
+    __device__ __forceinline__ void count_in(int bin, bool by_mass, u64 w) {
+        if (by_mass) {
+            atomicAdd(&fs->hist[0][bin], (unsigned)w & 0x7FFFu);
+            atomicAdd(&fs->hist[1][bin], (unsigned)(w >> 15) & 0x7FFFu);
+            atomicAdd(&fs->hist[2][bin], (unsigned)(w >> 30));
+        } else {
+            atomicAdd(&fs->hist[0][bin], 1u);
+        }
     }
 
     // The tokens for which f(x) into the first CTA's list, if there are at most
@@ -541,18 +692,16 @@ struct Sampler {
         u64 hit[3] = {0, 0, 0};  // of this thread's elements, 136 at most
         unsigned mine = 0;
         int at = 0;
-#pragma unroll 1
-        for (int c = c0 + lane; c < c1; c += 32, at += E) {
-            float v[E];
-            El::load(row[c - c0], v);
+        chunks([&](const float (&v)[E], int) {
             unsigned bits = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) bits |= f(clean(v[e])) ? 1u << e : 0u;
+            for (int e = 0; e < E; ++e) bits |= f(v[e]) ? 1u << e : 0u;
             mine += __popc(bits);
             if (at < 64) hit[0] |= (u64)bits << at;
             else if (at < 128) hit[1] |= (u64)bits << (at - 64);
             else hit[2] |= (u64)bits << (at - 128);
-        }
+            at += E;
+        });
         totals(0, mine);
         const unsigned n = all_cnt();
         if (n <= kListMax) {
@@ -596,54 +745,53 @@ struct Sampler {
     // Histogram of this CTA's elements with z > z_lo by the step of z (level
     // 0), or of those of an interval of keys: masses or counts.
     __device__ void histogram(bool by_mass, int level, float z_lo, unsigned lo, unsigned hi, int sft) {
-        for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&fs->hist[0][0])[i] = 0;
-        __syncthreads();
+        clear_histogram();
         const float x_lo = logit_of(lo), x_hi = logit_of(hi);
         each([&](float x, int) {
             const float zx = z(x);
             if (level == 0 ? zx > z_lo : x >= x_lo && x <= x_hi && x > -INFINITY) {
                 const int b = level == 0 ? (int)(zx * -kBinsPerZ) : (int)((hi - key_of(x)) >> sft);
-                if (by_mass) {
-                    const u64 w = mass_of(expf(zx));
-                    atomicAdd(&fs->hist[0][b], (unsigned)w & 0x7FFFu);
-                    atomicAdd(&fs->hist[1][b], (unsigned)(w >> 15) & 0x7FFFu);
-                    atomicAdd(&fs->hist[2][b], (unsigned)(w >> 30));
-                } else {
-                    atomicAdd(&fs->hist[0][b], 1u);
-                }
+                count_in(b, by_mass, by_mass ? mass_of(expf(zx)) : 0);
             }
         });
         cl.sync();
     }
 
     // The first bin whose end reaches the target, given what lies before the
-    // histogram, with what lies before the bin, at every CTA.
+    // histogram, with what lies before the bin, at every CTA.  A CTA merges
+    // kBins / C bins, four a thread, the peers' loads all in flight.
     __device__ void select(bool by_mass, u64 target, u64 base) {
-        constexpr int kPer = kBins / kThreads;           // bins a thread at most
-        const int seg = kBins / C;                       // bins this CTA merges
-        const int per = seg > kThreads ? seg / kThreads : 1;
-        u64 bin[kPer], own = 0;
-        const int first = rank * seg + (int)threadIdx.x * per;
-        const bool active = (int)threadIdx.x * per < seg;
+        constexpr int kPer = kBins / 4 / kThreads > 0 ? kBins / 4 / kThreads : 1;  // quads a thread
+        const int quads = kBins / 4 / C;  // of this CTA
+        const int per = quads > kThreads ? kPer : 1;
+        u64 bin[kPer][4], own = 0;
+        const int first = (int)threadIdx.x * per;
+        const bool active = first < quads;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            bin[j] = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) bin[j][q] = 0;
             if (active && j < per) {
-                // a peer past the cluster is read as this one and not counted, so
-                // that all the loads are in flight together
-                unsigned part[kMaxCluster];
+                const int at = 4 * (rank * quads + first + j);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     if (i > 0 && !by_mass) break;
+                    uint4 part[kMaxCluster];  // a peer past the cluster: this CTA's, not counted
 #pragma unroll
                     for (int r = 0; r < kMaxCluster; ++r)
-                        part[r] = cl.map_shared_rank(fs, r < C ? r : rank)->hist[i][first + j];
-                    u64 sum = 0;
+                        part[r] = *reinterpret_cast<const uint4 *>(
+                            &cl.map_shared_rank(fs, r < C ? r : rank)->hist[i][at]);
 #pragma unroll
-                    for (int r = 0; r < kMaxCluster; ++r) sum += r < C ? part[r] : 0;
-                    bin[j] += sum << (15 * i);
+                    for (int r = 0; r < kMaxCluster; ++r) {
+                        if (r >= C) break;
+                        bin[j][0] += (u64)part[r].x << (15 * i);
+                        bin[j][1] += (u64)part[r].y << (15 * i);
+                        bin[j][2] += (u64)part[r].z << (15 * i);
+                        bin[j][3] += (u64)part[r].w << (15 * i);
+                    }
                 }
-                own += bin[j];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) own += bin[j][q];
             }
         }
         u64 total, unused;
@@ -655,23 +803,26 @@ struct Sampler {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             if (active && j < per) {
-                if (at < target && at + bin[j] >= target) {
-                    for (int r = 0; r < C; ++r) {
-                        Shared *o = cl.map_shared_rank(sh, r);
-                        o->sel_bin = first + j;
-                        o->sel_mass = at;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (at < target && at + bin[j][q] >= target) {
+                        for (int r = 0; r < C; ++r) {
+                            Shared *o = cl.map_shared_rank(sh, r);
+                            o->sel_bin = 4 * (rank * quads + first + j) + q;
+                            o->sel_mass = at;
+                        }
                     }
+                    at += bin[j][q];
                 }
-                at += bin[j];
             }
         }
         cl.sync();
     }
 
     // The cut among tokens of one logit: the first `n` of them in index order.
-    __device__ void cut_ties(float x, unsigned n) {
+    __device__ void cut_ties(float logit, unsigned n) {
         unsigned mine = 0;
-        each([&](float v, int) { mine += v == x; });
+        each([&](float v, int) { mine += v == logit; });
         totals(0, mine);
         unsigned before = 0;
         for (int r = 0; r < rank; ++r) before += sh->rank_cnt[r];
@@ -683,9 +834,9 @@ struct Sampler {
                 float v[E];
                 unsigned t = 0;
                 if (c < c1) {
-                    El::load(row[c - c0], v);
+                    chunk(c, v);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) t += v[e] == x;
+                    for (int e = 0; e < E; ++e) t += v[e] == logit;
                 }
                 const unsigned inc = (unsigned)warp_scan(t, lane);
                 if (before + inc - t < n && n <= before + inc) {
@@ -693,14 +844,14 @@ struct Sampler {
                     int idx = 0;
 #pragma unroll
                     for (int e = 0; e < E; ++e)
-                        if (v[e] == x && ++at == n) idx = c * E + e - shift;
+                        if (v[e] == logit && ++at == n) idx = c * E + e - shift;
                     for (int r = 0; r < C; ++r) cl.map_shared_rank(sh, r)->cut_idx = idx;
                 }
                 before += __shfl_sync(0xffffffffu, inc, 31);
             }
         }
         cl.sync();
-        cut_x = x;
+        cut_x = logit;
         cut_idx = sh->cut_idx;
     }
 
@@ -736,10 +887,11 @@ struct Sampler {
             const unsigned n = gather(in_bin);
             if (n <= kListMax) {
                 if (rank == 0) {
-                    const unsigned bc = by_mass ? 0 : (unsigned)base, tc = by_mass ? 0 : (unsigned)target;
-                    const u64 bm = by_mass ? base : 0;
-                    if (n <= kThreads) cut_from_list<1>(n, by_mass, tc, target, bc, bm);
-                    else cut_from_list<kListMax / kThreads>(n, by_mass, tc, target, bc, bm);
+                    u64 r[kListMax / kThreads];
+                    load_list(r, n);
+                    const u64 entry = list_cut(r, by_mass, target - base, false);
+                    __syncthreads();
+                    to_all(&sh->cut_entry, entry);
                 }
                 cl.sync();
                 cut_x = logit_of(~(unsigned)(sh->cut_entry >> 32));
@@ -787,37 +939,37 @@ struct Sampler {
         }
     }
 
-    // Mass and number of the kept tokens (all of them at every CTA).
+    // Mass of the kept tokens; their totals at every CTA.
     __device__ u64 kept_totals() {
         MassSum s;
         unsigned n = 0, cnt = 0;
-#pragma unroll 1
-        for (int c = c0 + lane; c < c1; c += 32, n += E) {
-            float v[E], w[E];
-            El::load(row[c - c0], v);
+        const float low = fmaxf(cut_x, -0x1.fffffep127f);  // no -inf is kept
+        chunks([&](const float (&v)[E], int c) {
+            float w[E];
+            const int last = cut_idx - (c * E - shift);  // ties up to this element
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float x = clean(v[e]);
-                w[e] = expf(z(x));
-                const bool in = kept(x, w[e], c * E + e - shift);
+                w[e] = expf(z(v[e]));
+                const bool in = v[e] >= low && (v[e] > cut_x || e <= last) && w[e] >= min_w;
                 w[e] = in ? w[e] : 0.0f;
                 cnt += in;
             }
 #pragma unroll
             for (int e = 0; e < E; e += 2) s.add2(w[e], w[e + 1]);
-        }
+            n += E;
+        });
         totals(s.total(n), cnt);
         return all_mass();
     }
 
     __device__ void run(int64_t b) {
-        const typename El::T *x = static_cast<const typename El::T *>(a.x) + b * a.ld;
+        x = static_cast<const typename El::T *>(a.x) + b * a.ld;
         shift = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(typename El::T));
         const int chunks = (shift + a.V + E - 1) / E;
         c0 = min((rank * kWarps + warp) * a.chunks_per_warp, chunks);
         c1 = min(c0 + a.chunks_per_warp, chunks);
         unsigned cnt;
-        const float own_max = load_row(x, cnt);
+        const float own_max = load_row(cnt);
         float mx = own_max;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -833,6 +985,7 @@ struct Sampler {
         cl.sync();
         m = -INFINITY;
         for (int r = 0; r < C; ++r) m = fmaxf(m, sh->rank_max[r]);
+        if (m == INFINITY) m = lower_infinities();
         if (m == -INFINITY) {  // nothing can be drawn
             if (rank == 0 && threadIdx.x == 0) {
                 a.token[b] = -1;
@@ -844,8 +997,7 @@ struct Sampler {
         }
         const float T = kFilter && a.temperature ? a.temperature[b] : 1.0f;
         const bool greedy = !(T > 0.0f);
-        rt = __fdiv_rn(1.0f, greedy ? 1.0f : T);
-        regular = m < INFINITY && rt > 0.0f && rt < INFINITY;
+        rt = fminf(fmaxf(__fdiv_rn(1.0f, greedy ? 1.0f : T), 0x1p-126f), 0x1.fffffep127f);
         int k = 0x7FFFFFFF;
         float p = 1.0f;
         min_w = 0.0f;
@@ -857,7 +1009,7 @@ struct Sampler {
             if (a.min_p) min_w = fminf(fmaxf(a.min_p[b], 0.0f), 1.0f);
         }
         if (kFilter && k > 1 && k < 0x7FFFFFFF) {  // the threads' maxima, to every CTA
-            const float zx = z_of(own_max, m, rt);
+            const float zx = z(fminf(own_max, m));
             if (zx > -32.0f) atomicAdd(&fs->grp[rank][(int)(zx * -kGroupsPerZ)], 1u);
             __syncthreads();
             for (int i = threadIdx.x; i < C * kGroups; i += kThreads)
@@ -912,9 +1064,8 @@ struct Sampler {
                     if (n_c <= kListMax) {
                         if (rank != 0) return;
                         const unsigned kk = k_on ? (unsigned)k : finite;
-                        if (n_c <= kThreads) draw_from_list<1>(b, n_c, kk, k_on, p, S_all);
-                        else if (n_c <= 4 * kThreads) draw_from_list<4>(b, n_c, kk, k_on, p, S_all);
-                        else draw_from_list<kListMax / kThreads>(b, n_c, kk, k_on, p, S_all);
+                        if (n_c <= kThreads) draw_from_short(b, n_c, kk, k_on, p, S_all);
+                        else draw_from_long(b, n_c, kk, k_on, p, S_all);
                         return;
                     }
                 }
@@ -944,15 +1095,20 @@ struct Sampler {
         if (before > aim || before + sh->rank_mass[rank] <= aim) return;
         int wi = 0;
         while (wi < kWarps - 1 && before + sh->warp_mass[wi] <= aim) before += sh->warp_mass[wi++];
-        const typename El::T *src =
+        const typename El::T *held =
             reinterpret_cast<const typename El::T *>(row + (wi - warp) * a.chunks_per_warp);
         const int r0 = min((rank * kWarps + wi) * a.chunks_per_warp, chunks);
         const int n = (min(r0 + a.chunks_per_warp, chunks) - r0) * E;  // elements of the range
         const int per = (n + kThreads - 1) / kThreads;
         const int l0 = min((int)threadIdx.x * per, n), l1 = min(l0 + per, n);
         auto weight = [&](int i) -> u64 {
-            const float xv = clean(El::one(src + i)), w = expf(z(xv));
-            return kept(xv, w, r0 * E + i - shift) ? mass_of(w) : 0;
+            const int idx = r0 * E + i - shift;
+            float xv = -INFINITY;
+            if (kFilter) xv = clean(El::one(held + i));
+            else if (idx >= 0 && idx < a.V) xv = clean(El::one(x + idx));
+            if (!kFilter && xv == INFINITY) xv = El::largest();
+            const float w = expf(z(xv));
+            return kept(xv, w, idx) ? mass_of(w) : 0;
         };
         u64 own = 0, all;
 #pragma unroll 1
@@ -969,7 +1125,7 @@ struct Sampler {
 };
 
 template <bool kBf16, bool kFilter, int kThreads>
-__global__ void __launch_bounds__(kThreads, (kThreads == 256 ? 3 : 2) - kFilter)
+__global__ void __launch_bounds__(kThreads, kFilter ? 512 / kThreads : 1280 / kThreads)
 sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     jet::griddep_launch_dependents();
@@ -1043,8 +1199,9 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     a.kept = kept;
     const int64_t parts = (int64_t)C * (threads / 32);
     a.chunks_per_warp = (int)(((chunks + parts - 1) / parts + 31) / 32 * 32);
-    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + (filter ? sizeof(FilterShared) : 0) +
-                        (size_t)(threads / 32) * a.chunks_per_warp * 16;
+    const size_t smem =
+        (sizeof(Shared) + 15) / 16 * 16 +
+        (filter ? sizeof(FilterShared) + (size_t)(threads / 32) * a.chunks_per_warp * 16 : 0);
     void (*kernel)(SampleArgs) =
         threads == 512 ? kernel_for<512>(bf16, filter) : kernel_for<256>(bf16, filter);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
