@@ -288,46 +288,46 @@ struct Sampler {
         return El::largest();
     }
 
-    // f(values, chunk) for every chunk of this warp's range, the values as they
-    // are in global memory; kAhead loads in flight a thread.
+    // f(values) for every chunk of this warp's range, the values as they are in
+    // global memory: whole chunks four loads in flight a thread, then the row's
+    // ragged ends.
     template <typename F>
     __device__ __forceinline__ void global_chunks(F f) {
-        constexpr int kAhead = 4;
-        for (int base = c0 + lane; base < c1; base += 32 * kAhead) {
-            uint4 t[kAhead];
+        const int first = shift > 0, past = (shift + a.V) / E;  // the whole chunks
+        int c = max(c0, first) + lane;
+        const int end = min(c1, past);
+        const uint4 *p = reinterpret_cast<const uint4 *>(x - shift) + c;
+        float v[E];
+        for (; c + 96 < end; c += 128, p += 128) {
+            const uint4 t[4] = {p[0], p[32], p[64], p[96]};
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int c = base + 32 * i;
-                if (c < c1 && whole(c)) t[i] = *reinterpret_cast<const uint4 *>(x + (c * E - shift));
+            for (int i = 0; i < 4; ++i) {
+                El::load(t[i], v);
+                f(v);
             }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int c = base + 32 * i;
-                if (c >= c1) break;
-                float v[E];
-                if (whole(c)) El::load(t[i], v);
-                else ragged(c, v);
-                f(v, c);
+        }
+#pragma unroll 1
+        for (; c < end; c += 32, p += 32) {
+            El::load(*p, v);
+            f(v);
+        }
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {  // chunk 0 and chunk `past`, where they are not whole
+            const int r = i == 0 ? 0 : past;
+            if (lane == i && r >= c0 && r < c1 && !whole(r) && (i == 0 || past > 0)) {
+                ragged(r, v);
+                f(v);
             }
         }
     }
 
-    // f(values, chunk) for every chunk of this warp's range.
+    // f(values, chunk) for every chunk of this warp's range in shared memory.
     template <typename F>
     __device__ __forceinline__ void chunks(F f) {
-        if (kFilter) {
-            for (int c = c0 + lane; c < c1; c += 32) {
-                float v[E];
-                chunk(c, v);
-                f(v, c);
-            }
-        } else {
-            global_chunks([&](float (&v)[E], int c) {
-                if (infinite) lower(v);
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
-                f(v, c);
-            });
+        for (int c = c0 + lane; c < c1; c += 32) {
+            float v[E];
+            chunk(c, v);
+            f(v, c);
         }
     }
 
@@ -393,14 +393,20 @@ struct Sampler {
         float mx = -INFINITY;
         unsigned n = 0;
         auto take = [&](const float (&v)[E]) {
+            float sum = v[0];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 mx = fmaxf(mx, v[e]);  // a NaN leaves it as it is
-                n += v[e] > -INFINITY;
+                if (e > 0) sum += v[e];
+            }
+            n += E;
+            if (!(fabsf(sum) < INFINITY)) {  // some may be -inf or NaN
+#pragma unroll
+                for (int e = 0; e < E; ++e) n -= !(v[e] > -INFINITY);
             }
         };
         if (!kFilter) {
-            global_chunks([&](float (&v)[E], int) { take(v); });
+            global_chunks([&](float (&v)[E]) { take(v); });
             finite = n;
             return mx;
         }
@@ -441,14 +447,30 @@ struct Sampler {
         MassSum s;
         unsigned n = 0;
         const float2 nm = make_float2(-m, -m), r2 = make_float2(rt, rt);
-        chunks([&](const float (&v)[E], int) {
+        auto add = [&](const float (&v)[E]) {
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const float2 zz = __fmul2_rn(__fadd2_rn(make_float2(v[e], v[e + 1]), nm), r2);
                 s.add2(expf(zz.x), expf(zz.y));
             }
             n += E;
-        });
+        };
+        if (kFilter) {
+            chunks([&](const float (&v)[E], int) { add(v); });
+        } else if (!infinite) {
+            global_chunks([&](float (&v)[E]) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
+                add(v);
+            });
+        } else {
+            global_chunks([&](float (&v)[E]) {
+                lower(v);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
+                add(v);
+            });
+        }
         return s.total(n);
     }
 
@@ -1176,13 +1198,23 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     const bool filter = temperature || top_k || top_p || min_p;
     const int E = bf16 ? 8 : 4;
     const int64_t chunks = (V + E - 1 + E - 1) / E;  // a row may start inside a chunk
-    // CTAs per row: all eight while the rows alone cannot fill the SMs, else
-    // the fewest that keep a slice within 64 KB or so; a slice has 256 chunks at least.
-    int C = B * kMaxCluster <= 2 * (int64_t)dev.num_sms ? kMaxCluster : 1;
-    while (C < kMaxCluster && chunks * 16 > (int64_t)C * 64 * 1024 + 2048) C *= 2;
-    while (C > 1 && chunks < (int64_t)C * 256) C /= 2;
-    // 512 threads a CTA where the SMs are not full anyway
-    const int threads = B * C <= (int64_t)dev.num_sms ? 512 : 256;
+    // CTAs per row and threads per CTA.  Without a filter: two CTAs of 512
+    // threads an SM while the rows are few (128256 logits in binary32, us: 1 row
+    // 7.0 with 8 x 512, 8.7 with 8 x 256; 16 rows 8.9 and 12.2, 12.1 with 4 x 512;
+    // 64 rows 16.8 with 4 x 512, 19.3 with 8 x 512); then one CTA of 512 a row
+    // (300 rows of 32000: 17.0, 19.5 with 2 x 256), of 256 past two rows an SM
+    // (1024 rows of 32000: 39, 45 with 512), but eight of 256 where rows are
+    // long (256 rows of 128256 in binary32: 45, 53 with one of 512).  With a
+    // filter a CTA's slice has to fit into shared memory, 64 KB of it or so.
+    const int64_t sms = dev.num_sms;
+    int C = kMaxCluster, threads = 512;
+    while (C > 1 && (B * C > 2 * sms || chunks < (int64_t)C * 256)) C /= 2;
+    if (B * C > (filter ? 1 : 2) * sms) threads = 256;
+    if (!filter && B > sms && chunks * 16 > 384 * 1024) {
+        C = kMaxCluster;
+        threads = 256;
+    }
+    while (filter && C < kMaxCluster && chunks * 16 > (int64_t)C * 64 * 1024 + 2048) C *= 2;
     SampleArgs a = {};
     a.x = logits;
     a.ld = ld;
