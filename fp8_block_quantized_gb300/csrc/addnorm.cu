@@ -86,7 +86,73 @@ __device__ __forceinline__ void quant_chunk(const uint4 &hc, const uint4 &gc, fl
     }
 }
 
-// One warp per row at a time.  The first pass adds, writes h and sums the
+// One CTA of T threads per row, NI chunks a thread (K <= 8 T NI).  All of a
+// thread's loads go out at once; h stays in its registers for the
+// quantization, and a copy in shared memory lets warp 0 sum the squares in the
+// fixed order (its 32 lanes' chains of K / 32 additions are the only serial part).
+// h may be x or d (in place): a thread reads its chunks before it writes them.
+template <int T, int NI>
+__global__ void __launch_bounds__(T)
+add_rmsnorm_row_kernel(const uint16_t *x, const uint16_t *d, const uint16_t *__restrict__ g,
+                       int64_t M, int64_t K, float eps, uint16_t *h, uint8_t *q, float *s,
+                       float *rstd) {
+    extern __shared__ uint4 rowbuf[];  // the row's K / 8 chunks of h
+    __shared__ float r_sh;
+    jet::griddep_launch_dependents();
+    jet::griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int nchunks = (int)(K / 8), nj = (nchunks + 31) / 32;
+    const int64_t m = blockIdx.x;
+    const uint4 *xr = reinterpret_cast<const uint4 *>(x + m * K);
+    const uint4 *dr = reinterpret_cast<const uint4 *>(d + m * K);
+    uint4 *hr = reinterpret_cast<uint4 *>(h + m * K);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 c[NI], b[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int ci = threadIdx.x + i * T;
+        c[i] = ci < nchunks ? xr[ci] : zero;
+        b[i] = ci < nchunks ? dr[ci] : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int ci = threadIdx.x + i * T;
+        c[i] = add_chunk(c[i], b[i]);
+        if (ci < nchunks) {
+            rowbuf[ci] = c[i];
+            hr[ci] = c[i];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        float acc = 0.0f;
+#pragma unroll 4
+        for (int j = 0; j < nj; ++j) {
+            const int ci = 32 * j + lane;
+            acc = add_squares(acc, ci < nchunks ? rowbuf[ci] : zero);
+        }
+        const float r = rms_factor(acc, K, eps);
+        if (lane == 0) {
+            r_sh = r;
+            if (rstd) rstd[m] = r;
+        }
+    }
+    const uint4 *gain = reinterpret_cast<const uint4 *>(g);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int ci = threadIdx.x + i * T;
+        b[i] = ci < nchunks ? gain[ci] : zero;
+    }
+    __syncthreads();
+    const float nr = -r_sh;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int ci = threadIdx.x + i * T;
+        quant_chunk(c[i], b[i], nr, ci < nchunks, ci >> 4, m, M, K, lane, q, s);
+    }
+}
+
+// Rows too long for that: one warp per row at a time.  The first pass adds, writes h and sums the
 // squares; the second reads back this lane's own chunks of h.  h may be x or
 // d (in place), so none of the three is read-only to the compiler.
 constexpr int kAnThreads = 256;
@@ -157,102 +223,196 @@ __device__ __forceinline__ void unpack8(const uint4 &c, float (&f)[8]) {
     }
 }
 
-template <int NC>
+// The next row of the CTA is copied into shared memory (cp.async, every thread
+// its own chunks, so no barrier is needed for it) while this one is reduced and
+// written.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (unsigned)__cvta_generic_to_shared(dst)),
+                 "l"(src)
+                 : "memory");
+}
+
+struct BwdArgs {
+    const uint16_t *in[5];  // h, then the gradients: dy0 .. , and dres last if it is there
+    int ny, nt;             // output gradients; tensors in all
+    const uint16_t *g;
+    const float *rstd;
+    int64_t M, K;
+    uint16_t *dx;
+    float *part;
+};
+
+// dot over the CTA, the same in every thread; `red` alternates between rows, so
+// that one barrier a row is enough.
+__device__ __forceinline__ float block_sum(float v, float *red) {
+    const int lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < nwarps ? red[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                      pack_bf16(f[6], f[7]));
+}
+
+__device__ __forceinline__ void store_part(float *p, const float (&dg)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(dg[0], dg[1], dg[2], dg[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(dg[4], dg[5], dg[6], dg[7]);
+}
+
+// K <= 8192: one chunk a thread.
 __global__ void __launch_bounds__(1024)
-add_rmsnorm_bwd_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ g,
-                       const float *__restrict__ rstd, const uint16_t *__restrict__ dy0,
-                       const uint16_t *__restrict__ dy1, const uint16_t *__restrict__ dy2,
-                       const uint16_t *dres, int64_t M, int64_t K, uint16_t *dx, float *part) {
+add_rmsnorm_bwd_kernel(const BwdArgs a) {
+    extern __shared__ uint4 stage[];  // [2][nt][threads]
     __shared__ float red[2][32];
     jet::griddep_launch_dependents();
     jet::griddep_wait();
-    const int64_t nchunks = K / 8;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    const int64_t M = a.M;
+    const int nchunks = (int)(a.K / 8), T = blockDim.x, ci = threadIdx.x;
+    const bool ok = ci < nchunks, has_res = a.nt > a.ny + 1;
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 gain = ok ? reinterpret_cast<const uint4 *>(a.g)[ci] : zero;
+    float dg[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    auto fetch = [&](int64_t m, int ph) {
+        if (m < M && ok) {
+#pragma unroll
+            for (int k = 0; k < 5; ++k)
+                if (k < a.nt)
+                    cp_async16(stage + (ph * a.nt + k) * T + ci,
+                               reinterpret_cast<const uint4 *>(a.in[k]) + m * nchunks + ci);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(blockIdx.x, 0);
+    int phase = 0;
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x, phase ^= 1) {
+        const float r = a.rstd[m];
+        fetch(m + gridDim.x, phase ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const uint4 *in = stage + phase * a.nt * T + ci;
+        float xh[8], u[8], f[8], dot = 0.0f;
+        unpack8(ok ? in[0] : zero, xh);
+        unpack8(ok ? in[T] : zero, u);
+#pragma unroll
+        for (int k = 2; k < 4; ++k) {
+            if (k > a.ny) break;
+            unpack8(ok ? in[k * T] : zero, f);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) u[t] += f[t];
+        }
+        unpack8(gain, f);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            xh[t] *= r;
+            dg[t] = fmaf(u[t], xh[t], dg[t]);
+            u[t] *= f[t];
+            dot = fmaf(u[t], xh[t], dot);
+        }
+        const float mean = block_sum(dot, red[phase]) / (float)a.K;
+        if (!ok) continue;
+        unpack8(has_res ? in[(a.nt - 1) * T] : zero, f);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) f[t] = fmaf(r, fmaf(-xh[t], mean, u[t]), f[t]);
+        reinterpret_cast<uint4 *>(a.dx)[m * nchunks + ci] = pack8(f);
+    }
+    if (ok) store_part(a.part + blockIdx.x * a.K + 8 * (int64_t)ci, dg);
+}
+
+// Longer rows, NC chunks a thread: no room to keep a row, which is read again
+// (from L2) for its second pass.
+template <int NC>
+__global__ void __launch_bounds__(1024)
+add_rmsnorm_bwd_wide_kernel(const BwdArgs a) {
+    __shared__ float red[2][32];
+    jet::griddep_launch_dependents();
+    jet::griddep_wait();
+    const int nchunks = (int)(a.K / 8), T = blockDim.x;
+    const bool has_res = a.nt > a.ny + 1;
     float dg[NC][8];
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int t = 0; t < 8; ++t) dg[i][t] = 0.0f;
     int phase = 0;
-    for (int64_t m = blockIdx.x; m < M; m += gridDim.x, phase ^= 1) {
-        const float r = rstd[m];
-        float xh[NC][8], u[NC][8];
-        float dot = 0.0f;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, phase ^= 1) {
+        const float r = a.rstd[m];
+        auto load = [&](int k, int ci, float (&f)[8]) {
+            unpack8(reinterpret_cast<const uint4 *>(a.in[k])[m * nchunks + ci], f);
+        };
+        auto terms = [&](int ci, float (&xh)[8], float (&dy)[8]) {
+            float f[8];
+            load(0, ci, xh);
+            load(1, ci, dy);
+#pragma unroll 1
+            for (int k = 2; k <= a.ny; ++k) {
+                load(k, ci, f);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) dy[t] += f[t];
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t) xh[t] *= r;
+        };
+        float xh[8], u[8], f[8], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int64_t ci = threadIdx.x + (int64_t)i * blockDim.x;
-            const bool ok = ci < nchunks;
-            const int64_t at = m * nchunks + ci;
-            auto get = [&](const uint16_t *p, int64_t k) {
-                return ok ? reinterpret_cast<const uint4 *>(p)[k] : zero;
-            };
-            const uint4 hc = get(h, at), a = get(dy0, at), gc = get(g, ci);
-            const uint4 b = dy1 ? get(dy1, at) : zero, c = dy2 ? get(dy2, at) : zero;
-            float gf[8], t1[8], t2[8];
-            unpack8(hc, xh[i]);
-            unpack8(a, u[i]);
-            unpack8(b, t1);
-            unpack8(c, t2);
-            unpack8(gc, gf);
+            const int ci = threadIdx.x + i * T;
+            if (ci >= nchunks) continue;
+            terms(ci, xh, u);
+            unpack8(reinterpret_cast<const uint4 *>(a.g)[ci], f);
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                xh[i][t] *= r;
-                const float dy = u[i][t] + t1[t] + t2[t];
-                dg[i][t] = fmaf(dy, xh[i][t], dg[i][t]);
-                u[i][t] = dy * gf[t];
-                dot = fmaf(u[i][t], xh[i][t], dot);
+                dg[i][t] = fmaf(u[t], xh[t], dg[i][t]);
+                dot = fmaf(u[t] * f[t], xh[t], dot);
             }
         }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) red[phase][warp] = dot;
-        __syncthreads();
-        float sum = lane < nwarps ? red[phase][lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float a = sum / (float)K;
+        const float mean = block_sum(dot, red[phase]) / (float)a.K;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int64_t ci = threadIdx.x + (int64_t)i * blockDim.x;
+            const int ci = threadIdx.x + i * T;
             if (ci >= nchunks) continue;
-            const int64_t at = m * nchunks + ci;
-            float f[8];
-            unpack8(dres ? reinterpret_cast<const uint4 *>(dres)[at] : zero, f);
+            float gf[8];
+            terms(ci, xh, u);
+            unpack8(reinterpret_cast<const uint4 *>(a.g)[ci], gf);
+            unpack8(has_res ? reinterpret_cast<const uint4 *>(a.in[a.nt - 1])[m * nchunks + ci]
+                            : make_uint4(0, 0, 0, 0), f);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) f[t] = fmaf(r, fmaf(-xh[i][t], a, u[i][t]), f[t]);
-            reinterpret_cast<uint4 *>(dx)[at] =
-                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                           pack_bf16(f[6], f[7]));
+            for (int t = 0; t < 8; ++t) f[t] = fmaf(r, fmaf(-xh[t], mean, u[t] * gf[t]), f[t]);
+            reinterpret_cast<uint4 *>(a.dx)[m * nchunks + ci] = pack8(f);
         }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int64_t ci = threadIdx.x + (int64_t)i * blockDim.x;
-        if (ci >= nchunks) continue;
-        float4 *p = reinterpret_cast<float4 *>(part + blockIdx.x * K + 8 * ci);
-        p[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-        p[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+        const int ci = threadIdx.x + i * T;
+        if (ci < nchunks) store_part(a.part + blockIdx.x * a.K + 8 * (int64_t)ci, dg[i]);
     }
 }
 
-// dg[k] = the partial rows' sum in a fixed order: 8 row groups per CTA of 32
-// columns, each adding every eighth partial row, then the groups in order.
-__global__ void __launch_bounds__(256)
+// dg[k] = the partial rows' sum in a fixed order: 32 groups per CTA of 32
+// columns, each adding every 32nd partial row, then the groups in order.
+__global__ void __launch_bounds__(1024)
 dgain_reduce_kernel(const float *__restrict__ part, int parts, int64_t K, float *__restrict__ dg) {
-    __shared__ float sum[8][32];
+    __shared__ float sum[32][33];
     jet::griddep_launch_dependents();
     jet::griddep_wait();
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t k = blockIdx.x * (int64_t)32 + c;
-    float acc = 0.0f;
-#pragma unroll 8
-    for (int p = w; p < parts; p += 8) acc += part[p * K + k];
+    float v[(kBwdParts + 31) / 32], acc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (kBwdParts + 31) / 32; ++i) v[i] = w + 32 * i < parts ? part[(w + 32 * i) * K + k] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < (kBwdParts + 31) / 32; ++i) acc += v[i];
     sum[w][c] = acc;
     __syncthreads();
     if (w == 0) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) acc += sum[i][c];
+        for (int i = 1; i < 32; ++i) acc += sum[i][c];
         dg[k] = acc;
     }
 }
@@ -285,6 +445,30 @@ jet_status jet_add_rmsnorm_quant_1x128(const uint16_t *x, const uint16_t *d, con
     jet_status st = jet::current_device(&dev);
     if (st != JET_OK) return st;
     if (empty) return JET_OK;
+    cudaStream_t cs = jet::as_stream(stream);
+    const int64_t nchunks = K / 8;
+    if (nchunks <= 8 * 512) {
+        // Many rows: 128 threads each, several rows per SM in flight.  Few rows,
+        // or long ones: 512 threads, fewer chunks a thread.
+        const int T = M > 2 * (int64_t)dev.num_sms && nchunks <= 8 * 128 ? 128 : 512;
+        const int ni = (int)((nchunks + T - 1) / T);
+        auto *kernel =
+            T == 128 ? (ni <= 2 ? add_rmsnorm_row_kernel<128, 2>
+                                : ni <= 4 ? add_rmsnorm_row_kernel<128, 4>
+                                          : ni == 5 ? add_rmsnorm_row_kernel<128, 5> : add_rmsnorm_row_kernel<128, 8>)
+                     : (ni <= 1 ? add_rmsnorm_row_kernel<512, 1>
+                                : ni <= 2 ? add_rmsnorm_row_kernel<512, 2>
+                                          : ni <= 4 ? add_rmsnorm_row_kernel<512, 4> : add_rmsnorm_row_kernel<512, 8>);
+        const size_t smem = (size_t)K * 2;
+        if (smem > 48 * 1024 &&
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+                cudaSuccess) {
+            cudaGetLastError();
+            return JET_ERR_CUDA;
+        }
+        return jet::launch_pdl(kernel, dim3((unsigned)M), dim3((unsigned)T), smem, cs, x, d, g, M, K,
+                               eps, h, q, s, rstd);
+    }
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, add_rmsnorm_quant_kernel,
                                                       kAnThreads, 0) != cudaSuccess ||
@@ -295,8 +479,7 @@ jet_status jet_add_rmsnorm_quant_1x128(const uint16_t *x, const uint16_t *d, con
     const int64_t want = (M + kAnThreads / 32 - 1) / (kAnThreads / 32);
     const int64_t cap = (int64_t)dev.num_sms * per_sm;
     return jet::launch_pdl(add_rmsnorm_quant_kernel, dim3((unsigned)(want < cap ? want : cap)),
-                           dim3(kAnThreads), 0, jet::as_stream(stream), x, d, g, M, K, eps, h, q,
-                           s, rstd);
+                           dim3(kAnThreads), 0, cs, x, d, g, M, K, eps, h, q, s, rstd);
 }
 
 jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float *rstd,
@@ -324,16 +507,38 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
         cudaGetLastError();
         return JET_ERR_CUDA;
     }
-    const int parts = (int)bwd_parts(M);
     const int64_t nchunks = K / 8;
     const int nc = nchunks <= 1024 ? 1 : nchunks <= 2048 ? 2 : 4;
     const int threads = (int)(((nchunks + nc - 1) / nc + 31) / 32 * 32);
-    auto *kernel = nc == 1 ? add_rmsnorm_bwd_kernel<1>
-                           : nc == 2 ? add_rmsnorm_bwd_kernel<2> : add_rmsnorm_bwd_kernel<4>;
-    float *part = static_cast<float *>(ws);
-    st = jet::launch_pdl(kernel, dim3((unsigned)parts), dim3((unsigned)threads), 0, cs, h, g, rstd,
-                         dy0, dy1, dy2, dres, M, K, dx, part);
+    auto *kernel = nc == 1 ? add_rmsnorm_bwd_kernel
+                           : nc == 2 ? add_rmsnorm_bwd_wide_kernel<2> : add_rmsnorm_bwd_wide_kernel<4>;
+    BwdArgs a = {};
+    a.in[a.nt++] = h;
+    for (const uint16_t *dy : {dy0, dy1, dy2})
+        if (dy) a.in[a.nt++] = dy;
+    a.ny = a.nt - 1;
+    if (dres) a.in[a.nt++] = dres;
+    a.g = g;
+    a.rstd = rstd;
+    a.M = M;
+    a.K = K;
+    a.dx = dx;
+    a.part = static_cast<float *>(ws);
+    const size_t smem = nc == 1 ? (size_t)2 * a.nt * threads * 16 : 0;
+    int per_sm = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) !=
+            cudaSuccess ||
+        per_sm < 1) {
+        cudaGetLastError();
+        return JET_ERR_CUDA;
+    }
+    // persistent CTAs, as many as are resident and as there are partial rows
+    const int64_t resident = (int64_t)dev.num_sms * per_sm;
+    const int parts = (int)(bwd_parts(M) < resident ? bwd_parts(M) : resident);
+    st = jet::launch_pdl(kernel, dim3((unsigned)parts), dim3((unsigned)threads), smem, cs, a);
     if (st != JET_OK) return st;
-    return jet::launch_pdl(dgain_reduce_kernel, dim3((unsigned)(K / 32)), dim3(256), 0, cs, part,
-                           parts, K, dg);
+    return jet::launch_pdl(dgain_reduce_kernel, dim3((unsigned)(K / 32)), dim3(1024), 0, cs,
+                           (const float *)a.part, parts, K, dg);
 }
