@@ -223,9 +223,10 @@ __device__ __forceinline__ void unpack8(const uint4 &c, float (&f)[8]) {
     }
 }
 
-// The next row of the CTA is copied into shared memory (cp.async, every thread
-// its own chunks, so no barrier is needed for it) while this one is reduced and
-// written.
+// The CTA's next row is copied into shared memory (cp.async, every thread its
+// own chunks, so no barrier is needed for it) while this one is reduced and
+// written; three or four rows in flight were slower (8192 x 4096, three
+// gradients: 69 and 70 us against 61), as fewer CTAs fit.
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                      (unsigned)__cvta_generic_to_shared(dst)),
@@ -291,9 +292,11 @@ add_rmsnorm_bwd_kernel(const BwdArgs a) {
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     fetch(blockIdx.x, 0);
+    float r_next = (int64_t)blockIdx.x < M ? a.rstd[blockIdx.x] : 0.0f;
     int phase = 0;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, phase ^= 1) {
-        const float r = a.rstd[m];
+        const float r = r_next;
+        if (m + gridDim.x < M) r_next = a.rstd[m + gridDim.x];
         fetch(m + gridDim.x, phase ^ 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         const uint4 *in = stage + phase * a.nt * T + ci;
@@ -403,11 +406,14 @@ dgain_reduce_kernel(const float *__restrict__ part, int parts, int64_t K, float 
     jet::griddep_wait();
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t k = blockIdx.x * (int64_t)32 + c;
-    float v[(kBwdParts + 31) / 32], acc = 0.0f;
+    float acc = 0.0f;
+    for (int p0 = w; p0 < parts; p0 += 32 * 10) {
+        float v[10];
 #pragma unroll
-    for (int i = 0; i < (kBwdParts + 31) / 32; ++i) v[i] = w + 32 * i < parts ? part[(w + 32 * i) * K + k] : 0.0f;
+        for (int i = 0; i < 10; ++i) v[i] = p0 + 32 * i < parts ? part[(p0 + 32 * i) * K + k] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < (kBwdParts + 31) / 32; ++i) acc += v[i];
+        for (int i = 0; i < 10; ++i) acc += v[i];
+    }
     sum[w][c] = acc;
     __syncthreads();
     if (w == 0) {
@@ -417,7 +423,12 @@ dgain_reduce_kernel(const float *__restrict__ part, int parts, int64_t K, float 
     }
 }
 
-int64_t bwd_parts(int64_t M) { return M < kBwdParts ? M : kBwdParts; }
+// CTAs of the backward at most: short rows leave room for more of them
+// (16384 x 2048: 53 us with 608, 81 with 304; x 1024: 38 with 1216, 54 with 608).
+int64_t bwd_parts(int64_t M, int64_t K) {
+    const int64_t cap = K <= 1024 ? 4 * kBwdParts : K <= 2048 ? 2 * kBwdParts : kBwdParts;
+    return M < cap ? M : cap;
+}
 
 template <int kBytes>
 bool aligned_to(const void *p) { return (reinterpret_cast<uintptr_t>(p) & (kBytes - 1)) == 0; }
@@ -426,7 +437,7 @@ bool aligned_to(const void *p) { return (reinterpret_cast<uintptr_t>(p) & (kByte
 
 // Partial rows of dg.
 size_t jet_add_rmsnorm_bwd_workspace(int64_t M, int64_t K) {
-    return (size_t)bwd_parts(M) * (size_t)K * sizeof(float);
+    return (size_t)bwd_parts(M, K) * (size_t)K * sizeof(float);
 }
 
 jet_status jet_add_rmsnorm_quant_1x128(const uint16_t *x, const uint16_t *d, const uint16_t *g,
@@ -448,17 +459,21 @@ jet_status jet_add_rmsnorm_quant_1x128(const uint16_t *x, const uint16_t *d, con
     cudaStream_t cs = jet::as_stream(stream);
     const int64_t nchunks = K / 8;
     if (nchunks <= 8 * 512) {
-        // Many rows: 128 threads each, several rows per SM in flight.  Few rows,
-        // or long ones: 512 threads, fewer chunks a thread.
-        const int T = M > 2 * (int64_t)dev.num_sms && nchunks <= 8 * 128 ? 128 : 512;
+        // Threads of a row, by what keeps enough loads in flight (us, measured):
+        // up to four rows an SM 512 (600 x 4096: 5.0, 7.4 with 128); then 128 for
+        // K <= 5120 (16384 x 5120: 87, 99 with 256) and 256 for longer rows (4096 x
+        // 8192: 40, 45 with 128).
+        const int T = M <= 4 * (int64_t)dev.num_sms || nchunks > 8 * 256 ? 512 : nchunks > 640 ? 256 : 128;
         const int ni = (int)((nchunks + T - 1) / T);
-        auto *kernel =
-            T == 128 ? (ni <= 2 ? add_rmsnorm_row_kernel<128, 2>
-                                : ni <= 4 ? add_rmsnorm_row_kernel<128, 4>
-                                          : ni == 5 ? add_rmsnorm_row_kernel<128, 5> : add_rmsnorm_row_kernel<128, 8>)
-                     : (ni <= 1 ? add_rmsnorm_row_kernel<512, 1>
-                                : ni <= 2 ? add_rmsnorm_row_kernel<512, 2>
-                                          : ni <= 4 ? add_rmsnorm_row_kernel<512, 4> : add_rmsnorm_row_kernel<512, 8>);
+        void (*kernel)(const uint16_t *, const uint16_t *, const uint16_t *, int64_t, int64_t, float,
+                       uint16_t *, uint8_t *, float *, float *) =
+            T == 128 ? (ni == 1 ? add_rmsnorm_row_kernel<128, 1>
+                        : ni == 2 ? add_rmsnorm_row_kernel<128, 2>
+                        : ni <= 4 ? add_rmsnorm_row_kernel<128, 4> : add_rmsnorm_row_kernel<128, 5>)
+            : T == 256 ? (ni <= 4 ? add_rmsnorm_row_kernel<256, 4> : add_rmsnorm_row_kernel<256, 8>)
+                       : (ni == 1 ? add_rmsnorm_row_kernel<512, 1>
+                          : ni == 2 ? add_rmsnorm_row_kernel<512, 2>
+                          : ni <= 4 ? add_rmsnorm_row_kernel<512, 4> : add_rmsnorm_row_kernel<512, 8>);
         const size_t smem = (size_t)K * 2;
         if (smem > 48 * 1024 &&
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -510,8 +525,6 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
     const int64_t nchunks = K / 8;
     const int nc = nchunks <= 1024 ? 1 : nchunks <= 2048 ? 2 : 4;
     const int threads = (int)(((nchunks + nc - 1) / nc + 31) / 32 * 32);
-    auto *kernel = nc == 1 ? add_rmsnorm_bwd_kernel
-                           : nc == 2 ? add_rmsnorm_bwd_wide_kernel<2> : add_rmsnorm_bwd_wide_kernel<4>;
     BwdArgs a = {};
     a.in[a.nt++] = h;
     for (const uint16_t *dy : {dy0, dy1, dy2})
@@ -524,6 +537,8 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
     a.K = K;
     a.dx = dx;
     a.part = static_cast<float *>(ws);
+    auto *kernel = nc == 1 ? add_rmsnorm_bwd_kernel
+                           : nc == 2 ? add_rmsnorm_bwd_wide_kernel<2> : add_rmsnorm_bwd_wide_kernel<4>;
     const size_t smem = nc == 1 ? (size_t)2 * a.nt * threads * 16 : 0;
     int per_sm = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -536,7 +551,8 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
     }
     // persistent CTAs, as many as are resident and as there are partial rows
     const int64_t resident = (int64_t)dev.num_sms * per_sm;
-    const int parts = (int)(bwd_parts(M) < resident ? bwd_parts(M) : resident);
+    const int64_t most = bwd_parts(M, K);
+    const int parts = (int)(most < resident ? most : resident);
     st = jet::launch_pdl(kernel, dim3((unsigned)parts), dim3((unsigned)threads), smem, cs, a);
     if (st != JET_OK) return st;
     return jet::launch_pdl(dgain_reduce_kernel, dim3((unsigned)(K / 32)), dim3(1024), 0, cs,

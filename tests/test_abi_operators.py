@@ -47,7 +47,8 @@ def test_add_rmsnorm_bwd(lib):
     f = lib.jet_add_rmsnorm_bwd
     need = lib.jet_workspace_bytes(binding.OP["add_rmsnorm_bwd"], 100, 0, 256)
     assert need == 100 * 256 * 4
-    assert lib.jet_workspace_bytes(binding.OP["add_rmsnorm_bwd"], 10**6, 0, 256) == 304 * 256 * 4
+    assert lib.jet_workspace_bytes(binding.OP["add_rmsnorm_bwd"], 10**6, 0, 4096) == 304 * 4096 * 4
+    assert lib.jet_workspace_bytes(binding.OP["add_rmsnorm_bwd"], 10**6, 0, 256) == 1216 * 256 * 4
     assert lib.jet_workspace_bytes(binding.OP["add_rmsnorm_bwd"], 0, 0, 256) == 0
     ok = [P[0], P[1], P[2], P[3], P[4], P[5], P[6], 100, 256, P[7], P[8], P[9], need, None]
     for i in (0, 1, 2, 3, 9, 10):
