@@ -613,8 +613,8 @@ def _arg(t, dtype, shape, name):
 
 def _raw_stream(stream):
     import torch
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream() without its object: 0.3 against 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -705,17 +705,17 @@ def _heads(t, T, D, name):
     import torch
     if t is None:
         return None, 0, 0
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
         raise ValueError(f"{name}: expected shape ({T}, heads, {D}), got {tuple(t.shape)}")
     H = t.shape[1]
-    if t.numel() == 0:
+    if T == 0 or H == 0 or D == 0:
         return None, H * D, H
-    st = t.stride()
-    if not t.is_cuda or (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+    ld, sh, sd = t.stride()
+    if not t.is_cuda or (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}: must be a CUDA tensor whose tokens hold contiguous heads")
-    return t.data_ptr(), (st[0] if T > 1 else H * D), H
+    return t.data_ptr(), (ld if T > 1 else H * D), H
 
 
 def jet_rope(q, k, inv_freq, pos, q_out, k_out, layout="half", mscale=1.0, backward=False,
