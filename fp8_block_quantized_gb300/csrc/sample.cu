@@ -23,13 +23,11 @@
 // A bound z_lo is taken below which it cannot lie (top-k: a group of z up to
 // which k of the threads' own maxima lie; top-p: all tokens below w = (1 - p)
 // S / V together weigh less than (1 - p) S; min-p: its own weight).  When at
-// most kListMax tokens lie above it, they go to the first CTA, which sorts
-// them in registers, finds the cut and draws, while the others end.  Flat
-// distributions and large k take the general way: a histogram of counts and
-// masses over 2048 steps of z finds the step the cut lies in, and the few
-// tokens of that step are ranked against each other; a step with too many of
-// them is split again on the bits of the logits, and one of equal logits by
-// counting.
+// most kListMax tokens lie above it, they go to the first CTA, which finds the
+// cut and draws, while the others end.  Flat distributions and large k take the general way: a histogram of counts and
+// masses over 2048 steps of z finds the step the cut lies in, and the first CTA
+// finds it among the tokens of that step; a step with too many of them is
+// split again on the bits of the logits, and one of equal logits by counting.
 #include <cooperative_groups.h>
 
 #include "jet_common.cuh"
@@ -44,7 +42,7 @@ constexpr int kBins = 2048;           // steps of 1/64 of z; z <= -32 is bin kBi
 constexpr float kBinsPerZ = 64.0f;
 constexpr int kGroups = 128;          // groups of 16 steps: 1/4 of z
 constexpr float kGroupsPerZ = 4.0f;
-constexpr int kListMax = 4096;        // tokens sorted by the first CTA
+constexpr int kListMax = 2048;        // tokens the first CTA takes
 constexpr int64_t kSaMaxV = 262144;   // so that the sum of 2^45-scaled weights fits 64 bits
 
 typedef unsigned long long u64;
@@ -65,22 +63,20 @@ struct SampleArgs {
 // ranks are written by the peers and read after a cluster barrier.
 struct Shared {
     u64 warp_mass[kMaxWarps], rank_mass[kMaxCluster], seg_mass[kMaxCluster];
-    u64 scan[2][kMaxWarps], list_lo[kMaxWarps], list_hi[kMaxWarps], sel_mass, cut_entry;
+    u64 scan[2][kMaxWarps], list_lo, list_hi, sel_mass, cut_entry;
     unsigned warp_cnt[kMaxWarps], rank_cnt[kMaxCluster];
     float warp_max[kMaxWarps], rank_max[kMaxCluster];
-    unsigned warp_lo[kMaxWarps], warp_hi[kMaxWarps], rank_lo[kMaxCluster], rank_hi[kMaxCluster];
+    unsigned lo, hi, rank_lo[kMaxCluster], rank_hi[kMaxCluster];
     int sel_bin;  // the selected bin
     int cut_idx;
 };
 
-// The general way's histogram, or the list the first CTA sorts.
+// With a filter.
 struct FilterShared {
-    union {
-        // counts, or masses in three 15-bit parts: shared-memory atomics on 32
-        // bits run in hardware, and 2^17 tokens of one CTA cannot overflow a part
-        unsigned hist[3][kBins];
-        u64 sorted[kListMax];  // ~key, index
-    };
+    // counts, or masses in three 15-bit parts: shared-memory atomics on 32 bits
+    // run in hardware, and 2^17 tokens of one CTA cannot overflow a part
+    unsigned hist[3][kBins];
+    u64 list[kListMax];  // ~key, index; at the first CTA
     unsigned grp[kMaxCluster][kGroups];  // threads' maxima by group of z
 };
 
@@ -145,7 +141,7 @@ struct Elems<true> {
 __device__ __forceinline__ u64 mass_of(float w) { return __float2ull_rn(w * 0x1p45f); }
 
 // floor(f s) and ceil(f s) for 0 <= f < 1, exact: f = mant 2^-sh.
-__device__ __forceinline__ u64 share(float f, u64 s, bool up) {
+__device__ __noinline__ u64 share(float f, u64 s, bool up) {
     const unsigned bits = __float_as_uint(f), e = bits >> 23;
     const u64 mant = e ? (bits & 0x7FFFFFu) | 0x800000u : bits;
     const int sh = 150 - (e ? (int)e : 1);  // 24 .. 149
@@ -218,6 +214,66 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
         if (lane >= o) v += q;
     }
     return v;
+}
+
+// The code of a row runs once, and fetching it takes time: what is used in
+// several places is not inlined.
+
+struct Scan {
+    u64 before, total, other;
+};
+
+// Sums over the CTA: of v over the threads before this one and over all, and of
+// o over all.
+__device__ __noinline__ Scan block_scan(u64 v, u64 o, u64 (*sums)[kMaxWarps]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    const u64 inc = warp_scan(v, lane);
+    o = warp_sum(o);
+    __syncthreads();  // the sums may still be read
+    if (lane == 31) {
+        sums[0][warp] = inc;
+        sums[1][warp] = o;
+    }
+    __syncthreads();
+    const u64 w = warp_scan(lane < nwarps ? sums[0][lane] : 0, lane);
+    Scan r;
+    r.total = __shfl_sync(0xffffffffu, w, 31);
+    const u64 ahead = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
+    r.before = inc - v + (warp == 0 ? 0 : ahead);
+    r.other = warp_sum(lane < nwarps ? sums[1][lane] : 0);
+    return r;
+}
+
+// Bitonic sort of the first n values (the others are ~0 and stay), one a thread,
+// ascending: inside a warp by shuffles, across warps through `buf`.
+__device__ __noinline__ u64 block_sort(u64 r, unsigned n, u64 *buf) {
+    const int i = threadIdx.x;
+#pragma unroll 1
+    for (int size = 2; size < 2 * (int)n; size *= 2) {  // up to the power of two that holds n
+#pragma unroll 1
+        for (int d = size / 2; d >= 1; d /= 2) {
+            u64 o;
+            if (d >= 32) {
+                __syncthreads();
+                buf[i] = r;
+                __syncthreads();
+                o = buf[i ^ d];
+            } else {
+                o = __shfl_xor_sync(0xffffffffu, r, d);
+            }
+            const bool low = (i & d) == 0, up = (i & size) == 0;
+            r = (low == up) == (r < o) ? r : o;
+        }
+    }
+    __syncthreads();
+    return r;
+}
+
+// log(w / s), through log1p where the share is near one.
+__device__ __noinline__ float log_share(u64 w, u64 s) {
+    const float sf = __ull2float_rn(s);
+    return 2 * w > s ? log1pf(-__fdiv_rn(__ull2float_rn(s - w), sf))
+                     : logf(__fdiv_rn(__ull2float_rn(w), sf));
 }
 
 template <bool kBf16, bool kFilter, int kThreads>
@@ -331,7 +387,14 @@ struct Sampler {
         }
     }
 
-    // f(x, index) for every element of this warp's range.
+    // Element i of this warp's range in shared memory (its index is i - skip()).
+    __device__ __forceinline__ float element(int i) const {
+        return clean(El::one(reinterpret_cast<const typename El::T *>(row) + i));
+    }
+    __device__ __forceinline__ int elements() const { return (c1 - c0) * E; }
+    __device__ __forceinline__ int skip() const { return shift - c0 * E; }
+
+    // f(x, index) for every element of this warp's range in shared memory.
     template <typename F>
     __device__ __forceinline__ void each(F f) {
         chunks([&](const float (&v)[E], int c) {
@@ -361,14 +424,9 @@ struct Sampler {
             sh->warp_cnt[warp] = cnt;
         }
         __syncthreads();
-        if ((int)threadIdx.x < C) {
-            u64 t = 0;
-            unsigned n = 0;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                t += sh->warp_mass[i];
-                n += sh->warp_cnt[i];
-            }
+        if (warp == 0) {
+            const u64 t = warp_sum(lane < kWarps ? sh->warp_mass[lane] : 0);
+            const unsigned n = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh->warp_cnt[lane] : 0);
             to_all(&sh->rank_mass[rank], t);
             to_all(&sh->rank_cnt[rank], n);
         }
@@ -413,9 +471,11 @@ struct Sampler {
         const uint4 *src = reinterpret_cast<const uint4 *>(x - shift);
         uint4 *dst = row - c0;
         const int quarter = (a.chunks_per_warp / 32 + 3) / 4 * 32;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-            for (int c = c0 + i * quarter + lane; c < min(c0 + (i + 1) * quarter, c1); c += 32) {
+            const int end = min(c0 + (i + 1) * quarter, c1);
+#pragma unroll 1
+            for (int c = c0 + i * quarter + lane; c < end; c += 32) {
                 if (whole(c)) {
                     cp_async16(dst + c, src + c);
                 } else {
@@ -426,13 +486,15 @@ struct Sampler {
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
             if (i == 0) cp_wait<3>();
             if (i == 1) cp_wait<2>();
             if (i == 2) cp_wait<1>();
             if (i == 3) cp_wait<0>();
-            for (int c = c0 + i * quarter + lane; c < min(c0 + (i + 1) * quarter, c1); c += 32) {
+            const int end = min(c0 + (i + 1) * quarter, c1);
+#pragma unroll 2
+            for (int c = c0 + i * quarter + lane; c < end; c += 32) {
                 float v[E];
                 El::load(dst[c], v);
                 take(v);
@@ -474,52 +536,11 @@ struct Sampler {
         return s.total(n);
     }
 
-    // Exclusive sum of v over the CTA's threads, the total, and the total of o.
-    __device__ u64 block_scan(u64 v, u64 &total, u64 o, u64 &total_o) {
-        const u64 inc = warp_scan(v, lane);
-        o = warp_sum(o);
-        __syncthreads();  // the arrays may still be read
-        if (lane == 31) {
-            sh->scan[0][warp] = inc;
-            sh->scan[1][warp] = o;
-        }
-        __syncthreads();
-        u64 before = inc - v, t = 0;
-        total_o = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) before += t;
-            t += sh->scan[0][w];
-            total_o += sh->scan[1][w];
-        }
-        total = t;
-        return before;
-    }
+    __device__ __forceinline__ Scan scan(u64 v, u64 o = 0) { return block_scan(v, o, sh->scan); }
 
-    // Bitonic sort of the first n values (the others are ~0 and stay), one a
-    // thread, ascending: inside a warp by shuffles, across warps through
-    // shared memory.
-    __device__ void sort(u64 &r, unsigned n) {
-        u64 *buf = fs->sorted;
-        const int i = threadIdx.x;
-#pragma unroll 1
-        for (int size = 2; size < 2 * (int)n; size *= 2) {  // up to the power of two that holds n
-#pragma unroll 1
-            for (int d = size / 2; d >= 1; d /= 2) {
-                u64 o;
-                if (d >= 32) {
-                    __syncthreads();
-                    buf[i] = r;
-                    __syncthreads();
-                    o = buf[i ^ d];
-                } else {
-                    o = __shfl_xor_sync(0xffffffffu, r, d);
-                }
-                const bool low = (i & d) == 0, up = (i & size) == 0;
-                r = (low == up) == (r < o) ? r : o;
-            }
-        }
-        __syncthreads();
+    // A buffer of one value a thread.
+    __device__ __forceinline__ u64 sort(u64 r, unsigned n) {
+        return block_sort(r, n, reinterpret_cast<u64 *>(fs->hist));
     }
 
     __device__ __forceinline__ float weight_of(unsigned key) const {
@@ -533,128 +554,113 @@ struct Sampler {
     }
 
     // The first CTA's part of the list way for a short list: n candidates in
-    // fs->sorted, which hold the cut, one a thread.  Sorted by falling logit; the
+    // fs->list, which hold the cut, one a thread.  Sorted by falling logit; the
     // kept prefix is then sorted by index, and the draw is where its running
     // sum crosses u S.
     __device__ void draw_from_short(int64_t b, unsigned n, unsigned k, bool k_on, float p, u64 S_all) {
         const unsigned i = threadIdx.x;
-        u64 r = i < n ? fs->sorted[i] : ~0ull, S_k, S, nk, total;
-        __syncthreads();
-        sort(r, n);
+        u64 r = sort(i < n ? fs->list[i] : ~0ull, n);
         const float wf = i < n ? weight_of(~(unsigned)(r >> 32)) : 0.0f;
         u64 w = mass_of(wf);
-        const u64 at = block_scan(w, total, i < k ? w : 0, S_k);
-        const u64 target = p < 1.0f ? share(p, k_on ? S_k : S_all, true) : ~0ull;
-        const bool in = i < n && i < k && (i == 0 || at < target) && wf >= min_w;
-        r = in ? (r << 32) | (r >> 32) : ~0ull;  // index, ~key
-        block_scan(in ? w : 0, S, in, nk);
-        sort(r, (unsigned)nk);
-        w = i < (unsigned)nk ? mass_in(r, true) : 0;
-        const u64 before = block_scan(w, total, 0, total);
-        const u64 aim = share(uniform(b), S, false);
-        if (before <= aim && before + w > aim) put(b, (int)(r >> 32), w, S, S_all, (unsigned)nk);
+        const Scan by_logit = scan(w, i < k ? w : 0);
+        const u64 target = p < 1.0f ? share(p, k_on ? by_logit.other : S_all, true) : ~0ull;
+        const bool in = i < n && i < k && (i == 0 || by_logit.before < target) && wf >= min_w;
+        const Scan held = scan(in ? w : 0, in);
+        const unsigned nk = (unsigned)held.other;
+        r = sort(in ? (r << 32) | (r >> 32) : ~0ull, nk);  // index, ~key
+        w = i < nk ? mass_in(r, true) : 0;
+        const u64 before = scan(w).before;
+        const u64 aim = share(uniform(b), held.total, false);
+        if (before <= aim && before + w > aim) put(b, (int)(r >> 32), w, held.total, S_all, nk);
     }
 
-    // The same for a long list, N a thread: top-k, top-p and, by index, the draw
-    // are each a cut of what is left.
+    // The same for a long list: top-k, top-p and, by index, the draw are each a
+    // cut of what is left.  A thread keeps to its own entries, ~0 where dropped.
     __device__ void draw_from_long(int64_t b, unsigned n, unsigned k, bool k_on, float p, u64 S_all) {
-        constexpr int N = kListMax / kThreads;
-        u64 r[N], S = S_all, nk = n, last = 0;
-        load_list(r, n);
-        auto totals_of = [&](u64 &mass, u64 &number) {
-            u64 own = 0, own_n = 0;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                own += r[j] != ~0ull ? mass_in(r[j], false) : 0;
-                own_n += r[j] != ~0ull;
-            }
-            block_scan(own, mass, own_n, number);
-        };
+        u64 last = 0;
+        Scan held = {0, 0, n};
+#pragma unroll 1
         for (int step = 0; step < 3; ++step) {
             u64 target = k;
             if (step == 0 && (!k_on || k >= n)) continue;
-            if (step == 1) {
-                if (p >= 1.0f) continue;
-                if (k_on) totals_of(S, nk);
-                target = share(p, S, true);
+            if (step == 1 && p >= 1.0f) continue;
+            if (step > 0) {
+                // the mass of what is left (by step 2, of what min-p leaves)
+                u64 own = 0, own_n = 0;
+#pragma unroll 1
+                for (unsigned i = threadIdx.x; i < n; i += kThreads) {
+                    const u64 v = fs->list[i];
+                    if (v == ~0ull) continue;
+                    const float w = weight_of(~(unsigned)(v >> 32));
+                    const bool out = step == 2 && w < min_w;
+                    if (step == 2) fs->list[i] = out ? ~0ull : (v << 32) | (v >> 32);  // index, ~key
+                    own += out ? 0 : mass_of(w);
+                    own_n += !out;
+                }
+                held = scan(own, own_n);
+                target = step == 1 ? share(p, k_on ? held.total : S_all, true)
+                                   : share(uniform(b), held.total, false) + 1;
             }
-            if (step == 2) {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (r[j] != ~0ull && weight_of(~(unsigned)(r[j] >> 32)) < min_w) r[j] = ~0ull;
-                totals_of(S, nk);
-#pragma unroll
-                for (int j = 0; j < N; ++j) r[j] = (r[j] << 32) | (r[j] >> 32);  // index, ~key
-                target = share(uniform(b), S, false) + 1;
-            }
-            last = list_cut(r, step > 0, target, step == 2);
-            if (step == 2) break;
-#pragma unroll
-            for (int j = 0; j < N; ++j) r[j] = r[j] <= last ? r[j] : ~0ull;
+            last = list_cut(n, step > 0, target, step == 2);
+#pragma unroll 1
+            for (unsigned i = threadIdx.x; step < 2 && i < n; i += kThreads)
+                if (fs->list[i] > last) fs->list[i] = ~0ull;
         }
-        if (threadIdx.x == 0) put(b, (int)(last >> 32), mass_in(last, true), S, S_all, (unsigned)nk);
+        if (threadIdx.x == 0)
+            put(b, (int)(last >> 32), mass_in(last, true), held.total, S_all, (unsigned)held.other);
     }
 
-    template <int N>
-    __device__ __forceinline__ void load_list(u64 (&r)[N], unsigned n) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const unsigned i = j * kThreads + threadIdx.x;
-            r[j] = i < n ? fs->sorted[i] : ~0ull;
-        }
-        __syncthreads();
-    }
-
-    // Among the distinct values r (N a thread, ~0 for none), in rising order, the
-    // last one before which less than `target` lies: their number, or their
-    // mass.  A histogram of the values' range, then of its bin that holds the
-    // target, until a bin's values can be sorted one a thread.
-    template <int N>
-    __device__ u64 list_cut(const u64 (&r)[N], bool by_mass, u64 target, bool by_index) {
+    // Among the first n values of the list (distinct; ~0 for none), in rising
+    // order, the last one before which less than `target` lies: their number, or
+    // their mass.  A histogram of the values' range, then of its bin that holds
+    // the target, until a bin's values can be sorted one a thread.
+    __device__ u64 list_cut(unsigned n, bool by_mass, u64 target, bool by_index) {
         u64 lo = 0, hi = ~0ull - 1;
-        unsigned n;
+        unsigned left;
+#pragma unroll 1
         for (;;) {
-            u64 mn = ~0ull, mx = 0, cnt = 0, unused;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (r[j] < lo || r[j] > hi) continue;
-                mn = min(mn, r[j]);
-                mx = max(mx, r[j]);
+            __syncthreads();  // what is shared may still be read
+            if (threadIdx.x == 0) {
+                sh->list_lo = ~0ull;
+                sh->list_hi = 0;
+            }
+            u64 mn = ~0ull, mx = 0, cnt = 0;
+#pragma unroll 1
+            for (unsigned i = threadIdx.x; i < n; i += kThreads) {
+                const u64 v = fs->list[i];
+                if (v < lo || v > hi) continue;
+                mn = min(mn, v);
+                mx = max(mx, v);
                 ++cnt;
             }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) {
-                mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            left = (unsigned)scan(cnt).total;
+            if (left <= kThreads) break;
+            if (cnt) {
+                atomicMin(&sh->list_lo, mn);
+                atomicMax(&sh->list_hi, mx);
             }
-            if (lane == 0) {
-                sh->list_lo[warp] = mn;
-                sh->list_hi[warp] = mx;
-            }
-            block_scan(0, unused, cnt, cnt);
-            n = (unsigned)cnt;
-            for (int w = 0; w < kWarps; ++w) {
-                lo = w == 0 ? sh->list_lo[0] : min(lo, sh->list_lo[w]);
-                hi = w == 0 ? sh->list_hi[0] : max(hi, sh->list_hi[w]);
-            }
-            if (n <= kThreads) break;
-            const int sft = max(0, 64 - __clzll((long long)(hi - lo)) - 11);
             clear_histogram();
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (r[j] >= lo && r[j] <= hi)
-                    count_in((int)((r[j] - lo) >> sft), by_mass, by_mass ? mass_in(r[j], by_index) : 0);
+            lo = sh->list_lo;
+            hi = sh->list_hi;
+            const int sft = max(0, 64 - __clzll((long long)(hi - lo)) - 11);
+#pragma unroll 1
+            for (unsigned i = threadIdx.x; i < n; i += kThreads) {
+                const u64 v = fs->list[i];
+                if (v >= lo && v <= hi)
+                    count_in((int)((v - lo) >> sft), by_mass, by_mass ? mass_in(v, by_index) : 0);
+            }
             __syncthreads();
             constexpr int kPer = kBins / kThreads;
-            u64 bin[kPer], own = 0, total;
+            u64 bin[kPer], own = 0;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 const int i = threadIdx.x * kPer + j;
                 bin[j] = fs->hist[0][i] + ((u64)fs->hist[1][i] << 15) + ((u64)fs->hist[2][i] << 30);
                 own += bin[j];
             }
-            u64 at = block_scan(own, total, 0, unused);
-            if (total < target) return hi;  // all of them
+            const Scan s = scan(own);
+            if (s.total < target) return hi;  // all of them
+            u64 at = s.before;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 if (at < target && at + bin[j] >= target) {
@@ -667,25 +673,21 @@ struct Sampler {
             target -= sh->sel_mass;
             lo += (u64)sh->sel_bin << sft;
             hi = min(hi, lo + ((1ull << sft) - 1));
-            __syncthreads();  // before sel_bin, list_lo and the histogram are written again
         }
         // the values left, one a thread
-        u64 *buf = fs->sorted + kListMax - kThreads;  // past the histogram
+        u64 *buf = reinterpret_cast<u64 *>(fs->hist) + kThreads;  // past the sort's
         unsigned own = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) own += r[j] >= lo && r[j] <= hi;
-        u64 total, unused;
-        unsigned to = (unsigned)block_scan(own, total, 0, unused);
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (r[j] >= lo && r[j] <= hi) buf[to++] = r[j];
+#pragma unroll 1
+        for (unsigned i = threadIdx.x; i < n; i += kThreads) own += fs->list[i] >= lo && fs->list[i] <= hi;
+        unsigned to = (unsigned)scan(own).before;
+#pragma unroll 1
+        for (unsigned i = threadIdx.x; i < n; i += kThreads)
+            if (fs->list[i] >= lo && fs->list[i] <= hi) buf[to++] = fs->list[i];
         __syncthreads();
-        u64 v = threadIdx.x < n ? buf[threadIdx.x] : ~0ull;
-        __syncthreads();
-        sort(v, n);
-        const u64 w = threadIdx.x >= n ? 0 : by_mass ? mass_in(v, by_index) : 1;
-        const u64 at = block_scan(w, total, 0, unused);
-        if (threadIdx.x < n && at < target && (at + w >= target || threadIdx.x + 1 == n))
+        const u64 v = sort(threadIdx.x < left ? buf[threadIdx.x] : ~0ull, left);
+        const u64 w = threadIdx.x >= left ? 0 : by_mass ? mass_in(v, by_index) : 1;
+        const u64 at = scan(w).before;
+        if (threadIdx.x < left && at < target && (at + w >= target || threadIdx.x + 1 == left))
             sh->cut_entry = v;
         __syncthreads();
         return sh->cut_entry;
@@ -712,32 +714,32 @@ struct Sampler {
     template <typename F>
     __device__ unsigned gather(F f) {
         u64 hit[3] = {0, 0, 0};  // of this thread's elements, 136 at most
-        unsigned mine = 0;
         int at = 0;
         chunks([&](const float (&v)[E], int) {
             unsigned bits = 0;
 #pragma unroll
             for (int e = 0; e < E; ++e) bits |= f(v[e]) ? 1u << e : 0u;
-            mine += __popc(bits);
             if (at < 64) hit[0] |= (u64)bits << at;
             else if (at < 128) hit[1] |= (u64)bits << (at - 64);
             else hit[2] |= (u64)bits << (at - 128);
             at += E;
         });
+        const unsigned mine = __popcll(hit[0]) + __popcll(hit[1]) + __popcll(hit[2]);
         totals(0, mine);
         const unsigned n = all_cnt();
         if (n <= kListMax) {
             unsigned to = (unsigned)warp_scan(mine, lane) - mine;
             for (int r = 0; r < rank; ++r) to += sh->rank_cnt[r];
-            for (int w = 0; w < warp; ++w) to += sh->warp_cnt[w];
-            u64 *list = cl.map_shared_rank(fs, 0)->sorted;
-            for (int i0 = 0; i0 < 192; i0 += 64) {
-                u64 bits = i0 == 0 ? hit[0] : i0 == 64 ? hit[1] : hit[2];
+            to += __reduce_add_sync(0xffffffffu, lane < warp ? sh->warp_cnt[lane] : 0);
+            u64 *list = cl.map_shared_rank(fs, 0)->list;
+#pragma unroll 1
+            for (int j0 = 0; j0 < 192; j0 += 64) {
+                u64 bits = j0 == 0 ? hit[0] : j0 == 64 ? hit[1] : hit[2];
+#pragma unroll 1
                 for (; bits; bits &= bits - 1) {
-                    const int i = i0 + __ffsll((long long)bits) - 1;
-                    const int c = c0 + lane + 32 * (i / E), e = i % E;
-                    const float xv = El::one(reinterpret_cast<const typename El::T *>(row + (c - c0)) + e);
-                    list[to++] = ((u64)~key_of(xv) << 32) | (unsigned)(c * E + e - shift);
+                    const int j = j0 + __ffsll((long long)bits) - 1;
+                    const int i = (lane + 32 * (j / E)) * E + j % E;
+                    list[to++] = ((u64)~key_of(element(i)) << 32) | (unsigned)(i - skip());
                 }
             }
             cl.sync();
@@ -748,13 +750,6 @@ struct Sampler {
     __device__ __forceinline__ float uniform(int64_t b) const {
         const float u = a.u[b];
         return u >= 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
-    }
-
-    // log(w / s), through log1p where the share is near one.
-    static __device__ __forceinline__ float log_share(u64 w, u64 s) {
-        const float sf = __ull2float_rn(s);
-        return 2 * w > s ? log1pf(-__fdiv_rn(__ull2float_rn(s - w), sf))
-                         : logf(__fdiv_rn(__ull2float_rn(w), sf));
     }
 
     __device__ void put(int64_t b, int idx, u64 w, u64 S, u64 S_all, unsigned n_kept) {
@@ -795,9 +790,8 @@ struct Sampler {
             for (int q = 0; q < 4; ++q) bin[j][q] = 0;
             if (active && j < per) {
                 const int at = 4 * (rank * quads + first + j);
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    if (i > 0 && !by_mass) break;
+#pragma unroll 1
+                for (int i = 0; i < (by_mass ? 3 : 1); ++i) {
                     uint4 part[kMaxCluster];  // a peer past the cluster: this CTA's, not counted
 #pragma unroll
                     for (int r = 0; r < kMaxCluster; ++r)
@@ -816,10 +810,10 @@ struct Sampler {
                 for (int q = 0; q < 4; ++q) own += bin[j][q];
             }
         }
-        u64 total, unused;
-        u64 at = base + block_scan(own, total, 0, unused);
+        const Scan s = scan(own);
+        u64 at = base + s.before;
         if (threadIdx.x == 0) sh->sel_bin = kBins;
-        to_all(&sh->seg_mass[rank], total);
+        to_all(&sh->seg_mass[rank], s.total);
         cl.sync();
         for (int r = 0; r < rank; ++r) at += sh->seg_mass[r];
 #pragma unroll
@@ -848,28 +842,17 @@ struct Sampler {
         totals(0, mine);
         unsigned before = 0;
         for (int r = 0; r < rank; ++r) before += sh->rank_cnt[r];
-        for (int w = 0; w < warp; ++w) before += sh->warp_cnt[w];
+        before += __reduce_add_sync(0xffffffffu, lane < warp ? sh->warp_cnt[lane] : 0);
         const unsigned own = sh->warp_cnt[warp];
         if (before < n && n <= before + own) {  // one warp of the cluster
-            for (int base = c0; base < c1; base += 32) {
-                const int c = base + lane;
-                float v[E];
-                unsigned t = 0;
-                if (c < c1) {
-                    chunk(c, v);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) t += v[e] == logit;
+#pragma unroll 1
+            for (int i = lane; i - lane < elements(); i += 32) {
+                const bool tie = i < elements() && element(i) == logit;
+                const unsigned ties = __ballot_sync(0xffffffffu, tie);
+                if (tie && before + __popc(ties & ((1u << lane) - 1)) + 1 == n) {
+                    for (int r = 0; r < C; ++r) cl.map_shared_rank(sh, r)->cut_idx = i - skip();
                 }
-                const unsigned inc = (unsigned)warp_scan(t, lane);
-                if (before + inc - t < n && n <= before + inc) {
-                    unsigned at = before + inc - t;
-                    int idx = 0;
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (v[e] == logit && ++at == n) idx = c * E + e - shift;
-                    for (int r = 0; r < C; ++r) cl.map_shared_rank(sh, r)->cut_idx = idx;
-                }
-                before += __shfl_sync(0xffffffffu, inc, 31);
+                before += __popc(ties);
             }
         }
         cl.sync();
@@ -909,10 +892,7 @@ struct Sampler {
             const unsigned n = gather(in_bin);
             if (n <= kListMax) {
                 if (rank == 0) {
-                    u64 r[kListMax / kThreads];
-                    load_list(r, n);
-                    const u64 entry = list_cut(r, by_mass, target - base, false);
-                    __syncthreads();
+                    const u64 entry = list_cut(n, by_mass, target - base, false);
                     to_all(&sh->cut_entry, entry);
                 }
                 cl.sync();
@@ -928,21 +908,16 @@ struct Sampler {
                     khi = max(khi, key_of(x));
                 }
             });
-            klo = __reduce_min_sync(0xffffffffu, klo);
-            khi = __reduce_max_sync(0xffffffffu, khi);
-            if (lane == 0) {
-                sh->warp_lo[warp] = klo;
-                sh->warp_hi[warp] = khi;
+            if (threadIdx.x == 0) {
+                sh->lo = 0xFFFFFFFFu;
+                sh->hi = 0;
             }
             __syncthreads();
-            if ((int)threadIdx.x < C) {
-                for (int w = 0; w < kWarps; ++w) {
-                    klo = min(klo, sh->warp_lo[w]);
-                    khi = max(khi, sh->warp_hi[w]);
-                }
-                to_all(&sh->rank_lo[rank], klo);
-                to_all(&sh->rank_hi[rank], khi);
-            }
+            atomicMin(&sh->lo, klo);
+            atomicMax(&sh->hi, khi);
+            __syncthreads();
+            to_all(&sh->rank_lo[rank], sh->lo);
+            to_all(&sh->rank_hi[rank], sh->hi);
             cl.sync();
             lo = 0xFFFFFFFFu;
             hi = 0;
@@ -999,9 +974,10 @@ struct Sampler {
         if (kFilter)
             for (int i = threadIdx.x; i < kGroups; i += kThreads) fs->grp[rank][i] = 0;
         __syncthreads();
-        if ((int)threadIdx.x < C) {
+        if (warp == 0) {
+            mx = lane < kWarps ? sh->warp_max[lane] : -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh->warp_max[w]);
+            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             to_all(&sh->rank_max[rank], mx);
         }
         cl.sync();
@@ -1132,10 +1108,10 @@ struct Sampler {
             const float w = expf(z(xv));
             return kept(xv, w, idx) ? mass_of(w) : 0;
         };
-        u64 own = 0, all;
+        u64 own = 0;
 #pragma unroll 1
         for (int i = l0; i < l1; ++i) own += weight(i);
-        before += block_scan(own, all, 0, all);
+        before += scan(own).before;
         if (before > aim || before + own <= aim) return;
 #pragma unroll 1
         for (int i = l0; i < l1; ++i) {
