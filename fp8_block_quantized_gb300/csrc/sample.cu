@@ -72,6 +72,7 @@ struct Shared {
 };
 
 // With a filter.
+static_assert(kListMax >= kBins, "the list's room takes the peers' bins");
 struct FilterShared {
     // counts, or masses in three 15-bit parts: shared-memory atomics on 32 bits
     // run in hardware, and 2^17 tokens of one CTA cannot overflow a part
@@ -771,44 +772,40 @@ struct Sampler {
                 count_in(b, by_mass, by_mass ? mass_of(expf(zx)) : 0);
             }
         });
-        cl.sync();
+        __syncthreads();
     }
 
     // The first bin whose end reaches the target, given what lies before the
-    // histogram, with what lies before the bin, at every CTA.  A CTA merges
-    // kBins / C bins, four a thread, the peers' loads all in flight.
+    // histogram, with what lies before the bin, at every CTA.  Every CTA sends
+    // its bins to the CTA that adds them, kBins / C of them each (sent: stores
+    // into the peers' shared memory, a third of the time of loads from it).
     __device__ void select(bool by_mass, u64 target, u64 base) {
-        constexpr int kPer = kBins / 4 / kThreads > 0 ? kBins / 4 / kThreads : 1;  // quads a thread
-        const int quads = kBins / 4 / C;  // of this CTA
-        const int per = quads > kThreads ? kPer : 1;
-        u64 bin[kPer][4], own = 0;
-        const int first = (int)threadIdx.x * per;
-        const bool active = first < quads;
+        constexpr int kPer = kBins / kThreads;  // bins a thread
+        const int seg = kBins / C, first = (int)threadIdx.x * kPer;
+        ulonglong2 *to = reinterpret_cast<ulonglong2 *>(
+            cl.map_shared_rank(fs, first / seg)->list + rank * seg + first % seg);
+#pragma unroll
+        for (int j = 0; j < kPer; j += 2) {
+            u64 v[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int i = first + j + q;
+                v[q] = fs->hist[0][i];
+                if (by_mass) v[q] += ((u64)fs->hist[1][i] << 15) + ((u64)fs->hist[2][i] << 30);
+            }
+            to[j / 2] = make_ulonglong2(v[0], v[1]);
+        }
+        cl.sync();
+        // this CTA's bins: `per` a thread, from every rank
+        const int per = seg > kThreads ? seg / kThreads : 1;
+        const int at0 = (int)threadIdx.x * per;
+        u64 bin[kPer], own = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) bin[j][q] = 0;
-            if (active && j < per) {
-                const int at = 4 * (rank * quads + first + j);
-#pragma unroll 1
-                for (int i = 0; i < (by_mass ? 3 : 1); ++i) {
-                    uint4 part[kMaxCluster];  // a peer past the cluster: this CTA's, not counted
-#pragma unroll
-                    for (int r = 0; r < kMaxCluster; ++r)
-                        part[r] = *reinterpret_cast<const uint4 *>(
-                            &cl.map_shared_rank(fs, r < C ? r : rank)->hist[i][at]);
-#pragma unroll
-                    for (int r = 0; r < kMaxCluster; ++r) {
-                        if (r >= C) break;
-                        bin[j][0] += (u64)part[r].x << (15 * i);
-                        bin[j][1] += (u64)part[r].y << (15 * i);
-                        bin[j][2] += (u64)part[r].z << (15 * i);
-                        bin[j][3] += (u64)part[r].w << (15 * i);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) own += bin[j][q];
-            }
+            bin[j] = 0;
+            if (j < per && at0 < seg)
+                for (int r = 0; r < C; ++r) bin[j] += fs->list[r * seg + at0 + j];
+            own += bin[j];
         }
         const Scan s = scan(own);
         u64 at = base + s.before;
@@ -818,19 +815,14 @@ struct Sampler {
         for (int r = 0; r < rank; ++r) at += sh->seg_mass[r];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (active && j < per) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (at < target && at + bin[j][q] >= target) {
-                        for (int r = 0; r < C; ++r) {
-                            Shared *o = cl.map_shared_rank(sh, r);
-                            o->sel_bin = 4 * (rank * quads + first + j) + q;
-                            o->sel_mass = at;
-                        }
-                    }
-                    at += bin[j][q];
+            if (j < per && at0 < seg && at < target && at + bin[j] >= target) {
+                for (int r = 0; r < C; ++r) {
+                    Shared *o = cl.map_shared_rank(sh, r);
+                    o->sel_bin = rank * seg + at0 + j;
+                    o->sel_mass = at;
                 }
             }
+            at += bin[j];
         }
         cl.sync();
     }
