@@ -138,9 +138,10 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t x, float c, float s) {
     return pack_bf16(__fmaf_rn(a, c, -__fmul_rn(b, s)), __fmaf_rn(b, c, __fmul_rn(a, s)));
 }
 
-// A thread takes one item of up to kRopeBatch heads of one token.  Items of a
-// head: kHalf: R/16 pairs of 8-channel chunks (c, c + R/16), then the chunks
-// past R; interleaved: D/8 chunks.  Needs R % 16 == 0 (half) or R % 8 == 0.
+// A thread takes one item of up to kRopeBatch heads of one token, so that their
+// loads are in flight together and share one set of angles.  Items of a head:
+// kHalf (R % 16 == 0): R/16 pairs of 8-channel chunks (c, c + R/16), then the
+// chunks past R; interleaved (any R): D/8 chunks.
 template <bool kHalf, bool kCache>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const RopeArgs a) {
@@ -150,7 +151,7 @@ rope_kernel(const RopeArgs a) {
     for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) frac[i] = turn_fraction(a.freq[i]);
     __syncthreads();
     constexpr int kPairs = kHalf ? 8 : 4;
-    const int nrot = kHalf ? a.R / 16 : a.R / 8;
+    const int nrot = kHalf ? a.R / 16 : (a.R + 7) / 8;
     const int heads = a.Hq + a.Hk + a.Hv;
     const uint32_t per_token = (uint32_t)a.groups * a.items;
     const uint32_t total = (uint32_t)a.T * per_token;
@@ -179,23 +180,25 @@ rope_kernel(const RopeArgs a) {
             const int64_t pos = a.pos[t];
 #pragma unroll
             for (int i = 0; i < kPairs; ++i)
-                angle(frac[kPairs * item + i], pos, a.mscale, a.backward, c[i], s[i]);
+                if (kHalf || kPairs * item + i < a.R / 2)
+                    angle(frac[kPairs * item + i], pos, a.mscale, a.backward, c[i], s[i]);
         }
 #pragma unroll
         for (int b = 0; b < kRopeBatch; ++b) {
             if (h0 + b >= h1) break;
             const Head hd = head_of<kCache>(a, t, h0 + b, slot);
             if (rot && hd.rotate) {
-                if (kHalf) {
+                if constexpr (kHalf) {
                     turn_half(x[b].x, y[b].x, c, s);
                     turn_half(x[b].y, y[b].y, c + 2, s + 2);
                     turn_half(x[b].z, y[b].z, c + 4, s + 4);
                     turn_half(x[b].w, y[b].w, c + 6, s + 6);
                 } else {
+                    const int last = a.R / 2 - 4 * item;  // pairs of this chunk that turn
                     x[b].x = turn_pair(x[b].x, c[0], s[0]);
-                    x[b].y = turn_pair(x[b].y, c[1], s[1]);
-                    x[b].z = turn_pair(x[b].z, c[2], s[2]);
-                    x[b].w = turn_pair(x[b].w, c[3], s[3]);
+                    if (last > 1) x[b].y = turn_pair(x[b].y, c[1], s[1]);
+                    if (last > 2) x[b].z = turn_pair(x[b].z, c[2], s[2]);
+                    if (last > 3) x[b].w = turn_pair(x[b].w, c[3], s[3]);
                 }
             }
             store8<kCache>(hd, d0, x[b]);
@@ -214,9 +217,10 @@ __device__ __forceinline__ void store1(const Head &hd, int d, uint32_t bf16) {
     }
 }
 
-// Any even R (the pairs do not fill 16-byte chunks): items are the R/2 pairs,
-// then the single channels past R.
-template <bool kHalf, bool kCache>
+// The half layout where the second half starts inside a 16-byte chunk: items are
+// the R/2 pairs, channel by channel, the single channels up to the next chunk,
+// then the chunks past them.
+template <bool kCache>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_any_kernel(const RopeArgs a) {
     extern __shared__ unsigned long long frac[];
@@ -224,32 +228,31 @@ rope_any_kernel(const RopeArgs a) {
     jet::griddep_wait();
     for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) frac[i] = turn_fraction(a.freq[i]);
     __syncthreads();
-    const int heads = a.Hq + a.Hk + a.Hv;
+    const int heads = a.Hq + a.Hk + a.Hv, R8 = (a.R + 7) / 8 * 8;
     const uint32_t per_token = (uint32_t)a.groups * a.items;
     const uint32_t total = (uint32_t)a.T * per_token;
     for (uint64_t idx = blockIdx.x * (uint64_t)kRopeThreads + threadIdx.x; idx < total;
          idx += (uint64_t)gridDim.x * kRopeThreads) {
         const uint32_t t = (uint32_t)idx / per_token, rest = (uint32_t)idx - t * per_token;
         const uint32_t grp = rest / a.items;
-        const int item = (int)(rest - grp * a.items);
-        const bool rot = item < a.R / 2;
+        const int item = (int)(rest - grp * a.items), single = item - a.R / 2;
         const int h0 = (int)grp * a.hpt, h1 = min(h0 + a.hpt, heads);
         const int64_t slot = kCache ? a.slots[t] : 0;
-        const int d0 = !rot ? item + a.R / 2 : kHalf ? item : 2 * item;
-        const int d1 = kHalf ? item + a.R / 2 : 2 * item + 1;
         float c = 1.0f, s = 0.0f;
-        if (rot) angle(frac[item], a.pos[t], a.mscale, a.backward, c, s);
+        if (single < 0) angle(frac[item], a.pos[t], a.mscale, a.backward, c, s);
         for (int h = h0; h < h1; ++h) {
             const Head hd = head_of<kCache>(a, t, h, slot);
-            const uint32_t x = hd.in[d0];
-            if (!rot) {
-                store1<kCache>(hd, d0, x);
-                continue;
+            if (single < 0) {
+                uint32_t w = hd.in[item] | ((uint32_t)hd.in[item + a.R / 2] << 16);
+                if (hd.rotate) w = turn_pair(w, c, s);
+                store1<kCache>(hd, item, w & 0xFFFFu);
+                store1<kCache>(hd, item + a.R / 2, w >> 16);
+            } else if (single < R8 - a.R) {
+                store1<kCache>(hd, a.R + single, hd.in[a.R + single]);
+            } else {
+                const int d = R8 + 8 * (single - (R8 - a.R));
+                store8<kCache>(hd, d, *reinterpret_cast<const uint4 *>(hd.in + d));
             }
-            uint32_t w = x | ((uint32_t)hd.in[d1] << 16);
-            if (hd.rotate) w = turn_pair(w, c, s);
-            store1<kCache>(hd, d0, w & 0xFFFFu);
-            store1<kCache>(hd, d1, w >> 16);
         }
     }
 }
@@ -257,8 +260,10 @@ rope_any_kernel(const RopeArgs a) {
 jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo &dev,
                        jet_stream_t stream) {
     const bool half = layout == JET_ROPE_HALF;
-    const bool vec = half ? a.R % 16 == 0 : a.R % 8 == 0;
-    a.items = vec ? (half ? a.R / 16 + (a.D - a.R) / 8 : a.D / 8) : a.R / 2 + (a.D - a.R);
+    const bool vec = !half || a.R % 16 == 0;
+    const int R8 = (a.R + 7) / 8 * 8;
+    a.items = !half ? a.D / 8 : vec ? a.R / 16 + (a.D - a.R) / 8
+                                    : a.R / 2 + (R8 - a.R) + (a.D - R8) / 8;
     const int heads = a.Hq + a.Hk + a.Hv;
     // More heads per thread share one set of angles; fewer keep the SMs busy
     // when there are few tokens.
@@ -269,12 +274,14 @@ jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo
     const int64_t total = a.T * a.groups * a.items;
     if (total >= ((int64_t)1 << 32)) return JET_ERR_SHAPE;
     const int64_t want = (total + kRopeThreads - 1) / kRopeThreads;
-    const int64_t cap = (int64_t)dev.num_sms * 8;
+    // Twice the resident CTAs (3 per SM for the half layout, 5 interleaved; 6 for
+    // the channel-wise one): 16384 tokens of 64 + 8 + 8 heads take 110 us with 6
+    // per SM, 115 with 8, 140 with 5.
+    const int64_t cap = (int64_t)dev.num_sms * (half ? 6 : 10);
     void (*kernel)(RopeArgs) =
         vec ? (half ? (cache ? rope_kernel<true, true> : rope_kernel<true, false>)
                     : (cache ? rope_kernel<false, true> : rope_kernel<false, false>))
-            : (half ? (cache ? rope_any_kernel<true, true> : rope_any_kernel<true, false>)
-                    : (cache ? rope_any_kernel<false, true> : rope_any_kernel<false, false>));
+            : (cache ? rope_any_kernel<true> : rope_any_kernel<false>);
     return jet::launch_pdl(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kRopeThreads),
                            (size_t)a.R / 2 * sizeof(unsigned long long), jet::as_stream(stream), a);
 }
