@@ -611,6 +611,12 @@ def _arg(t, dtype, shape, name):
     return t.data_ptr() or None
 
 
+def _call(fn, *args):
+    code = getattr(_lib or load(), fn)(*args)
+    if code != 0:
+        raise JetError(fn, code)
+
+
 def _raw_stream(stream):
     import torch
     if stream is None:  # torch.cuda.current_stream() without its object: 0.3 against 3 us
@@ -636,10 +642,10 @@ def jet_add_rmsnorm_quant_1x128(x, d, g, eps, h, q, s, rstd=None, stream=None):
     import torch
     M, K = x.shape
     bf16, f32 = torch.bfloat16, torch.float32
-    _check("jet_add_rmsnorm_quant_1x128", load().jet_add_rmsnorm_quant_1x128(
-        _arg(x, bf16, (M, K), "x"), _arg(d, bf16, (M, K), "d"), _arg(g, bf16, (K,), "g"), M, K,
+    _call(
+        "jet_add_rmsnorm_quant_1x128", _arg(x, bf16, (M, K), "x"), _arg(d, bf16, (M, K), "d"), _arg(g, bf16, (K,), "g"), M, K,
         eps, _arg(h, bf16, (M, K), "h"), _arg(q, torch.uint8, (M, K), "q"),
-        _arg(s, f32, (K // 128, M), "s"), _arg(rstd, f32, (M,), "rstd"), _raw_stream(stream)))
+        _arg(s, f32, (K // 128, M), "s"), _arg(rstd, f32, (M,), "rstd"), _raw_stream(stream))
 
 
 def add_rmsnorm_quant_1x128(x, d, g, eps=1e-5, with_rstd=False, stream=None):
@@ -665,16 +671,16 @@ def jet_add_rmsnorm_bwd(h, g, rstd, dys, dres, dx, dg, ws=None, stream=None):
     bf16, f32 = torch.bfloat16, torch.float32
     if not 1 <= len(dys) <= 3:
         raise ValueError(f"dys: expected one to three gradients, got {len(dys)}")
-    dy = [_arg(t, bf16, (M, K), f"dys[{i}]") for i, t in enumerate(dys)] + [None, None]
+    dy = [_arg(t, bf16, h.shape, "dys") for t in dys] + [None, None]
     if ws is None:
         need = workspace_bytes("add_rmsnorm_bwd", M, 0, K)
         with _allocating_on(stream):
             ws = torch.empty((need,), dtype=torch.uint8, device=h.device)
-    _check("jet_add_rmsnorm_bwd", load().jet_add_rmsnorm_bwd(
-        _arg(h, bf16, (M, K), "h"), _arg(g, bf16, (K,), "g"), _arg(rstd, f32, (M,), "rstd"),
+    _call(
+        "jet_add_rmsnorm_bwd", _arg(h, bf16, (M, K), "h"), _arg(g, bf16, (K,), "g"), _arg(rstd, f32, (M,), "rstd"),
         dy[0], dy[1], dy[2], _arg(dres, bf16, (M, K), "dres"), M, K,
         _arg(dx, bf16, (M, K), "dx"), _arg(dg, f32, (K,), "dg"), ws.data_ptr() or None,
-        ws.numel() * ws.element_size(), _raw_stream(stream)))
+        ws.numel() * ws.element_size(), _raw_stream(stream))
 
 
 def add_rmsnorm_bwd(h, g, rstd, dys, dres=None, stream=None):
@@ -707,13 +713,14 @@ def _heads(t, T, D, name):
         return None, 0, 0
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
-        raise ValueError(f"{name}: expected shape ({T}, heads, {D}), got {tuple(t.shape)}")
-    H = t.shape[1]
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D:
+        raise ValueError(f"{name}: expected shape ({T}, heads, {D}), got {tuple(shape)}")
+    H = shape[1]
     if T == 0 or H == 0 or D == 0:
         return None, H * D, H
     ld, sh, sd = t.stride()
-    if not t.is_cuda or (sd != 1 and D > 1) or (sh != D and H > 1):
+    if (sd != 1 and D > 1) or (sh != D and H > 1) or not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor whose tokens hold contiguous heads")
     return t.data_ptr(), (ld if T > 1 else H * D), H
 
@@ -731,10 +738,10 @@ def jet_rope(q, k, inv_freq, pos, q_out, k_out, layout="half", mscale=1.0, backw
     ko, ldko, Hko = _heads(k_out, T, D, "k_out")
     if Hqo != Hq or Hko != Hk:
         raise ValueError("q_out and k_out must have the heads of q and k")
-    _check("jet_rope", load().jet_rope(
-        qp, ldq, Hq, kp, ldk, Hk, T, D, R, _arg(inv_freq, torch.float64, (R // 2,), "inv_freq"),
+    _call(
+        "jet_rope", qp, ldq, Hq, kp, ldk, Hk, T, D, R, _arg(inv_freq, torch.float64, (R // 2,), "inv_freq"),
         _arg(pos, torch.int64, (T,), "pos"), ROPE_LAYOUT[layout], mscale, int(backward), qo, ldqo,
-        ko, ldko, _raw_stream(stream)))
+        ko, ldko, _raw_stream(stream))
 
 
 def rope(q, k, inv_freq, pos, layout="half", mscale=1.0, backward=False, stream=None):
@@ -761,13 +768,13 @@ def jet_rope_kv_cache_write(q, k, v, inv_freq, pos, k_scale, v_scale, slots, q_o
     S = k_cache.shape[0]
     if Hqo != Hq or Hv != Hk:
         raise ValueError("q_out must have the heads of q, and v those of k")
-    _check("jet_rope_kv_cache_write", load().jet_rope_kv_cache_write(
-        qp, ldq, Hq, kp, ldk, vp, ldv, Hk, T, D, R,
+    _call(
+        "jet_rope_kv_cache_write", qp, ldq, Hq, kp, ldk, vp, ldv, Hk, T, D, R,
         _arg(inv_freq, torch.float64, (R // 2,), "inv_freq"), _arg(pos, torch.int64, (T,), "pos"),
         ROPE_LAYOUT[layout], mscale, _arg(k_scale, f32, (Hk,), "k_scale"),
         _arg(v_scale, f32, (Hk,), "v_scale"), _arg(slots, torch.int64, (T,), "slots"), qo, ldqo,
         _arg(k_cache, u8, (S, Hk, D), "k_cache"), _arg(v_cache, u8, (S, Hk, D), "v_cache"), S,
-        _raw_stream(stream)))
+        _raw_stream(stream))
 
 
 def jet_kv_slot_map(cached, added, block_size, table, free_blocks, free_next, offsets, positions,
@@ -777,14 +784,14 @@ def jet_kv_slot_map(cached, added, block_size, table, free_blocks, free_next, of
     import torch
     B, width, n_free, N = cached.numel(), table.shape[1], free_blocks.numel(), slots.numel()
     i32, i64 = torch.int32, torch.int64
-    _check("jet_kv_slot_map", load().jet_kv_slot_map(
-        _arg(cached, i32, (B,), "cached"), _arg(added, i32, (B,), "added"), B, block_size,
+    _call(
+        "jet_kv_slot_map", _arg(cached, i32, (B,), "cached"), _arg(added, i32, (B,), "added"), B, block_size,
         _arg(table, i32, (B, width), "table"), width,
         _arg(free_blocks, i32, (n_free,), "free_blocks"), n_free,
         _arg(free_next, i64, free_next.shape, "free_next"), N,
         _arg(offsets, i64, (B + 1,), "offsets"), _arg(positions, i64, (N,), "positions"),
         _arg(slots, i64, (N,), "slots"), _arg(rows, i32, (N,), "rows"),
-        _arg(counts, i64, (2,), "counts"), _raw_stream(stream)))
+        _arg(counts, i64, (2,), "counts"), _raw_stream(stream))
 
 
 def kv_slot_map(cached, added, block_size, table, free_blocks, free_next, capacity, stream=None):
@@ -815,13 +822,13 @@ def jet_sample(logits, u, temperature, top_k, top_p, min_p, token, logp, logp_al
     if logits.numel() and (not logits.is_cuda or (V > 1 and logits.stride(1) != 1)):
         raise ValueError("logits: must be a CUDA tensor with contiguous rows")
     ld = logits.stride(0) if B > 1 else V
-    _check("jet_sample", load().jet_sample(
-        logits.data_ptr() or None, int(logits.dtype == f32), B, V, ld, _arg(u, f32, (B,), "u"),
+    _call(
+        "jet_sample", logits.data_ptr() or None, int(logits.dtype == f32), B, V, ld, _arg(u, f32, (B,), "u"),
         _arg(temperature, f32, (B,), "temperature"), _arg(top_k, i32, (B,), "top_k"),
         _arg(top_p, f32, (B,), "top_p"), _arg(min_p, f32, (B,), "min_p"),
         _arg(token, torch.int64, (B,), "token"), _arg(logp, f32, (B,), "logp"),
         _arg(logp_all, f32, (B,), "logp_all"), _arg(kept, i32, (B,), "kept"),
-        _raw_stream(stream)))
+        _raw_stream(stream))
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):

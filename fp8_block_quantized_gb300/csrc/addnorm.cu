@@ -268,8 +268,10 @@ __device__ __forceinline__ void store_part(float *p, const float (&dg)[8]) {
     reinterpret_cast<float4 *>(p)[1] = make_float4(dg[4], dg[5], dg[6], dg[7]);
 }
 
-// K <= 8192: one chunk a thread.
-__global__ void __launch_bounds__(1024)
+// K <= 8192: one chunk a thread, at most kMax of them; two CTAs an SM where the
+// registers allow it.
+template <int kMax>
+__global__ void __launch_bounds__(kMax, kMax <= 640 ? 2 : 1)
 add_rmsnorm_bwd_kernel(const BwdArgs a) {
     extern __shared__ uint4 stage[];  // [2][nt][threads]
     __shared__ float red[2][32];
@@ -430,6 +432,17 @@ int64_t bwd_parts(int64_t M, int64_t K) {
     return M < cap ? M : cap;
 }
 
+// Allows a kernel more than the 48 KB of shared memory, its static part among
+// them, that every launch may have.
+template <typename K>
+bool allow_smem(K *kernel, size_t bytes) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+        cudaSuccess)
+        return true;
+    cudaGetLastError();
+    return false;
+}
+
 template <int kBytes>
 bool aligned_to(const void *p) { return (reinterpret_cast<uintptr_t>(p) & (kBytes - 1)) == 0; }
 
@@ -475,12 +488,7 @@ jet_status jet_add_rmsnorm_quant_1x128(const uint16_t *x, const uint16_t *d, con
                           : ni == 2 ? add_rmsnorm_row_kernel<512, 2>
                           : ni <= 4 ? add_rmsnorm_row_kernel<512, 4> : add_rmsnorm_row_kernel<512, 8>);
         const size_t smem = (size_t)K * 2;
-        if (smem > 48 * 1024 &&
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-                cudaSuccess) {
-            cudaGetLastError();
-            return JET_ERR_CUDA;
-        }
+        if (smem > 40 * 1024 && !allow_smem(kernel, smem)) return JET_ERR_CUDA;
         return jet::launch_pdl(kernel, dim3((unsigned)M), dim3((unsigned)T), smem, cs, x, d, g, M, K,
                                eps, h, q, s, rstd);
     }
@@ -537,20 +545,17 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
     a.K = K;
     a.dx = dx;
     a.part = static_cast<float *>(ws);
-    auto *kernel = nc == 1 ? add_rmsnorm_bwd_kernel
+    auto *kernel = nc == 1 ? (threads <= 512 ? add_rmsnorm_bwd_kernel<512>
+                              : threads <= 640 ? add_rmsnorm_bwd_kernel<640>
+                                               : add_rmsnorm_bwd_kernel<1024>)
                            : nc == 2 ? add_rmsnorm_bwd_wide_kernel<2> : add_rmsnorm_bwd_wide_kernel<4>;
     const size_t smem = nc == 1 ? (size_t)2 * a.nt * threads * 16 : 0;
-    int per_sm = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) !=
-            cudaSuccess ||
-        per_sm < 1) {
-        cudaGetLastError();
-        return JET_ERR_CUDA;
-    }
-    // persistent CTAs, as many as are resident and as there are partial rows
-    const int64_t resident = (int64_t)dev.num_sms * per_sm;
+    if (smem > 40 * 1024 && !allow_smem(kernel, smem)) return JET_ERR_CUDA;
+    // persistent CTAs, as many as fit (registers, shared memory with 1 KB
+    // of the system's) and as there are partial rows
+    const int64_t by_threads = threads > 512 && threads <= 640 ? 2 : 1024 / threads, by_smem = 228 * 1024 / (smem + 1024 + 256);
+    const int64_t per_sm = by_threads < by_smem ? by_threads : by_smem;
+    const int64_t resident = (int64_t)dev.num_sms * (per_sm > 0 ? per_sm : 1);
     const int64_t most = bwd_parts(M, K);
     const int parts = (int)(most < resident ? most : resident);
     st = jet::launch_pdl(kernel, dim3((unsigned)parts), dim3((unsigned)threads), smem, cs, a);

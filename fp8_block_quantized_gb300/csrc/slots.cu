@@ -152,7 +152,7 @@ jet_status jet_kv_slot_map(const int32_t *cached, const int32_t *added, int64_t 
     if (st != JET_OK) return st;
     constexpr size_t kMaxSmem = (kSmMaxRequests + 1) * 8 + kSmMaxRequests * 12;
     const size_t smem = (size_t)(B + 1) * 8 + (size_t)B * 12;
-    if (smem > 48 * 1024 &&
+    if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(kv_slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)kMaxSmem) != cudaSuccess) {
         cudaGetLastError();

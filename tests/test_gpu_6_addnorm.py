@@ -29,7 +29,7 @@ def stream_pair(M, K, seed):
 
 
 SHAPES = [(1, 128), (1, 4096), (2, 256), (7, 384), (16, 5120), (33, 1024), (150, 2048), (153, 8192),
-          (305, 4096), (700, 640), (1217, 8320), (3, 14336), (40, 25600), (2, 65536), (5000, 128)]
+          (305, 4096), (700, 640), (1217, 8320), (3, 14336), (5, 24576), (40, 25600), (2, 65536), (5000, 128)]
 
 
 @pytest.mark.parametrize("M,K", SHAPES)

@@ -65,7 +65,7 @@ def state(rng, B, most_cached, most_added, bs, spare=5):
 
 @pytest.mark.parametrize("B,most_cached,most_added,bs", [
     (1, 0, 1, 16), (1, 100, 1, 16), (3, 40, 9, 4), (256, 300, 1, 16), (48, 500, 200, 64), (513, 40, 3, 8),
-    (1030, 20, 2, 1), (7, 1000, 700, 24), (2, 5, 3000, 7), (5000, 10, 1, 3), (8192, 3, 1, 2)])
+    (1030, 20, 2, 1), (7, 1000, 700, 24), (2, 5, 3000, 7), (2457, 6, 2, 4), (5000, 10, 1, 3), (8192, 3, 1, 2)])
 @pytest.mark.parametrize("extra", [0, 37])
 def test_against_the_loop(jet, B, most_cached, most_added, bs, extra):
     rng = np.random.default_rng(B + bs)
