@@ -608,8 +608,9 @@ JET_API jet_status jet_kv_slot_map(const int32_t *cached, const int32_t *added, 
 /*
  * One token per row of logits, drawn with temperature, top-k, top-p and min-p
  * from given uniform numbers, and its log-probabilities (the logp_rollout of
- * the mismatch metric).  Per row, with m the largest logit:
- *   z_i = fl32(fl32(x_i - m) * fl32(1 / temperature)), w_i = fl32(e^z_i);
+ * the mismatch metric).  Per row, with m the largest logit and r =
+ * fl32(1 / temperature), brought into binary32's normal range:
+ *   z_i = fl32(fl32(x_i - m) * r), w_i = fl32(e^z_i) (CUDA's expf);
  * in the order of falling logit, ties by rising index, kept are the tokens of
  * rank < top_k, of those the ones before which less than top_p of their mass
  * lies, and of those the ones with w_i >= min_p (the largest w is 1).  Drawn
@@ -618,8 +619,8 @@ JET_API jet_status jet_kv_slot_map(const int32_t *cached, const int32_t *added, 
  * integers of w_i 2^45 (rounded to nearest), so the token does not depend on
  * the batch or the launch.
  *   logits: row b at logits + b*ld elements, BF16 or FP32 by `dtype`
- *       (jet_dtype).  -inf and NaN are never drawn; +inf entries share the
- *       row's whole weight.  ld >= V; rows need no alignment.
+ *       (jet_dtype).  -inf and NaN are never drawn; +inf counts as the type's
+ *       largest finite number.  ld >= V; rows need no alignment.
  *   u [B] FP32 in [0, 1) (others are brought to the nearest end).
  *   temperature, top_p, min_p [B] FP32, top_k [B] int32: one per row, or NULL:
  *       1, 1, 0, off.  temperature <= 0: the largest logit (lowest index);
