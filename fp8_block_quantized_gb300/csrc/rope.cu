@@ -271,9 +271,6 @@ jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo
     while (a.hpt > 1 && a.T * ((heads + a.hpt - 1) / a.hpt) * a.items < (int64_t)dev.num_sms * 2048)
         a.hpt /= 2;
     a.groups = (heads + a.hpt - 1) / a.hpt;
-    const int64_t total = a.T * a.groups * a.items;
-    if (total >= ((int64_t)1 << 32)) return JET_ERR_SHAPE;
-    const int64_t want = (total + kRopeThreads - 1) / kRopeThreads;
     // Twice the resident CTAs (3 per SM for the half layout, 5 interleaved; 6 for
     // the channel-wise one): 16384 tokens of 64 + 8 + 8 heads take 110 us with 6
     // per SM, 115 with 8, 140 with 5.
@@ -282,8 +279,25 @@ jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo
         vec ? (half ? (cache ? rope_kernel<true, true> : rope_kernel<true, false>)
                     : (cache ? rope_kernel<false, true> : rope_kernel<false, false>))
             : (cache ? rope_any_kernel<true> : rope_any_kernel<false>);
-    return jet::launch_pdl(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kRopeThreads),
-                           (size_t)a.R / 2 * sizeof(unsigned long long), jet::as_stream(stream), a);
+    // The kernels count a launch's items in 32 bits: more tokens take several launches.
+    const int64_t all = a.T, most = (((int64_t)1 << 32) - 1) / ((int64_t)a.groups * a.items);
+    for (int64_t t0 = 0; t0 < all; t0 += most) {
+        a.T = all - t0 < most ? all - t0 : most;
+        const int64_t want = (a.T * a.groups * a.items + kRopeThreads - 1) / kRopeThreads;
+        const jet_status st = jet::launch_pdl(
+            kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kRopeThreads),
+            (size_t)a.R / 2 * sizeof(unsigned long long), jet::as_stream(stream), a);
+        if (st != JET_OK) return st;
+        auto step = [&](const uint16_t *&p, int64_t ld) { p = p ? p + most * ld : p; };
+        step(a.q, a.ldq);
+        step(a.k, a.ldk);
+        step(a.v, a.ldv);
+        a.qo = a.qo ? a.qo + most * a.ldqo : a.qo;
+        a.ko = a.ko ? a.ko + most * a.ldko : a.ko;
+        a.pos += most;
+        a.slots = a.slots ? a.slots + most : a.slots;
+    }
+    return JET_OK;
 }
 
 // Sizes both entry points share.

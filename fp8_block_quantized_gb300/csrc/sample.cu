@@ -161,13 +161,15 @@ __device__ __noinline__ u64 share(float f, u64 s, bool up) {
     return q + (up && rest != 0);
 }
 
-// Sums of round(w 2^45) of one thread, in two 32-bit halves (weights of 1 at
-// most, 512 of them at most): adding 2^23 to w 2^22 leaves its integer part
-// `hi` in the low bits; what is left, times 2^23, is rounded the same way.
-// Exact, and without the 64-bit conversion, whose rate is a quarter of the
-// multiply-adds'.
+// Sums of round(w 2^45) of one thread, weights of 1 at most, in two 32-bit halves
+// that are carried into 64 bits before kRun weights could overflow them: adding
+// 2^23 to w 2^22 leaves its integer part `hi` in the low bits; what is left,
+// times 2^23, is rounded the same way.  Exact, and without the 64-bit
+// conversion, whose rate is a quarter of the multiply-adds'.
 struct MassSum {
-    unsigned hi = 0, lo = 0;
+    static constexpr unsigned kRun = 256;  // 2^8 2^22 in either half
+    u64 sum = 0;
+    unsigned hi = 0, lo = 0, n = 0;
     __device__ __forceinline__ void add2(float w0, float w1) {
         const float2 w = make_float2(w0, w1), up = make_float2(0x1p22f, 0x1p22f);
         const float2 big = make_float2(0x1p23f, 0x1p23f);
@@ -178,9 +180,18 @@ struct MassSum {
         hi += __float_as_uint(t.x) + __float_as_uint(t.y);
         lo += __float_as_uint(l.x) + __float_as_uint(l.y);
     }
-    // n: how many weights were added
-    __device__ __forceinline__ u64 total(unsigned n) const {
-        return ((u64)(hi - n * 0x4B000000u) << 23) + (u64)(int64_t)(int)(lo - n * 0x4B400000u);
+    // After `added` more weights, 32 at most.
+    __device__ __forceinline__ void count(unsigned added) {
+        n += added;
+        if (n >= kRun) carry();
+    }
+    __device__ __forceinline__ void carry() {
+        sum += ((u64)(hi - n * 0x4B000000u) << 23) + (u64)(int64_t)(int)(lo - n * 0x4B400000u);
+        hi = lo = n = 0;
+    }
+    __device__ __forceinline__ u64 total() {
+        carry();
+        return sum;
     }
 };
 
@@ -347,9 +358,9 @@ struct Sampler {
 
     // f(values) for every chunk of this warp's range, the values as they are in
     // global memory: whole chunks four loads in flight a thread, then the row's
-    // ragged ends.
-    template <typename F>
-    __device__ __forceinline__ void global_chunks(F f) {
+    // ragged ends.  After some of them, done(their number).
+    template <typename F, typename G>
+    __device__ __forceinline__ void global_chunks(F f, G done) {
         const int first = shift > 0, past = (shift + a.V) / E;  // the whole chunks
         int c = max(c0, first) + lane;
         const int end = min(c1, past);
@@ -362,11 +373,13 @@ struct Sampler {
                 El::load(t[i], v);
                 f(v);
             }
+            done(4);
         }
 #pragma unroll 1
         for (; c < end; c += 32, p += 32) {
             El::load(*p, v);
             f(v);
+            done(1);
         }
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {  // chunk 0 and chunk `past`, where they are not whole
@@ -374,6 +387,7 @@ struct Sampler {
             if (lane == i && r >= c0 && r < c1 && !whole(r) && (i == 0 || past > 0)) {
                 ragged(r, v);
                 f(v);
+                done(1);
             }
         }
     }
@@ -465,7 +479,7 @@ struct Sampler {
             }
         };
         if (!kFilter) {
-            global_chunks([&](float (&v)[E]) { take(v); });
+            global_chunks([&](float (&v)[E]) { take(v); }, [](int) {});
             finite = n;
             return mx;
         }
@@ -508,7 +522,6 @@ struct Sampler {
     // This thread's weights.
     __device__ __forceinline__ u64 weigh() {
         MassSum s;
-        unsigned n = 0;
         const float2 nm = make_float2(-m, -m), r2 = make_float2(rt, rt);
         auto add = [&](const float (&v)[E]) {
 #pragma unroll
@@ -516,25 +529,27 @@ struct Sampler {
                 const float2 zz = __fmul2_rn(__fadd2_rn(make_float2(v[e], v[e + 1]), nm), r2);
                 s.add2(expf(zz.x), expf(zz.y));
             }
-            n += E;
         };
         if (kFilter) {
-            chunks([&](const float (&v)[E], int) { add(v); });
+            chunks([&](const float (&v)[E], int) {
+                add(v);
+                s.count(E);
+            });
         } else if (!infinite) {
             global_chunks([&](float (&v)[E]) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
                 add(v);
-            });
+            }, [&](int n) { s.count(n * E); });
         } else {
             global_chunks([&](float (&v)[E]) {
                 lower(v);
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
                 add(v);
-            });
+            }, [&](int n) { s.count(n * E); });
         }
-        return s.total(n);
+        return s.total();
     }
 
     __device__ __forceinline__ Scan scan(u64 v, u64 o = 0) { return block_scan(v, o, sh->scan); }
@@ -931,7 +946,7 @@ struct Sampler {
     // Mass of the kept tokens; their totals at every CTA.
     __device__ u64 kept_totals() {
         MassSum s;
-        unsigned n = 0, cnt = 0;
+        unsigned cnt = 0;
         const float low = fmaxf(cut_x, -0x1.fffffep127f);  // no -inf is kept
         chunks([&](const float (&v)[E], int c) {
             float w[E];
@@ -945,9 +960,9 @@ struct Sampler {
             }
 #pragma unroll
             for (int e = 0; e < E; e += 2) s.add2(w[e], w[e + 1]);
-            n += E;
+            s.count(E);
         });
-        totals(s.total(n), cnt);
+        totals(s.total(), cnt);
         return all_mass();
     }
 

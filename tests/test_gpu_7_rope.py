@@ -167,3 +167,23 @@ def test_empty(jet):
     q, k = jet.rope(e, e, freqs(64), torch.empty((0,), dtype=torch.int64, device="cuda"))
     torch.cuda.synchronize()
     assert q.shape == (0, 4, 64)
+
+
+def test_more_tokens_than_one_launch_counts(jet):
+    """2^30 tokens of one small head (items past 32 bits, offsets past 2^33 bytes):
+    the last tokens are turned as in a small call, the others keep their zeros."""
+    T, D, at = (1 << 30) + 5, 8, [0, 3, (1 << 30) - 1, 1 << 30, (1 << 30) + 4]
+    if torch.cuda.get_device_properties(0).total_memory < 60 << 30:
+        pytest.skip("needs 40 GB")
+    f = freqs(D)
+    q = torch.zeros((T, 1, D), dtype=BF16, device="cuda")
+    pos = torch.arange(T, device="cuda")
+    rows = heads(len(at), 1, D, 3)
+    at = torch.tensor(at, device="cuda")
+    q[at] = rows
+    jet.jet_rope(q, None, f, pos, q, None)
+    small, _ = jet.rope(rows, None, f, pos[at])
+    torch.cuda.synchronize()
+    assert torch.equal(q[at], small)
+    q[at] = 0
+    assert not q.any()

@@ -207,3 +207,23 @@ def test_empty_batch(jet):
     out = jet.sample(torch.empty((0, 100), device="cuda"), torch.empty((0,), device="cuda"))
     torch.cuda.synchronize()
     assert out[0].shape == (0,)
+
+
+@pytest.mark.parametrize("gap", [0.3, 0.45, 1.7])
+def test_many_long_flat_rows(jet, gap):
+    """Hundreds of long rows (one CTA a row, hundreds of logits a thread) of two
+    levels, whose weights all carry large low-order parts: the same tokens and
+    log-probabilities as each row alone, and the sums of the definition."""
+    B, V = 310, 190001
+    x = torch.zeros((1, V), dtype=BF16, device="cuda")
+    x[0, 1:] = -gap
+    x = x.expand(B, V).contiguous()
+    u = (torch.arange(B) + 0.5) / B
+    out = jet.sample(x, u.cuda())
+    alone = jet.sample(x[7:8].clone(), u[7:8].cuda())
+    torch.cuda.synchronize()
+    for a, b in zip(out, alone):
+        assert torch.equal(a[7:8], b)
+    xs = x[0].float().cpu().numpy()
+    for b in (0, 1, 150, 309):
+        check_row(xs, float(u[b]), 1.0, 0, 1.0, 0.0, *(t[b].item() for t in out))
