@@ -4,7 +4,10 @@ Argument marshalling only: every function here takes CUDA tensors, checks
 their dtype/shape/device, and forwards the raw device pointers, sizes and the
 current CUDA stream to the C entry point of the same name.  All quantization,
 GEMM and reduction work happens in the library's kernels.  There is no CPU
-fallback: if the library is missing or fails to load, ``load()`` raises.
+fallback: if the library is missing or fails to load, ``load()`` raises.  The
+operators that a decoding step calls many times (residual norms, rotary
+positions, slot maps, sampling) are marshalled by a compiled module,
+``pysrc/marshal.cpp``, with the same checks.
 """
 from __future__ import annotations
 
@@ -16,6 +19,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None    # the compiled marshalling, bound to _lib's functions
 
 STATUS = {0: "JET_OK", 1: "JET_ERR_NULL", 2: "JET_ERR_SHAPE", 3: "JET_ERR_ALIGN",
           4: "JET_ERR_CUDA", 5: "JET_ERR_DEVICE", 6: "JET_ERR_WORKSPACE",
@@ -99,7 +103,33 @@ def load(build_if_missing: bool = True):
             f.argtypes = args
             f.restype = _RESTYPE.get(name, ctypes.c_int)
         _lib = lib
+        bind(lib)
         return lib
+
+
+# The C functions the compiled module calls, in the order it takes them.
+MARSHALLED = ("jet_add_rmsnorm_quant_1x128", "jet_add_rmsnorm_bwd", "jet_rope",
+              "jet_rope_kv_cache_write", "jet_kv_slot_map", "jet_sample", "jet_workspace_bytes")
+
+
+def bind(lib):
+    """Load the compiled marshalling and give it the library's functions."""
+    global _marshal
+    import importlib.util
+
+    import torch  # noqa: F401  (the module needs torch's libraries)
+    spec = importlib.util.spec_from_file_location("_marshal", _build.MARSHAL)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.bind(JetError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in MARSHALLED))
+    _marshal = m
+
+
+def _compiled():
+    """The compiled marshalling, the library loaded."""
+    if _marshal is None:
+        load()
+    return _marshal
 
 
 def _check(fn: str, code: int):
@@ -602,28 +632,6 @@ def token_mismatch_masked(logp_train, logp_rollout, mask=None, cap: float = 0.0,
 # Residual RMSNorm, rotary positions, slot maps, sampling
 # --------------------------------------------------------------------------
 
-def _arg(t, dtype, shape, name):
-    """The address of a contiguous CUDA tensor of this type and shape, or of None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _need(t, dtype, shape, name)
-    return t.data_ptr() or None
-
-
-def _call(fn, *args):
-    code = getattr(_lib or load(), fn)(*args)
-    if code != 0:
-        raise JetError(fn, code)
-
-
-def _raw_stream(stream):
-    import torch
-    if stream is None:  # torch.cuda.current_stream() without its object: 0.3 against 3 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
 def _allocating_on(stream):
     """Allocations inside belong to the stream the call runs on."""
     import contextlib
@@ -639,13 +647,7 @@ def _allocating_on(stream):
 def jet_add_rmsnorm_quant_1x128(x, d, g, eps, h, q, s, rstd=None, stream=None):
     """h = x + d (h may be x or d itself) and the 1x128 form (q, s) of its
     RMSNorm; rstd [M] receives what the backward needs, if given."""
-    import torch
-    M, K = x.shape
-    bf16, f32 = torch.bfloat16, torch.float32
-    _call(
-        "jet_add_rmsnorm_quant_1x128", _arg(x, bf16, (M, K), "x"), _arg(d, bf16, (M, K), "d"), _arg(g, bf16, (K,), "g"), M, K,
-        eps, _arg(h, bf16, (M, K), "h"), _arg(q, torch.uint8, (M, K), "q"),
-        _arg(s, f32, (K // 128, M), "s"), _arg(rstd, f32, (M,), "rstd"), _raw_stream(stream))
+    (_marshal or _compiled()).add_rmsnorm_quant_1x128(x, d, g, eps, h, q, s, rstd, stream)
 
 
 def add_rmsnorm_quant_1x128(x, d, g, eps=1e-5, with_rstd=False, stream=None):
@@ -666,21 +668,12 @@ def jet_add_rmsnorm_bwd(h, g, rstd, dys, dres, dx, dg, ws=None, stream=None):
     """dx [M,K] (of both summands; may be dres itself) and dg [K] from the one
     to three gradients `dys` of the normalised activation and the gradient
     `dres` arriving on the residual stream (or None)."""
-    import torch
-    M, K = h.shape
-    bf16, f32 = torch.bfloat16, torch.float32
-    if not 1 <= len(dys) <= 3:
-        raise ValueError(f"dys: expected one to three gradients, got {len(dys)}")
-    dy = [_arg(t, bf16, h.shape, "dys") for t in dys] + [None, None]
-    if ws is None:
-        need = workspace_bytes("add_rmsnorm_bwd", M, 0, K)
+    if ws is None and stream is not None:    # else the current stream's, by the compiled part
+        import torch
+        need = workspace_bytes("add_rmsnorm_bwd", h.shape[0], 0, h.shape[1])
         with _allocating_on(stream):
             ws = torch.empty((need,), dtype=torch.uint8, device=h.device)
-    _call(
-        "jet_add_rmsnorm_bwd", _arg(h, bf16, (M, K), "h"), _arg(g, bf16, (K,), "g"), _arg(rstd, f32, (M,), "rstd"),
-        dy[0], dy[1], dy[2], _arg(dres, bf16, (M, K), "dres"), M, K,
-        _arg(dx, bf16, (M, K), "dx"), _arg(dg, f32, (K,), "dg"), ws.data_ptr() or None,
-        ws.numel() * ws.element_size(), _raw_stream(stream))
+    (_marshal or _compiled()).add_rmsnorm_bwd(h, g, rstd, tuple(dys), dres, dx, dg, ws, stream)
 
 
 def add_rmsnorm_bwd(h, g, rstd, dys, dres=None, stream=None):
@@ -706,42 +699,12 @@ def rope_inv_freq(R, base=10000.0, scaling="none", factor=1.0, context=8192.0, l
     return freq.to(device), mscale.value
 
 
-def _heads(t, T, D, name):
-    """(address, token stride, heads) of [T, H, D] BF16 heads, dense within a token."""
-    import torch
-    if t is None:
-        return None, 0, 0
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != T or shape[2] != D:
-        raise ValueError(f"{name}: expected shape ({T}, heads, {D}), got {tuple(shape)}")
-    H = shape[1]
-    if T == 0 or H == 0 or D == 0:
-        return None, H * D, H
-    ld, sh, sd = t.stride()
-    if (sd != 1 and D > 1) or (sh != D and H > 1) or not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor whose tokens hold contiguous heads")
-    return t.data_ptr(), (ld if T > 1 else H * D), H
-
-
 def jet_rope(q, k, inv_freq, pos, q_out, k_out, layout="half", mscale=1.0, backward=False,
              stream=None):
     """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (or None) into q_out
     and k_out (which may be q and k); backward=True for the gradients."""
-    import torch
-    T, _, D = (q if q is not None else k).shape
-    R = 2 * inv_freq.numel()
-    qp, ldq, Hq = _heads(q, T, D, "q")
-    kp, ldk, Hk = _heads(k, T, D, "k")
-    qo, ldqo, Hqo = _heads(q_out, T, D, "q_out")
-    ko, ldko, Hko = _heads(k_out, T, D, "k_out")
-    if Hqo != Hq or Hko != Hk:
-        raise ValueError("q_out and k_out must have the heads of q and k")
-    _call(
-        "jet_rope", qp, ldq, Hq, kp, ldk, Hk, T, D, R, _arg(inv_freq, torch.float64, (R // 2,), "inv_freq"),
-        _arg(pos, torch.int64, (T,), "pos"), ROPE_LAYOUT[layout], mscale, int(backward), qo, ldqo,
-        ko, ldko, _raw_stream(stream))
+    (_marshal or _compiled()).rope(q, k, inv_freq, pos, q_out, k_out, ROPE_LAYOUT[layout], mscale,
+                                   backward, stream)
 
 
 def rope(q, k, inv_freq, pos, layout="half", mscale=1.0, backward=False, stream=None):
@@ -758,40 +721,17 @@ def jet_rope_kv_cache_write(q, k, v, inv_freq, pos, k_scale, v_scale, slots, q_o
                             v_cache, layout="half", mscale=1.0, stream=None):
     """q rotated into q_out; k rotated and v as E4M3 codes into rows `slots` of
     k_cache and v_cache [S, Hk, D]."""
-    import torch
-    T, _, D = q.shape
-    R, f32, u8 = 2 * inv_freq.numel(), torch.float32, torch.uint8
-    qp, ldq, Hq = _heads(q, T, D, "q")
-    kp, ldk, Hk = _heads(k, T, D, "k")
-    vp, ldv, Hv = _heads(v, T, D, "v")
-    qo, ldqo, Hqo = _heads(q_out, T, D, "q_out")
-    S = k_cache.shape[0]
-    if Hqo != Hq or Hv != Hk:
-        raise ValueError("q_out must have the heads of q, and v those of k")
-    _call(
-        "jet_rope_kv_cache_write", qp, ldq, Hq, kp, ldk, vp, ldv, Hk, T, D, R,
-        _arg(inv_freq, torch.float64, (R // 2,), "inv_freq"), _arg(pos, torch.int64, (T,), "pos"),
-        ROPE_LAYOUT[layout], mscale, _arg(k_scale, f32, (Hk,), "k_scale"),
-        _arg(v_scale, f32, (Hk,), "v_scale"), _arg(slots, torch.int64, (T,), "slots"), qo, ldqo,
-        _arg(k_cache, u8, (S, Hk, D), "k_cache"), _arg(v_cache, u8, (S, Hk, D), "v_cache"), S,
-        _raw_stream(stream))
+    (_marshal or _compiled()).rope_kv_cache_write(
+        q, k, v, inv_freq, pos, k_scale, v_scale, slots, q_out, k_cache, v_cache,
+        ROPE_LAYOUT[layout], mscale, stream)
 
 
 def jet_kv_slot_map(cached, added, block_size, table, free_blocks, free_next, offsets, positions,
                     slots, rows, counts, stream=None):
     """Block table entries, positions and cache slots of a step's new tokens
     from the requests' lengths; see the C header."""
-    import torch
-    B, width, n_free, N = cached.numel(), table.shape[1], free_blocks.numel(), slots.numel()
-    i32, i64 = torch.int32, torch.int64
-    _call(
-        "jet_kv_slot_map", _arg(cached, i32, (B,), "cached"), _arg(added, i32, (B,), "added"), B, block_size,
-        _arg(table, i32, (B, width), "table"), width,
-        _arg(free_blocks, i32, (n_free,), "free_blocks"), n_free,
-        _arg(free_next, i64, free_next.shape, "free_next"), N,
-        _arg(offsets, i64, (B + 1,), "offsets"), _arg(positions, i64, (N,), "positions"),
-        _arg(slots, i64, (N,), "slots"), _arg(rows, i32, (N,), "rows"),
-        _arg(counts, i64, (2,), "counts"), _raw_stream(stream))
+    (_marshal or _compiled()).kv_slot_map(cached, added, block_size, table, free_blocks, free_next,
+                                          offsets, positions, slots, rows, counts, stream)
 
 
 def kv_slot_map(cached, added, block_size, table, free_blocks, free_next, capacity, stream=None):
@@ -814,21 +754,8 @@ def jet_sample(logits, u, temperature, top_k, top_p, min_p, token, logp, logp_al
                stream=None):
     """One token per row of logits [B, V] (BF16 or FP32, rows may be strided)
     from the uniform numbers u [B]; the settings are per row, or None."""
-    import torch
-    B, V = logits.shape
-    f32, i32 = torch.float32, torch.int32
-    if logits.dtype not in (torch.bfloat16, f32):
-        raise TypeError(f"logits: expected torch.bfloat16 or torch.float32, got {logits.dtype}")
-    if logits.numel() and (not logits.is_cuda or (V > 1 and logits.stride(1) != 1)):
-        raise ValueError("logits: must be a CUDA tensor with contiguous rows")
-    ld = logits.stride(0) if B > 1 else V
-    _call(
-        "jet_sample", logits.data_ptr() or None, int(logits.dtype == f32), B, V, ld, _arg(u, f32, (B,), "u"),
-        _arg(temperature, f32, (B,), "temperature"), _arg(top_k, i32, (B,), "top_k"),
-        _arg(top_p, f32, (B,), "top_p"), _arg(min_p, f32, (B,), "min_p"),
-        _arg(token, torch.int64, (B,), "token"), _arg(logp, f32, (B,), "logp"),
-        _arg(logp_all, f32, (B,), "logp_all"), _arg(kept, i32, (B,), "kept"),
-        _raw_stream(stream))
+    (_marshal or _compiled()).sample(logits, u, temperature, top_k, top_p, min_p, token, logp,
+                                     logp_all, kept, stream)
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
