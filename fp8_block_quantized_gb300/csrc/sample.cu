@@ -13,21 +13,23 @@
 // The sums run over the 64-bit integers W_i = round(w_i 2^45): exact, so no
 // order of summation, number of CTAs or batch changes a token.
 //
-// A cluster of 1 to 8 CTAs holds one row in its shared memory, read from HBM
-// once (cp.async); each warp owns a contiguous range of the row, so that a
-// running sum in index order needs only one total per warp.  Without a filter
-// two passes over shared memory (maximum, weights) and two cluster barriers
-// lead to the draw.
+// A cluster of 1 to 8 CTAs takes one row; each warp owns a contiguous range of
+// it, so that a running sum in index order needs only one total per warp.
+// Without a filter the row is read twice, for the maximum and for the weights
+// (the second time mostly from L2), and two cluster barriers lead to the draw.
+// With one the CTAs hold the row in shared memory, read from HBM once
+// (cp.async).
 //
 // The filters' cut (the last kept token) is found without a sort of the row.
 // A bound z_lo is taken below which it cannot lie (top-k: a group of z up to
 // which k of the threads' own maxima lie; top-p: all tokens below w = (1 - p)
-// S / V together weigh less than (1 - p) S; min-p: its own weight).  When at
-// most kListMax tokens lie above it, they go to the first CTA, which finds the
-// cut and draws, while the others end.  Flat distributions and large k take the general way: a histogram of counts and
-// masses over 2048 steps of z finds the step the cut lies in, and the first CTA
-// finds it among the tokens of that step; a step with too many of them is
-// split again on the bits of the logits, and one of equal logits by counting.
+// S / V together have less weight than (1 - p) S; min-p: its own weight).  When
+// at most kListMax tokens lie above it, they go to the first CTA, which finds
+// the cut and draws, while the others end.  Flat distributions and large k take
+// the general way: a histogram of counts and masses over 2048 steps of z finds
+// the step the cut lies in, and the first CTA finds it among the tokens of that
+// step; a step with too many of them is split again on the bits of the logits,
+// and one of equal logits by counting.
 #include <cooperative_groups.h>
 
 #include "jet_common.cuh"
@@ -301,6 +303,7 @@ struct Sampler {
     uint4 *row;   // with a filter: this warp's chunk c0 is row[0]
     const typename El::T *x;  // the row in global memory
     bool infinite;  // the row holds +inf
+    bool odd;       // this thread's part of it holds a NaN
     int C, rank, lane, warp;
     int c0, c1;   // this warp's chunks of the row
     int shift;    // elements before the row in its first chunk
@@ -308,7 +311,7 @@ struct Sampler {
     float cut_x;
     int cut_idx;
 
-    __device__ Sampler(const SampleArgs &args) : a(args), cl(cg::this_cluster()), infinite(false) {}
+    __device__ Sampler(const SampleArgs &args) : a(args), cl(cg::this_cluster()), infinite(false), odd(false) {}
 
     // m is finite and rt a normal number, so x = -inf gives -inf and nothing else
     // is undefined.
@@ -357,8 +360,8 @@ struct Sampler {
     }
 
     // f(values) for every chunk of this warp's range, the values as they are in
-    // global memory: whole chunks four loads in flight a thread, then the row's
-    // ragged ends.  After some of them, done(their number).
+    // global memory: whole chunks several loads ahead, then the row's ragged
+    // ends.  After some of them, done(their number).
     template <typename F, typename G>
     __device__ __forceinline__ void global_chunks(F f, G done) {
         const int first = shift > 0, past = (shift + a.V) / E;  // the whole chunks
@@ -366,14 +369,17 @@ struct Sampler {
         const int end = min(c1, past);
         const uint4 *p = reinterpret_cast<const uint4 *>(x - shift) + c;
         float v[E];
-        for (; c + 96 < end; c += 128, p += 128) {
-            const uint4 t[4] = {p[0], p[32], p[64], p[96]};
+        constexpr int kN = 32 / E;  // loads ahead: 256 x 128256 binary32 take 43.4 us with 8, 46.7 with 4
+        for (; c + 32 * (kN - 1) < end; c += 32 * kN, p += 32 * kN) {
+            uint4 t[kN];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kN; ++i) t[i] = p[32 * i];
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
                 El::load(t[i], v);
                 f(v);
             }
-            done(4);
+            done(kN);
         }
 #pragma unroll 1
         for (; c < end; c += 32, p += 32) {
@@ -475,7 +481,10 @@ struct Sampler {
             n += E;
             if (!(fabsf(sum) < INFINITY)) {  // some may be -inf or NaN
 #pragma unroll
-                for (int e = 0; e < E; ++e) n -= !(v[e] > -INFINITY);
+                for (int e = 0; e < E; ++e) {
+                    n -= !(v[e] > -INFINITY);
+                    odd |= v[e] != v[e];
+                }
             }
         };
         if (!kFilter) {
@@ -526,7 +535,8 @@ struct Sampler {
         auto add = [&](const float (&v)[E]) {
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-                const float2 zz = __fmul2_rn(__fadd2_rn(make_float2(v[e], v[e + 1]), nm), r2);
+                float2 zz = __fadd2_rn(make_float2(v[e], v[e + 1]), nm);
+                if (kFilter) zz = __fmul2_rn(zz, r2);  // without one r2 is 1
                 s.add2(expf(zz.x), expf(zz.y));
             }
         };
@@ -535,15 +545,11 @@ struct Sampler {
                 add(v);
                 s.count(E);
             });
-        } else if (!infinite) {
-            global_chunks([&](float (&v)[E]) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
-                add(v);
-            }, [&](int n) { s.count(n * E); });
+        } else if (!odd && !infinite) {  // nothing to clean
+            global_chunks([&](float (&v)[E]) { add(v); }, [&](int n) { s.count(n * E); });
         } else {
             global_chunks([&](float (&v)[E]) {
-                lower(v);
+                if (infinite) lower(v);
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[e] = clean(v[e]);
                 add(v);
@@ -1013,7 +1019,8 @@ struct Sampler {
             if (a.top_p && a.top_p[b] < 1.0f) p = a.top_p[b];
             if (a.min_p) min_w = fminf(fmaxf(a.min_p[b], 0.0f), 1.0f);
         }
-        if (kFilter && k > 1 && k < 0x7FFFFFFF) {  // the threads' maxima, to every CTA
+        const bool filtered = kFilter && (k < 0x7FFFFFFF || p < 1.0f || min_w > 0.0f);
+        if (filtered && k > 1) {  // the threads' maxima, to every CTA
             const float zx = z(fminf(own_max, m));
             if (zx > -32.0f) atomicAdd(&fs->grp[rank][(int)(zx * -kGroupsPerZ)], 1u);
             __syncthreads();
@@ -1025,7 +1032,7 @@ struct Sampler {
         const u64 S_all = all_mass();
         u64 S = S_all;
         unsigned n_kept = all_cnt();
-        if (kFilter && (k < 0x7FFFFFFF || p < 1.0f || min_w > 0.0f)) {
+        if (filtered) {
             const unsigned finite = n_kept;
             const bool k_on = (unsigned)k < finite;
             bool cut_any = min_w > 0.0f;
@@ -1039,14 +1046,14 @@ struct Sampler {
                 if (!k_on && p < 1.0f)
                     z_p = z_below(0.999f * (1.0f - p) * (__ull2float_rn(S_all) * 0x1p-45f) / (float)a.V);
                 z_lo = fmaxf(z_lo, z_p);
-                if (k_on) {
-                    unsigned g4[kGroups / 32], sum = 0;  // every warp scans the groups itself
+                unsigned g4[kGroups / 32], sum = 0;  // every warp scans the groups itself
 #pragma unroll
-                    for (int j = 0; j < kGroups / 32; ++j) {
-                        g4[j] = 0;
-                        for (int r = 0; r < C; ++r) g4[j] += fs->grp[r][lane * (kGroups / 32) + j];
-                        sum += g4[j];
-                    }
+                for (int j = 0; j < kGroups / 32; ++j) {
+                    g4[j] = 0;
+                    for (int r = 0; r < C; ++r) g4[j] += fs->grp[r][lane * (kGroups / 32) + j];
+                    sum += g4[j];
+                }
+                if (k_on) {
                     unsigned upto = (unsigned)warp_scan(sum, lane) - sum;
                     int g = kGroups;
 #pragma unroll
@@ -1061,7 +1068,14 @@ struct Sampler {
                     z_lo = p < 1.0f ? z_k : fmaxf(z_lo, z_k);
                 }
                 const bool everything = finite <= kListMax;
-                if (everything || z_lo > -INFINITY) {
+                // the maxima in whole groups above z_lo: so many tokens at least (a
+                // flat 128256-token nucleus: 30 us, 34 with the vain gather)
+                const int above = (int)(fmaxf(z_lo, -32.0f) * -kGroupsPerZ);
+                unsigned sure = 0;
+#pragma unroll
+                for (int j = 0; j < kGroups / 32; ++j) sure += lane * (kGroups / 32) + j < above ? g4[j] : 0;
+                sure = __reduce_add_sync(0xffffffffu, sure);
+                if (everything || (z_lo > -INFINITY && sure <= kListMax)) {
                     auto in_list = [&](float xv) {
                         return everything ? xv > -INFINITY : z(xv) > z_lo;
                     };

@@ -137,6 +137,35 @@ def test_masked_and_odd_values(jet):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,V", [(3, 5), (6, 4097), (6, 128256), (400, 33001)])
+def test_a_few_odd_values(jet, dtype, B, V):
+    """Single NaN and infinities at a row's ends and inside: the threads that read
+    them and those that do not draw from the same weights."""
+    x, u = logits(B, V, 17)
+    x = x.to(dtype)
+    i = torch.arange(B)
+    x[i, (i * 7919) % V] = float("nan")
+    x[::3, 0] = float("nan")
+    x[1::3, V - 1] = float("nan")
+    x[2::3, V // 2] = -float("inf")
+    x[B - 1, V // 3] = float("inf")
+    run(jet, x, u)
+    run(jet, x, u, p=torch.full((B,), 0.9))
+
+
+@pytest.mark.parametrize("n", [2047, 2048, 2049, 4095, 4096, 6000])
+def test_as_many_candidates_as_the_list_takes(jet, n):
+    """n logits far above the others, one or several of them a thread."""
+    x = torch.full((8, 128256), -20.0, device="cuda")
+    for b, step in enumerate((1, 3, 8, 19, 21, 4, 16, 2)):
+        x[b, torch.arange(n) * step + 5 * b] = torch.linspace(0.0, 0.2, n, device="cuda")
+    u = torch.linspace(0.0, 0.999, 8)
+    run(jet, x, u, p=torch.tensor([0.1, 0.5, 0.9, 0.99, 0.999, 0.3, 0.7, 0.95]))
+    run(jet, x, u, mp=torch.full((8,), 0.5))
+    run(jet, x, u, k=torch.tensor([n - 1, n, n + 1, 5, 2048, 2049, 1000, n // 2]), p=torch.full((8,), 0.9))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("V", [600, 40000, 128256])
 def test_ties(jet, dtype, V):
     """Equal logits are kept by rising index, in numbers that no ranking list holds."""
