@@ -32,6 +32,8 @@
 // and one of equal logits by counting.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "jet_common.cuh"
 
 namespace {
@@ -74,14 +76,16 @@ struct Shared {
 };
 
 // With a filter.
-static_assert(kListMax >= kBins, "the list's room takes the peers' bins");
+static_assert(kListMax >= kBins, "the list's room takes the peers' bins, in rounded parts");
 struct FilterShared {
     // counts, or masses in three 15-bit parts: shared-memory atomics on 32 bits
     // run in hardware, and 2^17 tokens of one CTA cannot overflow a part
     unsigned hist[3][kBins];
-    u64 list[kListMax];  // ~key, index; at the first CTA
-    unsigned grp[kMaxCluster][kGroups];  // threads' maxima by group of z
+    u64 list[kListMax + 8 * kMaxCluster];  // ~key, index; at the first CTA
+    alignas(16) unsigned grp[kMaxCluster][kGroups];  // threads' maxima by group of z
 };
+
+constexpr size_t kHead = (sizeof(Shared) + 15) / 16 * 16;
 
 __device__ __forceinline__ unsigned key_of(float x) {  // orders as the logit does, zeros alike
     const unsigned b = __float_as_uint(x + 0.0f);
@@ -735,7 +739,7 @@ struct Sampler {
     // kListMax; their number.  Ends with a cluster barrier.
     template <typename F>
     __device__ unsigned gather(F f) {
-        u64 hit[3] = {0, 0, 0};  // of this thread's elements, 136 at most
+        u64 hit[3] = {0, 0, 0};  // of this thread's elements, 192 at most
         int at = 0;
         chunks([&](const float (&v)[E], int) {
             unsigned bits = 0;
@@ -798,11 +802,11 @@ struct Sampler {
 
     // The first bin whose end reaches the target, given what lies before the
     // histogram, with what lies before the bin, at every CTA.  Every CTA sends
-    // its bins to the CTA that adds them, kBins / C of them each (sent: stores
+    // its bins to the CTA that adds them, kBins / C or so each (sent: stores
     // into the peers' shared memory, a third of the time of loads from it).
     __device__ void select(bool by_mass, u64 target, u64 base) {
         constexpr int kPer = kBins / kThreads;  // bins a thread
-        const int seg = kBins / C, first = (int)threadIdx.x * kPer;
+        const int seg = (kBins / kPer + C - 1) / C * kPer, first = (int)threadIdx.x * kPer;
         ulonglong2 *to = reinterpret_cast<ulonglong2 *>(
             cl.map_shared_rank(fs, first / seg)->list + rank * seg + first % seg);
 #pragma unroll
@@ -818,13 +822,14 @@ struct Sampler {
         }
         cl.sync();
         // this CTA's bins: `per` a thread, from every rank
-        const int per = seg > kThreads ? seg / kThreads : 1;
+        const int past = min(seg, kBins - rank * seg);
+        const int per = (seg + kThreads - 1) / kThreads;
         const int at0 = (int)threadIdx.x * per;
         u64 bin[kPer], own = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             bin[j] = 0;
-            if (j < per && at0 < seg)
+            if (j < per && at0 + j < past)
                 for (int r = 0; r < C; ++r) bin[j] += fs->list[r * seg + at0 + j];
             own += bin[j];
         }
@@ -836,7 +841,7 @@ struct Sampler {
         for (int r = 0; r < rank; ++r) at += sh->seg_mass[r];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (j < per && at0 < seg && at < target && at + bin[j] >= target) {
+            if (j < per && at0 + j < past && at < target && at + bin[j] >= target) {
                 for (int r = 0; r < C; ++r) {
                     Shared *o = cl.map_shared_rank(sh, r);
                     o->sel_bin = rank * seg + at0 + j;
@@ -1046,13 +1051,17 @@ struct Sampler {
                 if (!k_on && p < 1.0f)
                     z_p = z_below(0.999f * (1.0f - p) * (__ull2float_rn(S_all) * 0x1p-45f) / (float)a.V);
                 z_lo = fmaxf(z_lo, z_p);
-                unsigned g4[kGroups / 32], sum = 0;  // every warp scans the groups itself
-#pragma unroll
-                for (int j = 0; j < kGroups / 32; ++j) {
-                    g4[j] = 0;
-                    for (int r = 0; r < C; ++r) g4[j] += fs->grp[r][lane * (kGroups / 32) + j];
-                    sum += g4[j];
+                // every warp scans the groups itself, four a lane
+                static_assert(kGroups == 4 * 32, "a quad a lane");
+                unsigned g4[4] = {0, 0, 0, 0};
+                for (int r = 0; r < C; ++r) {
+                    const uint4 q = reinterpret_cast<const uint4 *>(fs->grp[r])[lane];
+                    g4[0] += q.x;
+                    g4[1] += q.y;
+                    g4[2] += q.z;
+                    g4[3] += q.w;
                 }
+                const unsigned sum = g4[0] + g4[1] + g4[2] + g4[3];
                 if (k_on) {
                     unsigned upto = (unsigned)warp_scan(sum, lane) - sum;
                     int g = kGroups;
@@ -1143,8 +1152,8 @@ struct Sampler {
     }
 };
 
-template <bool kBf16, bool kFilter, int kThreads>
-__global__ void __launch_bounds__(kThreads, kFilter ? 512 / kThreads : 1280 / kThreads)
+template <bool kBf16, bool kFilter, int kThreads, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm)
 sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     jet::griddep_launch_dependents();
@@ -1154,7 +1163,6 @@ sample_kernel(const SampleArgs a) {
     s.rank = (int)s.cl.block_rank();
     s.lane = threadIdx.x & 31;
     s.warp = threadIdx.x >> 5;
-    constexpr size_t kHead = (sizeof(Shared) + 15) / 16 * 16;
     s.sh = reinterpret_cast<Shared *>(smem);
     s.fs = reinterpret_cast<FilterShared *>(smem + kHead);
     s.row = reinterpret_cast<uint4 *>(smem + kHead + (kFilter ? sizeof(FilterShared) : 0)) +
@@ -1162,10 +1170,20 @@ sample_kernel(const SampleArgs a) {
     s.run(blockIdx.x / s.C);
 }
 
-template <int kThreads>
-void (*kernel_for(bool bf16, bool filter))(SampleArgs) {
-    return bf16 ? (filter ? sample_kernel<true, true, kThreads> : sample_kernel<true, false, kThreads>)
-                : (filter ? sample_kernel<false, true, kThreads> : sample_kernel<false, false, kThreads>);
+template <bool kFilter, int kThreads, int kPerSm>
+void (*kernel_for(bool bf16))(SampleArgs) {
+    return bf16 ? sample_kernel<true, kFilter, kThreads, kPerSm>
+                : sample_kernel<false, kFilter, kThreads, kPerSm>;
+}
+
+// Chunks of 16 bytes that one warp takes, and the shared memory of a CTA of 512
+// threads that holds its slice of the row.
+int warp_chunks(int C, int threads, int64_t chunks) {
+    const int64_t parts = (int64_t)C * (threads / 32);
+    return (int)(((chunks + parts - 1) / parts + 31) / 32 * 32);
+}
+size_t filter_smem(int C, int64_t chunks) {
+    return kHead + sizeof(FilterShared) + (size_t)16 * 16 * warp_chunks(C, 512, chunks);
 }
 
 template <int kBytes>
@@ -1195,23 +1213,56 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     const bool filter = temperature || top_k || top_p || min_p;
     const int E = bf16 ? 8 : 4;
     const int64_t chunks = (V + E - 1 + E - 1) / E;  // a row may start inside a chunk
-    // CTAs per row and threads per CTA.  Without a filter: two CTAs of 512
-    // threads an SM while the rows are few (128256 logits in binary32, us: 1 row
-    // 7.0 with 8 x 512, 8.7 with 8 x 256; 16 rows 8.9 and 12.2, 12.1 with 4 x 512;
-    // 64 rows 16.8 with 4 x 512, 19.3 with 8 x 512); then one CTA of 512 a row
-    // (300 rows of 32000: 17.0, 19.5 with 2 x 256), of 256 past two rows an SM
-    // (1024 rows of 32000: 39, 45 with 512), but eight of 256 where rows are
-    // long (256 rows of 128256 in binary32: 45, 53 with one of 512).  With a
-    // filter a CTA's slice has to fit into shared memory, 64 KB of it or so.
     const int64_t sms = dev.num_sms;
     int C = kMaxCluster, threads = 512;
-    while (C > 1 && (B * C > 2 * sms || chunks < (int64_t)C * 256)) C /= 2;
-    if (B * C > (filter ? 1 : 2) * sms) threads = 256;
-    if (!filter && B > sms && chunks * 16 > 384 * 1024) {
-        C = kMaxCluster;
-        threads = 256;
+    bool pairs = true;  // two CTAs an SM
+    if (!filter) {
+        // CTAs per row and threads per CTA (128256 logits in binary32, us): two
+        // CTAs of 512 threads an SM while the rows are few (1 row 6.9 with
+        // 8 x 512, 8.3 with 8 x 256; 16 rows 9.0 and 12.6, 11.9 with 4 x 512; 64
+        // rows 16.4 with 4 x 512, 19.1 with 8 x 512); then one CTA of 512 a row
+        // (300 rows of 32000: 16.7, 19.9 with 2 x 256), of 256 past two rows an
+        // SM (1024 rows of 32000 in BF16: 40, 45 with 512), but eight of 256
+        // where rows are long (256 rows in binary32: 43, 54 with one of 512).
+        while (C > 1 && (B * C > 2 * sms || chunks < (int64_t)C * 256)) C /= 2;
+        if (B * C > 2 * sms) threads = 256;
+        if (B > sms && chunks * 16 > 384 * 1024) {
+            C = kMaxCluster;
+            threads = 256;
+        }
+    } else {
+        // Few rows: the largest cluster with which they run in about one wave,
+        // an SM a CTA.  The SMs' groups hold 15 clusters of 8 (and 15 of 7), 23
+        // of 6, 28 of 5, 36 of 4 (128256 BF16 logits, us, mixed filters / flat
+        // nuclei / top-k: 16 rows 32 / 53 / 25 with 8, 38 / 37 / 27 with 6; 20
+        // rows 38 / 37 / 27 with 6, 33 / 56 / 34 with 8; 32 rows 47 / 46 / 29
+        // with 4, 48 / 78 / 40 with 8).  More rows: two CTAs an SM of half the
+        // registers, again in about one wave while that can be (64 rows 63 / 74
+        // / 44, one CTA an SM 67 / 87 / 47; 256 rows 144 / 231 / 116 and 179 /
+        // 311 / 141), else as few CTAs a row as its slices allow (300 rows of
+        // 32000 binary32 93 / 91 / 78 with 2, 94 / 131 / 89 with 4).  Where
+        // slices are too long for two an SM: as few as one CTA can hold (128
+        // rows of 151937 binary32 127 / 195 / 90 with 4, 153 / 272 / 120 with 8).
+        const int longest = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxCluster, chunks / 256));
+        const int64_t wave = sms * 12 / 13;
+        auto fits = [&](int c, size_t room) { return c != 7 && filter_smem(c, chunks) <= room; };
+        constexpr size_t kOne = 227 * 1024, kHalf = 113 * 1024;
+        static_assert((kOne - kHead - sizeof(FilterShared)) / (512 * 16) * 8 <= 192, "a thread's bits in gather");
+        pairs = false;
+        for (C = longest; C > 0; --C)
+            if (fits(C, kOne) && B * C <= wave && (C >= 4 || C == longest)) break;
+        if (C == 0) {
+            pairs = true;
+            for (C = longest; C > 0; --C)
+                if (fits(C, kHalf) && B * C <= 2 * wave) break;
+            if (C == 0)
+                for (C = 1; C < kMaxCluster && !fits(C, kHalf);) ++C;
+            if (!fits(C, kHalf)) {
+                pairs = false;
+                for (C = 1; C < kMaxCluster && !fits(C, kOne);) ++C;
+            }
+        }
     }
-    while (filter && C < kMaxCluster && chunks * 16 > (int64_t)C * 64 * 1024 + 2048) C *= 2;
     SampleArgs a = {};
     a.x = logits;
     a.ld = ld;
@@ -1226,13 +1277,11 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     a.logp = logp;
     a.logp_all = logp_all;
     a.kept = kept;
-    const int64_t parts = (int64_t)C * (threads / 32);
-    a.chunks_per_warp = (int)(((chunks + parts - 1) / parts + 31) / 32 * 32);
-    const size_t smem =
-        (sizeof(Shared) + 15) / 16 * 16 +
-        (filter ? sizeof(FilterShared) + (size_t)(threads / 32) * a.chunks_per_warp * 16 : 0);
+    a.chunks_per_warp = warp_chunks(C, threads, chunks);
+    const size_t smem = filter ? filter_smem(C, chunks) : kHead;
     void (*kernel)(SampleArgs) =
-        threads == 512 ? kernel_for<512>(bf16, filter) : kernel_for<256>(bf16, filter);
+        filter ? (pairs ? kernel_for<true, 512, 2>(bf16) : kernel_for<true, 512, 1>(bf16))
+               : (threads == 512 ? kernel_for<false, 512, 2>(bf16) : kernel_for<false, 256, 5>(bf16));
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess) {
         cudaGetLastError();

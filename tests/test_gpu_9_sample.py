@@ -207,6 +207,25 @@ def test_the_batch_does_not_change_a_row(jet):
                 assert torch.equal(a, b[n:n + 1])
 
 
+@pytest.mark.parametrize("B", [17, 20, 26, 33, 60, 75, 100, 150, 300])
+@pytest.mark.parametrize("V,dtype", [(33001, F32), (128256, BF16), (151937, F32), (262144, BF16), (262143, F32)])
+def test_any_number_of_rows_gives_a_row_the_same(jet, B, V, dtype):
+    """Clusters of every size, one and two CTAs an SM: every 7th row as if alone."""
+    g = torch.Generator(device="cuda").manual_seed(B + V)
+    x = (torch.randn((B, V), generator=g, device="cuda") * 2.5).to(dtype)
+    u = torch.rand((B,), generator=g, device="cuda")
+    r = torch.arange(B, device="cuda")
+    pick = lambda v, t: torch.tensor(v, device="cuda", dtype=t)[r % len(v)]
+    T, k = pick([1.0, 0.6, 0.0, 1.7, 0.9], F32), pick([0, 50, 3000, V // 2], torch.int32)
+    p, mp = pick([0.95, 1.0, 0.5], F32), pick([0.0, 0.01], F32)
+    for f in ((T, k, p, mp), (None, None, p, None), (None, k, None, None)):
+        full = jet.sample(x, u, *f)
+        for i in range(0, B, 7):
+            one = jet.sample(x[i:i + 1].clone(), u[i:i + 1], *(None if v is None else v[i:i + 1] for v in f))
+            for a, b in zip(one, full):
+                assert torch.equal(a, b[i:i + 1]), (i, a, b[i])
+
+
 def test_frequencies_of_an_even_grid(jet):
     """u on a grid of n points draws every token n p times, up to one."""
     n, V = 4096, 300
