@@ -47,6 +47,7 @@ constexpr float kBinsPerZ = 64.0f;
 constexpr int kGroups = 128;          // groups of 16 steps: 1/4 of z
 constexpr float kGroupsPerZ = 4.0f;
 constexpr int kListMax = 2048;        // tokens the first CTA takes
+constexpr int kRankMax = 256;         // values sorted by counting
 constexpr int64_t kSaMaxV = 262144;   // so that the sum of 2^45-scaled weights fits 64 bits
 
 typedef unsigned long long u64;
@@ -262,10 +263,30 @@ __device__ __noinline__ Scan block_scan(u64 v, u64 o, u64 (*sums)[kMaxWarps]) {
     return r;
 }
 
-// Bitonic sort of the first n values (the others are ~0 and stay), one a thread,
-// ascending: inside a warp by shuffles, across warps through `buf`.
+// Sort of the first n values (distinct; the others are ~0 and stay), one a
+// thread, ascending.  Up to kRankMax of them: a value's place is the number of
+// smaller ones, counted by neighbouring threads in turn.  Else bitonic: inside a
+// warp by shuffles, across warps through `buf`.
+template <int kThreads>
 __device__ __noinline__ u64 block_sort(u64 r, unsigned n, u64 *buf) {
     const int i = threadIdx.x;
+    if (n <= kRankMax) {
+        const int sh = n <= kThreads / 8 ? 3 : n <= kThreads / 4 ? 2 : 1;  // 2^sh threads a value
+        __syncthreads();
+        buf[i] = r;
+        __syncthreads();
+        const u64 own = buf[i >> sh];
+        unsigned at = 0;
+#pragma unroll 8
+        for (unsigned j = i & ((1 << sh) - 1); j < n; j += 1 << sh) at += buf[j] < own;
+        for (int d = 1; d < 1 << sh; d *= 2) at += __shfl_xor_sync(0xffffffffu, at, d);
+        __syncthreads();
+        if ((i & ((1 << sh) - 1)) == 0 && (unsigned)(i >> sh) < n) buf[at] = own;
+        __syncthreads();
+        r = buf[i];
+        __syncthreads();
+        return r;
+    }
 #pragma unroll 1
     for (int size = 2; size < 2 * (int)n; size *= 2) {  // up to the power of two that holds n
 #pragma unroll 1
@@ -566,7 +587,7 @@ struct Sampler {
 
     // A buffer of one value a thread.
     __device__ __forceinline__ u64 sort(u64 r, unsigned n) {
-        return block_sort(r, n, reinterpret_cast<u64 *>(fs->hist));
+        return block_sort<kThreads>(r, n, reinterpret_cast<u64 *>(fs->hist));
     }
 
     __device__ __forceinline__ float weight_of(unsigned key) const {
@@ -642,9 +663,9 @@ struct Sampler {
     // the target, until a bin's values can be sorted one a thread.
     __device__ u64 list_cut(unsigned n, bool by_mass, u64 target, bool by_index) {
         u64 lo = 0, hi = ~0ull - 1;
-        unsigned left;
+        unsigned left = n;
 #pragma unroll 1
-        for (;;) {
+        while (n > kThreads) {
             __syncthreads();  // what is shared may still be read
             if (threadIdx.x == 0) {
                 sh->list_lo = ~0ull;
@@ -701,15 +722,19 @@ struct Sampler {
             hi = min(hi, lo + ((1ull << sft) - 1));
         }
         // the values left, one a thread
-        u64 *buf = reinterpret_cast<u64 *>(fs->hist) + kThreads;  // past the sort's
-        unsigned own = 0;
+        const u64 *buf = fs->list;
+        if (n > kThreads) {
+            u64 *some = reinterpret_cast<u64 *>(fs->hist) + kThreads;  // past the sort's
+            unsigned own = 0;
 #pragma unroll 1
-        for (unsigned i = threadIdx.x; i < n; i += kThreads) own += fs->list[i] >= lo && fs->list[i] <= hi;
-        unsigned to = (unsigned)scan(own).before;
+            for (unsigned i = threadIdx.x; i < n; i += kThreads) own += fs->list[i] >= lo && fs->list[i] <= hi;
+            unsigned to = (unsigned)scan(own).before;
 #pragma unroll 1
-        for (unsigned i = threadIdx.x; i < n; i += kThreads)
-            if (fs->list[i] >= lo && fs->list[i] <= hi) buf[to++] = fs->list[i];
-        __syncthreads();
+            for (unsigned i = threadIdx.x; i < n; i += kThreads)
+                if (fs->list[i] >= lo && fs->list[i] <= hi) some[to++] = fs->list[i];
+            __syncthreads();
+            buf = some;
+        }
         const u64 v = sort(threadIdx.x < left ? buf[threadIdx.x] : ~0ull, left);
         const u64 w = threadIdx.x >= left ? 0 : by_mass ? mass_in(v, by_index) : 1;
         const u64 at = scan(w).before;
