@@ -68,7 +68,8 @@ struct SampleArgs {
 // ranks are written by the peers and read after a cluster barrier.
 struct Shared {
     u64 warp_mass[kMaxWarps], rank_mass[kMaxCluster], seg_mass[kMaxCluster];
-    u64 scan[2][kMaxWarps], list_lo, list_hi, sel_mass, cut_entry;
+    u64 scan[2][kMaxWarps], sel_mass, cut_entry;
+    unsigned list_range[4][kMaxWarps], list_left;
     unsigned warp_cnt[kMaxWarps], rank_cnt[kMaxCluster];
     float warp_max[kMaxWarps], rank_max[kMaxCluster];
     unsigned lo, hi, rank_lo[kMaxCluster], rank_hi[kMaxCluster];
@@ -664,48 +665,53 @@ struct Sampler {
     __device__ u64 list_cut(unsigned n, bool by_mass, u64 target, bool by_index) {
         u64 lo = 0, hi = ~0ull - 1;
         unsigned left = n;
+        const u64 *buf = fs->list;
+        // f(v) for this thread's values in the range
+        auto own = [&](auto f) {
 #pragma unroll 1
-        while (n > kThreads) {
+            for (unsigned i = threadIdx.x; i < n; i += kThreads) {
+                const u64 v = fs->list[i];
+                if (v >= lo && v <= hi) f(v);
+            }
+        };
+        while (left > kThreads) {
+            // their range: by the upper halves, or the lower where those are equal
+            unsigned r[4] = {~0u, 0, ~0u, 0};
+            own([&](u64 v) {
+                r[0] = min(r[0], (unsigned)(v >> 32));
+                r[1] = max(r[1], (unsigned)(v >> 32));
+                r[2] = min(r[2], (unsigned)v);
+                r[3] = max(r[3], (unsigned)v);
+            });
             __syncthreads();  // what is shared may still be read
-            if (threadIdx.x == 0) {
-                sh->list_lo = ~0ull;
-                sh->list_hi = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                r[q] = q % 2 ? __reduce_max_sync(0xffffffffu, r[q]) : __reduce_min_sync(0xffffffffu, r[q]);
+                if (lane == 0) sh->list_range[q][warp] = r[q];
             }
-            u64 mn = ~0ull, mx = 0, cnt = 0;
-#pragma unroll 1
-            for (unsigned i = threadIdx.x; i < n; i += kThreads) {
-                const u64 v = fs->list[i];
-                if (v < lo || v > hi) continue;
-                mn = min(mn, v);
-                mx = max(mx, v);
-                ++cnt;
-            }
-            left = (unsigned)scan(cnt).total;
-            if (left <= kThreads) break;
-            if (cnt) {
-                atomicMin(&sh->list_lo, mn);
-                atomicMax(&sh->list_hi, mx);
-            }
+            if (threadIdx.x == 0) sh->list_left = 0;
             clear_histogram();
-            lo = sh->list_lo;
-            hi = sh->list_hi;
-            const int sft = max(0, 64 - __clzll((long long)(hi - lo)) - 11);
-#pragma unroll 1
-            for (unsigned i = threadIdx.x; i < n; i += kThreads) {
-                const u64 v = fs->list[i];
-                if (v >= lo && v <= hi)
-                    count_in((int)((v - lo) >> sft), by_mass, by_mass ? mass_in(v, by_index) : 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const unsigned w = sh->list_range[q][lane % kWarps];
+                r[q] = q % 2 ? __reduce_max_sync(0xffffffffu, w) : __reduce_min_sync(0xffffffffu, w);
             }
+            lo = (u64)r[0] << 32 | (r[0] == r[1] ? r[2] : 0);
+            hi = (u64)r[1] << 32 | (r[0] == r[1] ? r[3] : by_index ? ~0u : 0x7FFFFFFFu);
+            const int sft = max(0, 64 - __clzll((long long)(hi - lo)) - 11);
+            own([&](u64 v) {
+                count_in((int)((v - lo) >> sft), by_mass, by_mass ? mass_in(v, by_index) : 0);
+            });
             __syncthreads();
             constexpr int kPer = kBins / kThreads;
-            u64 bin[kPer], own = 0;
+            u64 bin[kPer], sum = 0;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 const int i = threadIdx.x * kPer + j;
                 bin[j] = fs->hist[0][i] + ((u64)fs->hist[1][i] << 15) + ((u64)fs->hist[2][i] << 30);
-                own += bin[j];
+                sum += bin[j];
             }
-            const Scan s = scan(own);
+            const Scan s = scan(sum);
             if (s.total < target) return hi;  // all of them
             u64 at = s.before;
 #pragma unroll
@@ -720,19 +726,14 @@ struct Sampler {
             target -= sh->sel_mass;
             lo += (u64)sh->sel_bin << sft;
             hi = min(hi, lo + ((1ull << sft) - 1));
-        }
-        // the values left, one a thread
-        const u64 *buf = fs->list;
-        if (n > kThreads) {
+            // the bin's values, in any order: they are sorted next
             u64 *some = reinterpret_cast<u64 *>(fs->hist) + kThreads;  // past the sort's
-            unsigned own = 0;
-#pragma unroll 1
-            for (unsigned i = threadIdx.x; i < n; i += kThreads) own += fs->list[i] >= lo && fs->list[i] <= hi;
-            unsigned to = (unsigned)scan(own).before;
-#pragma unroll 1
-            for (unsigned i = threadIdx.x; i < n; i += kThreads)
-                if (fs->list[i] >= lo && fs->list[i] <= hi) some[to++] = fs->list[i];
+            own([&](u64 v) {
+                const unsigned to = atomicAdd(&sh->list_left, 1u);
+                if (to < kThreads) some[to] = v;
+            });
             __syncthreads();
+            left = sh->list_left;
             buf = some;
         }
         const u64 v = sort(threadIdx.x < left ? buf[threadIdx.x] : ~0ull, left);
@@ -923,14 +924,16 @@ struct Sampler {
                 for (int r = 0; r < C; ++r) base += sh->seg_mass[r];
             }
             // the bin's tokens: an interval of z, or of logits
-            const float z0 = bin < kBins ? (float)(bin + 1) * (-1.0f / kBinsPerZ) : -INFINITY;
+            const float z0 = (float)(bin + 1) * (-1.0f / kBinsPerZ);
             const float z1 = (float)bin * (-1.0f / kBinsPerZ);
             const unsigned span = (unsigned)min((u64)(bin + 1) << sft, (u64)(hi - lo) + 1) - 1;
             const float x0 = logit_of(hi - span), x1 = logit_of(hi - ((unsigned)bin << sft));
+            const float below = level > 0 ? nextafterf(x0, -INFINITY) : bin < kBins ? z0 : NAN;
+            const float top = level > 0 ? x1 : z1;
+            const float off = level > 0 ? 0.0f : -m, mul = level > 0 ? 1.0f : rt;
             auto in_bin = [&](float x) {
-                if (level > 0) return x >= x0 && x <= x1 && x > -INFINITY;
-                const float zx = z(x);
-                return zx <= z1 && (zx > z0 || bin == kBins) && x > -INFINITY;
+                const float v = __fmul_rn(__fadd_rn(x, off), mul);
+                return v <= top && !(v <= below) && x > -INFINITY;
             };
             const unsigned n = gather(in_bin);
             if (n <= kListMax) {
