@@ -399,29 +399,43 @@ add_rmsnorm_bwd_wide_kernel(const BwdArgs a) {
     }
 }
 
-// dg[k] = the partial rows' sum in a fixed order: 32 groups per CTA of 32
-// columns, each adding every 32nd partial row, then the groups in order.
+// dg[k] = the partial rows' sum in a fixed order: a CTA takes 32 columns, eight
+// threads of four columns a row, 128 rows at a time (304 rows of 5120: 2.0 us;
+// 2.6 with one column a thread); then the lanes of a warp, then the warps.
 __global__ void __launch_bounds__(1024)
 dgain_reduce_kernel(const float *__restrict__ part, int parts, int64_t K, float *__restrict__ dg) {
-    __shared__ float sum[32][33];
+    __shared__ float4 sum[32][9];
     jet::griddep_launch_dependents();
     jet::griddep_wait();
-    const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t k = blockIdx.x * (int64_t)32 + c;
-    float acc = 0.0f;
-    for (int p0 = w; p0 < parts; p0 += 32 * 10) {
-        float v[10];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = lane & 7;
+    const float *col = part + blockIdx.x * (int64_t)32 + 4 * c;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float4 &v) {
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+    };
+    for (int p0 = threadIdx.x >> 3; p0 < parts; p0 += 128 * 3) {
+        float4 v[3];
 #pragma unroll
-        for (int i = 0; i < 10; ++i) v[i] = p0 + 32 * i < parts ? part[(p0 + 32 * i) * K + k] : 0.0f;
+        for (int i = 0; i < 3; ++i)
+            v[i] = p0 + 128 * i < parts ? *reinterpret_cast<const float4 *>(col + (p0 + 128 * i) * K)
+                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 10; ++i) acc += v[i];
+        for (int i = 0; i < 3; ++i) add(v[i]);
     }
-    sum[w][c] = acc;
+#pragma unroll
+    for (int o = 8; o < 32; o *= 2)
+        add(make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                        __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o)));
+    if (lane < 8) sum[w][c] = acc;
     __syncthreads();
     if (w == 0) {
+        float s = 0.0f;
 #pragma unroll
-        for (int i = 1; i < 32; ++i) acc += sum[i][c];
-        dg[k] = acc;
+        for (int i = 0; i < 32; ++i) s += reinterpret_cast<const float *>(sum[i])[lane];
+        dg[blockIdx.x * (int64_t)32 + lane] = s;
     }
 }
 
