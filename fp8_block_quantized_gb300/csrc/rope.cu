@@ -142,8 +142,12 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t x, float c, float s) {
 // loads are in flight together and share one set of angles.  Items of a head:
 // kHalf (R % 16 == 0): R/16 pairs of 8-channel chunks (c, c + R/16), then the
 // chunks past R; interleaved (any R): D/8 chunks.
-template <bool kHalf, bool kCache>
-__global__ void __launch_bounds__(kRopeThreads)
+// kBatch heads at a time: all of them, or two with the registers of four CTAs an
+// SM (the cache form of many tokens, whose encoding keeps the SMs busy: 16384
+// tokens of 64 + 8 + 8 heads 98 us, 110 with four; without a cache 8192 tokens
+// of 32 + 8 heads 28.4 with two, 27.3 with four).
+template <bool kHalf, bool kCache, int kBatch>
+__global__ void __launch_bounds__(kRopeThreads, kBatch < kRopeBatch ? 4 : 0)
 rope_kernel(const RopeArgs a) {
     extern __shared__ unsigned long long frac[];  // [R/2]
     jet::griddep_launch_dependents();
@@ -167,42 +171,46 @@ rope_kernel(const RopeArgs a) {
         const int64_t slot = kCache ? a.slots[t] : 0;
         const int d0 = kHalf ? (rot ? 8 * item : a.R + 8 * (item - nrot)) : 8 * item;
         const int d1 = kHalf ? a.R / 2 + 8 * item : 0;
-        uint4 x[kRopeBatch], y[kRopeBatch];
-#pragma unroll
-        for (int b = 0; b < kRopeBatch; ++b) {
-            if (h0 + b >= h1) break;
-            const Head hd = head_of<kCache>(a, t, h0 + b, -1);
-            x[b] = *reinterpret_cast<const uint4 *>(hd.in + d0);
-            if (kHalf && rot) y[b] = *reinterpret_cast<const uint4 *>(hd.in + d1);
-        }
         float c[kPairs], s[kPairs];
-        if (rot) {
-            const int64_t pos = a.pos[t];
+#pragma unroll 1
+        for (int hb = h0; hb < h1; hb += kBatch) {
+            uint4 x[kBatch], y[kBatch];
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i)
-                if (kHalf || kPairs * item + i < a.R / 2)
-                    angle(frac[kPairs * item + i], pos, a.mscale, a.backward, c[i], s[i]);
-        }
-#pragma unroll
-        for (int b = 0; b < kRopeBatch; ++b) {
-            if (h0 + b >= h1) break;
-            const Head hd = head_of<kCache>(a, t, h0 + b, slot);
-            if (rot && hd.rotate) {
-                if constexpr (kHalf) {
-                    turn_half(x[b].x, y[b].x, c, s);
-                    turn_half(x[b].y, y[b].y, c + 2, s + 2);
-                    turn_half(x[b].z, y[b].z, c + 4, s + 4);
-                    turn_half(x[b].w, y[b].w, c + 6, s + 6);
-                } else {
-                    const int last = a.R / 2 - 4 * item;  // pairs of this chunk that turn
-                    x[b].x = turn_pair(x[b].x, c[0], s[0]);
-                    if (last > 1) x[b].y = turn_pair(x[b].y, c[1], s[1]);
-                    if (last > 2) x[b].z = turn_pair(x[b].z, c[2], s[2]);
-                    if (last > 3) x[b].w = turn_pair(x[b].w, c[3], s[3]);
-                }
+            for (int b = 0; b < kBatch; ++b) {
+                if (hb + b >= h1) break;
+                const Head hd = head_of<kCache>(a, t, hb + b, -1);
+                x[b] = *reinterpret_cast<const uint4 *>(hd.in + d0);
+                if (kHalf && rot) y[b] = *reinterpret_cast<const uint4 *>(hd.in + d1);
             }
-            store8<kCache>(hd, d0, x[b]);
-            if (kHalf && rot) store8<kCache>(hd, d1, y[b]);
+            if (rot && hb == h0) {
+                const int64_t pos = a.pos[t];
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i)
+                    if (kHalf || kPairs * item + i < a.R / 2)
+                        angle(frac[kPairs * item + i], pos, a.mscale, a.backward, c[i], s[i]);
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (hb + b >= h1) break;
+                const Head hd = head_of<kCache>(a, t, hb + b, slot);
+                if (rot && hd.rotate) {
+                    if constexpr (kHalf) {
+                        turn_half(x[b].x, y[b].x, c, s);
+                        turn_half(x[b].y, y[b].y, c + 2, s + 2);
+                        turn_half(x[b].z, y[b].z, c + 4, s + 4);
+                        turn_half(x[b].w, y[b].w, c + 6, s + 6);
+                    } else {
+                        const int last = a.R / 2 - 4 * item;  // pairs of this chunk that turn
+                        x[b].x = turn_pair(x[b].x, c[0], s[0]);
+                        if (last > 1) x[b].y = turn_pair(x[b].y, c[1], s[1]);
+                        if (last > 2) x[b].z = turn_pair(x[b].z, c[2], s[2]);
+                        if (last > 3) x[b].w = turn_pair(x[b].w, c[3], s[3]);
+                    }
+                }
+                store8<kCache>(hd, d0, x[b]);
+                if (kHalf && rot) store8<kCache>(hd, d1, y[b]);
+            }
+            if (kBatch == kRopeBatch) break;  // all of them
         }
     }
 }
@@ -272,13 +280,15 @@ jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo
         a.hpt /= 2;
     a.groups = (heads + a.hpt - 1) / a.hpt;
     // Twice the resident CTAs (3 per SM for the half layout, 5 interleaved; 6 for
-    // the channel-wise one): 16384 tokens of 64 + 8 + 8 heads take 110 us with 6
-    // per SM, 115 with 8, 140 with 5.
-    const int64_t cap = (int64_t)dev.num_sms * (half ? 6 : 10);
+    // the channel-wise one; 8192 tokens of 32 + 8 heads 27.4 us with 6 per SM,
+    // 29.0 with 3), but as many as are resident, 4, of the kernel of pairs.
+    const bool pairs = vec && half && cache && a.hpt == kRopeBatch;
+    const int64_t cap = (int64_t)dev.num_sms * (pairs ? 4 : half ? 6 : 10);
     void (*kernel)(RopeArgs) =
-        vec ? (half ? (cache ? rope_kernel<true, true> : rope_kernel<true, false>)
-                    : (cache ? rope_kernel<false, true> : rope_kernel<false, false>))
-            : (cache ? rope_any_kernel<true> : rope_any_kernel<false>);
+        pairs ? rope_kernel<true, true, 2>
+        : vec ? (half ? (cache ? rope_kernel<true, true, kRopeBatch> : rope_kernel<true, false, kRopeBatch>)
+                      : (cache ? rope_kernel<false, true, kRopeBatch> : rope_kernel<false, false, kRopeBatch>))
+              : (cache ? rope_any_kernel<true> : rope_any_kernel<false>);
     // The kernels count a launch's items in 32 bits: more tokens take several launches.
     const int64_t all = a.T, most = (((int64_t)1 << 32) - 1) / ((int64_t)a.groups * a.items);
     for (int64_t t0 = 0; t0 < all; t0 += most) {
