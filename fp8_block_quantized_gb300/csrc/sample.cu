@@ -1245,18 +1245,30 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     int C = kMaxCluster, threads = 512;
     bool pairs = true;  // two CTAs an SM
     if (!filter) {
-        // CTAs per row and threads per CTA (128256 logits in binary32, us): two
-        // CTAs of 512 threads an SM while the rows are few (1 row 6.9 with
+        // CTAs per row and threads per CTA, with their times in us.  Few rows: two
+        // CTAs of 512 threads an SM (128256 logits in binary32: 1 row 6.9 with
         // 8 x 512, 8.3 with 8 x 256; 16 rows 9.0 and 12.6, 11.9 with 4 x 512; 64
-        // rows 16.4 with 4 x 512, 19.1 with 8 x 512); then one CTA of 512 a row
-        // (300 rows of 32000: 16.7, 19.9 with 2 x 256), of 256 past two rows an
-        // SM (1024 rows of 32000 in BF16: 40, 45 with 512), but eight of 256
-        // where rows are long (256 rows in binary32: 43, 54 with one of 512).
+        // rows 16.4 with 4 x 512, 19.1 with 8 x 512), so up to two rows an SM one
+        // of 512 a row (300 rows of 32000: 16.5, 19.6 with 2 x 256), except that
+        // five of 256 run on an SM (160 rows of 32000: 12.8 with 4 x 256, 14.3
+        // with 1 x 512).  More rows: CTAs of 256, as few a row as fill the SMs
+        // with slices of 104 KB at most (128256 in BF16: 340 rows 48 with 4, 84
+        // with 1; 1024 rows 116 and 146, 133 with 8; 1024 rows of 32000 in BF16:
+        // 39 with 1, 41 with 2).  Rows past 384 KB: 8 x 256 (256 rows of 128256
+        // in binary32: 44, 54 with 1 x 512).
         while (C > 1 && (B * C > 2 * sms || chunks < (int64_t)C * 256)) C /= 2;
-        if (B * C > 2 * sms) threads = 256;
-        if (B > sms && chunks * 16 > 384 * 1024) {
-            C = kMaxCluster;
-            threads = 256;
+        if (B > sms) {
+            auto room = [&](int c) { return c <= kMaxCluster && chunks >= (int64_t)c * 128; };
+            if (chunks * 16 > 384 * 1024) {
+                C = kMaxCluster;
+                threads = 256;
+            } else if (B * 8 <= 9 * sms && room(4)) {
+                C = 4;
+                threads = 256;
+            } else if (B > 2 * sms) {
+                threads = 256;
+                for (C = 1; room(2 * C) && (B * C < 4 * sms || chunks * 16 > (int64_t)C * 104 * 1024);) C *= 2;
+            }
         }
     } else {
         // Few rows: the largest cluster with which they run in about one wave,

@@ -207,6 +207,22 @@ def test_the_batch_does_not_change_a_row(jet):
                 assert torch.equal(a, b[n:n + 1])
 
 
+@pytest.mark.parametrize("B", [40, 120, 153, 185, 200, 310, 700, 1300])
+@pytest.mark.parametrize("V,dtype", [(700, F32), (4099, F32), (32000, BF16), (50257, F32), (128256, BF16), (151937, F32)])
+def test_any_number_of_rows_without_filters(jet, B, V, dtype):
+    """Every split of rows into CTAs: every 29th row as if alone."""
+    if B * V > 4e7:
+        B = max(40, int(4e7) // V)
+    g = torch.Generator(device="cuda").manual_seed(B + V)
+    x = (torch.randn((B, V), generator=g, device="cuda") * 2.5).to(dtype)
+    u = torch.rand((B,), generator=g, device="cuda")
+    full = jet.sample(x, u)
+    for i in range(0, B, 29):
+        one = jet.sample(x[i:i + 1].clone(), u[i:i + 1].clone())
+        for a, b in zip(one, full):
+            assert torch.equal(a, b[i:i + 1]), (i, a, b[i])
+
+
 @pytest.mark.parametrize("B", [17, 20, 26, 33, 60, 75, 100, 150, 300])
 @pytest.mark.parametrize("V,dtype", [(33001, F32), (128256, BF16), (151937, F32), (262144, BF16), (262143, F32)])
 def test_any_number_of_rows_gives_a_row_the_same(jet, B, V, dtype):
