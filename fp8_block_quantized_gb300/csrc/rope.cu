@@ -138,10 +138,19 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t x, float c, float s) {
     return pack_bf16(__fmaf_rn(a, c, -__fmul_rn(b, s)), __fmaf_rn(b, c, __fmul_rn(a, s)));
 }
 
+// Interleaved layout, the first `pairs` pairs of a chunk.
+__device__ __forceinline__ void turn_chunk(uint4 &x, const float *c, const float *s, int pairs) {
+    if (pairs > 0) x.x = turn_pair(x.x, c[0], s[0]);
+    if (pairs > 1) x.y = turn_pair(x.y, c[1], s[1]);
+    if (pairs > 2) x.z = turn_pair(x.z, c[2], s[2]);
+    if (pairs > 3) x.w = turn_pair(x.w, c[3], s[3]);
+}
+
 // A thread takes one item of up to kRopeBatch heads of one token, so that their
 // loads are in flight together and share one set of angles.  Items of a head:
 // kHalf (R % 16 == 0): R/16 pairs of 8-channel chunks (c, c + R/16), then the
-// chunks past R; interleaved (any R): D/8 chunks.
+// chunks past R in twos; interleaved (any R): chunks (c, c + n) of 2n or 2n - 1,
+// so that a warp's lanes turn alike where half of the channels turn.
 // kBatch heads at a time: all of them, or two with the registers of four CTAs an
 // SM (the cache form of many tokens, whose encoding keeps the SMs busy: 16384
 // tokens of 64 + 8 + 8 heads 98 us, 110 with four; without a cache 8192 tokens
@@ -154,8 +163,7 @@ rope_kernel(const RopeArgs a) {
     jet::griddep_wait();
     for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) frac[i] = turn_fraction(a.freq[i]);
     __syncthreads();
-    constexpr int kPairs = kHalf ? 8 : 4;
-    const int nrot = kHalf ? a.R / 16 : (a.R + 7) / 8;
+    const int nrot = a.R / 16;  // half layout
     const int heads = a.Hq + a.Hk + a.Hv;
     const uint32_t per_token = (uint32_t)a.groups * a.items;
     const uint32_t total = (uint32_t)a.T * per_token;
@@ -165,13 +173,17 @@ rope_kernel(const RopeArgs a) {
         const uint32_t t = (uint32_t)idx / per_token, rest = (uint32_t)idx - t * per_token;
         const uint32_t grp = rest / a.items;
         const int item = (int)(rest - grp * a.items);
-        const bool rot = item < nrot;
-        if (!rot && inplace) continue;
+        // the item's chunks, at channels d0 and d1, and the pairs of each that turn
+        // (half layout: the pairs between the two)
+        const int d0 = !kHalf ? 8 * item : item < nrot ? 8 * item : a.R + 16 * (item - nrot);
+        const int d1 = !kHalf ? 8 * (item + a.items) : item < nrot ? a.R / 2 + 8 * item : d0 + 8;
+        const bool both = d1 < a.D;
+        const int rot0 = kHalf ? (item < nrot ? 8 : 0) : min(max((a.R - d0) / 2, 0), 4);
+        const int rot1 = kHalf ? 0 : min(max((a.R - d1) / 2, 0), 4);
+        if (rot0 == 0 && inplace) continue;
         const int h0 = (int)grp * a.hpt, h1 = min(h0 + a.hpt, heads);
         const int64_t slot = kCache ? a.slots[t] : 0;
-        const int d0 = kHalf ? (rot ? 8 * item : a.R + 8 * (item - nrot)) : 8 * item;
-        const int d1 = kHalf ? a.R / 2 + 8 * item : 0;
-        float c[kPairs], s[kPairs];
+        float c[8], s[8];
 #pragma unroll 1
         for (int hb = h0; hb < h1; hb += kBatch) {
             uint4 x[kBatch], y[kBatch];
@@ -180,35 +192,33 @@ rope_kernel(const RopeArgs a) {
                 if (hb + b >= h1) break;
                 const Head hd = head_of<kCache>(a, t, hb + b, -1);
                 x[b] = *reinterpret_cast<const uint4 *>(hd.in + d0);
-                if (kHalf && rot) y[b] = *reinterpret_cast<const uint4 *>(hd.in + d1);
+                if (both) y[b] = *reinterpret_cast<const uint4 *>(hd.in + d1);
             }
-            if (rot && hb == h0) {
+            if (rot0 > 0 && hb == h0) {
                 const int64_t pos = a.pos[t];
 #pragma unroll
-                for (int i = 0; i < kPairs; ++i)
-                    if (kHalf || kPairs * item + i < a.R / 2)
-                        angle(frac[kPairs * item + i], pos, a.mscale, a.backward, c[i], s[i]);
+                for (int i = 0; i < 8; ++i)
+                    if (kHalf || i < rot0 || (i >= 4 && i - 4 < rot1))
+                        angle(frac[kHalf ? 8 * item + i : i < 4 ? d0 / 2 + i : d1 / 2 + i - 4], pos, a.mscale,
+                              a.backward, c[i], s[i]);
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 if (hb + b >= h1) break;
                 const Head hd = head_of<kCache>(a, t, hb + b, slot);
-                if (rot && hd.rotate) {
+                if (rot0 > 0 && hd.rotate) {
                     if constexpr (kHalf) {
                         turn_half(x[b].x, y[b].x, c, s);
                         turn_half(x[b].y, y[b].y, c + 2, s + 2);
                         turn_half(x[b].z, y[b].z, c + 4, s + 4);
                         turn_half(x[b].w, y[b].w, c + 6, s + 6);
                     } else {
-                        const int last = a.R / 2 - 4 * item;  // pairs of this chunk that turn
-                        x[b].x = turn_pair(x[b].x, c[0], s[0]);
-                        if (last > 1) x[b].y = turn_pair(x[b].y, c[1], s[1]);
-                        if (last > 2) x[b].z = turn_pair(x[b].z, c[2], s[2]);
-                        if (last > 3) x[b].w = turn_pair(x[b].w, c[3], s[3]);
+                        turn_chunk(x[b], c, s, rot0);
+                        turn_chunk(y[b], c + 4, s + 4, rot1);
                     }
                 }
                 store8<kCache>(hd, d0, x[b]);
-                if (kHalf && rot) store8<kCache>(hd, d1, y[b]);
+                if (both) store8<kCache>(hd, d1, y[b]);
             }
             if (kBatch == kRopeBatch) break;  // all of them
         }
@@ -270,22 +280,26 @@ jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo
     const bool half = layout == JET_ROPE_HALF;
     const bool vec = !half || a.R % 16 == 0;
     const int R8 = (a.R + 7) / 8 * 8;
-    a.items = !half ? a.D / 8 : vec ? a.R / 16 + (a.D - a.R) / 8
+    a.items = !half ? (a.D + 15) / 16 : vec ? a.R / 16 + (a.D - a.R + 15) / 16
                                     : a.R / 2 + (R8 - a.R) + (a.D - R8) / 8;
     const int heads = a.Hq + a.Hk + a.Hv;
     // More heads per thread share one set of angles; fewer keep the SMs busy
-    // when there are few tokens.
+    // when there are few tokens (with less than 512 items an SM: 1000 tokens of
+    // 32 + 8 heads 6.4 us with four heads, 8.8 with one; 256 tokens 3.5 with one).
     a.hpt = kRopeBatch;
-    while (a.hpt > 1 && a.T * ((heads + a.hpt - 1) / a.hpt) * a.items < (int64_t)dev.num_sms * 2048)
+    while (a.hpt > 1 && a.T * ((heads + a.hpt - 1) / a.hpt) * a.items < (int64_t)dev.num_sms * 512)
         a.hpt /= 2;
     a.groups = (heads + a.hpt - 1) / a.hpt;
-    // Twice the resident CTAs (3 per SM for the half layout, 5 interleaved; 6 for
-    // the channel-wise one; 8192 tokens of 32 + 8 heads 27.4 us with 6 per SM,
-    // 29.0 with 3), but as many as are resident, 4, of the kernel of pairs.
-    const bool pairs = vec && half && cache && a.hpt == kRopeBatch;
-    const int64_t cap = (int64_t)dev.num_sms * (pairs ? 4 : half ? 6 : 10);
+    // Twice the resident CTAs (3 per SM; those of the channel-wise kernel: 6; 8192
+    // tokens of 32 + 8 heads 27 us with 6 per SM, 29 with 3).  With a cache, items that
+    // 3 CTAs an SM cannot hold at once go to the kernel of pairs, with the 4 that
+    // are resident (1000 tokens of 32 + 8 + 8 heads 8.3 us, 9.4 in pairs; 1500
+    // tokens 9.7 in pairs, 12.4 without).
+    const int64_t sms = dev.num_sms;
+    const bool pairs = vec && cache && a.hpt == kRopeBatch && a.T * a.groups * a.items > 3 * kRopeThreads * sms;
+    const int64_t cap = sms * (pairs ? 4 : 6);
     void (*kernel)(RopeArgs) =
-        pairs ? rope_kernel<true, true, 2>
+        pairs ? (half ? rope_kernel<true, true, 2> : rope_kernel<false, true, 2>)
         : vec ? (half ? (cache ? rope_kernel<true, true, kRopeBatch> : rope_kernel<true, false, kRopeBatch>)
                       : (cache ? rope_kernel<false, true, kRopeBatch> : rope_kernel<false, false, kRopeBatch>))
               : (cache ? rope_any_kernel<true> : rope_any_kernel<false>);

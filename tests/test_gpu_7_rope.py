@@ -142,6 +142,46 @@ def test_fused_write_equals_the_separate_calls(jet, layout, T, Hq, Hk, D, R):
     assert torch.equal(kc, kc2) and torch.equal(vc, vc2)
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("T,Hq,Hk,D,R", [(70, 5, 2, 72, 32), (70, 5, 2, 72, 64), (70, 3, 1, 88, 16), (9, 2, 1, 8, 8),
+                                         (33, 4, 4, 24, 0), (2500, 9, 3, 128, 64), (2500, 7, 2, 256, 130),
+                                         (1300, 32, 8, 128, 128)])
+def test_channels_past_the_turned_ones(jet, layout, T, Hq, Hk, D, R):
+    """Odd numbers of chunks past R, heads that no thread's batch divides, in
+    numbers that take several rounds of the grid."""
+    q, k = heads(T, Hq, D, T + D), heads(T, Hk, D, T + D + 1, pad=8)
+    f, pos = freqs(max(R, 2))[:R // 2], torch.arange(T).cuda() * 3
+    for backward in (False, True):
+        qo, ko = jet.rope(q, k, f, pos, layout, 1.0, backward)
+        torch.cuda.synchronize()
+        check(qo, q, f, pos, layout, 1.0, backward)
+        check(ko, k, f, pos, layout, 1.0, backward)
+        assert torch.equal(qo[:, :, R:], q[:, :, R:]) and torch.equal(ko[:, :, R:], k[:, :, R:])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("T,Hq,Hk,D,R", [(1700, 32, 8, 128, 128), (1700, 32, 8, 128, 64), (3000, 9, 3, 80, 48),
+                                         (2600, 13, 1, 256, 128), (6000, 7, 1, 96, 26), (20000, 2, 1, 64, 64)])
+def test_fused_write_of_many_tokens(jet, layout, T, Hq, Hk, D, R):
+    """Equal to the two separate calls where a thread takes its heads in twos."""
+    S = T + 7
+    q, k, v = heads(T, Hq, D, 1), heads(T, Hk, D, 2, pad=16), heads(T, Hk, D, 3, pad=8)
+    g = torch.Generator().manual_seed(T)
+    f, pos = freqs(R, 500000.0), torch.randint(0, 100000, (T,), generator=g).cuda()
+    slots = torch.randperm(S, generator=g)[:T].cuda()
+    slots[11] = -1
+    ks, vs = ((torch.rand((Hk,), generator=g) * 0.01 + 0.003).cuda() for _ in range(2))
+    kc, vc = (torch.full((S, Hk, D), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2))
+    kc2, vc2 = kc.clone(), vc.clone()
+    qo, ko = jet.rope(q, k, f, pos, layout, 1.1)
+    jet.jet_kv_cache_write(ko, ks, slots, kc2)
+    jet.jet_kv_cache_write(v.contiguous(), vs, slots, vc2)
+    qf = torch.empty((T, Hq, D), dtype=BF16, device="cuda")
+    jet.jet_rope_kv_cache_write(q, k, v, f, pos, ks, vs, slots, qf, kc, vc, layout, 1.1)
+    torch.cuda.synchronize()
+    assert torch.equal(qf, qo) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
+
+
 def test_cache_past_32_bits(jet):
     """Slots whose byte offsets pass 2^32 land where they belong."""
     T, H, D = 3, 8, 128
