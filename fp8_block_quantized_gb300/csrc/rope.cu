@@ -13,6 +13,7 @@
 // a whole turn, in integer arithmetic with an error below |pos| 2^-54 turns (the
 // binary64 product) at any position; its top 32 bits, as a signed half-turn count,
 // go to sincospi in binary32.
+#include <algorithm>
 #include <cmath>
 
 #include "jet_common.cuh"
@@ -66,8 +67,9 @@ struct RopeArgs {
     const int64_t *slots;
     uint8_t *kc, *vc;
     int64_t S;
-    // split of the work: threads = T * groups * items, hpt heads each
+    // split of the work: T * groups * items threads, or T * groups tiles, of hpt heads
     int groups, items, hpt;
+    int by[4];  // rope_any_kernel's divisions
 };
 
 // One head's place: where it is read and where its result goes.
@@ -225,84 +227,136 @@ rope_kernel(const RopeArgs a) {
     }
 }
 
-template <bool kCache>
-__device__ __forceinline__ void store1(const Head &hd, int d, uint32_t bf16) {
-    if (!kCache || hd.out) {
-        hd.out[d] = (uint16_t)bf16;
-    } else if (hd.code) {
-        const float q = qdiv_neg(__uint_as_float((bf16 << 16) ^ 0x80000000u), make_divisor(hd.scale));
-        hd.code[d] = (uint8_t)f32x4_to_e4m3x4(q, q, q, q);
-    }
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (unsigned)__cvta_generic_to_shared(dst)),
+                 "l"(src)
+                 : "memory");
 }
 
-// The half layout where the second half starts inside a 16-byte chunk: items are
-// the R/2 pairs, channel by channel, the single channels up to the next chunk,
-// then the chunks past them.
-template <bool kCache>
-__global__ void __launch_bounds__(kRopeThreads)
-rope_any_kernel(const RopeArgs a) {
-    extern __shared__ unsigned long long frac[];
-    jet::griddep_launch_dependents();
-    jet::griddep_wait();
-    for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) frac[i] = turn_fraction(a.freq[i]);
-    __syncthreads();
-    const int heads = a.Hq + a.Hk + a.Hv, R8 = (a.R + 7) / 8 * 8;
-    const uint32_t per_token = (uint32_t)a.groups * a.items;
-    const uint32_t total = (uint32_t)a.T * per_token;
-    for (uint64_t idx = blockIdx.x * (uint64_t)kRopeThreads + threadIdx.x; idx < total;
-         idx += (uint64_t)gridDim.x * kRopeThreads) {
-        const uint32_t t = (uint32_t)idx / per_token, rest = (uint32_t)idx - t * per_token;
-        const uint32_t grp = rest / a.items;
-        const int item = (int)(rest - grp * a.items), single = item - a.R / 2;
-        const int h0 = (int)grp * a.hpt, h1 = min(h0 + a.hpt, heads);
-        const int64_t slot = kCache ? a.slots[t] : 0;
-        float c = 1.0f, s = 0.0f;
-        if (single < 0) angle(frac[item], a.pos[t], a.mscale, a.backward, c, s);
-        for (int h = h0; h < h1; ++h) {
-            const Head hd = head_of<kCache>(a, t, h, slot);
-            if (single < 0) {
-                uint32_t w = hd.in[item] | ((uint32_t)hd.in[item + a.R / 2] << 16);
-                if (hd.rotate) w = turn_pair(w, c, s);
-                store1<kCache>(hd, item, w & 0xFFFFu);
-                store1<kCache>(hd, item + a.R / 2, w >> 16);
-            } else if (single < R8 - a.R) {
-                store1<kCache>(hd, a.R + single, hd.in[a.R + single]);
-            } else {
-                const int d = R8 + 8 * (single - (R8 - a.R));
-                store8<kCache>(hd, d, *reinterpret_cast<const uint4 *>(hd.in + d));
+// The half layout where the second half starts inside a 16-byte chunk.  A CTA
+// takes whole heads of one token, about kAnyChunks chunks of them: those that hold
+// turned channels go to shared memory while the CTA computes the token's angles
+// once and copies the others, a thread then turns single pairs there, and chunks
+// go out (8192 tokens of 32 + 8 heads of 128, 34 turned: 34 us, 63 channel by
+// channel; with the cache write 44 and 102).
+constexpr int kAnyChunks = 1024;
+
+// The CTA's threads over `per` items of each head: this thread's first (head,
+// item) and the step to its next, without divisions (by is 2^16 / per, rounded
+// up: exact for the quotients of 0 .. 255, and of 256 up to per = 256).
+struct Walk {
+    int per, h0, i0, dh, di;
+    __device__ Walk(int n, int by) : per(n) {
+        h0 = n > 0 ? ((int)threadIdx.x * by) >> 16 : 1 << 30;
+        i0 = (int)threadIdx.x - h0 * n;
+        dh = n > kRopeThreads ? 0 : (kRopeThreads * by) >> 16;
+        di = kRopeThreads - dh * n;
+    }
+    template <typename F>
+    __device__ __forceinline__ void over(int heads, F f) const {
+        int h = h0, i = i0;
+#pragma unroll 1
+        while (h < heads) {
+            f(h, i);
+            h += dh;
+            i += di;
+            if (i >= per) {
+                i -= per;
+                ++h;
             }
         }
+    }
+};
+
+template <bool kCache>
+__global__ void __launch_bounds__(kRopeThreads, 8)
+rope_any_kernel(const RopeArgs a) {
+    extern __shared__ uint4 tile[];  // [hpt][R8], then the fractions and angles [R / 2]
+    const int R2 = a.R / 2, R8 = (a.R + 7) / 8, rest = a.D / 8 - R8, heads = a.Hq + a.Hk + a.Hv;
+    unsigned long long *frac = reinterpret_cast<unsigned long long *>(tile + a.hpt * R8);
+    float2 *cs = reinterpret_cast<float2 *>(frac + R2);
+    jet::griddep_launch_dependents();
+    jet::griddep_wait();
+    for (int i = threadIdx.x; i < R2; i += kRopeThreads) frac[i] = turn_fraction(a.freq[i]);
+    const bool inplace = !kCache && a.q == a.qo && a.k == a.ko;
+    const Walk chunks(R8, a.by[0]), pairs(R2, a.by[1]), others(inplace ? 0 : rest, a.by[2]),
+        whole(R8 + rest, a.by[3]);
+    for (int64_t unit = blockIdx.x; unit < a.T * a.groups; unit += gridDim.x) {
+        const int64_t t = unit / a.groups;
+        const int h0 = (int)(unit - t * a.groups) * a.hpt;
+        const int n = min(a.hpt, heads - h0), turned = min(n, max(a.Hq + a.Hk - h0, 0));
+        const int64_t pos = a.pos[t], slot = kCache ? a.slots[t] : 0;
+        __syncthreads();  // the last unit's tile and angles have been read
+        chunks.over(turned, [&](int h, int i) {
+            cp_async16(tile + h * R8 + i, head_of<kCache>(a, t, h0 + h, -1).in + 8 * i);
+        });
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        auto copy = [&](int h, int i) {
+            const Head hd = head_of<kCache>(a, t, h0 + h, slot);
+            store8<kCache>(hd, 8 * i, *reinterpret_cast<const uint4 *>(hd.in + 8 * i));
+        };
+        others.over(turned, [&](int h, int i) { copy(h, R8 + i); });
+        if (kCache) whole.over(n - turned, [&](int h, int i) { copy(turned + h, i); });
+        for (int i = threadIdx.x; i < R2; i += kRopeThreads) {
+            float c, s;
+            angle(frac[i], pos, a.mscale, a.backward, c, s);
+            cs[i] = make_float2(c, s);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        pairs.over(turned, [&](int h, int i) {
+            uint16_t *row = reinterpret_cast<uint16_t *>(tile + h * R8);
+            const float2 f = cs[i];
+            const uint32_t w = turn_pair(row[i] | ((uint32_t)row[i + R2] << 16), f.x, f.y);
+            row[i] = (uint16_t)w;
+            row[i + R2] = (uint16_t)(w >> 16);
+        });
+        __syncthreads();
+        chunks.over(turned, [&](int h, int i) {
+            store8<kCache>(head_of<kCache>(a, t, h0 + h, slot), 8 * i, tile[h * R8 + i]);
+        });
     }
 }
 
 jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo &dev,
                        jet_stream_t stream) {
     const bool half = layout == JET_ROPE_HALF;
-    const bool vec = !half || a.R % 16 == 0;
-    const int R8 = (a.R + 7) / 8 * 8;
-    a.items = !half ? (a.D + 15) / 16 : vec ? a.R / 16 + (a.D - a.R + 15) / 16
-                                    : a.R / 2 + (R8 - a.R) + (a.D - R8) / 8;
+    const int64_t sms = dev.num_sms;
     const int heads = a.Hq + a.Hk + a.Hv;
+    if (half && a.R % 16 != 0) {
+        // heads of kAnyChunks chunks a CTA, fewer while there are not two CTAs an SM
+        // (of 64 chunks at least; 300 tokens of 32 + 8 heads 3.2 us, 3.5 with four)
+        a.hpt = std::max(1, std::min(heads, kAnyChunks / (a.D / 8)));
+        while (a.hpt > 1 && a.hpt * a.D > 8 * 64 && a.T * ((heads + a.hpt - 1) / a.hpt) < 2 * sms)
+            a.hpt = (a.hpt + 1) / 2;
+        a.groups = (heads + a.hpt - 1) / a.hpt;
+        const int per[4] = {(a.R + 7) / 8, a.R / 2, a.D / 8 - (a.R + 7) / 8, a.D / 8};
+        for (int i = 0; i < 4; ++i) a.by[i] = per[i] ? (65536 + per[i] - 1) / per[i] : 0;
+        const int64_t want = a.T * a.groups, cap = 24 * sms;
+        return jet::launch_pdl(cache ? rope_any_kernel<true> : rope_any_kernel<false>,
+                               dim3((unsigned)(want < cap ? want : cap)), dim3(kRopeThreads),
+                               (size_t)a.hpt * ((a.R + 7) / 8) * 16 + (size_t)a.R / 2 * 16,
+                               jet::as_stream(stream), a);
+    }
+    a.items = half ? a.R / 16 + (a.D - a.R + 15) / 16 : (a.D + 15) / 16;
     // More heads per thread share one set of angles; fewer keep the SMs busy
     // when there are few tokens (with less than 512 items an SM: 1000 tokens of
     // 32 + 8 heads 6.4 us with four heads, 8.8 with one; 256 tokens 3.5 with one).
     a.hpt = kRopeBatch;
-    while (a.hpt > 1 && a.T * ((heads + a.hpt - 1) / a.hpt) * a.items < (int64_t)dev.num_sms * 512)
+    while (a.hpt > 1 && a.T * ((heads + a.hpt - 1) / a.hpt) * a.items < sms * 512)
         a.hpt /= 2;
     a.groups = (heads + a.hpt - 1) / a.hpt;
-    // Twice the resident CTAs (3 per SM; those of the channel-wise kernel: 6; 8192
-    // tokens of 32 + 8 heads 27 us with 6 per SM, 29 with 3).  With a cache, items that
-    // 3 CTAs an SM cannot hold at once go to the kernel of pairs, with the 4 that
-    // are resident (1000 tokens of 32 + 8 + 8 heads 8.3 us, 9.4 in pairs; 1500
+    // Twice the resident CTAs (3 per SM; 8192 tokens of 32 + 8 heads 27 us with 6
+    // per SM, 29 with 3).  With a cache, items that 3 CTAs an SM cannot hold at
+    // once go to the kernel of pairs, with the 4 that are resident (1000 tokens of 32 + 8 + 8 heads 8.3 us, 9.4 in pairs; 1500
     // tokens 9.7 in pairs, 12.4 without).
-    const int64_t sms = dev.num_sms;
-    const bool pairs = vec && cache && a.hpt == kRopeBatch && a.T * a.groups * a.items > 3 * kRopeThreads * sms;
+    const bool pairs = cache && a.hpt == kRopeBatch && a.T * a.groups * a.items > 3 * kRopeThreads * sms;
     const int64_t cap = sms * (pairs ? 4 : 6);
     void (*kernel)(RopeArgs) =
         pairs ? (half ? rope_kernel<true, true, 2> : rope_kernel<false, true, 2>)
-        : vec ? (half ? (cache ? rope_kernel<true, true, kRopeBatch> : rope_kernel<true, false, kRopeBatch>)
-                      : (cache ? rope_kernel<false, true, kRopeBatch> : rope_kernel<false, false, kRopeBatch>))
-              : (cache ? rope_any_kernel<true> : rope_any_kernel<false>);
+        : half ? (cache ? rope_kernel<true, true, kRopeBatch> : rope_kernel<true, false, kRopeBatch>)
+               : (cache ? rope_kernel<false, true, kRopeBatch> : rope_kernel<false, false, kRopeBatch>);
     // The kernels count a launch's items in 32 bits: more tokens take several launches.
     const int64_t all = a.T, most = (((int64_t)1 << 32) - 1) / ((int64_t)a.groups * a.items);
     for (int64_t t0 = 0; t0 < all; t0 += most) {

@@ -145,7 +145,9 @@ def test_fused_write_equals_the_separate_calls(jet, layout, T, Hq, Hk, D, R):
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("T,Hq,Hk,D,R", [(70, 5, 2, 72, 32), (70, 5, 2, 72, 64), (70, 3, 1, 88, 16), (9, 2, 1, 8, 8),
                                          (33, 4, 4, 24, 0), (2500, 9, 3, 128, 64), (2500, 7, 2, 256, 130),
-                                         (1300, 32, 8, 128, 128)])
+                                         (1300, 32, 8, 128, 128), (40, 3, 2, 1024, 514), (40, 3, 2, 1024, 1022),
+                                         (5, 9, 1, 512, 510), (700, 40, 8, 16, 14), (300, 100, 20, 64, 2),
+                                         (5000, 17, 3, 128, 34)])
 def test_channels_past_the_turned_ones(jet, layout, T, Hq, Hk, D, R):
     """Odd numbers of chunks past R, heads that no thread's batch divides, in
     numbers that take several rounds of the grid."""
@@ -161,7 +163,8 @@ def test_channels_past_the_turned_ones(jet, layout, T, Hq, Hk, D, R):
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("T,Hq,Hk,D,R", [(1700, 32, 8, 128, 128), (1700, 32, 8, 128, 64), (3000, 9, 3, 80, 48),
-                                         (2600, 13, 1, 256, 128), (6000, 7, 1, 96, 26), (20000, 2, 1, 64, 64)])
+                                         (2600, 13, 1, 256, 128), (6000, 7, 1, 96, 26), (20000, 2, 1, 64, 64), (5000, 17, 3, 128, 34),
+                                         (50, 3, 2, 1024, 514), (900, 40, 24, 16, 14)])
 def test_fused_write_of_many_tokens(jet, layout, T, Hq, Hk, D, R):
     """Equal to the two separate calls where a thread takes its heads in twos."""
     S = T + 7
