@@ -13,6 +13,11 @@
 // a whole turn, in integer arithmetic with an error below |pos| 2^-54 turns (the
 // binary64 product) at any position; its top 32 bits, as a signed half-turn count,
 // go to sincospi in binary32.
+//
+// Bound by HBM: every input is read once and every output written once, 16 bytes
+// at a time (8192 tokens of 32 + 8 heads of 128: 26.9 us, 6229 GB/s, 92% of a
+// copy's rate; with the cache write, 16384 tokens of 64 + 8 + 8 heads: 98.8 us,
+// 6453 GB/s, 95%).  Few tokens: latency (64 tokens of 32 + 8 + 8 heads 3.6 us).
 #include <algorithm>
 #include <cmath>
 
@@ -349,9 +354,10 @@ jet_status rope_launch(RopeArgs a, int layout, bool cache, const jet::DeviceInfo
     a.groups = (heads + a.hpt - 1) / a.hpt;
     // Twice the resident CTAs (3 per SM; 8192 tokens of 32 + 8 heads 27 us with 6
     // per SM, 29 with 3).  With a cache, items that 3 CTAs an SM cannot hold at
-    // once go to the kernel of pairs, with the 4 that are resident (1000 tokens of 32 + 8 + 8 heads 8.3 us, 9.4 in pairs; 1500
-    // tokens 9.7 in pairs, 12.4 without).
-    const bool pairs = cache && a.hpt == kRopeBatch && a.T * a.groups * a.items > 3 * kRopeThreads * sms;
+    // once go to the kernel of pairs, with the 4 that are resident (1000 tokens of
+    // 32 + 8 + 8 heads 8.3 us, 9.4 in pairs; 1500 tokens 9.7 in pairs, 12.4 without).
+    const bool pairs = cache && a.hpt == kRopeBatch &&
+                       a.T * a.groups * a.items > 3 * kRopeThreads * sms;
     const int64_t cap = sms * (pairs ? 4 : 6);
     void (*kernel)(RopeArgs) =
         pairs ? (half ? rope_kernel<true, true, 2> : rope_kernel<false, true, 2>)
@@ -487,7 +493,7 @@ jet_status jet_rope_kv_cache_write(const uint16_t *q, int64_t ldq, int64_t Hq, c
     a.kc = k_cache;
     a.vc = v_cache;
     a.S = S;
-    return rope_launch(a, layout, true, dev, stream);
+    return rope_launch(a, layout, hask, dev, stream);  // no heads to cache: slots may be null
 }
 
 jet_status jet_rope_inv_freq(int64_t R, double base, int scaling, double factor, double context,

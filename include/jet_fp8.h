@@ -561,7 +561,8 @@ JET_API jet_status jet_rope(const uint16_t *q, int64_t ldq, int64_t Hq, const ui
  * cache slots.  Equal bit for bit to jet_rope of q and k followed by
  * jet_kv_cache_write of the rotated k (k_scale, k_cache) and of v (v_scale,
  * v_cache).  Arguments as in those calls; a slot outside [0, S) is skipped
- * (its q is still rotated); D a multiple of 16.
+ * (its q is still rotated); D a multiple of 16.  With Hk = 0 k, v, the scales,
+ * the slots and the caches may be NULL.
  */
 JET_API jet_status jet_rope_kv_cache_write(const uint16_t *q, int64_t ldq, int64_t Hq,
                                            const uint16_t *k, int64_t ldk, const uint16_t *v,

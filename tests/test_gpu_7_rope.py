@@ -185,6 +185,20 @@ def test_fused_write_of_many_tokens(jet, layout, T, Hq, Hk, D, R):
     assert torch.equal(qf, qo) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
 
 
+@pytest.mark.parametrize("R", [64, 36])
+def test_no_heads_to_cache(jet, R):
+    """With Hk = 0 nothing of the cache's is read: its pointers and the slots may be null."""
+    T, H, D = 33, 4, 64
+    q, f, pos = heads(T, H, D, 3), freqs(R), torch.arange(T).cuda()
+    want, _ = jet.rope(q, None, f, pos, "half", 1.2)
+    out = torch.empty((T, H, D), dtype=BF16, device="cuda")
+    st = jet.load().jet_rope_kv_cache_write(
+        q.data_ptr(), q.stride(0), H, None, 0, None, 0, 0, T, D, R, f.data_ptr(), pos.data_ptr(), 0, 1.2,
+        None, None, None, out.data_ptr(), H * D, None, None, 0, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and torch.equal(out, want)
+
+
 def test_cache_past_32_bits(jet):
     """Slots whose byte offsets pass 2^32 land where they belong."""
     T, H, D = 3, 8, 128
