@@ -8,6 +8,11 @@
 // butterfly, ms = ss / K, r = 1 / sqrt(ms + eps), y = (h r) g in binary32 and
 // the 1x128 group rule.  So the codes and scales equal those of the separate
 // addition and jet_rmsnorm_quant_1x128 bit for bit, for any number of rows.
+//
+// Both directions are bound by HBM at many rows, each input read and each output
+// written once (forward 16384 x 5120: 87.5 us, 6742 GB/s, 99% of a copy's rate;
+// backward of 8192 x 4096 with three gradients and the residual's: 60.8 us, 6618
+// GB/s), and by latency at few (forward 16 x 4096: 2.3 us).
 #include <cuda_bf16.h>
 
 #include "jet_common.cuh"
@@ -490,7 +495,9 @@ jet_status jet_add_rmsnorm_quant_1x128(const uint16_t *x, const uint16_t *d, con
         // up to four rows an SM 512 (600 x 4096: 5.0, 7.4 with 128); then 128 for
         // K <= 5120 (16384 x 5120: 87, 99 with 256) and 256 for longer rows (4096 x
         // 8192: 40, 45 with 128).
-        const int T = M <= 4 * (int64_t)dev.num_sms || nchunks > 8 * 256 ? 512 : nchunks > 640 ? 256 : 128;
+        const int T = M <= 4 * (int64_t)dev.num_sms || nchunks > 8 * 256 ? 512
+                      : nchunks > 640                                    ? 256
+                                                                         : 128;
         const int ni = (int)((nchunks + T - 1) / T);
         void (*kernel)(const uint16_t *, const uint16_t *, const uint16_t *, int64_t, int64_t, float,
                        uint16_t *, uint8_t *, float *, float *) =
@@ -567,7 +574,8 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
     if (smem > 40 * 1024 && !allow_smem(kernel, smem)) return JET_ERR_CUDA;
     // persistent CTAs, as many as fit (registers, shared memory with 1 KB
     // of the system's) and as there are partial rows
-    const int64_t by_threads = threads > 512 && threads <= 640 ? 2 : 1024 / threads, by_smem = 228 * 1024 / (smem + 1024 + 256);
+    const int64_t by_threads = threads > 512 && threads <= 640 ? 2 : 1024 / threads;
+    const int64_t by_smem = 228 * 1024 / (smem + 1024 + 256);
     const int64_t per_sm = by_threads < by_smem ? by_threads : by_smem;
     const int64_t resident = (int64_t)dev.num_sms * (per_sm > 0 ? per_sm : 1);
     const int64_t most = bwd_parts(M, K);

@@ -30,6 +30,11 @@
 // the step the cut lies in, and the first CTA finds it among the tokens of that
 // step; a step with too many of them is split again on the bits of the logits,
 // and one of equal logits by counting.
+//
+// Without a filter, 256 rows of 128256 binary32 logits take 44 us (2.99 TB/s, 44%
+// of a copy's rate): 26 instructions a logit in two passes with a barrier behind
+// each.  With them, few rows are bound by those barriers and the passes over
+// shared memory (16 such rows in BF16: 13 us where lists suffice, 30 otherwise).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -1106,7 +1111,7 @@ struct Sampler {
                 }
                 const bool everything = finite <= kListMax;
                 // the maxima in whole groups above z_lo: so many tokens at least (a
-                // flat 128256-token nucleus: 30 us, 34 with the vain gather)
+                // flat nucleus in each of 16 rows: 54 us, 56 with the vain gather)
                 const int above = (int)(fmaxf(z_lo, -32.0f) * -kGroupsPerZ);
                 unsigned sure = 0;
 #pragma unroll

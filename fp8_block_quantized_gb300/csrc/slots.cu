@@ -12,7 +12,8 @@
 // All integers, and latency-bound at serving sizes: every CTA scans the
 // requests itself (two prefix sums in one pass, at most 8192 requests, kept in
 // shared memory), so one launch suffices and no CTA waits for another; a fresh
-// block's id is computed from the scan, never read back from the table.
+// block's id is computed from the scan, never read back from the table.  256
+// requests of one token take 3.2 us, 65536 tokens 4.4, half of it the launch.
 #include "jet_common.cuh"
 
 namespace {
