@@ -240,6 +240,7 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
 }
 
 struct BwdArgs {
+    int stages;  // rows in shared memory
     const uint16_t *in[5];  // h, then the gradients: dy0 .. , and dres last if it is there
     int ny, nt;             // output gradients; tensors in all
     const uint16_t *g;
@@ -335,11 +336,14 @@ add_rmsnorm_bwd_kernel(const BwdArgs a) {
     if (ok) store_part(a.part + blockIdx.x * a.K + 8 * (int64_t)ci, dg);
 }
 
-// Longer rows, NC chunks a thread: no room to keep a row, which is read again
-// (from L2) for its second pass.
-template <int NC>
+// Longer rows, NC chunks a thread: no registers to keep a row, which is read again
+// for its second pass, from shared memory where a.stages (1 or 2) rows fit, else
+// from L2 (4096 x 10240 with two gradients and the residual's: 97 us with two rows,
+// 102 with one, 147 from L2; 1024 x 20480: 64 with one, 98 from L2).
+template <int NC, bool kStaged>
 __global__ void __launch_bounds__(1024)
 add_rmsnorm_bwd_wide_kernel(const BwdArgs a) {
+    extern __shared__ uint4 stage[];  // [stages][nt][NC][threads]
     __shared__ float red[2][32];
     jet::griddep_launch_dependents();
     jet::griddep_wait();
@@ -350,19 +354,41 @@ add_rmsnorm_bwd_wide_kernel(const BwdArgs a) {
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int t = 0; t < 8; ++t) dg[i][t] = 0.0f;
+    auto fetch = [&](int64_t m, int ph) {
+        if (m < a.M) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int ci = threadIdx.x + i * T;
+                for (int k = 0; ci < nchunks && k < a.nt; ++k)
+                    cp_async16(stage + ((ph * a.nt + k) * NC + i) * T + threadIdx.x,
+                               reinterpret_cast<const uint4 *>(a.in[k]) + m * nchunks + ci);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (kStaged) fetch(blockIdx.x, 0);
     int phase = 0;
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, phase ^= 1) {
         const float r = a.rstd[m];
-        auto load = [&](int k, int ci, float (&f)[8]) {
-            unpack8(reinterpret_cast<const uint4 *>(a.in[k])[m * nchunks + ci], f);
+        const int ph = a.stages == 2 ? phase : 0;
+        if (kStaged && a.stages == 2) {
+            fetch(m + gridDim.x, phase ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else if (kStaged) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        // a thread reads what it fetched itself
+        auto chunk = [&](int k, int i) {
+            return kStaged ? stage[((ph * a.nt + k) * NC + i) * T + threadIdx.x]
+                           : reinterpret_cast<const uint4 *>(a.in[k])[m * nchunks + threadIdx.x + i * T];
         };
-        auto terms = [&](int ci, float (&xh)[8], float (&dy)[8]) {
+        auto terms = [&](int i, float (&xh)[8], float (&dy)[8]) {
             float f[8];
-            load(0, ci, xh);
-            load(1, ci, dy);
+            unpack8(chunk(0, i), xh);
+            unpack8(chunk(1, i), dy);
 #pragma unroll 1
             for (int k = 2; k <= a.ny; ++k) {
-                load(k, ci, f);
+                unpack8(chunk(k, i), f);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) dy[t] += f[t];
             }
@@ -374,7 +400,7 @@ add_rmsnorm_bwd_wide_kernel(const BwdArgs a) {
         for (int i = 0; i < NC; ++i) {
             const int ci = threadIdx.x + i * T;
             if (ci >= nchunks) continue;
-            terms(ci, xh, u);
+            terms(i, xh, u);
             unpack8(reinterpret_cast<const uint4 *>(a.g)[ci], f);
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
@@ -388,14 +414,14 @@ add_rmsnorm_bwd_wide_kernel(const BwdArgs a) {
             const int ci = threadIdx.x + i * T;
             if (ci >= nchunks) continue;
             float gf[8];
-            terms(ci, xh, u);
+            terms(i, xh, u);
             unpack8(reinterpret_cast<const uint4 *>(a.g)[ci], gf);
-            unpack8(has_res ? reinterpret_cast<const uint4 *>(a.in[a.nt - 1])[m * nchunks + ci]
-                            : make_uint4(0, 0, 0, 0), f);
+            unpack8(has_res ? chunk(a.nt - 1, i) : make_uint4(0, 0, 0, 0), f);
 #pragma unroll
             for (int t = 0; t < 8; ++t) f[t] = fmaf(r, fmaf(-xh[t], mean, u[t] * gf[t]), f[t]);
             reinterpret_cast<uint4 *>(a.dx)[m * nchunks + ci] = pack8(f);
         }
+        if (kStaged && a.stages == 1) fetch(m + gridDim.x, 0);
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -566,11 +592,15 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
     a.K = K;
     a.dx = dx;
     a.part = static_cast<float *>(ws);
-    auto *kernel = nc == 1 ? (threads <= 512 ? add_rmsnorm_bwd_kernel<512>
-                              : threads <= 640 ? add_rmsnorm_bwd_kernel<640>
-                                               : add_rmsnorm_bwd_kernel<1024>)
-                           : nc == 2 ? add_rmsnorm_bwd_wide_kernel<2> : add_rmsnorm_bwd_wide_kernel<4>;
-    const size_t smem = nc == 1 ? (size_t)2 * a.nt * threads * 16 : 0;
+    const size_t row = (size_t)a.nt * nc * threads * 16;  // in shared memory
+    a.stages = nc == 1 || 2 * row <= 225 * 1024 ? 2 : row <= 225 * 1024 ? 1 : 0;
+    auto *kernel = nc == 1       ? (threads <= 512   ? add_rmsnorm_bwd_kernel<512>
+                                    : threads <= 640 ? add_rmsnorm_bwd_kernel<640>
+                                                     : add_rmsnorm_bwd_kernel<1024>)
+                   : a.stages > 0 ? (nc == 2 ? add_rmsnorm_bwd_wide_kernel<2, true>
+                                             : add_rmsnorm_bwd_wide_kernel<4, true>)
+                                  : add_rmsnorm_bwd_wide_kernel<4, false>;
+    const size_t smem = a.stages * row;
     if (smem > 40 * 1024 && !allow_smem(kernel, smem)) return JET_ERR_CUDA;
     // persistent CTAs, as many as fit (registers, shared memory with 1 KB
     // of the system's) and as there are partial rows

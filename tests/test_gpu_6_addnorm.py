@@ -139,6 +139,23 @@ def test_backward(jet, M, K, n, dres):
     check_bwd(jet, h, g, rstd, dys, dr, dx, dg)
 
 
+@pytest.mark.parametrize("M,K", [(400, 8320), (333, 12288), (200, 16384), (170, 16512), (160, 20480), (9, 28672),
+                                 (160, 32768)])
+@pytest.mark.parametrize("n,dres", [(1, False), (2, True), (3, True)])
+def test_backward_of_long_rows(jet, M, K, n, dres):
+    """Rows of several chunks a thread, several rows a CTA: two, one or none in
+    shared memory; in place of the residual's gradient too."""
+    h, g, rstd, dys, dr = bwd_inputs(M, K, n, dres, M + K + n)
+    dx, dg = jet.add_rmsnorm_bwd(h, g, rstd, dys, dr)
+    torch.cuda.synchronize()
+    check_bwd(jet, h, g, rstd, dys, dr, dx, dg)
+    if dres:
+        dg2 = torch.empty_like(dg)
+        jet.jet_add_rmsnorm_bwd(h, g, rstd, dys, dr, dr, dg2)
+        torch.cuda.synchronize()
+        assert torch.equal(dr, dx) and torch.equal(dg, dg2)
+
+
 def test_backward_in_place_and_repeatable(jet):
     h, g, rstd, dys, dr = bwd_inputs(1000, 1024, 3, True, 1)
     dx, dg = jet.add_rmsnorm_bwd(h, g, rstd, dys, dr)
