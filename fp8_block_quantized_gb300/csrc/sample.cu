@@ -70,12 +70,15 @@ struct SampleArgs {
 };
 
 // What a CTA of the cluster holds besides its slice of the row.  Arrays over
-// ranks are written by the peers and read after a cluster barrier.
+// ranks are written by the peers and read after a cluster barrier, and between
+// those reads and the peers' next writes lies another one.  The totals have no
+// barrier of their own there: consecutive ones go to two copies in turn, so that
+// the barrier of each parts the reads of its copy's last use from the next writes.
 struct Shared {
-    u64 warp_mass[kMaxWarps], rank_mass[kMaxCluster], seg_mass[kMaxCluster];
+    u64 warp_mass[kMaxWarps], rank_mass[2][kMaxCluster], seg_mass[kMaxCluster];
     u64 scan[2][kMaxWarps], sel_mass, cut_entry;
     unsigned list_range[4][kMaxWarps], list_left;
-    unsigned warp_cnt[kMaxWarps], rank_cnt[kMaxCluster];
+    unsigned warp_cnt[kMaxWarps], rank_cnt[2][kMaxCluster];
     float warp_max[kMaxWarps], rank_max[kMaxCluster];
     unsigned lo, hi, rank_lo[kMaxCluster], rank_hi[kMaxCluster];
     int sel_bin;  // the selected bin
@@ -341,8 +344,9 @@ struct Sampler {
     float m, rt, min_w;
     float cut_x;
     int cut_idx;
+    int copy;     // of the last totals, the same in every thread of the cluster
 
-    __device__ Sampler(const SampleArgs &args) : a(args), cl(cg::this_cluster()), infinite(false), odd(false) {}
+    __device__ Sampler(const SampleArgs &args) : a(args), cl(cg::this_cluster()), infinite(false), odd(false), copy(1) {}
 
     // m is finite and rt a normal number, so x = -inf gives -inf and nothing else
     // is undefined.
@@ -467,8 +471,10 @@ struct Sampler {
     }
 
     // Warp, CTA and cluster totals of a mass and a count; ends with a cluster
-    // barrier, after which rank_mass / rank_cnt hold every CTA's totals.
+    // barrier, after which this copy of rank_mass / rank_cnt holds every CTA's
+    // totals.
     __device__ void totals(u64 mass, unsigned cnt) {
+        copy ^= 1;
         mass = warp_sum(mass);
         cnt = __reduce_add_sync(0xffffffffu, cnt);
         if (lane == 0) {
@@ -479,20 +485,20 @@ struct Sampler {
         if (warp == 0) {
             const u64 t = warp_sum(lane < kWarps ? sh->warp_mass[lane] : 0);
             const unsigned n = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh->warp_cnt[lane] : 0);
-            to_all(&sh->rank_mass[rank], t);
-            to_all(&sh->rank_cnt[rank], n);
+            to_all(&sh->rank_mass[copy][rank], t);
+            to_all(&sh->rank_cnt[copy][rank], n);
         }
         cl.sync();
     }
 
     __device__ u64 all_mass() const {
         u64 t = 0;
-        for (int r = 0; r < C; ++r) t += sh->rank_mass[r];
+        for (int r = 0; r < C; ++r) t += sh->rank_mass[copy][r];
         return t;
     }
     __device__ unsigned all_cnt() const {
         unsigned t = 0;
-        for (int r = 0; r < C; ++r) t += sh->rank_cnt[r];
+        for (int r = 0; r < C; ++r) t += sh->rank_cnt[copy][r];
         return t;
     }
 
@@ -786,7 +792,7 @@ struct Sampler {
         const unsigned n = all_cnt();
         if (n <= kListMax) {
             unsigned to = (unsigned)warp_scan(mine, lane) - mine;
-            for (int r = 0; r < rank; ++r) to += sh->rank_cnt[r];
+            for (int r = 0; r < rank; ++r) to += sh->rank_cnt[copy][r];
             to += __reduce_add_sync(0xffffffffu, lane < warp ? sh->warp_cnt[lane] : 0);
             u64 *list = cl.map_shared_rank(fs, 0)->list;
 #pragma unroll 1
@@ -890,7 +896,7 @@ struct Sampler {
         each([&](float v, int) { mine += v == logit; });
         totals(0, mine);
         unsigned before = 0;
-        for (int r = 0; r < rank; ++r) before += sh->rank_cnt[r];
+        for (int r = 0; r < rank; ++r) before += sh->rank_cnt[copy][r];
         before += __reduce_add_sync(0xffffffffu, lane < warp ? sh->warp_cnt[lane] : 0);
         const unsigned own = sh->warp_cnt[warp];
         if (before < n && n <= before + own) {  // one warp of the cluster
@@ -1152,8 +1158,8 @@ struct Sampler {
         // u S; then all warps sum a part of that range, then a lane its own
         const u64 aim = share(uniform(b), S, false);
         u64 before = 0;
-        for (int r = 0; r < rank; ++r) before += sh->rank_mass[r];
-        if (before > aim || before + sh->rank_mass[rank] <= aim) return;
+        for (int r = 0; r < rank; ++r) before += sh->rank_mass[copy][r];
+        if (before > aim || before + sh->rank_mass[copy][rank] <= aim) return;
         int wi = 0;
         while (wi < kWarps - 1 && before + sh->warp_mass[wi] <= aim) before += sh->warp_mass[wi++];
         const typename El::T *held =
