@@ -1031,6 +1031,7 @@ struct Sampler {
         if (kFilter)
             for (int i = threadIdx.x; i < kGroups; i += kThreads) fs->grp[rank][i] = 0;
         __syncthreads();
+        cl.barrier_wait();  // the peers have begun: their shared memory is there
         if (warp == 0) {
             mx = lane < kWarps ? sh->warp_max[lane] : -INFINITY;
 #pragma unroll
@@ -1195,9 +1196,10 @@ template <bool kBf16, bool kFilter, int kThreads, int kPerSm>
 __global__ void __launch_bounds__(kThreads, kPerSm)
 sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
+    Sampler<kBf16, kFilter, kThreads> s(a);
+    s.cl.barrier_arrive();  // waited for before the first store to a peer, behind the row's loads
     jet::griddep_launch_dependents();
     jet::griddep_wait();
-    Sampler<kBf16, kFilter, kThreads> s(a);
     s.C = (int)s.cl.num_blocks();
     s.rank = (int)s.cl.block_rank();
     s.lane = threadIdx.x & 31;

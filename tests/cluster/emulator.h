@@ -27,6 +27,7 @@ struct Fiber {
     bool begun = false, done = false;
     const unsigned *wait = nullptr;  // runs once *wait differs from value
     unsigned value = 0;
+    unsigned arrived = 0;  // the cluster barrier's generation at this thread's arrival
     Dim tid, bid;
     unsigned cta, warp;
 };
@@ -96,11 +97,11 @@ static const uint64_t *exchange(uint64_t v) {
 static Cta &cta() { return cluster.ctas[cur->cta]; }
 static unsigned char *smem() { return cta().smem.data(); }
 
-static void cluster_sync() {
-    const unsigned gen = arrive(cluster.bar);
-    if (gen != cluster.bar.gen) ++cluster.syncs;
-    await(cluster.bar, gen);
+static void cluster_arrive() {
+    cur->arrived = arrive(cluster.bar);
+    if (cur->arrived != cluster.bar.gen) ++cluster.syncs;
 }
+static void cluster_wait() { await(cluster.bar, cur->arrived); }
 
 static void enter() {
     Cta &c = cta();
@@ -198,7 +199,12 @@ using std::min;
 
 namespace cooperative_groups {
 struct cluster_group {
-    void sync() const { emu::cluster_sync(); }
+    void barrier_arrive() const { emu::cluster_arrive(); }
+    void barrier_wait() const { emu::cluster_wait(); }
+    void sync() const {
+        barrier_arrive();
+        barrier_wait();
+    }
     unsigned num_blocks() const { return (unsigned)emu::cluster.ctas.size(); }
     unsigned block_rank() const { return emu::cur->cta; }
     template <typename T>

@@ -114,3 +114,11 @@ def test_a_warp_that_falls_behind(emulated, way):
     """The first and the last warp of the first CTA and of another."""
     check_schedules(emulated, way, torch.float32, [(WARP, w) for w in (0, 15, 21, 31)], (1, 2, 4, 8, 12),
                     early=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("way", WAYS)
+def test_ctas_that_start_late(emulated, way, dtype):
+    """Nothing is stored into a CTA that has not begun or has ended: in BF16 the
+    last CTA's part of the row is empty, so it is the first to store."""
+    check_schedules(emulated, way, dtype, [(lag, who) for lag in (CTA, OTHERS) for who in range(C)], (0, 1, 2))
