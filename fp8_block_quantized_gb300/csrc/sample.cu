@@ -1226,6 +1226,8 @@ int warp_chunks(int C, int threads, int64_t chunks) {
 size_t filter_smem(int C, int64_t chunks) {
     return kHead + sizeof(FilterShared) + (size_t)16 * 16 * warp_chunks(C, 512, chunks);
 }
+// What one and two CTAs an SM may have of it.
+constexpr size_t kOne = 227 * 1024, kHalf = 113 * 1024;
 
 template <int kBytes>
 bool aligned_to(const void *p) { return (reinterpret_cast<uintptr_t>(p) & (kBytes - 1)) == 0; }
@@ -1299,7 +1301,6 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
         const int longest = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxCluster, chunks / 256));
         const int64_t wave = sms * 12 / 13;
         auto fits = [&](int c, size_t room) { return c != 7 && filter_smem(c, chunks) <= room; };
-        constexpr size_t kOne = 227 * 1024, kHalf = 113 * 1024;
         static_assert((kOne - kHead - sizeof(FilterShared)) / (512 * 16) * 8 <= 192, "a thread's bits in gather");
         pairs = false;
         for (C = longest; C > 0; --C)
@@ -1335,8 +1336,10 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
     void (*kernel)(SampleArgs) =
         filter ? (pairs ? kernel_for<true, 512, 2>(bf16) : kernel_for<true, 512, 1>(bf16))
                : (threads == 512 ? kernel_for<false, 512, 2>(bf16) : kernel_for<false, 256, 5>(bf16));
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess) {
+    // The limit is the kernel's, whatever this call needs: another thread may be
+    // about to launch it with other sizes.
+    if (filter && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(pairs ? kHalf : kOne)) != cudaSuccess) {
         cudaGetLastError();
         return JET_ERR_CUDA;
     }
