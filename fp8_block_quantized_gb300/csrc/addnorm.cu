@@ -478,10 +478,13 @@ int64_t bwd_parts(int64_t M, int64_t K) {
 }
 
 // Allows a kernel more than the 48 KB of shared memory, its static part among
-// them, that every launch may have.
+// them, that every launch may have.  The limit is the kernel's, whatever a call
+// needs: another thread may be about to launch it with other sizes.
+constexpr size_t kMostSmem = 225 * 1024;
+
 template <typename K>
-bool allow_smem(K *kernel, size_t bytes) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+bool allow_smem(K *kernel) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem) ==
         cudaSuccess)
         return true;
     cudaGetLastError();
@@ -535,7 +538,7 @@ jet_status jet_add_rmsnorm_quant_1x128(const uint16_t *x, const uint16_t *d, con
                           : ni == 2 ? add_rmsnorm_row_kernel<512, 2>
                           : ni <= 4 ? add_rmsnorm_row_kernel<512, 4> : add_rmsnorm_row_kernel<512, 8>);
         const size_t smem = (size_t)K * 2;
-        if (smem > 40 * 1024 && !allow_smem(kernel, smem)) return JET_ERR_CUDA;
+        if (smem > 40 * 1024 && !allow_smem(kernel)) return JET_ERR_CUDA;
         return jet::launch_pdl(kernel, dim3((unsigned)M), dim3((unsigned)T), smem, cs, x, d, g, M, K,
                                eps, h, q, s, rstd);
     }
@@ -593,7 +596,7 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
     a.dx = dx;
     a.part = static_cast<float *>(ws);
     const size_t row = (size_t)a.nt * nc * threads * 16;  // in shared memory
-    a.stages = nc == 1 || 2 * row <= 225 * 1024 ? 2 : row <= 225 * 1024 ? 1 : 0;
+    a.stages = nc == 1 || 2 * row <= kMostSmem ? 2 : row <= kMostSmem ? 1 : 0;
     auto *kernel = nc == 1       ? (threads <= 512   ? add_rmsnorm_bwd_kernel<512>
                                     : threads <= 640 ? add_rmsnorm_bwd_kernel<640>
                                                      : add_rmsnorm_bwd_kernel<1024>)
@@ -601,7 +604,7 @@ jet_status jet_add_rmsnorm_bwd(const uint16_t *h, const uint16_t *g, const float
                                              : add_rmsnorm_bwd_wide_kernel<4, true>)
                                   : add_rmsnorm_bwd_wide_kernel<4, false>;
     const size_t smem = a.stages * row;
-    if (smem > 40 * 1024 && !allow_smem(kernel, smem)) return JET_ERR_CUDA;
+    if (smem > 40 * 1024 && !allow_smem(kernel)) return JET_ERR_CUDA;
     // persistent CTAs, as many as fit (registers, shared memory with 1 KB
     // of the system's) and as there are partial rows
     const int64_t by_threads = threads > 512 && threads <= 640 ? 2 : 1024 / threads;
