@@ -19,7 +19,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
-_marshal = None    # the compiled marshalling, bound to _lib's functions
+_marshal = None    # the compiled marshalling, bound to _lib's functions at its first use
 
 STATUS = {0: "JET_OK", 1: "JET_ERR_NULL", 2: "JET_ERR_SHAPE", 3: "JET_ERR_ALIGN",
           4: "JET_ERR_CUDA", 5: "JET_ERR_DEVICE", 6: "JET_ERR_WORKSPACE",
@@ -103,7 +103,6 @@ def load(build_if_missing: bool = True):
             f.argtypes = args
             f.restype = _RESTYPE.get(name, ctypes.c_int)
         _lib = lib
-        bind(lib)
         return lib
 
 
@@ -112,24 +111,22 @@ MARSHALLED = ("jet_add_rmsnorm_quant_1x128", "jet_add_rmsnorm_bwd", "jet_rope",
               "jet_rope_kv_cache_write", "jet_kv_slot_map", "jet_sample", "jet_workspace_bytes")
 
 
-def bind(lib):
-    """Load the compiled marshalling and give it the library's functions."""
-    global _marshal
-    import importlib.util
-
-    import torch  # noqa: F401  (the module needs torch's libraries)
-    spec = importlib.util.spec_from_file_location("_marshal", _build.MARSHAL)
-    m = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(m)
-    m.bind(JetError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in MARSHALLED))
-    _marshal = m
-
-
 def _compiled():
-    """The compiled marshalling, the library loaded."""
-    if _marshal is None:
-        load()
-    return _marshal
+    """The compiled marshalling, bound to the library's functions (built first
+    if needed); raises if impossible, and leaves the library's other calls usable."""
+    global _marshal
+    lib = load()
+    with _lock:
+        if _marshal is None:
+            import importlib.util
+
+            import torch  # noqa: F401  (the module needs torch's libraries)
+            spec = importlib.util.spec_from_file_location("_marshal", _build.build_marshal())
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.bind(JetError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in MARSHALLED))
+            _marshal = m
+        return _marshal
 
 
 def _check(fn: str, code: int):

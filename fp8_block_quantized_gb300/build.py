@@ -5,7 +5,8 @@ Each ``csrc/*.cu`` is compiled to an object in parallel with
 are linked into ``_build/libjetfp8.so`` (CUDA runtime linked statically).
 ``pysrc/marshal.cpp``, the compiled part of the Python binding, becomes
 ``_build/_marshal.so`` (g++ against the installed torch's headers; it calls
-the library through addresses the binding gives it).
+the library through addresses the binding gives it).  The library needs nvcc
+alone: where the module cannot be built, only the operators it marshals fail.
 IEEE division and denormals are kept (no fast-math): the quantizers' codes must
 be bit-exact.
 """
@@ -15,6 +16,7 @@ import glob
 import os
 import shutil
 import subprocess
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -44,22 +46,31 @@ def sources():
 
 def _deps():
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [MARSHAL_SRC, os.path.abspath(__file__)])
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+
+
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    """Whether the library is (the binding's extension module apart)."""
+    return _newer(LIB, _deps())
 
 
-def build_marshal() -> None:
-    """Compile the binding's extension module against the installed torch."""
+def marshal_up_to_date() -> bool:
+    return _newer(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "jet_fp8.h"), os.path.abspath(__file__)])
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile the binding's extension module against the installed torch; returns its path."""
+    if not force and marshal_up_to_date():
+        return MARSHAL
     import sysconfig
 
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
+    os.makedirs(BUILD, exist_ok=True)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -73,12 +84,21 @@ def build_marshal() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for marshal.cpp:\n{r.stderr}")
     os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link the library; returns its path."""
-    if not force and up_to_date():
-        return LIB
+    """Compile and link the library, and beside it the binding's extension module;
+    returns the library's path.  A module that cannot be built is a warning."""
+    with ThreadPoolExecutor(1) as beside:
+        marshal = beside.submit(build_marshal, force)
+        path = LIB if not force and up_to_date() else _build_library(verbose, extra_flags)
+    if marshal.exception():
+        warnings.warn(f"the binding's extension module is not built: {marshal.exception()}")
+    return path
+
+
+def _build_library(verbose, extra_flags) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     srcs = sources()
@@ -93,10 +113,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        marshal = ex.submit(build_marshal)
+    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         objs = list(ex.map(compile_one, srcs))
-        marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs],
                        capture_output=True, text=True)
