@@ -4,7 +4,7 @@ Each ``csrc/*.cu`` is compiled to an object in parallel with
 ``nvcc -gencode arch=compute_103a,code=sm_103a -lineinfo -O3`` and the objects
 are linked into ``_build/libjetfp8.so`` (CUDA runtime linked statically).
 ``pysrc/marshal.cpp``, the compiled part of the Python binding, becomes
-``_build/_marshal.so`` (g++ against the installed torch's headers; it calls
+``_build/_marshal-*.so`` (g++ against the installed torch's headers; it calls
 the library through addresses the binding gives it).  The library needs nvcc
 alone: where the module cannot be built, only the operators it marshals fail.
 IEEE division and denormals are kept (no fast-math): the quantizers' codes must
@@ -13,9 +13,11 @@ be bit-exact.
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
+import sysconfig
 import warnings
 from concurrent.futures import ThreadPoolExecutor
 
@@ -24,7 +26,18 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libjetfp8.so")
 MARSHAL_SRC = os.path.join(PKG, "pysrc", "marshal.cpp")
-MARSHAL = os.path.join(BUILD, "_marshal.so")
+
+
+def _marshal_name() -> str:
+    """Of the module for this torch and this Python, whose binary interfaces it holds."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "none"
+    return f"_marshal-torch{version}{sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+MARSHAL = os.path.join(BUILD, _marshal_name())
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -66,8 +79,6 @@ def build_marshal(force: bool = False) -> str:
     """Compile the binding's extension module against the installed torch; returns its path."""
     if not force and marshal_up_to_date():
         return MARSHAL
-    import sysconfig
-
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     os.makedirs(BUILD, exist_ok=True)

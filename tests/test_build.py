@@ -35,3 +35,25 @@ def test_the_operators_say_what_is_missing(no_module):
 def test_the_library_is_built_without_the_module(no_module):
     with pytest.warns(UserWarning, match="no headers"):
         assert build.build() == build.LIB
+
+
+def test_another_torch_or_python_has_a_module_of_its_own(monkeypatch):
+    """The module holds one torch's and one interpreter's binary interface: after a
+    change of either the one built before is not taken for current."""
+    import importlib.metadata
+    import importlib.util
+    import sysconfig
+
+    def path_under(torch_version, suffix):
+        with monkeypatch.context() as m:
+            version, var = importlib.metadata.version, sysconfig.get_config_var
+            m.setattr(importlib.metadata, "version", lambda n: torch_version if n == "torch" else version(n))
+            m.setattr(sysconfig, "get_config_var", lambda n: suffix if n == "EXT_SUFFIX" else var(n))
+            spec = importlib.util.spec_from_file_location("build_again", build.__file__)
+            again = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(again)
+            return again.MARSHAL
+    here = sysconfig.get_config_var("EXT_SUFFIX")
+    assert path_under(importlib.metadata.version("torch"), here) == build.MARSHAL
+    paths = {build.MARSHAL, path_under("1.0+cu0", here), path_under("1.0+cu0", ".cpython-39-x.so")}
+    assert len(paths) == 3
