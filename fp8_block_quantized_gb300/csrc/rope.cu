@@ -393,6 +393,11 @@ bool rope_sizes_ok(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int 
 
 bool ld_ok(int64_t ld, int64_t H, int64_t D) { return ld >= H * D && ld < ((int64_t)1 << 40); }
 
+// In place with another stride, a token would be written before it is read.
+bool in_place_ok(const uint16_t *in, int64_t ld, const uint16_t *out, int64_t ldo, int64_t T) {
+    return in != out || ld == ldo || T <= 1;
+}
+
 template <int kBytes>
 bool aligned_to(const void *p) { return (reinterpret_cast<uintptr_t>(p) & (kBytes - 1)) == 0; }
 
@@ -407,8 +412,10 @@ jet_status jet_rope(const uint16_t *q, int64_t ldq, int64_t Hq, const uint16_t *
     JET_REQUIRE((!hasq || (q && qo)) && (!hask || (k && ko)), JET_ERR_NULL);
     JET_REQUIRE((!hasq && !hask) || (pos && (R <= 0 || inv_freq)), JET_ERR_NULL);
     JET_REQUIRE(rope_sizes_ok(T, Hq, Hk, D, R, layout), JET_ERR_SHAPE);
-    JET_REQUIRE(!hasq || (ld_ok(ldq, Hq, D) && ld_ok(ldqo, Hq, D)), JET_ERR_SHAPE);
-    JET_REQUIRE(!hask || (ld_ok(ldk, Hk, D) && ld_ok(ldko, Hk, D)), JET_ERR_SHAPE);
+    JET_REQUIRE(!hasq || (ld_ok(ldq, Hq, D) && ld_ok(ldqo, Hq, D) && in_place_ok(q, ldq, qo, ldqo, T)),
+                JET_ERR_SHAPE);
+    JET_REQUIRE(!hask || (ld_ok(ldk, Hk, D) && ld_ok(ldko, Hk, D) && in_place_ok(k, ldk, ko, ldko, T)),
+                JET_ERR_SHAPE);
     JET_REQUIRE(!hasq || (ldq % 8 == 0 && ldqo % 8 == 0 && jet::aligned16(q) && jet::aligned16(qo)),
                 JET_ERR_ALIGN);
     JET_REQUIRE(!hask || (ldk % 8 == 0 && ldko % 8 == 0 && jet::aligned16(k) && jet::aligned16(ko)),
@@ -455,7 +462,8 @@ jet_status jet_rope_kv_cache_write(const uint16_t *q, int64_t ldq, int64_t Hq, c
     JET_REQUIRE((!hasq && !hask) || (pos && (R <= 0 || inv_freq)), JET_ERR_NULL);
     JET_REQUIRE(rope_sizes_ok(T, Hq, Hk, D, R, layout) && D % 16 == 0 && S < ((int64_t)1 << 40),
                 JET_ERR_SHAPE);
-    JET_REQUIRE(!hasq || (ld_ok(ldq, Hq, D) && ld_ok(ldqo, Hq, D)), JET_ERR_SHAPE);
+    JET_REQUIRE(!hasq || (ld_ok(ldq, Hq, D) && ld_ok(ldqo, Hq, D) && in_place_ok(q, ldq, qo, ldqo, T)),
+                JET_ERR_SHAPE);
     JET_REQUIRE(!hask || (ld_ok(ldk, Hk, D) && ld_ok(ldv, Hk, D)), JET_ERR_SHAPE);
     JET_REQUIRE(!hasq || (ldq % 8 == 0 && ldqo % 8 == 0 && jet::aligned16(q) && jet::aligned16(qo)),
                 JET_ERR_ALIGN);

@@ -543,8 +543,8 @@ JET_API jet_status jet_rope_inv_freq(int64_t R, double base, int scaling, double
  * may be any int64; products in binary32, one rounding to BF16.
  *   q: token t, head h at q + t*ldq + h*D (BF16 bits), h < Hq; k likewise
  *       with ldk, Hk.  qo, ko: outputs, strides ldqo, ldko; they may be q and
- *       k themselves with the same strides (in place).  A tensor with no head
- *       may be NULL.
+ *       k themselves with the same strides (in place; with others of more than
+ *       one token JET_ERR_SHAPE).  A tensor with no head may be NULL.
  *   inv_freq [R/2] FP64, pos [T] int64: DEVICE arrays.
  * T, Hq, Hk >= 0, at most 1024 heads each; D a multiple of 8, at most 1024;
  * R even, 0 <= R <= D; strides >= H*D and multiples of 8.
