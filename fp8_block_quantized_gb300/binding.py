@@ -66,6 +66,7 @@ SIGNATURES = {
                                 P, I, P, P, I, P],
     "jet_kv_slot_map": [P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P],
     "jet_sample": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
+    "jet_sample_unaligned": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
     "jet_workspace_bytes": [ctypes.c_int, I, I, I],
     "jet_device_status": [P, ctypes.POINTER(ctypes.c_uint32)],
     "jet_selftest_bounded_wait": [ctypes.c_uint32, P],
@@ -108,7 +109,8 @@ def load(build_if_missing: bool = True):
 
 # The C functions the compiled module calls, in the order it takes them.
 MARSHALLED = ("jet_add_rmsnorm_quant_1x128", "jet_add_rmsnorm_bwd", "jet_rope",
-              "jet_rope_kv_cache_write", "jet_kv_slot_map", "jet_sample", "jet_workspace_bytes")
+              "jet_rope_kv_cache_write", "jet_kv_slot_map", "jet_sample_unaligned",
+              "jet_workspace_bytes")
 
 
 def _compiled():
@@ -749,8 +751,8 @@ def kv_slot_map(cached, added, block_size, table, free_blocks, free_next, capaci
 
 def jet_sample(logits, u, temperature, top_k, top_p, min_p, token, logp, logp_all, kept,
                stream=None):
-    """One token per row of logits [B, V] (BF16 or FP32, rows may be strided)
-    from the uniform numbers u [B]; the settings are per row, or None."""
+    """One token per row of logits [B, V] (BF16 or FP32, rows may be strided and
+    start at any element) from the uniform numbers u [B]; the settings are per row, or None."""
     (_marshal or _compiled()).sample(logits, u, temperature, top_k, top_p, min_p, token, logp,
                                      logp_all, kept, stream)
 

@@ -1232,18 +1232,16 @@ constexpr size_t kOne = 227 * 1024, kHalf = 113 * 1024;
 template <int kBytes>
 bool aligned_to(const void *p) { return (reinterpret_cast<uintptr_t>(p) & (kBytes - 1)) == 0; }
 
-}  // namespace
-
-jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64_t ld,
-                      const float *u, const float *temperature, const int32_t *top_k,
-                      const float *top_p, const float *min_p, int64_t *token, float *logp,
-                      float *logp_all, int32_t *kept, jet_stream_t stream) {
+jet_status sample(const void *logits, bool logits_aligned, int dtype, int64_t B, int64_t V,
+                  int64_t ld, const float *u, const float *temperature, const int32_t *top_k,
+                  const float *top_p, const float *min_p, int64_t *token, float *logp,
+                  float *logp_all, int32_t *kept, jet_stream_t stream) {
     JET_REQUIRE(B >= 0 && V >= 0, JET_ERR_SHAPE);
     JET_REQUIRE(B == 0 || (logits && u && token && logp && logp_all && kept), JET_ERR_NULL);
     JET_REQUIRE((B == 0 || V >= 1) && V <= kSaMaxV && B < ((int64_t)1 << 28) && ld >= V &&
                     ld < ((int64_t)1 << 40) && (dtype == JET_BF16 || dtype == JET_FP32),
                 JET_ERR_SHAPE);
-    JET_REQUIRE(jet::aligned16(logits) && aligned_to<4>(u) && aligned_to<4>(temperature) &&
+    JET_REQUIRE(logits_aligned && aligned_to<4>(u) && aligned_to<4>(temperature) &&
                     aligned_to<4>(top_k) && aligned_to<4>(top_p) && aligned_to<4>(min_p) &&
                     aligned_to<8>(token) && aligned_to<4>(logp) && aligned_to<4>(logp_all) &&
                     aligned_to<4>(kept),
@@ -1362,4 +1360,23 @@ jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64
         return JET_ERR_CUDA;
     }
     return jet::launch_status();
+}
+
+}  // namespace
+
+jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t V, int64_t ld,
+                      const float *u, const float *temperature, const int32_t *top_k,
+                      const float *top_p, const float *min_p, int64_t *token, float *logp,
+                      float *logp_all, int32_t *kept, jet_stream_t stream) {
+    return sample(logits, jet::aligned16(logits), dtype, B, V, ld, u, temperature, top_k, top_p,
+                  min_p, token, logp, logp_all, kept, stream);
+}
+
+jet_status jet_sample_unaligned(const void *logits, int dtype, int64_t B, int64_t V, int64_t ld,
+                                const float *u, const float *temperature, const int32_t *top_k,
+                                const float *top_p, const float *min_p, int64_t *token,
+                                float *logp, float *logp_all, int32_t *kept, jet_stream_t stream) {
+    const bool aligned = dtype == JET_FP32 ? aligned_to<4>(logits) : aligned_to<2>(logits);
+    return sample(logits, aligned, dtype, B, V, ld, u, temperature, top_k, top_p, min_p, token,
+                  logp, logp_all, kept, stream);
 }

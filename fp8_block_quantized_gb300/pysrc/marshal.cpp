@@ -24,7 +24,7 @@ decltype(&jet_add_rmsnorm_bwd) f_norm_bwd;
 decltype(&jet_rope) f_rope;
 decltype(&jet_rope_kv_cache_write) f_rope_kv;
 decltype(&jet_kv_slot_map) f_slots;
-decltype(&jet_sample) f_sample;
+decltype(&jet_sample_unaligned) f_sample;
 decltype(&jet_workspace_bytes) f_workspace;
 PyObject *jet_error;
 

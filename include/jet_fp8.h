@@ -621,7 +621,8 @@ JET_API jet_status jet_kv_slot_map(const int32_t *cached, const int32_t *added, 
  * the batch or the launch.
  *   logits: row b at logits + b*ld elements, BF16 or FP32 by `dtype`
  *       (jet_dtype).  -inf and NaN are never drawn; +inf counts as the type's
- *       largest finite number.  ld >= V; rows need no alignment.
+ *       largest finite number.  ld >= V; rows after the first need no
+ *       alignment.
  *   u [B] FP32 in [0, 1) (others are brought to the nearest end).
  *   temperature, top_p, min_p [B] FP32, top_k [B] int32: one per row, or NULL:
  *       1, 1, 0, off.  temperature <= 0: the largest logit (lowest index);
@@ -638,6 +639,18 @@ JET_API jet_status jet_sample(const void *logits, int dtype, int64_t B, int64_t 
                               const float *u, const float *temperature, const int32_t *top_k,
                               const float *top_p, const float *min_p, int64_t *token, float *logp,
                               float *logp_all, int32_t *kept, jet_stream_t stream);
+
+/*
+ * The same for logits that start at any element of their type, as the later
+ * rows of a batch with an odd vocabulary do.  The results are the same bits; a
+ * row's first and last elements up to a 16-byte boundary are read one by one,
+ * in either call.
+ */
+JET_API jet_status jet_sample_unaligned(const void *logits, int dtype, int64_t B, int64_t V,
+                                        int64_t ld, const float *u, const float *temperature,
+                                        const int32_t *top_k, const float *top_p,
+                                        const float *min_p, int64_t *token, float *logp,
+                                        float *logp_all, int32_t *kept, jet_stream_t stream);
 
 /*
  * Workspace bytes an operation needs for the given sizes (0 if none).
