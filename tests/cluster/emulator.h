@@ -197,6 +197,8 @@ static int launch(void (*kernel)(const void *), const void *args, unsigned C, un
 using std::max;
 using std::min;
 
+inline void __cluster_barrier_arrive_relaxed() { emu::cluster_arrive(); }
+
 namespace cooperative_groups {
 struct cluster_group {
     void barrier_arrive() const { emu::cluster_arrive(); }
