@@ -86,10 +86,17 @@ T *arg(PyObject *o, const char *name, at::ScalarType type, std::initializer_list
     return static_cast<T *>(address(t));
 }
 
+void need_dims(const at::Tensor &t, int64_t n, const char *name) {
+    if (t.dim() == n) return;
+    PyErr_Format(PyExc_ValueError, "%s: expected %s dimensions, got %lld", name, n == 2 ? "two" : "three",
+                 (long long)t.dim());
+    throw Raised();
+}
+
 // A tensor of two dimensions; its sizes.
 std::pair<int64_t, int64_t> matrix(PyObject *o, const char *name) {
     const at::Tensor &t = tensor(o, name);
-    if (t.dim() != 2) raise(PyExc_ValueError, "%s: expected two dimensions, got %R", name, o);
+    need_dims(t, 2, name);
     return {t.size(0), t.size(1)};
 }
 
@@ -220,7 +227,7 @@ void norm_bwd(PyObject *const *a) {  // h, g, rstd, dys (a tuple), dres, dx, dg,
 void rope(PyObject *const *a) {  // q, k, inv_freq, pos, q_out, k_out, layout, mscale, backward, stream
     const char *first = a[0] != Py_None ? "q" : "k";
     const at::Tensor &t = tensor(a[0] != Py_None ? a[0] : a[1], first);
-    if (t.dim() != 3) raise(PyExc_ValueError, "%s: expected three dimensions, got %R", first, a[0]);
+    need_dims(t, 3, first);
     const int64_t T = t.size(0), D = t.size(2), R = 2 * numel(a[2], "inv_freq");
     const Heads q = heads(a[0], "q", T, D), k = heads(a[1], "k", T, D);
     const Heads qo = heads(a[4], "q_out", T, D), ko = heads(a[5], "k_out", T, D);
@@ -242,7 +249,7 @@ void rope(PyObject *const *a) {  // q, k, inv_freq, pos, q_out, k_out, layout, m
 void rope_kv(PyObject *const *a) {  // q, k, v, inv_freq, pos, k_scale, v_scale, slots, q_out,
                                     // k_cache, v_cache, layout, mscale, stream
     const at::Tensor &t = tensor(a[0], "q");
-    if (t.dim() != 3) raise(PyExc_ValueError, "%s: expected three dimensions, got %R", "q", a[0]);
+    need_dims(t, 3, "q");
     const int64_t T = t.size(0), D = t.size(2), R = 2 * numel(a[3], "inv_freq");
     const Heads q = heads(a[0], "q", T, D), k = heads(a[1], "k", T, D), v = heads(a[2], "v", T, D);
     const Heads qo = heads(a[8], "q_out", T, D);
