@@ -31,10 +31,11 @@
 // step; a step with too many of them is split again on the bits of the logits,
 // and one of equal logits by counting.
 //
-// Without a filter, 256 rows of 128256 binary32 logits take 44 us (2.99 TB/s, 44%
-// of a copy's rate): 26 instructions a logit in two passes with a barrier behind
-// each.  With them, few rows are bound by those barriers and the passes over
-// shared memory (16 such rows in BF16: 13 us where lists suffice, 30 otherwise).
+// Without a filter, 256 rows of 128256 binary32 logits take 44.3 us (2.96 TB/s,
+// 44% of a copy's rate), in BF16 38.3: 26 instructions a logit in two passes with
+// a barrier behind each.  With them, few rows are bound by those barriers and the
+// passes over shared memory (15 such rows in BF16, one wave of clusters: 13 us
+// where short lists suffice, 19 with long ones, 28 for flat nuclei).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -404,7 +405,7 @@ struct Sampler {
         const int end = min(c1, past);
         const uint4 *p = reinterpret_cast<const uint4 *>(x - shift) + c;
         float v[E];
-        constexpr int kN = 32 / E;  // loads ahead: 256 x 128256 binary32 take 43.4 us with 8, 46.7 with 4
+        constexpr int kN = 32 / E;  // loads ahead: 256 x 128256 binary32 take 44.2 us with 8, 46.1 with 4
         for (; c + 32 * (kN - 1) < end; c += 32 * kN, p += 32 * kN) {
             uint4 t[kN];
 #pragma unroll
@@ -1118,7 +1119,7 @@ struct Sampler {
                 }
                 const bool everything = finite <= kListMax;
                 // the maxima in whole groups above z_lo: so many tokens at least (a
-                // flat nucleus in each of 16 rows: 54 us, 56 with the vain gather)
+                // flat nucleus in each of 16 rows: 47 us, 52 with the vain gather)
                 const int above = (int)(fmaxf(z_lo, -32.0f) * -kGroupsPerZ);
                 unsigned sure = 0;
 #pragma unroll
@@ -1290,15 +1291,15 @@ jet_status sample(const void *logits, bool logits_aligned, int dtype, int64_t B,
         // Few rows: the largest cluster with which they run in about one wave,
         // an SM a CTA.  The SMs' groups hold 15 clusters of 8 (and 15 of 7), 23
         // of 6, 28 of 5, 36 of 4 (128256 BF16 logits, us, mixed filters / flat
-        // nuclei / top-k: 16 rows 32 / 53 / 25 with 8, 38 / 37 / 27 with 6; 20
-        // rows 38 / 37 / 27 with 6, 33 / 56 / 34 with 8; 32 rows 47 / 46 / 29
-        // with 4, 48 / 78 / 40 with 8).  More rows: two CTAs an SM of half the
-        // registers, again in about one wave while that can be (64 rows 63 / 74
-        // / 44, one CTA an SM 67 / 87 / 47; 256 rows 144 / 231 / 116 and 179 /
-        // 311 / 141), else as few CTAs a row as its slices allow (300 rows of
-        // 32000 binary32 93 / 91 / 78 with 2, 94 / 131 / 89 with 4).  Where
+        // nuclei / top-k: 16 rows 30 / 47 / 23 with 8, 36 / 34 / 21 with 6; 20
+        // rows 36 / 34 / 21 with 6, 30 / 50 / 28 with 8; 32 rows 43 / 42 / 23
+        // with 4, 42 / 71 / 33 with 8).  More rows: two CTAs an SM of half the
+        // registers, again in about one wave while that can be (64 rows 58 / 67
+        // / 35, one CTA an SM 62 / 79 / 39; 256 rows 132 / 207 / 100 and 167 /
+        // 281 / 125), else as few CTAs a row as its slices allow (300 rows of
+        // 32000 binary32 82 / 80 / 65 with 2, 82 / 117 / 74 with 4).  Where
         // slices are too long for two an SM: as few as one CTA can hold (128
-        // rows of 151937 binary32 127 / 195 / 90 with 4, 153 / 272 / 120 with 8).
+        // rows of 151937 binary32 119 / 178 / 81 with 4, 146 / 246 / 111 with 8).
         const int longest = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxCluster, chunks / 256));
         const int64_t wave = sms * 12 / 13;
         auto fits = [&](int c, size_t room) { return c != 7 && filter_smem(c, chunks) <= room; };

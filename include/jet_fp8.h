@@ -28,8 +28,8 @@
  *    the first violation without launching anything: JET_ERR_NULL,
  *    JET_ERR_SHAPE, JET_ERR_ALIGN (every pointer must be 16-byte aligned, but
  *    for the arrays of one value per token, row, request or head of
- *    jet_add_rmsnorm_*, jet_rope*, jet_kv_slot_map and jet_sample, which need
- *    their type's alignment),
+ *    jet_add_rmsnorm_*, jet_rope*, jet_kv_slot_map and jet_sample*, and the
+ *    logits of jet_sample_unaligned, which need their type's alignment),
  *    JET_ERR_WORKSPACE, JET_ERR_DEVICE (current device must be sm_103).
  *    A pointer may be NULL only when its tensor is empty.
  *  - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL is the
