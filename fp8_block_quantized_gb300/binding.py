@@ -6,7 +6,7 @@ current CUDA stream to the C entry point of the same name.  All quantization,
 GEMM and reduction work happens in the library's kernels.  There is no CPU
 fallback: if the library is missing or fails to load, ``load()`` raises.  The
 operators that a decoding step calls many times (residual norms, rotary
-positions, slot maps, sampling) are marshalled by a compiled module,
+positions, slot maps, attention, sampling) are marshalled by a compiled module,
 ``pysrc/marshal.cpp``, with the same checks.
 """
 from __future__ import annotations
@@ -30,7 +30,7 @@ OP = {"quant_act_1x128": 0, "quant_w_128x128": 1, "requant_128x1": 2,
       "swiglu_quant_1x128": 9, "kv_calibrate": 10, "kv_cache_write": 11,
       "token_mismatch_per_sequence": 12, "rmsnorm_quant_1x128": 13,
       "add_rmsnorm_quant_1x128": 14, "add_rmsnorm_bwd": 15, "rope": 16,
-      "rope_kv_cache_write": 17, "kv_slot_map": 18, "sample": 19}
+      "rope_kv_cache_write": 17, "kv_slot_map": 18, "sample": 19, "kv_attention": 20}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "wavelength": 2, "ramp": 3}
 
@@ -67,6 +67,9 @@ SIGNATURES = {
     "jet_kv_slot_map": [P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P],
     "jet_sample": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
     "jet_sample_unaligned": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
+    "jet_kv_attention": [P, I, I, I, I, I, P, P, I, P, P, P, I, I, P, P, I, P, P, I, F, P, I, P, P, Z,
+                         P],
+    "jet_kv_attention_workspace": [I, I, I, I, I, I],
     "jet_workspace_bytes": [ctypes.c_int, I, I, I],
     "jet_device_status": [P, ctypes.POINTER(ctypes.c_uint32)],
     "jet_selftest_bounded_wait": [ctypes.c_uint32, P],
@@ -74,7 +77,7 @@ SIGNATURES = {
     "jet_selftest_quotient": [P, P, I, P, P],
 }
 _RESTYPE = {"jet_status_str": ctypes.c_char_p, "jet_version": ctypes.c_int,
-            "jet_workspace_bytes": ctypes.c_size_t}
+            "jet_workspace_bytes": ctypes.c_size_t, "jet_kv_attention_workspace": ctypes.c_size_t}
 
 
 class JetError(RuntimeError):
@@ -110,7 +113,7 @@ def load(build_if_missing: bool = True):
 # The C functions the compiled module calls, in the order it takes them.
 MARSHALLED = ("jet_add_rmsnorm_quant_1x128", "jet_add_rmsnorm_bwd", "jet_rope",
               "jet_rope_kv_cache_write", "jet_kv_slot_map", "jet_sample_unaligned",
-              "jet_workspace_bytes")
+              "jet_workspace_bytes", "jet_kv_attention", "jet_kv_attention_workspace")
 
 
 def _compiled():
@@ -768,3 +771,41 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stre
         kept = torch.empty((B,), dtype=torch.int32, device=dev)
     jet_sample(logits, u, temperature, top_k, top_p, min_p, token, logp, logp_all, kept, stream)
     return token, logp, logp_all, kept
+
+
+# --------------------------------------------------------------------------
+# Attention over the paged cache
+# --------------------------------------------------------------------------
+
+def jet_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, block_size, offsets, lengths, out,
+                     lse=None, prefix_offsets=None, prefix_lengths=None, scale=None, ws=None,
+                     stream=None):
+    """Causal attention of the new tokens q [T, Hq, D] of B requests over the
+    cache rows [S, Hk, D] behind their table rows, into out [T, Hq, D] and lse
+    [T, Hq]; scale is D^-0.5 unless given.  The requests of group i
+    (prefix_offsets[i] .. prefix_offsets[i+1]-1) share their first
+    prefix_lengths[i] keys, which are read once; see the C header."""
+    m = _marshal or _compiled()
+    if ws is None and stream is not None:    # else the current stream's, by the compiled part
+        import torch
+        T, Hq, D = q.shape
+        need = load().jet_kv_attention_workspace(
+            T, Hq, k_cache.shape[1], D, lengths.numel(),
+            0 if prefix_lengths is None else prefix_lengths.numel())
+        with _allocating_on(stream):
+            ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    m.kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, block_size, offsets, lengths, out, lse,
+                   prefix_offsets, prefix_lengths, scale, ws, stream)
+
+
+def kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, block_size, offsets, lengths,
+                 prefix_offsets=None, prefix_lengths=None, scale=None, with_lse=False, stream=None):
+    """out [T, Hq, D], or (out, lse [T, Hq]), of jet_kv_attention; rows of no
+    request are zeros (lse -inf)."""
+    import torch
+    with _allocating_on(stream):
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.full(q.shape[:2], float("-inf"), device=q.device) if with_lse else None
+    jet_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, block_size, offsets, lengths, out, lse,
+                     prefix_offsets, prefix_lengths, scale, None, stream)
+    return (out, lse) if with_lse else out

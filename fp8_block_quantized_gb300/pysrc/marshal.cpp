@@ -10,9 +10,11 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 
 #include "jet_fp8.h"
@@ -26,6 +28,8 @@ decltype(&jet_rope_kv_cache_write) f_rope_kv;
 decltype(&jet_kv_slot_map) f_slots;
 decltype(&jet_sample_unaligned) f_sample;
 decltype(&jet_workspace_bytes) f_workspace;
+decltype(&jet_kv_attention) f_attention;
+decltype(&jet_kv_attention_workspace) f_attention_workspace;
 PyObject *jet_error;
 
 // Thrown once a Python exception is set.
@@ -329,6 +333,61 @@ void sample(PyObject *const *a) {  // logits, u, temperature, top_k, top_p, min_
     });
 }
 
+void attention(PyObject *const *a) {  // q, k_cache, v_cache, k_scale, v_scale, table, block_size,
+                                      // offsets, lengths, out, lse, prefix_offsets,
+                                      // prefix_lengths, scale, ws, stream
+    const at::Tensor &t = tensor(a[0], "q"), &cache = tensor(a[1], "k_cache");
+    need_dims(t, 3, "q");
+    need_dims(cache, 3, "k_cache");
+    const int64_t T = t.size(0), D = t.size(2), S = cache.size(0), Hk = cache.size(1);
+    const Heads q = heads(a[0], "q", T, D), out = heads(a[9], "out", T, D);
+    if (out.H != q.H) {
+        PyErr_SetString(PyExc_ValueError, "out must have the heads of q");
+        throw Raised();
+    }
+    for (int i = 0; i < 13; ++i)
+        if (i != 6 && a[i] != Py_None) {
+            const at::Tensor &x = tensor(a[i], "argument");
+            if (x.numel() && x.is_cuda() && x.get_device() != c10::cuda::current_device()) {
+                PyErr_SetString(PyExc_ValueError, "the tensors must be on the current device");
+                throw Raised();
+            }
+        }
+    const auto *kc = arg<uint8_t>(a[1], "k_cache", at::kByte, {S, Hk, D});
+    const auto *vc = arg<uint8_t>(a[2], "v_cache", at::kByte, {S, Hk, D});
+    const auto *ks = arg<float>(a[3], "k_scale", at::kFloat, {Hk});
+    const auto *vs = arg<float>(a[4], "v_scale", at::kFloat, {Hk});
+    const int64_t B = numel(a[8], "lengths"), width = matrix(a[5], "table").second;
+    const auto *table = arg<int32_t>(a[5], "table", at::kInt, {B, width});
+    const int64_t block_size = integer(a[6]);
+    const auto *offsets = arg<int64_t>(a[7], "offsets", at::kLong, {B + 1});
+    const auto *lengths = arg<int32_t>(a[8], "lengths", at::kInt, {B});
+    auto *lse = arg<float>(a[10], "lse", at::kFloat, {T, q.H});
+    const int64_t Ng = a[12] == Py_None ? 0 : numel(a[12], "prefix_lengths");
+    if ((a[11] == Py_None) != (a[12] == Py_None)) {
+        PyErr_SetString(PyExc_ValueError, "prefix_offsets and prefix_lengths come together");
+        throw Raised();
+    }
+    const auto *po = arg<int64_t>(a[11], "prefix_offsets", at::kLong, {Ng + 1});
+    const auto *pl = arg<int32_t>(a[12], "prefix_lengths", at::kInt, {Ng});
+    const float scale = a[13] == Py_None ? 1.0f / std::sqrt((float)(D > 0 ? D : 1)) : (float)number(a[13]);
+    at::Tensor ws;  // given, or allocated on the current stream
+    if (a[14] == Py_None) {
+        const size_t need = f_attention_workspace(T, q.H, Hk, D, B, Ng);
+        if (need) ws = at::empty({(int64_t)need}, t.options().dtype(at::kByte));
+    } else {
+        ws = tensor(a[14], "ws");
+        arg<void>(a[14], "ws", ws.scalar_type(), {ws.numel()});
+    }
+    void *room = ws.defined() ? address(ws) : nullptr, *stream = stream_of(a[15]);
+    const size_t bytes = ws.defined() ? ws.nbytes() : 0;
+    call("jet_kv_attention", [&] {
+        return f_attention(q.p, q.ld, T, q.H, Hk, D, kc, vc, S, ks, vs, table, width, block_size,
+                           offsets, lengths, B, po, pl, Ng, scale, out.p, out.ld, lse, room, bytes,
+                           stream);
+    });
+}
+
 // ------------------------------------------------------------------ the module
 
 template <void (*F)(PyObject *const *), int kArgs>
@@ -349,14 +408,14 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-// bind(JetError, the addresses of the seven C functions in the order above)
+// bind(JetError, the addresses of the nine C functions in the order above)
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "bind: expected the error class and seven addresses");
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "bind: expected the error class and nine addresses");
         return nullptr;
     }
-    void *p[7];
-    for (int i = 0; i < 7; ++i) {
+    void *p[9];
+    for (int i = 0; i < 9; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i + 1]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -367,6 +426,8 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     f_slots = reinterpret_cast<decltype(f_slots)>(p[4]);
     f_sample = reinterpret_cast<decltype(f_sample)>(p[5]);
     f_workspace = reinterpret_cast<decltype(f_workspace)>(p[6]);
+    f_attention = reinterpret_cast<decltype(f_attention)>(p[7]);
+    f_attention_workspace = reinterpret_cast<decltype(f_attention_workspace)>(p[8]);
     Py_XSETREF(jet_error, Py_NewRef(args[0]));
     Py_RETURN_NONE;
 }
@@ -378,6 +439,7 @@ PyMethodDef methods[] = {ENTRY("add_rmsnorm_quant_1x128", norm, 9),
                          ENTRY("rope_kv_cache_write", rope_kv, 14),
                          ENTRY("kv_slot_map", slots, 12),
                          ENTRY("sample", sample, 11),
+                         ENTRY("kv_attention", attention, 16),
                          {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,

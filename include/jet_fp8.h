@@ -28,8 +28,8 @@
  *    the first violation without launching anything: JET_ERR_NULL,
  *    JET_ERR_SHAPE, JET_ERR_ALIGN (every pointer must be 16-byte aligned, but
  *    for the arrays of one value per token, row, request or head of
- *    jet_add_rmsnorm_*, jet_rope*, jet_kv_slot_map and jet_sample*, and the
- *    logits of jet_sample_unaligned, which need their type's alignment),
+ *    jet_add_rmsnorm_*, jet_rope*, jet_kv_slot_map, jet_sample* and
+ *    jet_kv_attention, and the logits of jet_sample_unaligned, which need their type's alignment),
  *    JET_ERR_WORKSPACE, JET_ERR_DEVICE (current device must be sm_103).
  *    A pointer may be NULL only when its tensor is empty.
  *  - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL is the
@@ -90,7 +90,8 @@ typedef enum {
     JET_OP_ROPE = 16,
     JET_OP_ROPE_KV_CACHE_WRITE = 17,
     JET_OP_KV_SLOT_MAP = 18,
-    JET_OP_SAMPLE = 19
+    JET_OP_SAMPLE = 19,
+    JET_OP_KV_ATTENTION = 20 /* its workspace: jet_kv_attention_workspace() */
 } jet_op;
 
 /* Pair layouts of jet_rope: (i, i + R/2) or (2 i, 2 i + 1). */
@@ -651,6 +652,57 @@ JET_API jet_status jet_sample_unaligned(const void *logits, int dtype, int64_t B
                                         const int32_t *top_k, const float *top_p,
                                         const float *min_p, int64_t *token, float *logp,
                                         float *logp_all, int32_t *kept, jet_stream_t stream);
+
+/*
+ * Attention of a step's new tokens over the paged FP8 cache, grouped-query and
+ * causal; for decoding (one token a request), chunks of a prompt (any number),
+ * and groups of requests that share a prefix, whose keys are then read once for
+ * all of them.  Request b holds lengths[b] keys behind its row of the block
+ * table, its own new ones among them (jet_rope_kv_cache_write comes first); its
+ * new tokens are rows offsets[b] .. offsets[b+1]-1 of q, the last of them at
+ * position lengths[b]-1.  For the query at position pos, head hq of KV head
+ * h = hq / (Hq / Hk), over the keys p <= pos:
+ *   x_p = scale k_scale[h] (q . k_p),  lse = ln sum_p e^x_p,
+ *   out = v_scale[h] sum_p e^(x_p - lse) v_p,
+ * k_p, v_p the codes in slot table[b][p / block_size] * block_size +
+ * p % block_size.  A key without a slot (a negative table entry, a slot >= S, a
+ * position past the table's width) is left out; a query that sees no key gets
+ * out 0 and lse -inf.  Products of the queries with the codes are exact to 2^-38
+ * of the query's largest channel, sums in binary32, weights rounded to 11 bits,
+ * one rounding to BF16; the result is the same for the same call, whatever ran
+ * before.
+ * Groups: group i is the requests prefix_offsets[i] .. prefix_offsets[i+1]-1,
+ * whose first prefix_lengths[i] keys are the same; they are read through the
+ * table row of the group's first request (a longer prefix than that one's
+ * length counts as that length), whatever the other rows hold there.  Requests
+ * before prefix_offsets[0] or from prefix_offsets[n_prefix] on are in no group.
+ *   q: token t, head hq at q + t*ldq + hq*D (BF16 bits); out likewise with ldo.
+ *       Tokens outside [offsets[0], offsets[B]) are not written.
+ *   k_cache, v_cache [S][Hk][D] E4M3 codes; k_scale, v_scale [Hk] FP32.
+ *   table [B][width] int32, offsets [B+1] int64 (non-decreasing), lengths [B]
+ *       int32 (jet_kv_slot_map's cached + added): DEVICE arrays.
+ *   prefix_offsets [n_prefix+1] int64 (non-decreasing), prefix_lengths
+ *       [n_prefix] int32: DEVICE arrays, or NULL with n_prefix = 0.
+ *   lse [T][Hq] FP32 (out), or NULL.
+ *   ws / ws_bytes: at least jet_kv_attention_workspace() bytes of device
+ *       memory; scratch, not initialised.
+ * 0 <= T < 2^24; Hq <= 1024, a multiple of Hk; D = 64, 128 or 256; B <= 8192;
+ * n_prefix <= B; S, width < 2^31; 1 <= block_size < 2^30; scale > 0; strides
+ * >= Hq*D and multiples of 8.
+ */
+JET_API jet_status jet_kv_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t Hq,
+                                    int64_t Hk, int64_t D, const uint8_t *k_cache,
+                                    const uint8_t *v_cache, int64_t S, const float *k_scale,
+                                    const float *v_scale, const int32_t *table, int64_t width,
+                                    int64_t block_size, const int64_t *offsets,
+                                    const int32_t *lengths, int64_t B,
+                                    const int64_t *prefix_offsets, const int32_t *prefix_lengths,
+                                    int64_t n_prefix, float scale, uint16_t *out, int64_t ldo,
+                                    float *lse, void *ws, size_t ws_bytes, jet_stream_t stream);
+
+/* Workspace bytes of jet_kv_attention (0 for sizes it refuses).  Host function. */
+JET_API size_t jet_kv_attention_workspace(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
+                                          int64_t n_prefix);
 
 /*
  * Workspace bytes an operation needs for the given sizes (0 if none).

@@ -1,0 +1,59 @@
+"""Host-side argument checks of the attention over the paged cache, the head's
+log-probabilities and the gated activation's backward; CPU only."""
+import ctypes
+
+import pytest
+
+from fp8_block_quantized_gb300 import binding
+
+OK, NULL, SHAPE, ALIGN, CUDA, DEVICE, WORKSPACE, TIMEOUT = range(8)
+P = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(16)]   # aligned, never dereferenced
+MIS = ctypes.c_void_p(0x10008)
+ODD = ctypes.c_void_p(0x10002)       # below any 4- or 8-byte type's alignment
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.load()
+
+
+def swap(args, **kw):
+    """args with the entries named _i replaced."""
+    out = list(args)
+    for k, v in kw.items():
+        out[int(k[1:])] = v
+    return out
+
+
+def test_kv_attention(lib):
+    f = lib.jet_kv_attention
+    need = lib.jet_kv_attention_workspace(10, 8, 2, 128, 4, 2)
+    assert need > 0
+    #     q     ldq  T  Hq Hk  D    kc    vc   S    ks    vs   table width bs off lens B  po    pl   Ng
+    ok = [P[0], 1024, 10, 8, 2, 128, P[1], P[2], 640, P[3], P[4], P[5], 7, 16, P[6], P[7], 4, P[8], P[9], 2,
+          0.1, P[10], 1024, P[11], P[12], need, None]
+    for i in (0, 6, 7, 9, 10, 11, 14, 15, 17, 18, 21):
+        assert f(*swap(ok, **{f"_{i}": None})) == NULL, i
+        assert f(*swap(ok, **{f"_{i}": ODD})) == ALIGN, i
+    for i in (0, 6, 7, 21, 24):
+        assert f(*swap(ok, **{f"_{i}": MIS})) == ALIGN, i
+    assert f(*swap(ok, _23=ODD)) == ALIGN
+    for i, v in ((1, 1016), (22, 1016), (2, -1), (2, 1 << 24), (3, 7), (3, 1026), (3, -8), (4, 0), (4, 3),
+                 (5, 80), (5, 0), (5, 512), (8, -1), (8, 1 << 31), (12, -1), (12, 1 << 31), (13, 0),
+                 (13, 1 << 30), (16, -1), (16, 8193), (19, -1), (19, 5), (20, 0.0), (20, -1.0),
+                 (20, float("inf")), (20, float("nan"))):
+        assert f(*swap(ok, **{f"_{i}": v})) == SHAPE, (i, v)
+    for i in (1, 22):
+        assert f(*swap(ok, **{f"_{i}": 1028})) == ALIGN
+    assert f(*swap(ok, _24=None)) == WORKSPACE
+    assert f(*swap(ok, _25=need - 1)) == WORKSPACE
+
+
+def test_kv_attention_workspace(lib):
+    f = lib.jet_kv_attention_workspace
+    one = f(1, 8, 2, 128, 1, 0)
+    assert one < f(1, 8, 2, 256, 1, 0)
+    assert f(64, 8, 2, 128, 64, 4) >= one + 2 * 64 * 8 * 130 * 4
+    for bad in ((-1, 8, 2, 128, 1, 0), (1, 8, 3, 128, 1, 0), (1, 8, 2, 96, 1, 0), (1, 8, 2, 128, 9000, 0),
+                (1, 8, 2, 128, 1, 2), (0, 8, 2, 128, 1, 0), (1, 0, 0, 128, 1, 0), (1, 8, 2, 128, 0, 0)):
+        assert f(*bad) == 0
