@@ -30,7 +30,8 @@ OP = {"quant_act_1x128": 0, "quant_w_128x128": 1, "requant_128x1": 2,
       "swiglu_quant_1x128": 9, "kv_calibrate": 10, "kv_cache_write": 11,
       "token_mismatch_per_sequence": 12, "rmsnorm_quant_1x128": 13,
       "add_rmsnorm_quant_1x128": 14, "add_rmsnorm_bwd": 15, "rope": 16,
-      "rope_kv_cache_write": 17, "kv_slot_map": 18, "sample": 19, "kv_attention": 20}
+      "rope_kv_cache_write": 17, "kv_slot_map": 18, "sample": 19, "kv_attention": 20,
+      "swiglu_bwd_quant_1x128": 21}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "wavelength": 2, "ramp": 3}
 
@@ -67,6 +68,7 @@ SIGNATURES = {
     "jet_kv_slot_map": [P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P],
     "jet_sample": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
     "jet_sample_unaligned": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
+    "jet_swiglu_bwd_quant_1x128": [P, P, I, P, I, I, P, P, P, P, P],
     "jet_kv_attention": [P, I, I, I, I, I, P, P, I, P, P, P, I, I, P, P, I, P, P, I, F, P, I, P, P, Z,
                          P],
     "jet_kv_attention_workspace": [I, I, I, I, I, I],
@@ -270,6 +272,30 @@ def jet_swiglu_quant_1x128(gate, up, q, s, stream=None):
     _need(s, torch.float32, (F // 128, M), "s")
     _check("jet_swiglu_quant_1x128", load().jet_swiglu_quant_1x128(
         _ptr(gate), _ptr(up), ld, M, F, _ptr(q), _ptr(s), _stream(stream)))
+
+
+def jet_swiglu_bwd_quant_1x128(gate, up, dh, qg, sg, qu, su, stream=None):
+    """The gradients of gate and up (views as in jet_swiglu_quant_1x128) from
+    dh [M, F] of the activation, in the 1x128 form: codes qg, qu [M, F],
+    scales sg, su [F/128, M]."""
+    import torch
+    M, F = gate.shape
+    for t, name in ((gate, "gate"), (up, "up")):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (M, F):
+            raise ValueError(f"{name}: expected bfloat16 [{M}, {F}]")
+        if t.numel() and (not t.is_cuda or t.stride(1) != 1):
+            raise ValueError(f"{name}: must be a CUDA tensor with contiguous rows")
+    ld = gate.stride(0) if M > 1 else F
+    if M > 1 and up.stride(0) != ld:
+        raise ValueError("gate and up must have the same row stride")
+    _need(dh, torch.bfloat16, (M, F), "dh")
+    for t, name in ((qg, "qg"), (qu, "qu")):
+        _need(t, torch.uint8, (M, F), name)
+    for t, name in ((sg, "sg"), (su, "su")):
+        _need(t, torch.float32, (F // 128, M), name)
+    _check("jet_swiglu_bwd_quant_1x128", load().jet_swiglu_bwd_quant_1x128(
+        _ptr(gate), _ptr(up), ld, _ptr(dh), M, F, _ptr(qg), _ptr(sg), _ptr(qu), _ptr(su),
+        _stream(stream)))
 
 
 def jet_rmsnorm_quant_1x128(x, g, eps, q, s, stream=None):
@@ -771,6 +797,18 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stre
         kept = torch.empty((B,), dtype=torch.int32, device=dev)
     jet_sample(logits, u, temperature, top_k, top_p, min_p, token, logp, logp_all, kept, stream)
     return token, logp, logp_all, kept
+
+
+def swiglu_bwd_quant_1x128(gate, up, dh, stream=None):
+    """(qg, sg, qu, su): the 1x128 forms of the gradients of gate and up."""
+    import torch
+    M, F = gate.shape
+    dev = gate.device
+    with _allocating_on(stream):
+        qg, qu = (torch.empty((M, F), dtype=torch.uint8, device=dev) for _ in range(2))
+        sg, su = (torch.empty((F // 128, M), dtype=torch.float32, device=dev) for _ in range(2))
+    jet_swiglu_bwd_quant_1x128(gate, up, dh, qg, sg, qu, su, stream)
+    return qg, sg, qu, su
 
 
 # --------------------------------------------------------------------------

@@ -91,7 +91,8 @@ typedef enum {
     JET_OP_ROPE_KV_CACHE_WRITE = 17,
     JET_OP_KV_SLOT_MAP = 18,
     JET_OP_SAMPLE = 19,
-    JET_OP_KV_ATTENTION = 20 /* its workspace: jet_kv_attention_workspace() */
+    JET_OP_KV_ATTENTION = 20, /* its workspace: jet_kv_attention_workspace() */
+    JET_OP_SWIGLU_BWD_QUANT_1X128 = 21
 } jet_op;
 
 /* Pair layouts of jet_rope: (i, i + R/2) or (2 i, 2 i + 1). */
@@ -703,6 +704,25 @@ JET_API jet_status jet_kv_attention(const uint16_t *q, int64_t ldq, int64_t T, i
 /* Workspace bytes of jet_kv_attention (0 for sizes it refuses).  Host function. */
 JET_API size_t jet_kv_attention_workspace(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
                                           int64_t n_prefix);
+
+/*
+ * Backward of the SwiGLU of jet_swiglu_quant_1x128 (the quantization passes
+ * gradients straight through), its two gradients quantized for the DGrads of the
+ * gate and up projections.  With s = 1 / (1 + e^-gate) in binary32:
+ *   dup = dh gate s,  dgate = dh up s (1 + gate (1 - s)),
+ * within a few 2^-22 relative; the 1x128 group rule applies to the binary32
+ * values.  The 128x1 forms for the WGrads come from jet_requant_128x1, as for
+ * every other operand.
+ *   gate, up [M][F] BF16 bits (in) with row stride ld (two halves of a gate_up
+ *       product, or two dense tensors with ld = F).
+ *   dh [M][F] BF16 bits (in; the down projection's DGrad), dense.
+ *   qg, qu [M][F] E4M3 codes, sg, su [F/128][M] FP32 scales (out) of dgate, dup.
+ * M, F >= 0, F a multiple of 128, ld >= F a multiple of 8.
+ */
+JET_API jet_status jet_swiglu_bwd_quant_1x128(const uint16_t *gate, const uint16_t *up, int64_t ld,
+                                              const uint16_t *dh, int64_t M, int64_t F, uint8_t *qg,
+                                              float *sg, uint8_t *qu, float *su,
+                                              jet_stream_t stream);
 
 /*
  * Workspace bytes an operation needs for the given sizes (0 if none).

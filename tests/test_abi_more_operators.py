@@ -57,3 +57,14 @@ def test_kv_attention_workspace(lib):
     for bad in ((-1, 8, 2, 128, 1, 0), (1, 8, 3, 128, 1, 0), (1, 8, 2, 96, 1, 0), (1, 8, 2, 128, 9000, 0),
                 (1, 8, 2, 128, 1, 2), (0, 8, 2, 128, 1, 0), (1, 0, 0, 128, 1, 0), (1, 8, 2, 128, 0, 0)):
         assert f(*bad) == 0
+
+
+def test_swiglu_bwd_quant(lib):
+    f = lib.jet_swiglu_bwd_quant_1x128
+    ok = [P[0], P[1], 512, P[2], 4, 256, P[3], P[4], P[5], P[6], None]
+    for i in (0, 1, 3, 6, 7, 8, 9):
+        assert f(*swap(ok, **{f"_{i}": None})) == NULL
+        assert f(*swap(ok, **{f"_{i}": MIS})) == ALIGN
+    for i, v in ((2, 248), (4, -1), (4, 1 << 31), (5, -128), (5, 200)):
+        assert f(*swap(ok, **{f"_{i}": v})) == SHAPE
+    assert f(*swap(ok, _2=516)) == ALIGN
