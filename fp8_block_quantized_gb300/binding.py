@@ -31,7 +31,7 @@ OP = {"quant_act_1x128": 0, "quant_w_128x128": 1, "requant_128x1": 2,
       "token_mismatch_per_sequence": 12, "rmsnorm_quant_1x128": 13,
       "add_rmsnorm_quant_1x128": 14, "add_rmsnorm_bwd": 15, "rope": 16,
       "rope_kv_cache_write": 17, "kv_slot_map": 18, "sample": 19, "kv_attention": 20,
-      "swiglu_bwd_quant_1x128": 21}
+      "swiglu_bwd_quant_1x128": 21, "head_logp": 22, "head_logp_bwd": 23}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "wavelength": 2, "ramp": 3}
 
@@ -69,6 +69,8 @@ SIGNATURES = {
     "jet_sample": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
     "jet_sample_unaligned": [P, ctypes.c_int, I, I, I, P, P, P, P, P, P, P, P, P, P],
     "jet_swiglu_bwd_quant_1x128": [P, P, I, P, I, I, P, P, P, P, P],
+    "jet_head_logp": [P, P, I, I, I, P, F, P, P, P, Z, P],
+    "jet_head_logp_bwd": [P, P, I, I, I, P, P, P, F, P, P, P, Z, P],
     "jet_kv_attention": [P, I, I, I, I, I, P, P, I, P, P, P, I, I, P, P, I, P, P, I, F, P, I, P, P, Z,
                          P],
     "jet_kv_attention_workspace": [I, I, I, I, I, I],
@@ -847,3 +849,77 @@ def kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, block_size, offse
     jet_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, block_size, offsets, lengths, out, lse,
                      prefix_offsets, prefix_lengths, scale, None, stream)
     return (out, lse) if with_lse else out
+
+
+# --------------------------------------------------------------------------
+# The head's log-probabilities and their gradient
+# --------------------------------------------------------------------------
+
+def _head_args(x, w, target):
+    import torch
+    T, K = x.shape
+    V = w.shape[0]
+    _need(x, torch.bfloat16, (T, K), "x")
+    _need(w, torch.bfloat16, (V, K), "w")
+    _need(target, torch.int64, (T,), "target")
+    for t in (x, w, target):
+        if t.numel() and t.device.index != torch.cuda.current_device():
+            raise ValueError("the tensors must be on the current device")
+    return T, K, V
+
+
+def _head_ws(op, T, V, K, ws, device, stream):
+    import torch
+    if ws is None:
+        with _allocating_on(stream):
+            ws = torch.empty((workspace_bytes(op, T, V, K),), dtype=torch.uint8, device=device)
+    return ws
+
+
+def jet_head_logp(x, w, target, scale, logp, lse, ws=None, stream=None):
+    """logp and lse [T] of the tokens target [T] (int64) under the head w [V, K]
+    for x [T, K]: the logits scale * x w^T are not kept; a target outside
+    [0, V) is ignored (logp 0)."""
+    import torch
+    T, K, V = _head_args(x, w, target)
+    _need(logp, torch.float32, (T,), "logp")
+    _need(lse, torch.float32, (T,), "lse")
+    ws = _head_ws("head_logp", T, V, K, ws, x.device, stream)
+    _check("jet_head_logp", load().jet_head_logp(
+        _ptr(x), _ptr(w), T, K, V, _ptr(target), float(scale), _ptr(logp), _ptr(lse), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def head_logp(x, w, target, scale=1.0, stream=None):
+    """(logp, lse), each float32 [T], of jet_head_logp."""
+    import torch
+    with _allocating_on(stream):
+        logp, lse = (torch.empty((x.shape[0],), dtype=torch.float32, device=x.device) for _ in range(2))
+    jet_head_logp(x, w, target, scale, logp, lse, None, stream)
+    return logp, lse
+
+
+def jet_head_logp_bwd(x, w, target, lse, dlogp, scale, dx, dw, ws=None, stream=None):
+    """dx [T, K] and dw [V, K] (BF16; either may be None) of sum(dlogp * logp)
+    from jet_head_logp's lse."""
+    import torch
+    T, K, V = _head_args(x, w, target)
+    _need(lse, torch.float32, (T,), "lse")
+    _need(dlogp, torch.float32, (T,), "dlogp")
+    if dx is not None:
+        _need(dx, torch.bfloat16, (T, K), "dx")
+    if dw is not None:
+        _need(dw, torch.bfloat16, (V, K), "dw")
+    ws = _head_ws("head_logp_bwd", T, V, K, ws, x.device, stream)
+    _check("jet_head_logp_bwd", load().jet_head_logp_bwd(
+        _ptr(x), _ptr(w), T, K, V, _ptr(target), _ptr(lse), _ptr(dlogp), float(scale), _ptr(dx),
+        _ptr(dw), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def head_logp_bwd(x, w, target, lse, dlogp, scale=1.0, stream=None):
+    """(dx, dw) of jet_head_logp_bwd."""
+    import torch
+    with _allocating_on(stream):
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+    jet_head_logp_bwd(x, w, target, lse, dlogp, scale, dx, dw, None, stream)
+    return dx, dw

@@ -28,8 +28,8 @@
  *    the first violation without launching anything: JET_ERR_NULL,
  *    JET_ERR_SHAPE, JET_ERR_ALIGN (every pointer must be 16-byte aligned, but
  *    for the arrays of one value per token, row, request or head of
- *    jet_add_rmsnorm_*, jet_rope*, jet_kv_slot_map, jet_sample* and
- *    jet_kv_attention, and the logits of jet_sample_unaligned, which need their type's alignment),
+ *    jet_add_rmsnorm_*, jet_rope*, jet_kv_slot_map, jet_sample*,
+ *    jet_kv_attention and jet_head_logp*, and the logits of jet_sample_unaligned, which need their type's alignment),
  *    JET_ERR_WORKSPACE, JET_ERR_DEVICE (current device must be sm_103).
  *    A pointer may be NULL only when its tensor is empty.
  *  - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL is the
@@ -92,7 +92,9 @@ typedef enum {
     JET_OP_KV_SLOT_MAP = 18,
     JET_OP_SAMPLE = 19,
     JET_OP_KV_ATTENTION = 20, /* its workspace: jet_kv_attention_workspace() */
-    JET_OP_SWIGLU_BWD_QUANT_1X128 = 21
+    JET_OP_SWIGLU_BWD_QUANT_1X128 = 21,
+    JET_OP_HEAD_LOGP = 22,
+    JET_OP_HEAD_LOGP_BWD = 23
 } jet_op;
 
 /* Pair layouts of jet_rope: (i, i + R/2) or (2 i, 2 i + 1). */
@@ -723,6 +725,46 @@ JET_API jet_status jet_swiglu_bwd_quant_1x128(const uint16_t *gate, const uint16
                                               const uint16_t *dh, int64_t M, int64_t F, uint8_t *qg,
                                               float *sg, uint8_t *qu, float *su,
                                               jet_stream_t stream);
+
+/*
+ * Log-probabilities of given tokens under the head, without its logits: the
+ * logp_train of the mismatch metric and of a policy or cross-entropy loss.
+ *   z_tv = scale (x_t . w_v),  lse_t = ln sum_v e^z_tv,
+ *   logp_t = z_t,target[t] - lse_t,
+ * products of BF16 values with binary32 sums, exponentials and sums in binary32;
+ * the vocabulary is walked in tiles, each row's maxima and sums joined in a fixed
+ * order.  A target outside [0, V) is ignored: logp 0 (lse is still that row's).
+ *   x [T][K] BF16 bits (in; the final norm's output), w [V][K] BF16 bits (in;
+ *       the head), target [T] int64 (in).
+ *   scale: 1, or 1 / temperature.
+ *   logp, lse [T] FP32 (out).
+ *   ws / ws_bytes: at least jet_workspace_bytes(JET_OP_HEAD_LOGP, T, V, K) bytes
+ *       of device memory; scratch, not initialised.
+ * 0 <= T < 2^22; 1 <= V < 2^24; 8 <= K <= 65536, a multiple of 8; scale > 0.
+ */
+JET_API jet_status jet_head_logp(const uint16_t *x, const uint16_t *w, int64_t T, int64_t K,
+                                 int64_t V, const int64_t *target, float scale, float *logp,
+                                 float *lse, void *ws, size_t ws_bytes, jet_stream_t stream);
+
+/*
+ * Gradients of sum_t dlogp_t logp_t (any loss of the logp is written so by its
+ * dlogp: -1/T for the mean cross entropy):
+ *   d_tv = scale dlogp_t ([v = target[t]] - e^(z_tv - lse_t)), 0 for ignored rows,
+ *   dx = d w,  dw = d^T x.
+ * The logits are computed again, a piece of the vocabulary at a time (at most
+ * 512 MB of d, 4096 entries at least); d is rounded to BF16 (2^-9 relative a
+ * value), sums are binary32, dx and dw rounded once to BF16.
+ *   x, w, target, scale, lse: as in and from jet_head_logp.  dlogp [T] FP32 (in;
+ *       not read for ignored rows).
+ *   dx [T][K], dw [V][K] BF16 bits (out); either may be NULL.  dw is zeros for
+ *       T = 0.
+ *   ws / ws_bytes: at least jet_workspace_bytes(JET_OP_HEAD_LOGP_BWD, T, V, K)
+ *       bytes of device memory; scratch, not initialised.
+ */
+JET_API jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, int64_t K,
+                                     int64_t V, const int64_t *target, const float *lse,
+                                     const float *dlogp, float scale, uint16_t *dx, uint16_t *dw,
+                                     void *ws, size_t ws_bytes, jet_stream_t stream);
 
 /*
  * Workspace bytes an operation needs for the given sizes (0 if none).

@@ -68,3 +68,45 @@ def test_swiglu_bwd_quant(lib):
     for i, v in ((2, 248), (4, -1), (4, 1 << 31), (5, -128), (5, 200)):
         assert f(*swap(ok, **{f"_{i}": v})) == SHAPE
     assert f(*swap(ok, _2=516)) == ALIGN
+
+
+def test_head_logp(lib):
+    f = lib.jet_head_logp
+    need = lib.jet_workspace_bytes(binding.OP["head_logp"], 100, 1000, 64)
+    assert need > 0
+    ok = [P[0], P[1], 100, 64, 1000, P[2], 1.0, P[3], P[4], P[5], need, None]
+    for i in (0, 1, 5, 7, 8):
+        assert f(*swap(ok, **{f"_{i}": None})) == NULL
+        assert f(*swap(ok, **{f"_{i}": ODD})) == ALIGN
+    for i in (0, 1, 9):
+        assert f(*swap(ok, **{f"_{i}": MIS})) == ALIGN
+    for i, v in ((2, -1), (2, 1 << 22), (3, 0), (3, 60), (3, 65544), (4, 0), (4, 1 << 24), (6, 0.0),
+                 (6, -1.0), (6, float("inf")), (6, float("nan"))):
+        assert f(*swap(ok, **{f"_{i}": v})) == SHAPE, (i, v)
+    assert f(*swap(ok, _9=None)) == WORKSPACE
+    assert f(*swap(ok, _10=need - 1)) == WORKSPACE
+
+
+def test_head_logp_bwd(lib):
+    f = lib.jet_head_logp_bwd
+    need = lib.jet_workspace_bytes(binding.OP["head_logp_bwd"], 100, 1000, 64)
+    assert need >= 100 * 1000 * 2
+    ok = [P[0], P[1], 100, 64, 1000, P[2], P[3], P[4], 1.0, P[5], P[6], P[7], need, None]
+    for i in (0, 1, 5, 6, 7):
+        assert f(*swap(ok, **{f"_{i}": None})) == NULL
+        assert f(*swap(ok, **{f"_{i}": ODD})) == ALIGN
+    assert f(*swap(ok, _9=None, _10=None)) == NULL
+    for i in (0, 1, 9, 10, 11):
+        assert f(*swap(ok, **{f"_{i}": MIS})) == ALIGN
+    for i, v in ((2, -1), (2, 1 << 22), (3, 0), (3, 60), (4, 0), (8, 0.0), (8, float("nan"))):
+        assert f(*swap(ok, **{f"_{i}": v})) == SHAPE, (i, v)
+    assert f(*swap(ok, _11=None)) == WORKSPACE
+    assert f(*swap(ok, _12=need - 1)) == WORKSPACE
+
+
+def test_head_workspaces(lib):
+    f, op = lib.jet_workspace_bytes, binding.OP
+    assert f(op["head_logp"], 0, 1000, 64) == 0 and f(op["head_logp"], 100, 1000, 60) == 0
+    # d of a piece stays at half a gigabyte, or 4096 entries
+    assert f(op["head_logp_bwd"], 4096, 128256, 512) < (1 << 30)
+    assert f(op["head_logp_bwd"], 1 << 20, 128256, 64) < 2 * (4096 + 256) * (1 << 20) + 4 * (1 << 30)
