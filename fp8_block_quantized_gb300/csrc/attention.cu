@@ -29,6 +29,7 @@
 
 #include <mutex>
 
+#include "attention_common.cuh"
 #include "jet_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -37,128 +38,9 @@ namespace {
 using namespace jet;
 using jet::ptx::smem_u32;
 
-constexpr int kRows = 16;          // rows of a unit
-constexpr int kTile = 128;         // keys of a tile, 32 for each warp
+using namespace jet::attn;
+
 constexpr int kThreads = 128;
-constexpr int kMaxCtas = 320;      // most CTAs of a launch (two on each of 152 SMs)
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-struct Args {
-    const uint16_t *q;
-    int64_t ldq;
-    int64_t T;
-    int Hq, Hk, G;                 // G = Hq / Hk
-    const uint8_t *kc, *vc;
-    int64_t S;
-    const float *ks, *vs;
-    const int32_t *table;
-    int64_t width, bs;
-    const int64_t *off;
-    const int32_t *len;
-    int B;
-    const int64_t *po;
-    const int32_t *pl;
-    int Ng;
-    float scale;
-    uint16_t *out;
-    int64_t ldo;
-    float *lse;
-    // workspace: pieces of units that several CTAs share, two a CTA; with
-    // groups, whole units by row (prefix, then own); the tiles before each segment
-    float *part, *part_ml;         // [2 kMaxCtas][kRows][D], [..][kRows][2]
-    float *whole, *whole_ml;       // [2][T * Hq][D], [..][2]
-    int64_t *before;               // [B + Ng + 1]
-};
-
-struct Segment {
-    int64_t t0;        // first token
-    int ntok;
-    int k0, k1;        // keys
-    int row;           // table row
-    int rtiles, ktiles;
-    __device__ int64_t tiles(int Hk) const { return (int64_t)rtiles * ktiles * Hk; }
-};
-
-__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
-    return v < lo ? lo : (v > hi ? hi : v);
-}
-
-// The number of entries a[1 .. n] that are <= x: the interval of [a[i], a[i+1])
-// that holds x, for x >= a[0].
-__device__ __forceinline__ int upper(const int64_t *a, int n, int64_t x) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a[mid + 1] <= x) lo = mid + 1; else hi = mid;
-    }
-    return lo;
-}
-
-// Keys request b has behind its table row.
-__device__ __forceinline__ int keys_of(const Args &a, int b) {
-    return (int)clamp64(a.len[b], 0, a.width * a.bs);
-}
-
-// The prefix length of group i: at most the keys of its first request.
-__device__ __forceinline__ int prefix_of(const Args &a, int i) {
-    const int64_t first = a.po[i];
-    if (first < 0 || first >= a.B) return 0;
-    return (int)clamp64(a.pl[i], 0, keys_of(a, (int)first));
-}
-
-__device__ Segment segment(const Args &a, int s) {
-    Segment g;
-    int64_t r0, r1;
-    if (s < a.B) {
-        r0 = s;
-        r1 = s + 1;
-        g.row = s;
-        g.k1 = keys_of(a, s);
-        g.k0 = 0;
-        if (a.Ng > 0 && s >= a.po[0]) {
-            const int i = upper(a.po, a.Ng, s);
-            if (i < a.Ng) g.k0 = min(prefix_of(a, i), g.k1);
-        }
-    } else {
-        const int i = s - a.B;
-        r0 = clamp64(a.po[i], 0, a.B);
-        r1 = clamp64(a.po[i + 1], r0, a.B);
-        g.row = (int)r0;
-        g.k0 = 0;
-        g.k1 = r1 > r0 ? prefix_of(a, i) : 0;
-    }
-    const int64_t t0 = clamp64(a.off[r0], 0, a.T), t1 = clamp64(a.off[r1], t0, a.T);
-    g.t0 = t0;
-    g.ntok = (int)(t1 - t0);
-    g.rtiles = (int)(((t1 - t0) * a.G + kRows - 1) / kRows);
-    g.ktiles = (g.k1 - g.k0 + kTile - 1) / kTile;
-    return g;
-}
-
-// Position of token t of request b.
-__device__ __forceinline__ int position(const Args &a, int b, int64_t t) {
-    return (int)clamp64((int64_t)a.len[b] - (a.off[b + 1] - t), -1, 0x7FFFFFFF);
-}
-
-__device__ __forceinline__ uint32_t codes_f16(uint32_t two) {  // low two codes -> f16x2
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-        : "=r"(r)
-        : "r"(two));
-    return r;
-}
-__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t two) {  // high two codes
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
-        : "=r"(r)
-        : "r"(two));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -166,12 +48,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 // 16-byte copy global -> shared, zeros where !ok.
@@ -214,6 +90,17 @@ struct Cfg {
     static_assert(4 * kWarpBytes >= 4 * kRows * D * 4, "the warps' join reuses the ring");
 };
 
+// The rows of a segment without keys (only without groups: with them the join
+// writes every row).
+template <int D>
+__device__ void no_keys(const Args &a, const Segment &g) {
+    for (int64_t t = g.t0; t < g.t0 + g.ntok; ++t) {
+        for (int64_t i = 0; i < (int64_t)a.Hq * D; i += 8)
+            *reinterpret_cast<uint4 *>(a.out + t * a.ldo + i) = make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < a.Hq && a.lse; ++h) a.lse[t * a.Hq + h] = -INFINITY;
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel(const Args a) {
     using C = Cfg<D>;
@@ -226,64 +113,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
     griddep_wait();
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
-    // tiles before each thread's stretch of segments
-    const int nseg = a.B + a.Ng, per = (nseg + kThreads - 1) / kThreads;
-    {
-        int64_t mine = 0;
-        const int s0 = tid * per, s1 = min(nseg, s0 + per);
-        for (int s = s0; s < s1; ++s) mine += segment(a, s).tiles(a.Hk);
-        int64_t incl = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t v = __shfl_up_sync(~0u, incl, d);
-            if (lane >= d) incl += v;
-        }
-        if (lane == 31) sh_pre[warp] = incl;
-        __syncthreads();
-        int64_t base = 0;
-        for (int w = 0; w < warp; ++w) base += sh_pre[w];
-        __syncthreads();
-        sh_pre[tid + 1] = base + incl;
-        if (tid == 0) sh_pre[0] = 0;
-        __syncthreads();
-        if (blockIdx.x == 0) {
-            int64_t at = sh_pre[tid];
-            for (int s = s0; s < s1; ++s) {
-                a.before[s] = at;
-                at += segment(a, s).tiles(a.Hk);
-            }
-            if (tid == 0) a.before[nseg] = sh_pre[kThreads];
-        }
-    }
+    const int lo = a.wide_own ? a.B : 0, hi = a.wide_prefix ? a.B : a.B + a.Ng;
+    const int per = deal_segments<kThreads>(lo, hi, sh_pre, a.before, a.total, [&](int s) {
+        const Segment g = segment(a, s);
+        const Narrow n(a, g);
+        if (blockIdx.x == 0 && a.Ng == 0 && n.ktiles == 0) no_keys<D>(a, g);
+        return n.tiles(a);
+    });
     const int64_t total = sh_pre[kThreads];
-    const int64_t ctas = min((int64_t)gridDim.x, total);  // none of them without a tile
+    const int64_t ctas = min((int64_t)a.narrow_ctas, total);  // none of them without a tile
     if (blockIdx.x >= ctas) return;
     const int64_t x0 = total * blockIdx.x / ctas, x1 = total * (blockIdx.x + 1) / ctas;
-    int s;
-    int64_t at;  // first tile of segment s
-    {
-        int lo = 0, hi = kThreads - 1;  // the last stretch that begins at or before x0
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (sh_pre[mid] <= x0) lo = mid; else hi = mid - 1;
-        }
-        s = lo * per;
-        at = sh_pre[lo];
-    }
+    const int stretch = stretch_of<kThreads>(sh_pre, x0);
+    int s = lo + stretch * per;
+    int64_t at = sh_pre[stretch];  // first tile of segment s
     const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
     uint2 *qs = reinterpret_cast<uint2 *>(smem + 4 * C::kWarpBytes);  // [KS][kRows / 8][32] (D > 128)
 
     int64_t x = x0;
     while (x < x1) {
         Segment sg = segment(a, s);
-        while (at + sg.tiles(a.Hk) <= x) {
-            at += sg.tiles(a.Hk);
+        Narrow nw(a, sg);
+        while (at + nw.tiles(a) <= x) {
+            at += nw.tiles(a);
             sg = segment(a, ++s);
+            nw = Narrow(a, sg);
         }
-        const int unit = (int)((x - at) / sg.ktiles);
-        const int kt0 = (int)((x - at) - (int64_t)unit * sg.ktiles);
-        const int kt1 = (int)min((int64_t)sg.ktiles, kt0 + (x1 - x));
-        const int h = unit / sg.rtiles, rt = unit - h * sg.rtiles;
+        const int unit = (int)((x - at) / nw.ktiles);
+        const int kt0 = (int)((x - at) - (int64_t)unit * nw.ktiles);
+        const int kt1 = (int)min((int64_t)nw.ktiles, kt0 + (x1 - x));
+        const int h = unit / nw.rtiles, rt = unit - h * nw.rtiles;
         const int64_t nrows = (int64_t)sg.ntok * a.G, row0 = (int64_t)rt * kRows;
 
         // queries: rows g and g + 8 of the tile, channels 64 i + 16 j .. + 15
@@ -311,8 +170,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
             }
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const int e = min(254, 268 - (int)(__float_as_uint(top) >> 23));
-            const float up = top == 0.0f ? 1.0f : __uint_as_float((uint32_t)max(e, 1) << 23);
+            const float up = row_power(top);
             f[r] = a.scale * a.ks[h] * kLog2e / up;
             pos[r] = 0x7FFFFFFF;
             if (ok) pos[r] = position(a, s < a.B ? s : min(upper(a.off, a.B, t), a.B - 1), t);
@@ -534,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
                 }
                 const int64_t t = sg.t0 + rr / a.G;
                 const int hq = h * a.G + (int)(rr % a.G);
-                const bool full = kt1 - kt0 == sg.ktiles, direct = full && a.Ng == 0;
+                const bool full = kt1 - kt0 == nw.ktiles, direct = full && a.Ng == 0;
                 const int64_t slot =
                     full ? ((s < a.B ? a.T : 0) + t) * a.Hq + hq
                          : (int64_t)(2 * blockIdx.x + (x == x0 ? 0 : 1)) * kRows + r;
@@ -578,86 +436,217 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
     }
 }
 
-// Joins the pieces of every row that no CTA had whole (with groups: of every
-// row), in order, and writes the rows that see no key.  One warp a row.
+// One row's join: the running maximum, sum and output of a warp (channels lane +
+// 32 e).
 template <int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(const Args a, int grid) {
+struct Row {
+    static constexpr int E = D / 32;
+    float m = -INFINITY, l = 0.0f, o[E] = {};
+    // n partial results; piece(i) is the row of the i-th in o and ml
+    template <typename F>
+    __device__ void add(const float *po, const float *ml, int n, F piece) {
+        const int lane = threadIdx.x & 31;
+        for (int b = 0; b < n; b += 32) {
+            float mi = -INFINITY, li = 0.0f;
+            if (b + lane < n) {
+                const float2 v = *reinterpret_cast<const float2 *>(ml + 2 * piece(b + lane));
+                mi = v.x, li = v.y;
+            }
+            float top = fmaxf(m, mi);
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            const float use = top == -INFINITY ? 0.0f : top, c = ex2(m - use), w = ex2(mi - use);
+            li *= w;
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) li += __shfl_xor_sync(~0u, li, d);
+            l = l * c + li;
+            m = top;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= c;
+            const int cnt = min(32, n - b);
+#pragma unroll 4
+            for (int i = 0; i < cnt; ++i) {
+                const float wi = __shfl_sync(~0u, w, i);
+                const float *src = po + piece(b + i) * D + lane;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] += wi * src[32 * e];
+            }
+        }
+    }
+    __device__ void write(const Args &a, int64_t t, int hq) const {
+        const int lane = threadIdx.x & 31;
+        const float inv = l > 0.0f ? a.vs[hq / a.G] / l : 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const __nv_bfloat16 v = __float2bfloat16_rn(o[e] * inv);
+            a.out[t * a.ldo + (int64_t)hq * D + lane + 32 * e] = *reinterpret_cast<const uint16_t *>(&v);
+        }
+        if (a.lse && lane == 0) a.lse[t * a.Hq + hq] = l > 0.0f ? kLn2 * (m + log2f(l)) : -INFINITY;
+    }
+};
+
+// The pieces of a unit of `n` tiles from u0 on, dealt to several CTAs: CTA c's is
+// its first piece (slot 2 c) where its range begins in the unit, else its last.
+struct Pieces {
+    int c0, n, first;  // CTAs, and the first one's slot
+    __device__ Pieces(int64_t u0, int64_t tiles, int64_t total, int64_t ctas) {
+        c0 = cta_of(u0, total, ctas);
+        n = cta_of(u0 + tiles - 1, total, ctas) - c0 + 1;
+        first = 2 * c0 + (total * c0 / ctas >= u0 ? 0 : 1);
+    }
+    __device__ int64_t slot(int i) const { return i == 0 ? first : 2 * (c0 + i); }
+};
+
+// Without groups: the rows of the units that more than one CTA had.  The ranges'
+// borders are gone through; a unit is joined at the first border inside it.  A
+// CTA takes kJoinRows rows of a border's unit.
+constexpr int kJoinRows = 16;
+
+template <int D>
+__global__ void __launch_bounds__(256, 4) attention_join_split_kernel(const Args a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const bool wide = a.wide_own;
+    const int rows = wide ? kWideRows : kRows, per = rows / kJoinRows;
+    const int border = blockIdx.x / per + 1, r0 = (blockIdx.x % per) * kJoinRows;
+    const int64_t total = a.total[wide], ctas = min((int64_t)(wide ? a.wide_ctas : a.narrow_ctas), total);
+    if (border >= ctas) return;
+    const int64_t x = total * border / ctas;
+    int lo = 0, hi = a.B - 1;  // the last segment that begins at or before x (one with tiles)
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.before[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    const Segment g = segment(a, lo);
+    int64_t u0 = a.before[lo], row0;
+    int n, h, count;
+    if (wide) {
+        const Wide w(a, g);
+        int rt = 0;
+        while (u0 + (int64_t)w.ktiles(g, rt) * a.Hk <= x) u0 += (int64_t)w.ktiles(g, rt++) * a.Hk;
+        n = w.ktiles(g, rt);
+        h = (int)((x - u0) / n);
+        row0 = (int64_t)rt * w.tokens * a.G;
+        count = (int)min((int64_t)w.tokens * a.G, (int64_t)g.ntok * a.G - row0);
+        u0 += (int64_t)h * n;
+    } else {
+        const Narrow w(a, g);
+        n = w.ktiles;
+        const int unit = (int)((x - u0) / n);
+        h = unit / w.rtiles;
+        row0 = (int64_t)(unit - h * w.rtiles) * kRows;
+        count = (int)min((int64_t)kRows, (int64_t)g.ntok * a.G - row0);
+        u0 += (int64_t)unit * n;
+    }
+    if (u0 == x || total * (border - 1) / ctas > u0) return;
+    const Pieces p(u0, n, total, ctas);
+    const float *po = wide ? a.wpart : a.part, *ml = wide ? a.wpart_ml : a.part_ml;
+    for (int r = r0 + (threadIdx.x >> 5); r < min(count, r0 + kJoinRows); r += 8) {
+        Row<D> row;
+        row.add(po, ml, p.n, [&](int i) { return p.slot(i) * rows + r; });
+        const int64_t rr = row0 + r;
+        row.write(a, g.t0 + rr / a.G, h * a.G + (int)(rr % a.G));
+    }
+}
+
+// With groups: every row, from its prefix and its request's own part.  One warp a
+// row.
+template <int D>
+__global__ void __launch_bounds__(256, 4) attention_join_kernel(const Args a) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    constexpr int E = D / 32;
     const int64_t first = clamp64(a.off[0], 0, a.T), last = clamp64(a.off[a.B], 0, a.T);
-    const int64_t total = a.before[a.B + a.Ng], ctas = min((int64_t)grid, total);
     for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < a.T * a.Hq; i += gridDim.x * 8ll) {
         const int64_t t = i / a.Hq;
         const int hq = (int)(i - t * a.Hq), h = hq / a.G;
         if (t < first || t >= last) continue;
         const int b = upper(a.off, a.B, t);
         if (b >= a.B) continue;
-        float m = -INFINITY, l = 0.0f, o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.0f;
-        auto add = [&](const float *po, const float *ml) {
-            const float mi = ml[0], li = ml[1], top = fmaxf(m, mi);
-            const float base = top == -INFINITY ? 0.0f : top;
-            const float c = ex2(m - base), ci = ex2(mi - base);
-            l = l * c + li * ci;
-            m = top;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * c + po[lane + 32 * e] * ci;
-        };
-        bool written = false;
+        Row<D> row;
         for (int k = 0; k < 2; ++k) {
             int s = b;
             if (k == 0) {  // the prefix
-                if (a.Ng == 0 || b < a.po[0]) continue;
+                if (b < a.po[0]) continue;
                 const int gi = upper(a.po, a.Ng, b);
                 if (gi >= a.Ng) continue;
                 s = a.B + gi;
             }
-            const Segment sg = segment(a, s);
-            if (sg.ktiles == 0 || t < sg.t0 || t >= sg.t0 + sg.ntok) continue;
-            const int64_t row = (t - sg.t0) * a.G + hq % a.G;
-            const int64_t u0 = a.before[s] + (h * (int64_t)sg.rtiles + row / kRows) * sg.ktiles;
-            const int c0 = (int)(((u0 + 1) * ctas - 1) / total);
-            const int c1 = (int)(((u0 + sg.ktiles) * ctas - 1) / total);
-            if (c0 == c1) {
-                written = a.Ng == 0;
-                const int64_t slot = ((s < a.B ? a.T : 0) + t) * a.Hq + hq;
-                if (!written) add(a.whole + slot * D, a.whole_ml + slot * 2);
-            } else {
-                for (int c = c0; c <= c1; ++c) {
-                    const bool at_start = total * c / ctas >= u0;
-                    const int64_t slot = (int64_t)(2 * c + (at_start || c > c0 ? 0 : 1)) * kRows + row % kRows;
-                    add(a.part + slot * D, a.part_ml + slot * 2);
+            const Segment g = segment(a, s);
+            if (g.k1 <= g.k0 || t < g.t0 || t >= g.t0 + g.ntok) continue;
+            const bool wide = s < a.B ? a.wide_own : a.wide_prefix;
+            const int64_t rr = (t - g.t0) * a.G + hq % a.G;
+            int64_t u0 = a.before[s];
+            int n, r;
+            if (wide) {
+                const Wide w(a, g);
+                const int rt = (int)((t - g.t0) / w.tokens);
+                int64_t skip;
+                if (g.base >= 0) {
+                    skip = w.head_tiles(g, lane, rt, 32);
+#pragma unroll
+                    for (int d = 16; d >= 1; d >>= 1) skip += __shfl_xor_sync(~0u, skip, d);
+                } else {
+                    skip = w.head_tiles(g, 0, rt);
                 }
+                n = w.ktiles(g, rt);
+                u0 += skip * a.Hk + (int64_t)h * n;
+                r = (int)(rr - (int64_t)rt * w.tokens * a.G);
+            } else {
+                const Narrow w(a, g);
+                n = w.ktiles;
+                u0 += (h * (int64_t)w.rtiles + rr / kRows) * n;
+                r = (int)(rr % kRows);
+            }
+            const int64_t total = a.total[wide], ctas = min((int64_t)(wide ? a.wide_ctas : a.narrow_ctas), total);
+            const Pieces p(u0, n, total, ctas);
+            if (p.n == 1) {
+                const int64_t at = (s < a.B ? a.T * a.Hq : 0) + i;
+                row.add(a.whole, a.whole_ml, 1, [&](int) { return at; });
+            } else if (wide) {
+                row.add(a.wpart, a.wpart_ml, p.n, [&](int j) { return p.slot(j) * kWideRows + r; });
+            } else {
+                row.add(a.part, a.part_ml, p.n, [&](int j) { return p.slot(j) * kRows + r; });
             }
         }
-        if (written) continue;
-        const float inv = l > 0.0f ? a.vs[h] / l : 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const __nv_bfloat16 v = __float2bfloat16_rn(o[e] * inv);
-            a.out[t * a.ldo + (int64_t)hq * D + lane + 32 * e] = *reinterpret_cast<const uint16_t *>(&v);
-        }
-        if (a.lse && lane == 0) a.lse[i] = l > 0.0f ? kLn2 * (m + log2f(l)) : -INFINITY;
+        row.write(a, t, hq);
     }
 }
 
+// Which segments go to the wide kernel, by the rows that a unit has on average:
+// requests' own parts and prefixes.
+constexpr int64_t kWideFrom = 32;
+
 struct Layout {
-    size_t part, part_ml, whole, whole_ml, before, bytes;
+    bool wide_own, wide_prefix;
+    size_t part, part_ml, wpart, wpart_ml, whole, whole_ml, before, total, bytes;
 };
 
-Layout layout(int64_t T, int64_t Hq, int64_t D, int64_t B, int64_t Ng) {
+Layout layout(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B, int64_t Ng) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const int64_t G = Hq / Hk;
     Layout w;
-    const size_t slots = 2 * kMaxCtas * kRows, rows = Ng > 0 ? (size_t)(2 * T * Hq) : 0;
-    w.part = 0;
-    w.part_ml = w.part + up(slots * D * 4);
-    w.whole = w.part_ml + up(slots * 8);
-    w.whole_ml = w.whole + up(rows * D * 4);
-    w.before = w.whole_ml + up(rows * 8);
-    w.bytes = w.before + up((size_t)(B + Ng + 1) * 8);
+    const bool can = D <= 128 && G <= 128;
+    w.wide_own = can && T * G >= kWideFrom * B;
+    w.wide_prefix = can && Ng > 0 && T * G >= kWideFrom * Ng;
+    const size_t slots = !w.wide_own || (Ng > 0 && !w.wide_prefix) ? 2 * kNarrowCtas * kRows : 0,
+                 wslots = w.wide_own || w.wide_prefix ? 2 * kWideCtas * kWideRows : 0,
+                 rows = Ng > 0 ? (size_t)(2 * T * Hq) : 0;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t p = at;
+        at += up(n);
+        return p;
+    };
+    w.part = take(slots * D * 4);
+    w.part_ml = take(slots * 8);
+    w.wpart = take(wslots * D * 4);
+    w.wpart_ml = take(wslots * 8);
+    w.whole = take(rows * D * 4);
+    w.whole_ml = take(rows * 8);
+    w.before = take((size_t)(B + Ng) * 8);
+    w.total = take(16);
+    w.bytes = at;
     return w;
 }
 
@@ -685,14 +674,21 @@ jet_status launch(const DeviceInfo &dev, const Args &a, cudaStream_t stream) {
             done[dev.ordinal] = dev.context;
         }
     }
-    int ctas = dev.num_sms * C::kCtasPerSm;
-    if (ctas > kMaxCtas) ctas = kMaxCtas;
-    const jet_status st = launch_pdl(attention_kernel<D>, dim3((unsigned)ctas), dim3(kThreads),
-                                     C::kSmem, stream, a);
+    jet_status st = JET_OK;
+    if (!a.wide_own || (a.Ng > 0 && !a.wide_prefix))
+        st = launch_pdl(attention_kernel<D>, dim3((unsigned)a.narrow_ctas), dim3(kThreads), C::kSmem,
+                        stream, a);
+    if (st == JET_OK && (a.wide_own || a.wide_prefix)) st = launch_attention_wide(dev, a, D, stream);
     if (st != JET_OK) return st;
-    const int64_t want = (a.T * a.Hq + 7) / 8, cap = (int64_t)dev.num_sms * 8;
-    return launch_pdl(attention_join_kernel<D>, dim3((unsigned)(want < cap ? want : cap)), dim3(256),
-                      0, stream, a, ctas);
+    if (a.Ng > 0) {
+        const int64_t want = (a.T * a.Hq + 7) / 8, cap = (int64_t)dev.num_sms * 8;
+        return launch_pdl(attention_join_kernel<D>, dim3((unsigned)(want < cap ? want : cap)), dim3(256),
+                          0, stream, a);
+    }
+    const int borders = (a.wide_own ? a.wide_ctas : a.narrow_ctas) - 1;
+    const int per = (a.wide_own ? kWideRows : kRows) / kJoinRows;
+    if (borders <= 0) return JET_OK;
+    return launch_pdl(attention_join_split_kernel<D>, dim3((unsigned)(borders * per)), dim3(256), 0, stream, a);
 }
 
 inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -702,7 +698,7 @@ inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<ui
 size_t jet_kv_attention_workspace(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
                                   int64_t n_prefix) {
     if (!shape_ok(T, Hq, Hk, D, B, n_prefix) || T == 0 || Hq == 0 || B == 0) return 0;
-    return layout(T, Hq, D, B, n_prefix).bytes;
+    return layout(T, Hq, Hk, D, B, n_prefix).bytes;
 }
 
 jet_status jet_kv_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hk,
@@ -733,7 +729,8 @@ jet_status jet_kv_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H
                     aligned_to(prefix_offsets, 8) && aligned_to(prefix_lengths, 4) &&
                     aligned_to(lse, 4),
                 JET_ERR_ALIGN);
-    const Layout w = layout(T, Hq, D, B, n_prefix);
+    Layout w = {};
+    if (!empty) w = layout(T, Hq, Hk, D, B, n_prefix);
     JET_REQUIRE(empty || (ws && ws_bytes >= w.bytes), JET_ERR_WORKSPACE);
     DeviceInfo dev;
     const jet_status st = current_device(&dev);
@@ -750,7 +747,14 @@ jet_status jet_kv_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H
     a.part_ml = reinterpret_cast<float *>(base + w.part_ml);
     a.whole = reinterpret_cast<float *>(base + w.whole);
     a.whole_ml = reinterpret_cast<float *>(base + w.whole_ml);
+    a.wpart = reinterpret_cast<float *>(base + w.wpart);
+    a.wpart_ml = reinterpret_cast<float *>(base + w.wpart_ml);
     a.before = reinterpret_cast<int64_t *>(base + w.before);
+    a.total = reinterpret_cast<int64_t *>(base + w.total);
+    a.wide_own = w.wide_own, a.wide_prefix = w.wide_prefix;
+    const int per_sm = D > 128 ? 1 : 2;  // narrow CTAs on an SM
+    a.narrow_ctas = dev.num_sms * per_sm < kNarrowCtas ? dev.num_sms * per_sm : kNarrowCtas;
+    a.wide_ctas = dev.num_sms < kWideCtas ? dev.num_sms : kWideCtas;
     const cudaStream_t s = as_stream(stream);
     return D == 64 ? launch<64>(dev, a, s) : D == 128 ? launch<128>(dev, a, s) : launch<256>(dev, a, s);
 }

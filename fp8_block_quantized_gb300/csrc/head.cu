@@ -155,6 +155,10 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
         k1 = (int)((int64_t)(sp + 1) * nk / splits);
     };
 
+    // A wait of a whole warp; all lanes leave alike.
+    auto wait = [&](uint64_t *bar, uint32_t parity, unsigned site) -> bool {
+        return __all_sync(~0u, mbar_wait(bar, parity, abort, status, site));
+    };
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
@@ -212,10 +216,10 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             int m0, n0, k0, k1, sp;
             coords(t, m0, n0, k0, k1, sp);
             const uint32_t buf = tiles & 1u;
-            if (!mbar_wait(&tempty_bar[buf], ((tiles >> 1) & 1u) ^ 1u, abort, status, kSiteMmaTmem)) break;
+            if (!wait(&tempty_bar[buf], ((tiles >> 1) & 1u) ^ 1u, kSiteMmaTmem)) break;
             for (int kb = k0; kb < k1; ++kb, ++it) {
                 const int s = it % S;
-                if (!mbar_wait(&full_bar[s], (it / S) & 1u, abort, status, kSiteMma)) {
+                if (!wait(&full_bar[s], (it / S) & 1u, kSiteMma)) {
                     ok = false;
                     break;
                 }
@@ -272,7 +276,7 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                 }
                 if (P == kGrad) lse2 = ep.lse[row] * kLog2e;
             }
-            if (!mbar_wait(&tfull_bar[buf], (tiles >> 1) & 1u, abort, status, kSiteEpilogue)) break;
+            if (!wait(&tfull_bar[buf], (tiles >> 1) & 1u, kSiteEpilogue)) break;
             tc_fence_after();
             const uint32_t acc0 = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
             float top = -INFINITY, sum = 0.0f;

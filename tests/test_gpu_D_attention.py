@@ -233,6 +233,55 @@ def test_a_prefix_equals_no_prefix_where_the_tables_agree(jet):
     assert (out.float() - alone.float()).abs().max() <= 2.0 ** -7 * alone.float().abs().max()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (3, 1), (4, 2), (16, 2), (128, 1)])
+@pytest.mark.parametrize("requests", [
+    [(300, 300)], [(100, 1000), (256, 256), (1, 5), (64, 64)], [(513, 700)], [(40, 2000)], [(33, 33)] * 9])
+def test_many_rows(jet, D, Hq, Hk, requests):
+    """Units of up to 256 rows: of whole tokens, of one head's or of a request's."""
+    Batch(requests, Hq, Hk, D, 16, seed=D + Hq + len(requests)).check(jet)
+
+
+def test_many_rows_of_odd_batches(jet):
+    """Lengths below the number of new tokens, of zero, tables without blocks, rows of no request."""
+    b = Batch([(300, 300), (150, 600), (200, 200), (90, 90), (120, 400)], 8, 2, 128, 24, seed=31, behind=9)
+    b.lengths[2], b.lengths[3] = 50, 0
+    b.table[1, 3] = -1
+    b.table[1, 7] = b.S // b.bs
+    b.table[4] = -1
+    b.lengths[0] = 100000                  # past the table's width
+    b.check(jet)
+
+
+@pytest.mark.parametrize("groups", [[(0, 3, 500)], [(0, 2, 100), (2, 4, 700)], [(1, 3, 333)], [(0, 4, 0)]])
+def test_many_rows_behind_a_shared_prefix(jet, groups):
+    Batch([(200, 900), (64, 600), (300, 1000), (7, 900)], 8, 2, 128, 16, seed=33, groups=groups).check(jet)
+
+
+def test_maxima_that_keep_growing(jet):
+    """Scores rise by far more than 2^8 from tile to tile, and fall again."""
+    for rising in (True, False):
+        b = Batch([(300, 1500)], 4, 1, 128, 16, seed=35)
+        at = torch.arange(1500).cuda()
+        slot = b.table[0].long()[at // 16] * 16 + at % 16
+        size = (at if rising else 1499 - at).float() / 1500 * 400
+        b.k[slot, 0] = (size[:, None] * torch.sign(b.q[299, 0].float())).to(F8).view(U8)
+        b.check(jet)
+
+
+def test_nan_behind_the_length_does_not_show_in_many_rows(jet):
+    b = Batch([(100, 137), (200, 330)], 4, 2, 128, 64, seed=37, groups=[(0, 2, 100)])
+    want = b.call(jet)
+    used = torch.zeros((b.S,), dtype=torch.bool)
+    for r, l in enumerate(b.lengths.tolist()):
+        for p in range(l):
+            used[int(b.table[r, p // b.bs]) * b.bs + p % b.bs] = True
+    b.k[~used.cuda()] = 0x7F
+    b.v[~used.cuda()] = 0xFF
+    got = b.call(jet)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_long_context(jet):
     """Many pieces of one unit."""
     g = torch.Generator().manual_seed(1)
@@ -295,3 +344,8 @@ def test_nothing_to_do(jet):
                          b.lengths[:0], out)
     torch.cuda.synchronize()
     assert (out == 7).all()
+
+
+def test_no_wait_ran_out(jet):
+    code, word = jet.device_status()
+    assert code == 0, hex(word)
