@@ -11,14 +11,19 @@
 // The work is a list of key tiles: a segment is the own part of a request or
 // the prefix of a group, a unit one 16-row tile (rows = (token, query head of
 // the KV head's group)) of a segment and one KV head, and a unit's keys come in
-// tiles of 128.  Every CTA takes an equal range of the tiles of all units in
+// tiles of 32.  Every worker takes an equal range of the tiles of all units in
 // order, so the loads are even whatever the lengths; each stretch of one unit
-// in a CTA's range (a piece) ends in a partial result, joined by a second kernel
-// in a fixed order.  A unit that one CTA has whole is written at once.
+// in a worker's range (a piece) ends in a partial result, joined by a last kernel
+// in a fixed order.  A unit that one worker has whole is written at once.  The
+// first kernel, one CTA, lists the segments with work and where each worker's
+// range begins, so that the others find it with two reads.
 //
-// In a tile each of four warps takes 32 keys on its own: a ring of cp.async
-// stages (K and V codes, 16 bytes a copy, so any page size and order), scores
-// and values by 16-bit tensor core instructions.  E4M3 codes are exact in FP16;
+// A narrow worker is up to eight warps, one for each of as many KV heads: they read the
+// same tokens, whose heads lie side by side in memory, at about the same time (with
+// a head's units one after another the rows of 128 bytes a kilobyte apart came at
+// half the rate).  A CTA has as many workers as its warps allow.  A warp has its own ring of
+// cp.async stages (K and V codes, 16 bytes a copy, so any page size and order);
+// scores and values by 16-bit tensor core instructions.  E4M3 codes are exact in FP16;
 // the queries are brought to FP16 by a power of two a row that puts their
 // largest channel at 2^14, so that a channel's rounding is below 2^-38 of that
 // (BF16 has eight bits, FP16 eleven: only channels 2^-25 of the largest lose
@@ -40,7 +45,6 @@ using jet::ptx::smem_u32;
 
 using namespace jet::attn;
 
-constexpr int kThreads = 128;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -78,72 +82,188 @@ __device__ __forceinline__ uint32_t place(int r, int c) {
     return r * D + ((c ^ s) << 4);
 }
 
-template <int D>
-struct Cfg {
-    static constexpr int kStageBytes = 2 * 32 * D;             // a warp's K and V
-    static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
-    static constexpr int kWarpBytes = kStages * kStageBytes;
-    static constexpr int kQBytes = D > 128 ? kRows * D * 2 : 0;  // query fragments
-    static constexpr int kSmem = 4 * kWarpBytes + kQBytes;
-    static constexpr int kCtasPerSm = D > 128 ? 1 : 2;
-    static_assert(kSmem * kCtasPerSm <= 227 * 1024, "shared memory");
-    static_assert(4 * kWarpBytes >= 4 * kRows * D * 4, "the warps' join reuses the ring");
-};
+// The plan: every segment, the tiles before it in its kernel's list (narrow, wide),
+// the lists without the segments that have none, and the workers' starts.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanHeld = 1024;  // groups, and segments of a list, that fit its shared memory
 
-// The rows of a segment without keys (only without groups: with them the join
-// writes every row).
-template <int D>
-__device__ void no_keys(const Args &a, const Segment &g) {
-    for (int64_t t = g.t0; t < g.t0 + g.ntok; ++t) {
-        for (int64_t i = 0; i < (int64_t)a.Hq * D; i += 8)
-            *reinterpret_cast<uint4 *>(a.out + t * a.ldo + i) = make_uint4(0, 0, 0, 0);
-        for (int h = 0; h < a.Hq && a.lse; ++h) a.lse[t * a.Hq + h] = -INFINITY;
+__global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Args a) {
+    __shared__ int64_t sh_po[kPlanHeld + 1];
+    __shared__ int64_t sh_before[2][kPlanHeld];
+    __shared__ int64_t sh_tiles[2][kPlanThreads / 32];
+    __shared__ int sh_count[2][kPlanThreads / 32];
+    __shared__ int sh_empty;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nseg = a.B + a.Ng;
+    const bool held = a.Ng <= kPlanHeld;
+    if (held && a.Ng > 0)
+        for (int i = tid; i <= a.Ng; i += kPlanThreads) sh_po[i] = a.po[i];
+    if (tid == 0) sh_empty = 0;
+    __syncthreads();
+    const int64_t *po = held ? sh_po : a.po;
+    int64_t tiles0[2] = {0, 0};  // before this round's segments
+    int count0[2] = {0, 0};
+    int *order[2] = {a.order, a.order + nseg};
+    for (int s0 = 0; s0 < nseg; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int64_t mine[2] = {0, 0};
+        Segment g;
+        bool wide = false;
+        if (s < nseg) {
+            int64_t r0, r1;
+            g.base = g.group = -1;
+            g.k0 = 0;
+            if (s < a.B) {
+                r0 = s;
+                r1 = s + 1;
+                g.row = s;
+                g.k1 = keys_of(a, s);
+                if (a.Ng > 0 && s >= po[0]) {
+                    const int i = upper(po, a.Ng, s);
+                    if (i < a.Ng) g.group = i, g.k0 = min(prefix_of(a, i), g.k1);
+                }
+            } else {
+                const int i = s - a.B;
+                r0 = clamp64(po[i], 0, a.B);
+                r1 = clamp64(po[i + 1], r0, a.B);
+                g.row = (int)r0;
+                g.k1 = r1 > r0 ? prefix_of(a, i) : 0;
+            }
+            g.r0 = (int)r0, g.r1 = (int)r1;
+            const int64_t o0 = a.off[r0], o1 = a.off[r1];
+            const int64_t t0 = clamp64(o0, 0, a.T), t1 = clamp64(o1, t0, a.T);
+            g.t0 = t0;
+            g.ntok = (int)(t1 - t0);
+            if (s < a.B && o0 == t0 && o1 == t1 && g.k1 == a.len[s] && g.k1 - g.ntok >= g.k0)
+                g.base = g.k1 - g.ntok;
+            wide = s < a.B ? a.wide_own : a.wide_prefix;
+            mine[wide] = wide ? Wide(a, g).tiles(a, g) : Narrow(a, g).tiles();
+            if (g.ntok > 0 && g.k1 <= g.k0) atomicAdd(&sh_empty, 1);
+        }
+        int64_t incl[2];
+        int cnt[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            incl[w] = mine[w];
+            cnt[w] = mine[w] > 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t v = __shfl_up_sync(~0u, incl[w], d);
+                const int c = __shfl_up_sync(~0u, cnt[w], d);
+                if (lane >= d) incl[w] += v, cnt[w] += c;
+            }
+            if (lane == 31) sh_tiles[w][warp] = incl[w], sh_count[w][warp] = cnt[w];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            int64_t before = tiles0[w];
+            int at = count0[w];
+            for (int i = 0; i < kPlanThreads / 32; ++i) {
+                if (i < warp) before += sh_tiles[w][i], at += sh_count[w][i];
+                tiles0[w] += sh_tiles[w][i];
+                count0[w] += sh_count[w][i];
+            }
+            if (s < nseg && wide == (w == 1)) g.before = before + incl[w] - mine[w];
+            if (mine[w] > 0) {
+                order[w][at + cnt[w] - 1] = s;
+                if (at + cnt[w] <= kPlanHeld) sh_before[w][at + cnt[w] - 1] = before + incl[w] - mine[w];
+            }
+        }
+        if (s < nseg) a.segs[s] = g;
+        __syncthreads();
     }
+    int workers[2];
+    workers[0] = (int)min(tiles0[0], (int64_t)a.ctas * a.phases);
+    workers[1] = (int)min(tiles0[1], (int64_t)a.ctas);
+    if (tid == 0) {
+        Plan p;
+        p.total[0] = tiles0[0], p.total[1] = tiles0[1];
+        p.workers[0] = workers[0], p.workers[1] = workers[1];
+        p.empty = sh_empty;
+        *a.plan = p;
+    }
+    __threadfence_block();  // the segments written above, before other threads read them
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+        for (int c = tid; c < workers[w]; c += kPlanThreads) {
+            const int64_t x = tiles0[w] * c / workers[w];
+            int lo = 0, hi = count0[w] - 1;  // the last listed segment that begins at or before x
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((mid < kPlanHeld ? sh_before[w][mid] : a.segs[order[w][mid]].before) <= x) lo = mid;
+                else hi = mid - 1;
+            }
+            Start st;
+            st.at = lo;
+            st.tiles = x - (lo < kPlanHeld ? sh_before[w][lo] : a.segs[order[w][lo]].before);
+            a.starts[w * kNarrowWorkers + c] = st;
+        }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel(const Args a) {
+struct Cfg {
+    static constexpr int kWarps = D > 128 ? 4 : kNarrowWarps;  // of a CTA
+    static constexpr int kStageBytes = 2 * kStep * D;          // a warp's K and V
+    static constexpr int kStages = D == 64 ? 5 : D == 128 ? 3 : 2;
+    static constexpr int kWarpBytes = kStages * kStageBytes;
+    static constexpr int kQBytes = D > 128 ? kRows * D * 2 : 0;  // a warp's query fragments
+    static constexpr int kSmem = kWarps * (kWarpBytes + kQBytes);
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const Args a) {
     using C = Cfg<D>;
     constexpr int ST = C::kStages, KS = D / 16, NT = D / 8, H = D / 64;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int64_t sh_pre[kThreads + 1];
-    __shared__ uint32_t sh_mask[4][ST];
-    __shared__ float sh_m[4][kRows], sh_l[4][kRows];
+    __shared__ uint32_t sh_mask[C::kWarps][ST];
     griddep_launch_dependents();
     griddep_wait();
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
-    const int lo = a.wide_own ? a.B : 0, hi = a.wide_prefix ? a.B : a.B + a.Ng;
-    const int per = deal_segments<kThreads>(lo, hi, sh_pre, a.before, a.total, [&](int s) {
-        const Segment g = segment(a, s);
-        const Narrow n(a, g);
-        if (blockIdx.x == 0 && a.Ng == 0 && n.ktiles == 0) no_keys<D>(a, g);
-        return n.tiles(a);
-    });
-    const int64_t total = sh_pre[kThreads];
-    const int64_t ctas = min((int64_t)a.narrow_ctas, total);  // none of them without a tile
-    if (blockIdx.x >= ctas) return;
-    const int64_t x0 = total * blockIdx.x / ctas, x1 = total * (blockIdx.x + 1) / ctas;
-    const int stretch = stretch_of<kThreads>(sh_pre, x0);
-    int s = lo + stretch * per;
-    int64_t at = sh_pre[stretch];  // first tile of segment s
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
+    if (a.Ng == 0 && a.plan->empty > 0) clear_rows<D>(a);
+    // this warp's worker, and its head among the worker's
+    const int me = blockIdx.x * a.phases + warp / a.heads, hw = warp % a.heads;
+    const int64_t total = a.plan->total[0], workers = a.plan->workers[0];
+    if (warp >= a.phases * a.heads || me >= workers) return;
+    int64_t left = total * (me + 1) / workers - total * me / workers;  // tiles of the range
+    int64_t from = a.starts[me].tiles, at = a.starts[me].at;           // next: in its segment; that one
+    bool first = true;
     const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
-    uint2 *qs = reinterpret_cast<uint2 *>(smem + 4 * C::kWarpBytes);  // [KS][kRows / 8][32] (D > 128)
+    uint2 *qs = reinterpret_cast<uint2 *>(smem + C::kWarps * C::kWarpBytes + warp * C::kQBytes);  // [KS][2][32]
 
-    int64_t x = x0;
-    while (x < x1) {
-        Segment sg = segment(a, s);
-        Narrow nw(a, sg);
-        while (at + nw.tiles(a) <= x) {
-            at += nw.tiles(a);
-            sg = segment(a, ++s);
-            nw = Narrow(a, sg);
-        }
-        const int unit = (int)((x - at) / nw.ktiles);
-        const int kt0 = (int)((x - at) - (int64_t)unit * nw.ktiles);
-        const int kt1 = (int)min((int64_t)nw.ktiles, kt0 + (x1 - x));
-        const int h = unit / nw.rtiles, rt = unit - h * nw.rtiles;
+    while (left > 0) {
+        const int s = a.order[at];
+        const Segment sg = a.segs[s];
+        const Narrow nw(a, sg);
+        const int ktiles = nw.ktiles;
+        const int unit = (int)(from / ktiles);
+        const int kt0 = (int)(from - (int64_t)unit * ktiles);
+        const int kt1 = (int)min((int64_t)ktiles, kt0 + left);
+        const int rt = unit / nw.groups, h = (unit - rt * nw.groups) * a.heads + hw;
         const int64_t nrows = (int64_t)sg.ntok * a.G, row0 = (int64_t)rt * kRows;
+        if (first && a.Ng == 0 && hw == 0 && lane == 0) {
+            // the range begins in the middle of a unit: what the join will need
+            Split sp;
+            sp.rows = 0;
+            const int64_t u0 = sg.before + from - kt0;
+            if (kt0 > 0 && total * (me - 1) / workers <= u0) {
+                const Pieces pc(u0, ktiles, total, workers);
+                sp.token = sg.t0 + row0 / a.G, sp.sub = (int)(row0 % a.G), sp.head = h;
+                sp.rows = (int)min((int64_t)kRows, nrows - row0);
+                sp.n = pc.n, sp.c0 = pc.c0, sp.first = pc.first;
+            }
+            a.splits[me] = sp;
+        }
+        left -= kt1 - kt0;
+        from += kt1 - kt0;
+        if (from == nw.tiles()) from = 0, ++at;
+        const bool begins = first;
+        first = false;
+        if (h >= a.Hk) continue;  // (the last group of heads may be short)
 
         // queries: rows g and g + 8 of the tile, channels 64 i + 16 j .. + 15
         uint32_t qf[D <= 128 ? KS : 1][4];
@@ -171,9 +291,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
             const float up = row_power(top);
-            f[r] = a.scale * a.ks[h] * kLog2e / up;
+            f[r] = a.scale * a.ks[h] * kLog2e * inverse_power(up);
             pos[r] = 0x7FFFFFFF;
-            if (ok) pos[r] = position(a, s < a.B ? s : min(upper(a.off, a.B, t), a.B - 1), t);
+            if (ok) {
+                int b = s;
+                if (s >= a.B) b = min(sg.r0 + upper(a.off + sg.r0, sg.r1 - sg.r0, t), a.B - 1);
+                pos[r] = position(a, b, t);
+            }
 #pragma unroll
             for (int i = 0; i < 2 * H; ++i) {
                 const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -189,19 +313,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
                     if constexpr (D <= 128) {
                         qf[ks][r] = v[2 * k];
                         qf[ks][2 + r] = v[2 * k + 1];
-                    } else if (warp == 0) {
+                    } else {
                         qs[(ks * 2 + r) * 32 + lane] = make_uint2(v[2 * k], v[2 * k + 1]);
                     }
                 }
             }
         }
-        if (D > 128) __syncthreads();
+        if (D > 128) __syncwarp();
         const bool causal = __any_sync(~0u, min(pos[0], pos[1]) < sg.k1 - 1);
 
         const int32_t *tab = a.table + (int64_t)sg.row * a.width;
         // this lane's key of tile kt: its cache row, or -1
         auto slot_of = [&](int kt) -> int {
-            const int64_t p = (int64_t)sg.k0 + (int64_t)kt * kTile + warp * 32 + lane;
+            const int64_t p = (int64_t)sg.k0 + (int64_t)kt * kStep + lane;
             if (kt >= kt1 || p >= sg.k1) return -1;
             const uint32_t blk = (uint32_t)p / (uint32_t)a.bs;
             const int64_t id = tab[blk];
@@ -209,8 +333,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
             const int64_t slot = id * a.bs + ((uint32_t)p - blk * (uint32_t)a.bs);
             return slot < a.S ? (int)slot : -1;
         };
-        auto issue = [&](int kt, int slot) {
-            const int st = kt % ST;
+        auto issue = [&](int kt, int st, int slot) {
             const uint32_t mask = __ballot_sync(~0u, slot >= 0);
             if (lane == 0) sh_mask[warp][st] = mask;
             const uint32_t dst = ring + st * C::kStageBytes;
@@ -232,17 +355,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
         for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) issue(kt0 + i, slot_of(kt0 + i));
+        for (int i = 0; i < ST - 1; ++i) issue(kt0 + i, i, slot_of(kt0 + i));
         int next = slot_of(kt0 + ST - 1);
+        int st = 0, fill = ST - 1;  // stages in turn
         for (int kt = kt0; kt < kt1; ++kt) {
             __syncwarp();  // the stage written below has been read by all lanes
-            issue(kt + ST - 1, next);
+            issue(kt + ST - 1, fill, next);
             next = slot_of(kt + ST);
             asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
             __syncwarp();
-            const int st = kt % ST;
-            const uint32_t kb = ring + st * C::kStageBytes, vb = kb + 32 * D;
-            const uint32_t mask = sh_mask[warp][st];
+            const int use_st = st;
+            st = st + 1 == ST ? 0 : st + 1;
+            fill = fill + 1 == ST ? 0 : fill + 1;
+            const uint32_t kb = ring + use_st * C::kStageBytes, vb = kb + 32 * D;
+            const uint32_t mask = sh_mask[warp][use_st];
             if (mask == 0) continue;
             // scores of keys 8 t + 2 j, + 1 for rows g and g + 8
             float sc[4][4];
@@ -269,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
             }
             float top[2] = {-INFINITY, -INFINITY};
             // a key of the mask lies below 2^31, and so do its tile's others but for the last few
-            const uint32_t p0 = (uint32_t)sg.k0 + (uint32_t)kt * kTile + warp * 32 + 2 * j;
+            const uint32_t p0 = (uint32_t)sg.k0 + (uint32_t)kt * kStep + 2 * j;
             const bool all = mask == ~0u && !causal;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -356,83 +482,49 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kCtasPerSm) attention_kernel
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();
-        // join of the four warps in the ring's memory
-        float *red = reinterpret_cast<float *>(smem);
+        const bool full = kt1 - kt0 == ktiles, direct = full && a.Ng == 0;
+        constexpr int W = D == 64 ? 8 : 16;  // channels of one column of a fragment
+        float *const po = full ? a.whole : a.part, *const pml = full ? a.whole_ml : a.part_ml;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             l[r] += __shfl_xor_sync(~0u, l[r], 1);
             l[r] += __shfl_xor_sync(~0u, l[r], 2);
-            if (j == 0) {
-                sh_m[warp][g + 8 * r] = m[r];
-                sh_l[warp][g + 8 * r] = l[r];
-            }
-            float *dst = red + (warp * kRows + g + 8 * r) * D;
-            constexpr int W = D == 64 ? 8 : 16;  // channels of one column of a fragment
+            const int64_t rr = row0 + g + 8 * r;
+            if (rr >= nrows) continue;
+            const int64_t t = sg.t0 + rr / a.G;
+            const int hq = h * a.G + (int)(rr % a.G);
+            const int64_t slot = full ? ((s < a.B ? a.T : 0) + t) * a.Hq + hq
+                                      : ((int64_t)(2 * me + (begins ? 0 : 1)) * a.heads + hw) * kRows + g + 8 * r;
+            const float inv = l[r] > 0.0f ? a.vs[h] / l[r] : 0.0f;
+            // the thread's channels of a row are 2 W neighbours (of each 128)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int base = (n / W) * 128 + n % W;
-                dst[base + W * (2 * j)] = o[n][2 * r];
-                dst[base + W * (2 * j + 1)] = o[n][2 * r + 1];
-            }
-        }
-        __syncthreads();
-        {
-            const int r = tid >> 3, d0 = (tid & 7) * 4;
-            const int64_t rr = row0 + r;
-            if (rr < nrows) {
-                float top = -INFINITY, wt[4], sum = 0.0f;
+            for (int n = 0; n < NT; n += 4)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) top = fmaxf(top, sh_m[w][r]);
-                const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    wt[w] = ex2(sh_m[w][r] - base);
-                    sum += wt[w] * sh_l[w][r];
-                }
-                const int64_t t = sg.t0 + rr / a.G;
-                const int hq = h * a.G + (int)(rr % a.G);
-                const bool full = kt1 - kt0 == nw.ktiles, direct = full && a.Ng == 0;
-                const int64_t slot =
-                    full ? ((s < a.B ? a.T : 0) + t) * a.Hq + hq
-                         : (int64_t)(2 * blockIdx.x + (x == x0 ? 0 : 1)) * kRows + r;
-                float *po = (full ? a.whole : a.part) + slot * D;
-                float *ml = (full ? a.whole_ml : a.part_ml) + slot * 2;
-                const float inv = sum > 0.0f ? a.vs[h] / sum : 0.0f;
-#pragma unroll
-                for (int d = d0; d < D; d += 32) {
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float4 p = *reinterpret_cast<const float4 *>(red + (w * kRows + r) * D + d);
-                        v.x += wt[w] * p.x;
-                        v.y += wt[w] * p.y;
-                        v.z += wt[w] * p.z;
-                        v.w += wt[w] * p.w;
-                    }
+                for (int c = 0; c < 2; ++c) {
+                    const int d = (n / W) * 128 + n % W + W * (2 * j + c);
+                    const float v0 = o[n][2 * r + c], v1 = o[n + 1][2 * r + c], v2 = o[n + 2][2 * r + c],
+                                v3 = o[n + 3][2 * r + c];
                     if (direct) {
-                        const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x * inv, v.y * inv),
-                                             b1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+                        const __nv_bfloat162 b0 = __floats2bfloat162_rn(v0 * inv, v1 * inv),
+                                             b1 = __floats2bfloat162_rn(v2 * inv, v3 * inv);
                         uint2 w;
                         w.x = *reinterpret_cast<const uint32_t *>(&b0);
                         w.y = *reinterpret_cast<const uint32_t *>(&b1);
                         *reinterpret_cast<uint2 *>(a.out + t * a.ldo + (int64_t)hq * D + d) = w;
                     } else {
-                        *reinterpret_cast<float4 *>(po + d) = v;
+                        *reinterpret_cast<float4 *>(po + slot * D + d) = make_float4(v0, v1, v2, v3);
                     }
                 }
-                if ((tid & 7) == 0) {
-                    if (!direct) {
-                        ml[0] = top;
-                        ml[1] = sum;
-                    } else if (a.lse) {
-                        a.lse[t * a.Hq + hq] = sum > 0.0f ? kLn2 * (top + log2f(sum)) : -INFINITY;
-                    }
+            if (j == 0) {
+                if (!direct) {
+                    pml[slot * 2] = m[r];
+                    pml[slot * 2 + 1] = l[r];
+                } else if (a.lse) {
+                    a.lse[t * a.Hq + hq] = l[r] > 0.0f ? kLn2 * (m[r] + log2f(l[r])) : -INFINITY;
                 }
             }
         }
-        __syncthreads();
-        x += kt1 - kt0;
+        __syncwarp();
     }
 }
 
@@ -485,102 +577,83 @@ struct Row {
     }
 };
 
-// The pieces of a unit of `n` tiles from u0 on, dealt to several CTAs: CTA c's is
-// its first piece (slot 2 c) where its range begins in the unit, else its last.
-struct Pieces {
-    int c0, n, first;  // CTAs, and the first one's slot
-    __device__ Pieces(int64_t u0, int64_t tiles, int64_t total, int64_t ctas) {
-        c0 = cta_of(u0, total, ctas);
-        n = cta_of(u0 + tiles - 1, total, ctas) - c0 + 1;
-        first = 2 * c0 + (total * c0 / ctas >= u0 ? 0 : 1);
-    }
-    __device__ int64_t slot(int i) const { return i == 0 ? first : 2 * (c0 + i); }
-};
-
-// Without groups: the rows of the units that more than one CTA had.  The ranges'
-// borders are gone through; a unit is joined at the first border inside it.  A
-// CTA takes kJoinRows rows of a border's unit.
-constexpr int kJoinRows = 16;
+// Without groups: the rows of the units that more than one worker had, each found by
+// the first worker that began in its middle.  A CTA takes the rows r0, r0 + 4, ... of one
+// of them (and one head); a row's pieces are shared by one warp, or by eight where there
+// are many.
+constexpr int kJoinRows = 4;
 
 template <int D>
 __global__ void __launch_bounds__(256, 4) attention_join_split_kernel(const Args a) {
     griddep_launch_dependents();
     griddep_wait();
+    __shared__ float sh_o[8][D];
+    __shared__ float2 sh_ml[8];
     const bool wide = a.wide_own;
-    const int rows = wide ? kWideRows : kRows, per = rows / kJoinRows;
-    const int border = blockIdx.x / per + 1, r0 = (blockIdx.x % per) * kJoinRows;
-    const int64_t total = a.total[wide], ctas = min((int64_t)(wide ? a.wide_ctas : a.narrow_ctas), total);
-    if (border >= ctas) return;
-    const int64_t x = total * border / ctas;
-    int lo = 0, hi = a.B - 1;  // the last segment that begins at or before x (one with tiles)
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.before[mid] <= x) lo = mid; else hi = mid - 1;
-    }
-    const Segment g = segment(a, lo);
-    int64_t u0 = a.before[lo], row0;
-    int n, h, count;
-    if (wide) {
-        const Wide w(a, g);
-        int rt = 0;
-        while (u0 + (int64_t)w.ktiles(g, rt) * a.Hk <= x) u0 += (int64_t)w.ktiles(g, rt++) * a.Hk;
-        n = w.ktiles(g, rt);
-        h = (int)((x - u0) / n);
-        row0 = (int64_t)rt * w.tokens * a.G;
-        count = (int)min((int64_t)w.tokens * a.G, (int64_t)g.ntok * a.G - row0);
-        u0 += (int64_t)h * n;
-    } else {
-        const Narrow w(a, g);
-        n = w.ktiles;
-        const int unit = (int)((x - u0) / n);
-        h = unit / w.rtiles;
-        row0 = (int64_t)(unit - h * w.rtiles) * kRows;
-        count = (int)min((int64_t)kRows, (int64_t)g.ntok * a.G - row0);
-        u0 += (int64_t)unit * n;
-    }
-    if (u0 == x || total * (border - 1) / ctas > u0) return;
-    const Pieces p(u0, n, total, ctas);
+    const int heads = wide ? 1 : a.heads, rows = wide ? kWideRows : kRows;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int worker = blockIdx.x / heads, hw = blockIdx.x % heads;
+    if (worker >= a.plan->workers[wide]) return;
+    const Split sp = a.splits[(wide ? kNarrowWorkers : 0) + worker];
+    const int h = sp.head + hw;
+    if (sp.rows == 0 || h >= a.Hk) return;
     const float *po = wide ? a.wpart : a.part, *ml = wide ? a.wpart_ml : a.part_ml;
-    for (int r = r0 + (threadIdx.x >> 5); r < min(count, r0 + kJoinRows); r += 8) {
+    const int each = sp.n > 8 ? 8 : 1;  // warps a row
+    for (int r = blockIdx.y + gridDim.y * (warp / each); r < sp.rows; r += gridDim.y * (8 / each)) {
+        auto slot = [&](int i) -> int64_t {
+            return ((i == 0 ? sp.first : 2 * (sp.c0 + i)) * (int64_t)heads + hw) * rows + r;
+        };
         Row<D> row;
-        row.add(po, ml, p.n, [&](int i) { return p.slot(i) * rows + r; });
-        const int64_t rr = row0 + r;
-        row.write(a, g.t0 + rr / a.G, h * a.G + (int)(rr % a.G));
+        const uint32_t rr = sp.sub + r, tok = rr / (uint32_t)a.G;
+        const int64_t t = sp.token + tok;
+        const int hq = h * a.G + (int)(rr - tok * a.G);
+        if (each == 1) {
+            row.add(po, ml, sp.n, slot);
+            row.write(a, t, hq);
+            continue;
+        }
+        const int i0 = sp.n * warp / 8, i1 = sp.n * (warp + 1) / 8;
+        row.add(po, ml, i1 - i0, [&](int i) { return slot(i0 + i); });
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) sh_o[warp][lane + 32 * e] = row.o[e];
+        if (lane == 0) sh_ml[warp] = make_float2(row.m, row.l);
+        __syncthreads();
+        if (warp == 0) {
+            Row<D> all;
+            all.add(&sh_o[0][0], reinterpret_cast<const float *>(sh_ml), 8, [](int i) { return (int64_t)i; });
+            all.write(a, t, hq);
+        }
+        __syncthreads();
     }
 }
 
-// With groups: every row, from its prefix and its request's own part.  One warp a
-// row.
+// With groups: every row, from its prefix and its request's own part.  A CTA takes
+// rows of request blockIdx.x, a warp one at a time.
 template <int D>
 __global__ void __launch_bounds__(256, 4) attention_join_kernel(const Args a) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t first = clamp64(a.off[0], 0, a.T), last = clamp64(a.off[a.B], 0, a.T);
-    for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < a.T * a.Hq; i += gridDim.x * 8ll) {
-        const int64_t t = i / a.Hq;
-        const int hq = (int)(i - t * a.Hq), h = hq / a.G;
-        if (t < first || t >= last) continue;
-        const int b = upper(a.off, a.B, t);
-        if (b >= a.B) continue;
+    const Segment own = a.segs[blockIdx.x];
+    Segment pre;
+    pre.k0 = pre.k1 = 0;
+    if (own.group >= 0) pre = a.segs[a.B + own.group];
+    const Plan plan = *a.plan;
+    const int64_t rows = (int64_t)own.ntok * a.Hq;
+    for (int64_t i = blockIdx.y * 8ll + (threadIdx.x >> 5); i < rows; i += gridDim.y * 8ll) {
+        const uint32_t tok = (uint32_t)(i / a.Hq);
+        const int64_t t = own.t0 + tok;
+        const int hq = (int)(i - (int64_t)tok * a.Hq), h = hq / a.G, gi = hq - h * a.G;
         Row<D> row;
-        for (int k = 0; k < 2; ++k) {
-            int s = b;
-            if (k == 0) {  // the prefix
-                if (b < a.po[0]) continue;
-                const int gi = upper(a.po, a.Ng, b);
-                if (gi >= a.Ng) continue;
-                s = a.B + gi;
-            }
-            const Segment g = segment(a, s);
+        for (int k = 0; k < 2; ++k) {  // the prefix, then the own part
+            const Segment &g = k == 0 ? pre : own;
             if (g.k1 <= g.k0 || t < g.t0 || t >= g.t0 + g.ntok) continue;
-            const bool wide = s < a.B ? a.wide_own : a.wide_prefix;
-            const int64_t rr = (t - g.t0) * a.G + hq % a.G;
-            int64_t u0 = a.before[s];
+            const bool wide = k == 0 ? a.wide_prefix : a.wide_own;
+            int64_t u0 = g.before;
             int n, r;
             if (wide) {
                 const Wide w(a, g);
-                const int rt = (int)((t - g.t0) / w.tokens);
+                const int rt = (int)((uint32_t)(t - g.t0) / (uint32_t)w.tokens);
                 int64_t skip;
                 if (g.base >= 0) {
                     skip = w.head_tiles(g, lane, rt, 32);
@@ -591,22 +664,23 @@ __global__ void __launch_bounds__(256, 4) attention_join_kernel(const Args a) {
                 }
                 n = w.ktiles(g, rt);
                 u0 += skip * a.Hk + (int64_t)h * n;
-                r = (int)(rr - (int64_t)rt * w.tokens * a.G);
+                r = (int)((t - g.t0) - (int64_t)rt * w.tokens) * a.G + gi;
             } else {
                 const Narrow w(a, g);
+                const int64_t rr = (t - g.t0) * a.G + gi;
                 n = w.ktiles;
-                u0 += (h * (int64_t)w.rtiles + rr / kRows) * n;
+                u0 += (rr / kRows * w.groups + h / a.heads) * n;
                 r = (int)(rr % kRows);
             }
-            const int64_t total = a.total[wide], ctas = min((int64_t)(wide ? a.wide_ctas : a.narrow_ctas), total);
-            const Pieces p(u0, n, total, ctas);
+            const Pieces p(u0, n, plan.total[wide], plan.workers[wide]);
             if (p.n == 1) {
-                const int64_t at = (s < a.B ? a.T * a.Hq : 0) + i;
+                const int64_t at = ((k == 1 ? a.T : 0) + t) * a.Hq + hq;
                 row.add(a.whole, a.whole_ml, 1, [&](int) { return at; });
             } else if (wide) {
                 row.add(a.wpart, a.wpart_ml, p.n, [&](int j) { return p.slot(j) * kWideRows + r; });
             } else {
-                row.add(a.part, a.part_ml, p.n, [&](int j) { return p.slot(j) * kRows + r; });
+                row.add(a.part, a.part_ml, p.n,
+                        [&](int j) { return (p.slot(j) * a.heads + h % a.heads) * kRows + r; });
             }
         }
         row.write(a, t, hq);
@@ -619,7 +693,7 @@ constexpr int64_t kWideFrom = 32;
 
 struct Layout {
     bool wide_own, wide_prefix;
-    size_t part, part_ml, wpart, wpart_ml, whole, whole_ml, before, total, bytes;
+    size_t part, part_ml, wpart, wpart_ml, whole, whole_ml, segs, order, starts, splits, plan, bytes;
 };
 
 Layout layout(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B, int64_t Ng) {
@@ -629,10 +703,10 @@ Layout layout(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B, int64_t N
     const bool can = D <= 128 && G <= 128;
     w.wide_own = can && T * G >= kWideFrom * B;
     w.wide_prefix = can && Ng > 0 && T * G >= kWideFrom * Ng;
-    const size_t slots = !w.wide_own || (Ng > 0 && !w.wide_prefix) ? 2 * kNarrowCtas * kRows : 0,
-                 wslots = w.wide_own || w.wide_prefix ? 2 * kWideCtas * kWideRows : 0,
+    const size_t slots = !w.wide_own || (Ng > 0 && !w.wide_prefix) ? 2 * kNarrowWorkers * kRows : 0,
+                 wslots = w.wide_own || w.wide_prefix ? 2 * kMaxCtas * kWideRows : 0,
                  rows = Ng > 0 ? (size_t)(2 * T * Hq) : 0;
-    size_t at = 0;
+    size_t at = 256;  // (room to begin at a multiple of 256)
     auto take = [&](size_t n) {
         const size_t p = at;
         at += up(n);
@@ -644,8 +718,11 @@ Layout layout(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B, int64_t N
     w.wpart_ml = take(wslots * 8);
     w.whole = take(rows * D * 4);
     w.whole_ml = take(rows * 8);
-    w.before = take((size_t)(B + Ng) * 8);
-    w.total = take(16);
+    w.segs = take((size_t)(B + Ng) * sizeof(Segment));
+    w.order = take((size_t)(B + Ng) * 2 * sizeof(int));
+    w.starts = take((kNarrowWorkers + kMaxCtas) * sizeof(Start));
+    w.splits = take((kNarrowWorkers + kMaxCtas) * sizeof(Split));
+    w.plan = take(sizeof(Plan));
     w.bytes = at;
     return w;
 }
@@ -674,21 +751,20 @@ jet_status launch(const DeviceInfo &dev, const Args &a, cudaStream_t stream) {
             done[dev.ordinal] = dev.context;
         }
     }
-    jet_status st = JET_OK;
-    if (!a.wide_own || (a.Ng > 0 && !a.wide_prefix))
-        st = launch_pdl(attention_kernel<D>, dim3((unsigned)a.narrow_ctas), dim3(kThreads), C::kSmem,
-                        stream, a);
+    jet_status st = launch_pdl(attention_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+    if (st == JET_OK && (!a.wide_own || (a.Ng > 0 && !a.wide_prefix)))
+        st = launch_pdl(attention_kernel<D>, dim3((unsigned)a.ctas), dim3(32 * C::kWarps), C::kSmem, stream, a);
     if (st == JET_OK && (a.wide_own || a.wide_prefix)) st = launch_attention_wide(dev, a, D, stream);
     if (st != JET_OK) return st;
     if (a.Ng > 0) {
-        const int64_t want = (a.T * a.Hq + 7) / 8, cap = (int64_t)dev.num_sms * 8;
-        return launch_pdl(attention_join_kernel<D>, dim3((unsigned)(want < cap ? want : cap)), dim3(256),
-                          0, stream, a);
+        // rows of a request on average, eight warps a CTA
+        const int64_t want = (a.T * a.Hq / a.B + 7) / 8;
+        return launch_pdl(attention_join_kernel<D>, dim3((unsigned)a.B, (unsigned)(want < 1 ? 1 : want > 1024 ? 1024 : want)),
+                          dim3(256), 0, stream, a);
     }
-    const int borders = (a.wide_own ? a.wide_ctas : a.narrow_ctas) - 1;
-    const int per = (a.wide_own ? kWideRows : kRows) / kJoinRows;
-    if (borders <= 0) return JET_OK;
-    return launch_pdl(attention_join_split_kernel<D>, dim3((unsigned)(borders * per)), dim3(256), 0, stream, a);
+    const int units = a.wide_own ? a.ctas : a.ctas * a.phases * a.heads;
+    return launch_pdl(attention_join_split_kernel<D>, dim3((unsigned)units, a.wide_own ? 8 : kJoinRows), dim3(256),
+                      0, stream, a);
 }
 
 inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -742,19 +818,24 @@ jet_status jet_kv_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H
     a.table = table, a.width = width, a.bs = block_size, a.off = offsets, a.len = lengths;
     a.B = (int)B, a.po = prefix_offsets, a.pl = prefix_lengths, a.Ng = (int)n_prefix;
     a.scale = scale, a.out = out, a.ldo = ldo, a.lse = lse;
-    uint8_t *base = static_cast<uint8_t *>(ws);
+    // arrays begin at multiples of 256
+    uint8_t *base = static_cast<uint8_t *>(ws) - (reinterpret_cast<uintptr_t>(ws) & 255);
     a.part = reinterpret_cast<float *>(base + w.part);
     a.part_ml = reinterpret_cast<float *>(base + w.part_ml);
     a.whole = reinterpret_cast<float *>(base + w.whole);
     a.whole_ml = reinterpret_cast<float *>(base + w.whole_ml);
     a.wpart = reinterpret_cast<float *>(base + w.wpart);
     a.wpart_ml = reinterpret_cast<float *>(base + w.wpart_ml);
-    a.before = reinterpret_cast<int64_t *>(base + w.before);
-    a.total = reinterpret_cast<int64_t *>(base + w.total);
+    a.segs = reinterpret_cast<Segment *>(base + w.segs);
+    a.order = reinterpret_cast<int *>(base + w.order);
+    a.starts = reinterpret_cast<Start *>(base + w.starts);
+    a.splits = reinterpret_cast<Split *>(base + w.splits);
+    a.plan = reinterpret_cast<Plan *>(base + w.plan);
     a.wide_own = w.wide_own, a.wide_prefix = w.wide_prefix;
-    const int per_sm = D > 128 ? 1 : 2;  // narrow CTAs on an SM
-    a.narrow_ctas = dev.num_sms * per_sm < kNarrowCtas ? dev.num_sms * per_sm : kNarrowCtas;
-    a.wide_ctas = dev.num_sms < kWideCtas ? dev.num_sms : kWideCtas;
+    a.ctas = dev.num_sms < kMaxCtas ? dev.num_sms : kMaxCtas;
+    const int warps = D > 128 ? Cfg<256>::kWarps : kNarrowWarps;
+    a.heads = a.Hk < warps ? a.Hk : warps;
+    a.phases = warps / a.heads;
     const cudaStream_t s = as_stream(stream);
     return D == 64 ? launch<64>(dev, a, s) : D == 128 ? launch<128>(dev, a, s) : launch<256>(dev, a, s);
 }

@@ -9,11 +9,13 @@
 namespace jet {
 namespace attn {
 
-constexpr int kTile = 128;         // keys of a tile
+constexpr int kTile = 128;         // keys of a wide tile
+constexpr int kStep = 32;          // keys of a narrow tile
 constexpr int kRows = 16;          // rows of a narrow unit
-constexpr int kNarrowCtas = 320;   // most CTAs of the narrow kernel (two on each SM)
+constexpr int kMaxCtas = 160;      // most CTAs of a launch (one on each SM)
+constexpr int kNarrowWarps = 8;    // most of a CTA
+constexpr int kNarrowWorkers = kMaxCtas * kNarrowWarps;
 constexpr int kWideRows = 256;     // rows of a wide unit's pieces
-constexpr int kWideCtas = 160;     // most CTAs of the wide kernel (one on each SM)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -38,14 +40,18 @@ struct Args {
     float *lse;
     // Which segments the wide kernel takes: requests' own parts, groups' prefixes.
     bool wide_own, wide_prefix;
-    int narrow_ctas, wide_ctas;    // CTAs of each launch
-    // Workspace.  Pieces of units that several CTAs share, two a CTA (narrow:
-    // kRows rows each, wide: kWideRows); with groups, whole units by row (prefix,
-    // then own); the tiles of the same kernel before each segment, and their totals
-    // (narrow, wide).
+    int ctas;                      // of a launch
+    int heads, phases;             // narrow: KV heads a worker has, workers a CTA has
+    // Workspace.  Partial results of pieces of units that several workers share, two
+    // a worker (narrow: heads x kRows rows each, wide: kWideRows); with groups, whole
+    // units by row (prefix, then own); and the plan.
     float *part, *part_ml, *wpart, *wpart_ml;
     float *whole, *whole_ml;       // [2][T * Hq][D], [..][2]
-    int64_t *before, *total;       // [B + Ng], [2]
+    struct Segment *segs;          // [B + Ng]
+    int *order;                    // [2][B + Ng] the segments with work (narrow, wide)
+    struct Start *starts;          // [kNarrowWorkers + kMaxCtas] of the workers' ranges
+    struct Split *splits;          // the same, of the units that the ranges begin in
+    struct Plan *plan;
 };
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
@@ -78,57 +84,52 @@ __device__ __forceinline__ int prefix_of(const Args &a, int i) {
 // Segment s < B: the own part of request s; B + i: the prefix of group i.
 struct Segment {
     int64_t t0;        // first token
+    int64_t before;    // tiles of its kernel's segments before it
     int ntok;
     int k0, k1;        // keys
     int row;           // table row
+    int r0, r1;        // requests r0 .. r1 - 1
     int base;          // own part: the first new token's position, if its queries see k0 and
                        // the last one's position is k1 - 1; else -1
+    int group;         // own part: the request's group, or -1
 };
 
-__device__ inline Segment segment(const Args &a, int s) {
-    Segment g;
-    int64_t r0, r1;
-    g.base = -1;
-    g.k0 = 0;
-    if (s < a.B) {
-        r0 = s;
-        r1 = s + 1;
-        g.row = s;
-        g.k1 = keys_of(a, s);
-        if (a.Ng > 0 && s >= a.po[0]) {
-            const int i = upper(a.po, a.Ng, s);
-            if (i < a.Ng) g.k0 = min(prefix_of(a, i), g.k1);
-        }
-    } else {
-        const int i = s - a.B;
-        r0 = clamp64(a.po[i], 0, a.B);
-        r1 = clamp64(a.po[i + 1], r0, a.B);
-        g.row = (int)r0;
-        g.k1 = r1 > r0 ? prefix_of(a, i) : 0;
-    }
-    const int64_t o0 = a.off[r0], o1 = a.off[r1];
-    const int64_t t0 = clamp64(o0, 0, a.T), t1 = clamp64(o1, t0, a.T);
-    g.t0 = t0;
-    g.ntok = (int)(t1 - t0);
-    if (s < a.B && o0 == t0 && o1 == t1 && g.k1 == a.len[s] && g.k1 - g.ntok >= g.k0)
-        g.base = g.k1 - g.ntok;
-    return g;
-}
+// Where a worker's range begins: the segment order[at], `tiles` tiles into it.
+struct Start {
+    int64_t tiles;
+    int64_t at;
+};
+
+struct Plan {
+    int64_t total[2];  // tiles (narrow, wide)
+    int workers[2];    // none of them without a tile
+    int empty;         // segments with tokens and no keys
+};
+
+// The unit that a worker's range begins in the middle of, if that is the unit's first
+// such worker: what is to be joined.
+struct Split {
+    int64_t token;     // the unit's first row: token and query head within the KV head's group
+    int sub;
+    int head;          // its first KV head
+    int rows;          // 0: nothing to join
+    int n, c0, first;  // pieces: their number, the first one's worker and slot
+};
 
 // Position of token t of request b.
 __device__ __forceinline__ int position(const Args &a, int b, int64_t t) {
     return (int)clamp64((int64_t)a.len[b] - (a.off[b + 1] - t), -1, 0x7FFFFFFF);
 }
 
-// Narrow units: 16 rows, a row tile of one KV head; all tiles of a head's row
-// tiles one after another.
+// Narrow units: 16 rows of each of `heads` KV heads, whose keys lie side by side.
 struct Narrow {
-    int rtiles, ktiles;
+    int rtiles, groups, ktiles;  // row tiles, groups of heads, key tiles
     __device__ Narrow(const Args &a, const Segment &g) {
         rtiles = (int)(((int64_t)g.ntok * a.G + kRows - 1) / kRows);
-        ktiles = (int)(((int64_t)g.k1 - g.k0 + kTile - 1) / kTile);
+        groups = (a.Hk + a.heads - 1) / a.heads;
+        ktiles = (int)(((int64_t)g.k1 - g.k0 + kStep - 1) / kStep);
     }
-    __device__ int64_t tiles(const Args &a) const { return (int64_t)rtiles * ktiles * a.Hk; }
+    __device__ int64_t tiles() const { return (int64_t)rtiles * groups * ktiles; }
 };
 
 // Wide units: up to 256 rows of whole tokens with tiles of 128 keys, or, where a
@@ -157,11 +158,23 @@ struct Wide {
     __device__ int64_t tiles(const Args &a, const Segment &g) const { return head_tiles(g, 0, rtiles) * a.Hk; }
 };
 
-// The CTA that has tile x when `total` tiles are dealt to `ctas` CTAs in equal
-// ranges (CTA c: from total c / ctas on).
-__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int64_t ctas) {
-    return (int)(((x + 1) * ctas - 1) / total);
+// The worker that has tile x when `total` tiles are dealt to `workers` in equal
+// ranges (worker c: from total c / workers on).
+__device__ __forceinline__ int worker_of(int64_t x, int64_t total, int64_t workers) {
+    return (int)(((x + 1) * workers - 1) / total);
 }
+
+// The pieces of a unit of `tiles` tiles from u0 on, dealt to several workers: worker
+// c's is its first piece (slot 2 c) where its range begins in the unit, else its last.
+struct Pieces {
+    int c0, n, first;  // the first worker and its slot; their number
+    __device__ Pieces(int64_t u0, int64_t tiles, int64_t total, int64_t workers) {
+        c0 = worker_of(u0, total, workers);
+        n = worker_of(u0 + tiles - 1, total, workers) - c0 + 1;
+        first = 2 * c0 + (total * c0 / workers >= u0 ? 0 : 1);
+    }
+    __device__ int64_t slot(int i) const { return i == 0 ? first : 2 * (c0 + i); }
+};
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -195,50 +208,28 @@ __device__ __forceinline__ float row_power(float top) {
     return top == 0.0f ? 1.0f : __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-// The tiles before each of a CTA's threads' stretches of the segments [s0, s1),
-// in pre[0 .. N] (shared memory); CTA 0 leaves those before each segment and the
-// total in the workspace.  tiles(s) is the segment's.  Returns the stretch.
-template <int N, typename F>
-__device__ int deal_segments(int s0, int s1, int64_t *pre, int64_t *before, int64_t *total, F tiles) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (s1 - s0 + N - 1) / N;
-    const int b = min(s1, s0 + tid * per), e = min(s1, b + per);
-    int64_t mine = 0;
-    for (int s = b; s < e; ++s) mine += tiles(s);
-    int64_t incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t v = __shfl_up_sync(~0u, incl, d);
-        if (lane >= d) incl += v;
-    }
-    if (lane == 31) pre[warp] = incl;
-    __syncthreads();
-    int64_t at = 0;
-    for (int w = 0; w < warp; ++w) at += pre[w];
-    __syncthreads();
-    pre[tid + 1] = at + incl;
-    if (tid == 0) pre[0] = 0;
-    __syncthreads();
-    if (blockIdx.x == 0) {
-        at += incl - mine;
-        for (int s = b; s < e; ++s) {
-            before[s] = at;
-            at += tiles(s);
-        }
-        if (tid == 0) *total = pre[N];
-    }
-    return per;
+// 1 / v of a power of two from 2^-126 to 2^127.
+__device__ __forceinline__ float inverse_power(float v) {
+    const uint32_t e = __float_as_uint(v) >> 23;
+    return __uint_as_float(e == 254 ? 1u << 22 : (254u - e) << 23);
 }
 
-// The last of the N stretches that begins at or before tile x.
-template <int N>
-__device__ __forceinline__ int stretch_of(const int64_t *pre, int64_t x) {
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= x) lo = mid; else hi = mid - 1;
+// The rows of the segments without keys, where no join writes them (without
+// groups).
+template <int D>
+__device__ __forceinline__ void clear_rows(const Args &a) {
+    for (int s = blockIdx.x; s < a.B; s += gridDim.x) {
+        const Segment &g = a.segs[s];
+        if (g.k1 > g.k0) continue;
+        const int64_t n = (int64_t)g.ntok * a.Hq * (D / 8);
+        for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
+            const int64_t t = g.t0 + i / (a.Hq * (D / 8)), c = i % (a.Hq * (D / 8));
+            *reinterpret_cast<uint4 *>(a.out + t * a.ldo + c * 8) = make_uint4(0, 0, 0, 0);
+        }
+        if (a.lse)
+            for (int64_t i = threadIdx.x; i < (int64_t)g.ntok * a.Hq; i += blockDim.x)
+                a.lse[g.t0 * a.Hq + i] = -INFINITY;
     }
-    return lo;
 }
 
 }  // namespace attn

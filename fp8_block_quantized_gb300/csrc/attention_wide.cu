@@ -3,23 +3,29 @@
 // and the deal of the key tiles are those of attention.cu; here a tile is two
 // 128 x 128 score products on the 5th-generation tensor core.
 //
-// One CTA an SM, 13 warps:
+// One CTA an SM, 20 warps:
 //   warps 0-3, 4-7  two halves (A, B), one thread a row: the row's query to FP16 in
-//                   shared memory, then for every tile its scores from TMEM,
-//                   maxima, weights e^(x - max) as FP16 back to TMEM over the
-//                   scores, and at a piece's end its output;
-//   warps 8-11      the tiles' codes: read through the block table a tile ahead
+//                   shared memory, then for every tile its scores from TMEM, their
+//                   maximum, weights e^(x - max) as FP16 back to TMEM over the
+//                   scores (handed on 64 keys at a time), and at a piece's end its
+//                   output;
+//   warps 8-15      the tiles' codes: read through the block table a tile ahead
 //                   (32 KB in flight), turned to FP16 (exact) and laid out in
 //                   shared memory, K and V alike as rows of keys with the 128-byte
 //                   swizzle: K-major for the scores, MN-major for the values;
-//   warp 12         issues the MMAs: scores S = Q K^T (both operands in shared
-//                   memory) and O += P V (P in TMEM).
+//   warps 16, 17    issue the MMAs of A and of B: scores S = Q K^T (both operands in
+//                   shared memory) and O += P V (P in TMEM); one thread for both
+//                   could not issue them fast enough beside the others' instructions
+//                   (5300 cycles a tile against 4000);
+//   warp 18         walks the CTA's range and tells the others its pieces.
 // In a wide unit A and B are the two halves of 256 rows at the same keys; a unit
 // of at most 128 rows has them at alternate tiles of the same rows, whose results
 // are added at the end.  While one half's weights are computed the tensor core
 // works for the other.  A row's output is rescaled in TMEM only when its maximum
 // has grown by more than 2^8 since the last time: weights then reach 2^8 at most,
 // within FP16, and are summed in binary32.
+//
+// What bounds it: a 256 x 128 tile is 2048 cycles of MMAs.
 //
 // Every wait is bounded (jet_common.cuh); a role that gives up sets the CTA's abort
 // flag, MMAs in flight are awaited and TMEM is freed.
@@ -37,83 +43,61 @@ using namespace jet;
 using namespace jet::attn;
 using namespace jet::ptx;
 
-constexpr int kThreads = 416;
-constexpr int kStages = 2;
+constexpr int kThreads = 640;
+constexpr int kLoaders = 8;
+// Registers a thread of each warpgroup after setmaxnreg: 2 x 128 x 128 + 2 x 128 x 80 +
+// 128 x 64 = 640 x 96, what the block is launched with.
+constexpr uint32_t kRegsRows = 128, kRegsLoad = 80, kRegsControl = 64;
+static_assert(256 * kRegsRows + 256 * kRegsLoad + 128 * kRegsControl <= kThreads * 96, "registers");
+constexpr int kStages = 3;  // of which units of 256 rows use two
 // Wait sites in the status word (after those of head.cu).
 constexpr unsigned kSiteLoad = 24, kSiteQuery = 25, kSiteTile = 26, kSiteWeights = 27, kSiteScores = 28,
-                   kSiteOutput = 29, kSiteDrain = 30;
+                   kSiteOutput = 29, kSiteDrain = 30, kSitePiece = 31;
 
 template <int D>
 struct Cfg {
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kKBytes = 128 * D * 2;
     static constexpr int kStageBytes = 2 * kKBytes;
-    static constexpr int kUsed = 2 * kQBytes + kStages * kStageBytes + 1024;
+    // Two queries' tiles and two stages; the third stage's keys are in the place of
+    // the second queries' tile (units of at most 128 rows have one), its values behind.
+    static constexpr int kUsed = 2 * kQBytes + 2 * kStageBytes + kKBytes + 1024;
     // at least half of an SM's, so that no second CTA waits there for TMEM
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// One stretch of a unit in a CTA's range; the same for all roles.
+// One stretch of a unit in a CTA's range, as warp 17 tells it the others.
 struct Piece {
-    Segment g;
-    int s, h, rt;
-    int kt0, n;        // first tile (or pair) and their number
+    int64_t token;     // the unit's first
+    int s, r0, r1;     // segment; its requests
+    int k0, k1, row;   // keys, table row
+    int h;
+    int kt0, n;        // first tile (or pair of tiles) and their number; n = 0: no more
     int ktiles;        // of the unit
-    bool pairs;        // A and B at alternate tiles
-    bool both;         // B takes part
-    int64_t row0;      // the unit's first row
     int rows;
-    bool first;        // of this CTA
+    int pairs, both;   // A and B at alternate tiles; B takes part
+    int first;         // of this CTA
 };
 
-struct Walk {
-    int64_t x, x0, x1, at;  // tiles: next, the CTA's range, the segment's first
-    int s;
-    __device__ bool next(const Args &a, Piece &p) {
-        if (x >= x1) return false;
-        p.g = segment(a, s);
-        Wide w(a, p.g);
-        int64_t tiles = w.tiles(a, p.g);
-        while (at + tiles <= x) {
-            at += tiles;
-            p.g = segment(a, ++s);
-            w = Wide(a, p.g);
-            tiles = w.tiles(a, p.g);
-        }
-        int64_t u = at;
-        int rt = 0;
-        if (p.g.base < 0) {
-            rt = (int)((x - u) / ((int64_t)w.ktiles(p.g, 0) * a.Hk));
-            u += (int64_t)rt * w.ktiles(p.g, 0) * a.Hk;
+// The stages of a piece's tiles, in turn from the first one on, and how often each
+// was used before; the same for all roles.
+struct Ring {
+    uint32_t used[kStages] = {0, 0, 0};
+    // stage of a tile and its use of it
+    __device__ static int stage(bool pairs, int tile) { return pairs ? tile % 3 : tile & 1; }
+    __device__ uint32_t use(bool pairs, int tile) const {
+        const int st = stage(pairs, tile);
+        return (st == 0 ? used[0] : st == 1 ? used[1] : used[2]) + (pairs ? tile / 3 : tile >> 1);
+    }
+    __device__ void end(bool pairs, int tiles) {
+        if (pairs) {
+            used[0] += (tiles + 2) / 3, used[1] += (tiles + 1) / 3, used[2] += tiles / 3;
         } else {
-            while (u + (int64_t)w.ktiles(p.g, rt) * a.Hk <= x) u += (int64_t)w.ktiles(p.g, rt++) * a.Hk;
+            used[0] += (tiles + 1) >> 1, used[1] += tiles >> 1;
         }
-        p.s = s;
-        p.rt = rt;
-        p.ktiles = w.ktiles(p.g, rt);
-        p.h = (int)((x - u) / p.ktiles);
-        p.kt0 = (int)((x - u) - (int64_t)p.h * p.ktiles);
-        p.n = (int)min((int64_t)(p.ktiles - p.kt0), x1 - x);
-        p.pairs = w.keys != kTile;
-        p.row0 = (int64_t)rt * w.tokens * a.G;
-        p.rows = (int)min((int64_t)w.tokens * a.G, (int64_t)p.g.ntok * a.G - p.row0);
-        p.both = p.pairs || p.rows > 128;
-        p.first = x == x0;
-        x += p.n;
-        return true;
     }
 };
-
-// Without groups nobody else writes the rows of a segment without keys.
-template <int D>
-__device__ void no_keys(const Args &a, const Segment &g) {
-    for (int64_t t = g.t0; t < g.t0 + g.ntok; ++t) {
-        for (int64_t i = 0; i < (int64_t)a.Hq * D; i += 8)
-            *reinterpret_cast<uint4 *>(a.out + t * a.ldo + i) = make_uint4(0, 0, 0, 0);
-        for (int h = 0; h < a.Hq && a.lse; ++h) a.lse[t * a.Hq + h] = -INFINITY;
-    }
-}
 
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
@@ -126,38 +110,76 @@ __device__ __forceinline__ uint32_t place(int r, int c) {
     return (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// max(a, b, c) in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void stg32(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
+                                      uint32_t f, uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b),
+                 "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mma_16bit_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void mma_16bit_ta_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead) : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args a, unsigned *status) {
     using C = Cfg<D>;
     extern __shared__ uint8_t dyn[];
-    __shared__ int64_t sh_pre[kThreads + 1];
-    __shared__ uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2],
-        ml_full, drain_bar;
-    __shared__ uint32_t sh_mask[kStages][4];
+    __shared__ uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2],
+        o_full[2], ml_full, drain_bar, piece_full[2], piece_empty[2];
+    __shared__ Piece pieces[2];
+    __shared__ __align__(16) uint16_t sh_mask[kStages][8];
     __shared__ float sh_m[128], sh_l[128];
+    __shared__ uint64_t in_turn[4][2];
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const uint32_t smem = (smem_u32(dyn) + 1023u) & ~1023u;
     volatile int *abort = &abort_sh;
 
     if (tid == 0) {
-        mbar_init(&q_full, 256);
-        mbar_init(&ml_full, 128);
-        mbar_init(&drain_bar, 1);
+        mbar_init(&q_full, 8);
+        mbar_init(&ml_full, 4);
+        mbar_init(&drain_bar, 2);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&kv_full[i], 128);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&kv_full[i], kLoaders);
+            mbar_init(&kv_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&p_full[i][0], 4);
+            mbar_init(&p_full[i][1], 4);
             mbar_init(&o_full[i], 1);
+            for (int q = 0; q < 4; ++q) mbar_init(&in_turn[q][i], 1);
+            mbar_init(&piece_full[i], 1);
+            mbar_init(&piece_empty[i], 8 + kLoaders + 2);
         }
         abort_sh = 0;
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == 16) {
         tmem_alloc(&tmem_sh, 512);
         tmem_relinquish();
     }
@@ -167,278 +189,412 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
     const uint32_t tmem = tmem_sh;
     griddep_launch_dependents();
     griddep_wait();
+    if (a.Ng == 0 && a.plan->empty > 0) clear_rows<D>(a);
 
-    const int lo = a.wide_own ? 0 : a.B, hi = a.wide_prefix ? a.B + a.Ng : a.B;
-    const int per = deal_segments<kThreads>(lo, hi, sh_pre, a.before, a.total + 1, [&](int s) {
-        const Segment g = segment(a, s);
-        if (blockIdx.x == 0 && a.Ng == 0 && g.k1 <= g.k0) no_keys<D>(a, g);
-        return Wide(a, g).tiles(a, g);
-    });
-    const int64_t total = sh_pre[kThreads], ctas = min((int64_t)a.wide_ctas, total);
-    Walk walk;
-    walk.x = walk.x0 = walk.x1 = walk.at = 0, walk.s = lo;
-    if (blockIdx.x < ctas) {
-        walk.x = walk.x0 = total * blockIdx.x / ctas;
-        walk.x1 = total * (blockIdx.x + 1) / ctas;
-        const int stretch = stretch_of<kThreads>(sh_pre, walk.x);
-        walk.s = lo + stretch * per;
-        walk.at = sh_pre[stretch];
-    }
-    // A wait of a whole warp for the n-th phase of a barrier; all lanes leave alike.
+    // A warp's wait for the n-th phase of a barrier, and its arrival.  One lane does
+    // either: every lane's would be one operation on the barrier after another, in
+    // shared memory's way (a tile took 4700 cycles so, 3200 with one lane).
     auto wait = [&](uint64_t *bar, uint32_t n, unsigned site) -> bool {
         return __all_sync(~0u, mbar_wait(bar, n & 1u, abort, status, site));
     };
-    const uint32_t q_s = smem, kv_s = smem + 2 * C::kQBytes;
-    Piece p;
+    auto arrive = [&](uint64_t *bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    const uint32_t q_s = smem;
+    auto keys_at = [&](int st) -> uint32_t {
+        return st < 2 ? smem + 2 * C::kQBytes + st * C::kStageBytes : smem + C::kQBytes;
+    };
+    auto values_at = [&](int st) -> uint32_t {
+        return smem + 2 * C::kQBytes + (st < 2 ? st * C::kStageBytes + C::kKBytes : 2 * C::kStageBytes);
+    };
+    uint32_t np = 0;  // pieces so far
+    Ring ring;
+    // The next piece (a warp's calls): waited for, and given back when done with.  It
+    // stays in shared memory: registers are short.
+    auto next = [&]() -> bool {
+        return wait(&piece_full[np & 1], np >> 1, kSitePiece) && pieces[np & 1].n > 0;
+    };
+    auto done = [&]() {
+        arrive(&piece_empty[np & 1]);
+        ++np;
+    };
 
-    if (warp >= 8 && warp < 12) {
+    if (warp >= 16) {
+        reg_dealloc<kRegsControl>();
+        if (warp == 18) {
+            // ------------------------------------------------------ the walk
+            const int64_t total = a.plan->total[1], workers = a.plan->workers[1];
+            int64_t left = 0, from = 0;  // tiles of the CTA's range; the next one in its segment
+            int64_t at = 0;
+            if (blockIdx.x < workers) {
+                const Start &st = a.starts[kNarrowWorkers + blockIdx.x];
+                left = total * (blockIdx.x + 1) / workers - total * blockIdx.x / workers;
+                from = st.tiles, at = st.at;
+            }
+            const int *order = a.order + a.B + a.Ng;
+            bool more = true, first = true;
+            for (uint32_t i = 0; more; ++i) {
+                Piece p;
+                p.n = 0;
+                if (left > 0) {
+                    int s = order[at];
+                    Segment g = a.segs[s];
+                    Wide w(a, g);
+                    // the row tile that holds tile `from`
+                    int64_t u = from;
+                    int rt = 0;
+                    if (g.base < 0) {
+                        const int64_t each = (int64_t)w.ktiles(g, 0) * a.Hk;
+                        rt = (int)(u / each);
+                        u -= rt * each;
+                    } else {
+                        while (u >= (int64_t)w.ktiles(g, rt) * a.Hk) u -= (int64_t)w.ktiles(g, rt++) * a.Hk;
+                    }
+                    p.token = g.t0 + (int64_t)rt * w.tokens;
+                    p.s = s;
+                    p.r0 = g.r0, p.r1 = g.r1;
+                    p.k0 = g.k0, p.k1 = g.k1, p.row = g.row;
+                    p.ktiles = w.ktiles(g, rt);
+                    p.h = (int)((uint32_t)u / (uint32_t)p.ktiles);
+                    p.kt0 = (int)((uint32_t)u - (uint32_t)p.h * p.ktiles);
+                    p.n = (int)min((int64_t)(p.ktiles - p.kt0), left);
+                    p.pairs = w.keys != kTile;
+                    p.rows = min(w.tokens, g.ntok - rt * w.tokens) * a.G;
+                    p.both = p.pairs || p.rows > 128;
+                    if (lane == 0 && first && a.Ng == 0) {
+                        // the range begins in the middle of a unit: what the join will need
+                        Split sp;
+                        sp.rows = 0;
+                        const int64_t u0 = g.before + from - p.kt0;
+                        if (p.kt0 > 0 && total * ((int64_t)blockIdx.x - 1) / workers <= u0) {
+                            const Pieces pc(u0, p.ktiles, total, workers);
+                            sp.token = p.token, sp.sub = 0, sp.head = p.h, sp.rows = p.rows;
+                            sp.n = pc.n, sp.c0 = pc.c0, sp.first = pc.first;
+                        }
+                        a.splits[kNarrowWorkers + blockIdx.x] = sp;
+                    }
+                    p.first = first;
+                    first = false;
+                    left -= p.n;
+                    from += p.n;
+                    if (rt == w.rtiles - 1 && p.h == a.Hk - 1 && p.kt0 + p.n == p.ktiles) from = 0, ++at;
+                }
+                more = p.n > 0;
+                if (!wait(&piece_empty[i & 1], (i >> 1) + 1, kSitePiece)) break;
+                if (lane == 0) {
+                    pieces[i & 1] = p;
+                    mbar_arrive(&piece_full[i & 1]);
+                }
+                __syncwarp();
+            }
+        } else if (warp < 18) {
+            // ---------------------------------------------------------- MMAs
+            constexpr uint32_t kS = idesc_16bit(128, 128, false, false, false);
+            constexpr uint32_t kO = idesc_16bit(128, D, false, false, true);
+            // descriptors: their upper words are constant, the lower ones an address / 16
+            constexpr uint64_t kKMajor = (uint64_t)1 << 16 | (uint64_t)64 << 32 | (uint64_t)1 << 46 |
+                                         (uint64_t)kSwizzle128B << 61;  // offsets 16, 1024
+            constexpr uint64_t kMnMajor = (uint64_t)1024 << 16 | (uint64_t)64 << 32 | (uint64_t)1 << 46 |
+                                          (uint64_t)kSwizzle128B << 61;  // offsets 16384, 1024
+            const int hf = warp - 16;
+            const uint32_t s_t = tmem + hf * 128, o_t = tmem + 256 + hf * D;
+            const uint32_t lead = elect_one();
+            uint32_t nt = 0;  // the half's tiles so far
+            bool ok = true;
+            while (ok && wait(&piece_full[np & 1], np >> 1, kSitePiece)) {
+                const Piece &p = pieces[np & 1];
+                const bool pairs = __shfl_sync(~0u, p.pairs, 0), both = __shfl_sync(~0u, p.both, 0);
+                const int all = __shfl_sync(~0u, p.n, 0), n = hf == 0 || both ? all : 0, each = pairs ? 2 : 1;
+                if (all == 0) break;
+                const bool alone = pairs || !both;  // nobody else reads this half's tiles
+                if (!wait(&q_full, np, kSiteQuery)) break;
+                done();
+                const uint64_t qa = kKMajor + ((q_s + (pairs ? 0 : hf) * C::kQBytes) >> 4);
+                auto scores = [&](int i) -> bool {
+                    const int tile = i * each + (pairs ? hf : 0), st = Ring::stage(pairs, tile);
+                    if (!wait(&kv_full[st], ring.use(pairs, tile), kSiteTile)) return false;
+                    tc_fence_after();
+                    const uint64_t kb = kKMajor + (keys_at(st) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                        mma_16bit_if(lead, s_t, qa + o, kb + o, kS, ks > 0);
+                    }
+                    commit_if(lead, &s_full[hf]);
+                    return true;
+                };
+                if (n > 0) ok = scores(0);
+                for (int i = 0; ok && i < n; ++i, ++nt) {
+                    const int st = Ring::stage(pairs, i * each + (pairs ? hf : 0));
+                    const uint64_t vb = kMnMajor + (values_at(st) >> 4);
+                    // values, 64 keys at a time, the later ones first
+#pragma unroll
+                    for (int b = 1; b >= 0; --b) {
+                        ok = ok && wait(&p_full[hf][b], nt, kSiteWeights);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_16bit_ta_if(lead, o_t, s_t + 64 + b * 32 + ks * 8, vb + (b * 8192 + ks * 2048) / 16, kO,
+                                            i > 0 || b == 0 || ks > 0);
+                    }
+                    if (!ok) break;
+                    commit_if(lead, &kv_empty[st]);
+                    if (alone) commit_if(lead, &kv_empty[st]);
+                    if (i + 1 == n) commit_if(lead, &o_full[hf]);
+                    else ok = scores(i + 1);
+                }
+                ring.end(pairs, all * each);
+            }
+            commit_if(lead, &drain_bar);
+            __syncwarp();
+            mbar_wait(&drain_bar, 0, nullptr, status, kSiteDrain);
+        }
+    } else if (warp >= 8) {
         // ------------------------------------------------------------- codes
+        reg_dealloc<kRegsLoad>();
         constexpr int CH = D / 16;          // 16-byte chunks of a key's codes
         constexpr int RW = 32 / CH;         // rows a warp reads at once
-        constexpr int NI = 32 / RW;
+        constexpr int KW = kTile / kLoaders;  // rows of a warp
+        constexpr int NI = KW / RW;
         const int w = warp - 8;
-        uint32_t n = 0;                     // tiles so far
-        bool ok = true;
-        while (ok && walk.next(a, p)) {
-            const int tiles = p.n * (p.pairs ? 2 : 1), t0 = p.kt0 * (p.pairs ? 2 : 1);
-            const int32_t *tab = a.table + (int64_t)p.g.row * a.width;
-            // the cache row of key 32 w + lane of tile kt, or -1
-            auto slot_of = [&](int i) -> int {
-                const int64_t at = (int64_t)p.g.k0 + (int64_t)(t0 + i) * kTile + 32 * w + lane;
-                if (i >= tiles || at >= p.g.k1) return -1;
-                const uint32_t blk = (uint32_t)at / (uint32_t)a.bs;
-                const int64_t id = tab[blk];
-                if (id < 0) return -1;
-                const int64_t slot = id * a.bs + ((uint32_t)at - blk * (uint32_t)a.bs);
-                return slot < a.S ? (int)slot : -1;
+        uint32_t no = 0;                    // outputs of B so far
+        bool ok = true, queries = false;    // the last piece had queries in B's place
+        while (ok && next()) {
+            const Piece &p = pieces[np & 1];
+            const bool pairs = p.pairs;
+            const int64_t key0 = (int64_t)p.k0 + (int64_t)p.kt0 * (pairs ? 2 : 1) * kTile + KW * w + lane;
+            const int k1 = lane < KW ? p.k1 : 0, tiles = p.n * (pairs ? 2 : 1);
+            const int64_t head = (int64_t)p.h * D;
+            // the third stage takes their place once the last piece's products are done
+            if (pairs && queries && !wait(&o_full[1], no - 1, kSiteLoad)) break;
+            queries = p.both && !pairs;
+            no += p.both;
+            const int32_t *tab = a.table + (int64_t)p.row * a.width;
+            // the block of key KW w + lane of tile i (the table's entry, or -1) and the
+            // key's place in it
+            struct Entry {
+                int id;
+                uint32_t at;
             };
-            uint4 kr[NI], vr[NI];
+            auto entry_of = [&](int i) -> Entry {
+                const int64_t key = key0 + (int64_t)i * kTile;
+                Entry e = {-1, 0u};
+                if (i < tiles && key < k1) {
+                    const uint32_t blk = (uint32_t)key / (uint32_t)a.bs;
+                    e.at = (uint32_t)key - blk * (uint32_t)a.bs;
+                    e.id = tab[blk];
+                }
+                return e;
+            };
+            auto slot_of = [&](Entry e) -> int {
+                const int64_t slot = (int64_t)e.id * a.bs + e.at;
+                return e.id >= 0 && slot < a.S ? (int)slot : -1;
+            };
+            uint4 kr[NI] = {}, vr[NI] = {};
             const int c = lane % CH, rq = lane / CH;
+            // (a missing key reads slot 0: its score is left out, its value zeroed)
             auto load = [&](int slot) {
+                if (a.S == 0) return;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const int sl = __shfl_sync(~0u, slot, RW * i + rq);
-                    kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-                    if (sl >= 0) {
-                        const int64_t from = ((int64_t)sl * a.Hk + p.h) * D + c * 16;
-                        kr[i] = *reinterpret_cast<const uint4 *>(a.kc + from);
-                        vr[i] = *reinterpret_cast<const uint4 *>(a.vc + from);
-                    }
+                    const int64_t from = (int64_t)max(sl, 0) * a.Hk * D + head + c * 16;
+                    kr[i] = __ldg(reinterpret_cast<const uint4 *>(a.kc + from));
+                    vr[i] = __ldg(reinterpret_cast<const uint4 *>(a.vc + from));
                 }
             };
             auto store = [&](uint32_t dst, const uint4 (&v)[NI]) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const int r = 32 * w + RW * i + rq;
-                    uint32_t lo8[4] = {codes_f16(v[i].x), codes_f16_hi(v[i].x), codes_f16(v[i].y),
-                                       codes_f16_hi(v[i].y)};
-                    uint32_t hi8[4] = {codes_f16(v[i].z), codes_f16_hi(v[i].z), codes_f16(v[i].w),
-                                       codes_f16_hi(v[i].w)};
+                    const int r = KW * w + RW * i + rq;
                     // chunks 2 c and 2 c + 1; the lanes of the upper half of a row (and of odd
                     // rows where a row has four chunks) write the odd one first, so that
                     // eight lanes touch every bank once
                     const bool swap = D == 128 ? c >= 4 : (rq & 1);
-                    const uint32_t e = dst + place(r, 2 * c), o = dst + place(r, 2 * c + 1);
-                    if (!swap) {
-                        sts16(e, lo8[0], lo8[1], lo8[2], lo8[3]);
-                        sts16(o, hi8[0], hi8[1], hi8[2], hi8[3]);
-                    } else {
-                        sts16(o, hi8[0], hi8[1], hi8[2], hi8[3]);
-                        sts16(e, lo8[0], lo8[1], lo8[2], lo8[3]);
-                    }
+                    const uint32_t f = swap ? v[i].z : v[i].x, g = swap ? v[i].w : v[i].y,
+                                   y = swap ? v[i].x : v[i].z, z = swap ? v[i].y : v[i].w;
+                    sts16(dst + place(r, 2 * c + swap), codes_f16(f), codes_f16_hi(f), codes_f16(g),
+                          codes_f16_hi(g));
+                    sts16(dst + place(r, 2 * c + !swap), codes_f16(y), codes_f16_hi(y), codes_f16(z),
+                          codes_f16_hi(z));
                 }
             };
-            int cur = slot_of(0);
+            // Loads come back in order: the entry of a tile is asked for before the
+            // codes of the tile before it, and used behind them.
+            Entry nxt = entry_of(1);
+            int cur = slot_of(entry_of(0));
             load(cur);
-            int nxt = slot_of(1);
-            for (int i = 0; i < tiles; ++i, ++n) {
-                const int st = n % kStages;
-                if (!wait(&kv_empty[st], n / kStages + 1, kSiteLoad)) {
+            for (int i = 0; i < tiles; ++i) {
+                const int st = Ring::stage(pairs, i);
+                if (!wait(&kv_empty[st], ring.use(pairs, i) + 1, kSiteLoad)) {
                     ok = false;
                     break;
                 }
                 const uint32_t mask = __ballot_sync(~0u, cur >= 0);
-                if (lane == 0) sh_mask[st][w] = mask;
-                const uint32_t dst = kv_s + st * C::kStageBytes;
-                store(dst, kr);
-                store(dst + C::kKBytes, vr);
+                if (lane == 0) sh_mask[st][w] = (uint16_t)mask;
+                if (mask != (1u << KW) - 1u) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+                        if (!((mask >> (RW * j + rq)) & 1u)) vr[j] = make_uint4(0, 0, 0, 0);
+                }
+                store(keys_at(st), kr);
+                store(values_at(st), vr);
                 fence_proxy_async();
-                mbar_arrive(&kv_full[st]);
-                cur = nxt;
+                arrive(&kv_full[st]);
+                cur = slot_of(nxt);
+                nxt = entry_of(i + 2);
                 if (i + 1 < tiles) load(cur);
-                nxt = slot_of(i + 2);
             }
+            ring.end(pairs, tiles);
+            done();
         }
-    } else if (warp == 12) {
-        // -------------------------------------------------------------- MMAs
-        constexpr uint32_t kS = idesc_16bit(128, 128, false, false, false);
-        constexpr uint32_t kO = idesc_16bit(128, D, false, false, true);
-        uint32_t n = 0, piece = 0, np[2] = {0, 0};  // tiles, pieces, weights so far
-        bool ok = true;
-        while (ok && walk.next(a, p)) {
-            if (!wait(&q_full, piece, kSiteQuery)) break;
-            ++piece;
-            const int each = p.pairs ? 2 : 1;
-            // scores of half hf in its i-th tile
-            auto scores = [&](int hf, int i) -> bool {
-                const uint32_t t = n + i * each + (p.pairs ? hf : 0), st = t % kStages;
-                if (!wait(&kv_full[st], t / kStages, kSiteTile)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t qa = q_s + (p.pairs ? 0 : hf) * C::kQBytes;
-                    const uint32_t kb = kv_s + st * C::kStageBytes;
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t o = (ks >> 2) * 16384 + (ks & 3) * 32;
-                        mma_16bit(tmem + hf * 128, smem_desc(qa + o, 16, 1024, kSwizzle128B),
-                                  smem_desc(kb + o, 16, 1024, kSwizzle128B), kS, ks > 0);
-                    }
-                    mma_commit(&s_full[hf]);
-                }
-                __syncwarp();
-                return true;
-            };
-            const int halves = p.both ? 2 : 1;
-            for (int hf = 0; ok && hf < halves; ++hf) ok = scores(hf, 0);
-            for (int i = 0; ok && i < p.n; ++i) {
-                for (int hf = 0; ok && hf < halves; ++hf) {
-                    if (!wait(&p_full[hf], np[hf], kSiteWeights)) {
-                        ok = false;
-                        break;
-                    }
-                    ++np[hf];
-                    tc_fence_after();
-                    const uint32_t t = n + i * each + (p.pairs ? hf : 0), st = t % kStages;
-                    if (lane == 0) {
-                        const uint32_t vb = kv_s + st * C::kStageBytes + C::kKBytes;
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_16bit_ta(tmem + 256 + hf * D, tmem + hf * 128 + 64 + ks * 8,
-                                         smem_desc(vb + ks * 2048, 16384, 1024, kSwizzle128B), kO,
-                                         i > 0 || ks > 0);
-                        if (p.pairs || hf == halves - 1) mma_commit(&kv_empty[st]);
-                        if (i + 1 == p.n) mma_commit(&o_full[hf]);
-                    }
-                    __syncwarp();
-                    if (i + 1 < p.n) ok = scores(hf, i + 1);
-                }
-            }
-            n += p.n * each;
-        }
-        if (lane == 0) mma_commit(&drain_bar);
-        __syncwarp();
-        mbar_wait(&drain_bar, 0, nullptr, status, kSiteDrain);
-    } else if (warp < 8) {
+    } else {
         // ----------------------------------------------- weights and outputs
+        reg_alloc<kRegsRows>();
         const int hf = warp >> 2, r = tid & 127;  // half, its row = TMEM lane
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_t = lanes + hf * 128, o_t = lanes + 256 + hf * D;
-        uint32_t n = 0, nt = 0, no[2] = {0, 0}, nml = 0;  // tiles, scores, outputs, merges so far
+        const bool wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.ldo % 16 == 0;
+        uint32_t turns = 0, nt = 0, no[2] = {0, 0}, nml = 0;  // the half's tiles, outputs, merges so far
         bool ok = true;
-        while (ok && walk.next(a, p)) {
-            // the query
-            const int64_t lr = r + (p.pairs ? 0 : 128 * hf);
+        while (ok && next()) {
+            const Piece &p = pieces[np & 1];
+            const bool pairs = p.pairs, active = hf == 0 || p.both;
+            const int n = active ? p.n : 0;
+            const int lr = r + (pairs ? 0 : 128 * hf);
             const bool row_ok = lr < p.rows;
-            const int64_t rr = p.row0 + (row_ok ? lr : 0);
-            const int64_t t = p.g.t0 + rr / a.G;
-            const int hq = p.h * a.G + (int)(rr % a.G);
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + t * a.ldq + (int64_t)hq * D);
-            float top = 0.0f;
-            if (row_ok) {
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = src[i];
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            // token and query head of the row
+            auto place_of = [&](int64_t &t, int &hq) {
+                const uint32_t row = row_ok ? lr : 0, tok = row / (uint32_t)a.G;
+                t = p.token + tok;
+                hq = p.h * a.G + (int)(row - tok * a.G);
+            };
+            // the query
+            float f, ref = -INFINITY, l = 0.0f;  // factor of the scores; the weights' reference
+                                                 // (a power of two) and sum
+            int pos = 0x7FFFFFFF;                // a row past the unit's last hides no key
+            {
+                int64_t t;
+                int hq;
+                place_of(t, hq);
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + t * a.ldq + (int64_t)hq * D);
+                // (half a row at a time: registers are short)
+                constexpr int NH = 8, NQ = D / 8 / NH;
+                uint4 v[NH];
+                auto read = [&](int part) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[k] << 16)),
-                                               fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
-                }
-            }
-            float up = row_power(top);
-            float f = a.scale * a.ks[p.h] * kLog2e / up;
-            if (f < 0.0f) f = -f, up = -up;  // maxima are of the raw scores
-            f = fmaxf(f, 0x1p-126f);
-            int pos = 0x7FFFFFFF;  // a row past the unit's last hides no key
-            if (row_ok) pos = position(a, p.s < a.B ? p.s : min(upper(a.off, a.B, t), a.B - 1), t);
-            if (!p.pairs || hf == 0) {
-                const uint32_t dst = q_s + hf * C::kQBytes;
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = row_ok ? src[i] : make_uint4(0, 0, 0, 0);
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t w[4];
+                    for (int i = 0; i < NH; ++i) v[i] = row_ok ? src[part * NH + i] : make_uint4(0, 0, 0, 0);
+                };
+                float top = 0.0f;
+#pragma unroll 1
+                for (int part = NQ - 1; part >= 0; --part) {
+                    read(part);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = pack_f16(__uint_as_float(u[k] << 16) * up,
-                                        __uint_as_float(u[k] & 0xFFFF0000u) * up);
-                    sts16(dst + place(r, i), w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < NH; ++i) {
+                        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            top = max3(top, fabsf(__uint_as_float(u[k] << 16)),
+                                       fabsf(__uint_as_float(u[k] & 0xFFFF0000u)));
+                    }
                 }
-                fence_proxy_async();
+                if (row_ok) {
+                    int b = p.r0;
+                    if (p.s >= a.B) b = min(p.r0 + upper(a.off + p.r0, p.r1 - p.r0, t), a.B - 1);
+                    pos = position(a, b, t);
+                }
+                float up = row_power(top);
+                f = a.scale * a.ks[p.h] * kLog2e * inverse_power(up);
+                if (f < 0.0f) f = -f, up = -up;  // maxima are of the raw scores
+                f = fmaxf(f, 0x1p-126f);
+                if (!pairs || hf == 0) {
+                    const uint32_t dst = q_s + hf * C::kQBytes;
+#pragma unroll 1
+                    for (int part = 0; part < NQ; ++part) {
+                        if (part > 0) read(part);
+#pragma unroll
+                        for (int i = 0; i < NH; ++i) {
+                            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack_f16(__uint_as_float(u[k] << 16) * up,
+                                                __uint_as_float(u[k] & 0xFFFF0000u) * up);
+                            sts16(dst + place(r, part * NH + i), w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    fence_proxy_async();
+                }
             }
             tc_fence_before();  // the last piece's reads of TMEM
-            mbar_arrive(&q_full);
-            const int each = p.pairs ? 2 : 1;
-            if (hf == 1 && !p.both && !wait(&q_full, no[0], kSiteQuery)) break;  // its next arrival is the next piece's
-            float m = -INFINITY, l = 0.0f;  // reference of the weights (a power of two), their sum
-            const bool active = hf == 0 || p.both;
-            for (int i = 0; active && i < p.n; ++i) {
-                const int kt = each * (p.kt0 + i) + (p.pairs ? hf : 0);
-                const uint32_t seq = n + i * each + (p.pairs ? hf : 0), st = seq % kStages;
-                if (!wait(&s_full[hf], nt, kSiteScores) ||
-                    !wait(&kv_full[st], seq / kStages, kSiteScores)) {
+            arrive(&q_full);
+            const int each = pairs ? 2 : 1;
+            const int64_t key0 = (int64_t)p.k0 + (int64_t)p.kt0 * each * kTile;
+            if (!active && !wait(&q_full, no[0], kSiteQuery)) break;  // its next arrival is the next piece's
+            for (int i = 0; i < n; ++i, ++nt) {
+                const int tile = i * each + (pairs ? hf : 0), st = Ring::stage(pairs, tile);
+                if (!wait(&s_full[hf], nt, kSiteScores) || !wait(&kv_full[st], ring.use(pairs, tile), kSiteScores)) {
                     ok = false;
                     break;
                 }
-                ++nt;
-                __syncwarp();
+                // (the two halves' warps of an SM sub-partition compute in turn)
+                if (p.both && !wait(&in_turn[warp & 3][hf], turns + 1 - hf, kSiteScores)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 // the keys that the row sees, where some are hidden
-                uint32_t see[4];
-                bool all = true;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int64_t left = pos - ((int64_t)p.g.k0 + (int64_t)kt * kTile + 32 * c);
-                    see[c] = sh_mask[st][c];
-                    if (left < 31) see[c] &= left < 0 ? 0u : (2u << (int)left) - 1u;
-                    all = all && see[c] == ~0u;
-                }
-                const bool hidden = __any_sync(~0u, !all);
-                auto hide = [&](uint32_t (&v)[32], uint32_t bits, float with) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!((bits >> k) & 1u)) v[k] = __float_as_uint(with);
-                };
+                const int64_t left = pos - (key0 + (int64_t)tile * kTile);
+                const uint4 there = *reinterpret_cast<const uint4 *>(&sh_mask[st][0]);
+                const bool hidden = __any_sync(~0u, left < kTile - 1 || (there.x & there.y & there.z & there.w) != ~0u);
+                // the scores of keys 64 h .. 64 h + 63, -inf for those the row does not see
+                // (rolled loops below: more code than the instruction cache holds beside the
+                // other warps' slows every role)
                 uint32_t v0[32], v1[32];
-                float top0 = -INFINITY, top1 = -INFINITY;
-                auto largest = [&](uint32_t (&v)[32]) {
+                auto read = [&](int h) {
+                    __syncwarp();
+                    tmem_ld32(s_t + 64 * h, v0);
+                    tmem_ld32(s_t + 64 * h + 32, v1);
+                    tmem_wait32(v0);
+                    tmem_wait32(v1);
+                    if (hidden) {
+                        uint32_t see[2] = {h ? there.z : there.x, h ? there.w : there.y};
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        top0 = fmaxf(top0, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
-                        top1 = fmaxf(top1, fmaxf(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])));
+                        for (int c = 0; c < 2; ++c) {
+                            const int64_t l = left - 64 * h - 32 * c;
+                            if (l < 31) see[c] &= l < 0 ? 0u : (2u << (int)l) - 1u;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            if (!((see[0] >> k) & 1u)) v0[k] = __float_as_uint(-INFINITY);
+                            if (!((see[1] >> k) & 1u)) v1[k] = __float_as_uint(-INFINITY);
+                        }
                     }
                 };
-                tmem_ld32(s_t, v0);
-                tmem_ld32(s_t + 32, v1);
-                tmem_wait32(v0);
-                tmem_wait32(v1);
-                if (hidden) hide(v0, see[0], -INFINITY), hide(v1, see[1], -INFINITY);
-                largest(v0);
-                largest(v1);
-                __syncwarp();
-                tmem_ld32(s_t + 64, v0);
-                tmem_ld32(s_t + 96, v1);
-                tmem_wait32(v0);
-                tmem_wait32(v1);
-                if (hidden) hide(v0, see[2], -INFINITY), hide(v1, see[3], -INFINITY);
-                largest(v0);
-                largest(v1);
-                const float tile = fmaxf(top0, top1) * f;
-                const bool grown = i > 0 && tile > m + 8.0f;
-                if (i == 0) m = tile;
+                float top = -INFINITY, top1 = -INFINITY;
+                auto largest = [&](const uint32_t (&v)[32]) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        top = max3(top, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                        top1 = max3(top1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+                    }
+                };
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    read(h);
+                    largest(v0);
+                    largest(v1);
+                }
+                top = fmaxf(top, top1) * f;
+                const bool grown = i > 0 && top > ref + 8.0f;
+                if (i == 0) ref = top;
                 if (__any_sync(~0u, grown)) {
-                    const float c = grown ? ex2(m - tile) : 1.0f;
-                    if (grown) m = tile;
+                    // (the products of the last weights are in the output: they were issued
+                    // before these scores, whose arrival was waited for)
+                    const float c = grown ? ex2(ref - top) : 1.0f;
+                    if (grown) ref = top;
                     l *= c;
 #pragma unroll 1
                     for (int ch = 0; ch < D / 16; ++ch) {
@@ -450,65 +606,69 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                         tmem_st16(o_t + ch * 16, o);
                     }
                 }
-                __syncwarp();
                 const float2 f2 = make_float2(f, f);
-                const float nm = m == -INFINITY ? 0.0f : -m;
+                const float nm = ref == -INFINITY ? 0.0f : -ref;
                 const float2 nm2 = make_float2(nm, nm);
                 float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-                // weights of 32 keys, to 16 columns over the upper half of the scores
-                auto weigh = [&](uint32_t (&v)[32], uint32_t bits, int col) {
+                // weights (hidden keys' scores are -inf) of 32 keys, to 16 columns over the
+                // upper half of the scores: the later 64 keys, in registers, first; the
+                // others' scores are read again
+                auto weigh = [&](const uint32_t (&v)[32], int col) {
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const float2 x = __ffma2_rn(
                             make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), f2, nm2);
-                        float2 e = make_float2(ex2(x.x), ex2(x.y));
-                        if (hidden) {
-                            if (!((bits >> (2 * k)) & 1u)) e.x = 0.0f;
-                            if (!((bits >> (2 * k + 1)) & 1u)) e.y = 0.0f;
-                        }
+                        const float2 e = make_float2(ex2(x.x), ex2(x.y));
                         if (k & 1) s1 = __fadd2_rn(s1, e); else s0 = __fadd2_rn(s0, e);
                         w[k] = pack_f16(e.x, e.y);
                     }
                     __syncwarp();
                     tmem_st16(s_t + 64 + col, w);
                 };
-                weigh(v0, see[2], 32);
-                tmem_ld32(s_t, v0);
-                weigh(v1, see[3], 48);
-                tmem_ld32(s_t + 32, v1);
-                tmem_wait32(v0);
-                weigh(v0, see[0], 0);
-                tmem_wait32(v1);
-                weigh(v1, see[1], 16);
+#pragma unroll
+                for (int h = 1; h >= 0; --h) {
+                    if (h == 0) read(0);
+                    weigh(v0, 32 * h);
+                    weigh(v1, 32 * h + 16);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    arrive(&p_full[hf][h]);
+                }
                 l += (s0.x + s0.y) + (s1.x + s1.y);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&p_full[hf]);
+                if (p.both) {
+                    arrive(&in_turn[warp & 3][1 - hf]);
+                    ++turns;
+                }
             }
-            n += p.n * each;
+            ring.end(pairs, p.n * each);
             if (!ok) break;
             // the output
             if (active) {
                 if (!wait(&o_full[hf], no[hf], kSiteOutput)) break;
-                if (p.pairs && hf == 1) {
-                    sh_m[r] = m;
+                if (pairs && hf == 1) {
+                    // (A's products too, before the next piece's queries take the third stage's place)
+                    if (!wait(&o_full[0], no[0], kSiteOutput)) break;
+                    sh_m[r] = ref;
                     sh_l[r] = l;
-                    mbar_arrive(&ml_full);
+                    arrive(&ml_full);
                 } else {
                     float ca = 1.0f, cb = 0.0f;
-                    if (p.pairs) {
+                    if (pairs) {
                         if (!wait(&o_full[1], no[1], kSiteOutput) ||
                             !wait(&ml_full, nml, kSiteOutput))
                             break;
-                        const float mb = sh_m[r], both = fmaxf(m, mb), use = both == -INFINITY ? 0.0f : both;
-                        ca = ex2(m - use);
+                        const float mb = sh_m[r], both = fmaxf(ref, mb), use = both == -INFINITY ? 0.0f : both;
+                        ca = ex2(ref - use);
                         cb = ex2(mb - use);
                         l = l * ca + sh_l[r] * cb;
-                        m = both;
+                        ref = both;
                     }
                     __syncwarp();
                     tc_fence_after();
+                    int64_t t;
+                    int hq;
+                    place_of(t, hq);
                     const bool full = p.n == p.ktiles, direct = full && a.Ng == 0;
                     const int64_t slot = full ? ((p.s < a.B ? a.T : 0) + t) * a.Hq + hq
                                               : (int64_t)(2 * blockIdx.x + (p.first ? 0 : 1)) * kWideRows + lr;
@@ -521,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                         __syncwarp();
                         tmem_ld32(o_t + ch * 32, v);
                         tmem_wait32(v);
-                        if (p.pairs) {
+                        if (pairs) {
                             uint32_t w[32];
                             tmem_ld32(o_t + D + ch * 32, w);
                             tmem_wait32(w);
@@ -531,43 +691,53 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                         }
                         if (!row_ok) continue;
                         if (direct) {
+                            uint32_t w[16];
 #pragma unroll
-                            for (int k = 0; k < 32; k += 8) {
-                                uint32_t w[4];
+                            for (int k = 0; k < 16; ++k) {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(
+                                    __uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+                                w[k] = *reinterpret_cast<const uint32_t *>(&b);
+                            }
+                            uint16_t *to = out + ch * 32;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const __nv_bfloat162 b = __floats2bfloat162_rn(
-                                        __uint_as_float(v[k + 2 * e]) * inv, __uint_as_float(v[k + 2 * e + 1]) * inv);
-                                    w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                            for (int k = 0; k < 16; k += 8) {
+                                if (wide_out) {
+                                    stg32(to + 2 * k, w[k], w[k + 1], w[k + 2], w[k + 3], w[k + 4], w[k + 5],
+                                          w[k + 6], w[k + 7]);
+                                } else {
+                                    *reinterpret_cast<uint4 *>(to + 2 * k) =
+                                        make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                                    *reinterpret_cast<uint4 *>(to + 2 * k + 8) =
+                                        make_uint4(w[k + 4], w[k + 5], w[k + 6], w[k + 7]);
                                 }
-                                *reinterpret_cast<uint4 *>(out + ch * 32 + k) = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                *reinterpret_cast<uint4 *>(po + ch * 32 + k) =
-                                    make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                            for (int k = 0; k < 32; k += 8)
+                                stg32(po + ch * 32 + k, v[k], v[k + 1], v[k + 2], v[k + 3], v[k + 4], v[k + 5],
+                                      v[k + 6], v[k + 7]);
                         }
                     }
                     if (row_ok) {
                         if (!direct) {
                             float *ml = (full ? a.whole_ml : a.wpart_ml) + slot * 2;
-                            ml[0] = m;
+                            ml[0] = ref;
                             ml[1] = l;
                         } else if (a.lse) {
-                            a.lse[t * a.Hq + hq] = l > 0.0f ? kLn2 * (m + log2f(l)) : -INFINITY;
+                            a.lse[t * a.Hq + hq] = l > 0.0f ? kLn2 * (ref + log2f(l)) : -INFINITY;
                         }
                     }
                 }
             }
             ++no[0];
             if (p.both) ++no[1];
-            if (p.pairs) ++nml;
+            if (pairs) ++nml;
+            done();
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -589,7 +759,7 @@ jet_status launch(const DeviceInfo &dev, const Args &a, cudaStream_t stream) {
             done[dev.ordinal] = dev.context;
         }
     }
-    return launch_pdl(attention_wide_kernel<D>, dim3((unsigned)a.wide_ctas), dim3(kThreads), Cfg<D>::kSmem,
+    return launch_pdl(attention_wide_kernel<D>, dim3((unsigned)a.ctas), dim3(kThreads), Cfg<D>::kSmem,
                       stream, a, dev.status_word);
 }
 
