@@ -158,13 +158,21 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Args
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            int64_t before = tiles0[w];
-            int at = count0[w];
-            for (int i = 0; i < kPlanThreads / 32; ++i) {
-                if (i < warp) before += sh_tiles[w][i], at += sh_count[w][i];
-                tiles0[w] += sh_tiles[w][i];
-                count0[w] += sh_count[w][i];
+            // the warps' sums, scanned by every warp for itself
+            int64_t v = sh_tiles[w][lane];
+            int c = sh_count[w][lane];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t v1 = __shfl_up_sync(~0u, v, d);
+                const int c1 = __shfl_up_sync(~0u, c, d);
+                if (lane >= d) v += v1, c += c1;
             }
+            const int64_t vb = __shfl_sync(~0u, v, warp > 0 ? warp - 1 : 0);
+            const int cb = __shfl_sync(~0u, c, warp > 0 ? warp - 1 : 0);
+            const int64_t before = tiles0[w] + (warp > 0 ? vb : 0);
+            const int at = count0[w] + (warp > 0 ? cb : 0);
+            tiles0[w] += __shfl_sync(~0u, v, 31);
+            count0[w] += __shfl_sync(~0u, c, 31);
             if (s < nseg && wide == (w == 1)) g.before = before + incl[w] - mine[w];
             if (mine[w] > 0) {
                 order[w][at + cnt[w] - 1] = s;
@@ -182,13 +190,19 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Args
         p.total[0] = tiles0[0], p.total[1] = tiles0[1];
         p.workers[0] = workers[0], p.workers[1] = workers[1];
         p.empty = sh_empty;
+        p.splits = p.many = 0;
         *a.plan = p;
     }
     __threadfence_block();  // the segments written above, before other threads read them
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-        for (int c = tid; c < workers[w]; c += kPlanThreads) {
+    for (int w = 0; w < 2; ++w) {
+        const int all = w == 0 ? a.ctas * a.phases : a.ctas;
+        for (int c = tid; c < all; c += kPlanThreads) {
+            Start &st = a.starts[w * kNarrowWorkers + c];
+            st.empty = sh_empty;
+            st.left = 0;
+            if (c >= workers[w]) continue;
             const int64_t x = tiles0[w] * c / workers[w];
             int lo = 0, hi = count0[w] - 1;  // the last listed segment that begins at or before x
             while (lo < hi) {
@@ -196,21 +210,22 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Args
                 if ((mid < kPlanHeld ? sh_before[w][mid] : a.segs[order[w][mid]].before) <= x) lo = mid;
                 else hi = mid - 1;
             }
-            Start st;
             st.at = lo;
-            st.tiles = x - (lo < kPlanHeld ? sh_before[w][lo] : a.segs[order[w][lo]].before);
-            a.starts[w * kNarrowWorkers + c] = st;
+            st.s = order[w][lo];
+            st.g = a.segs[st.s];
+            st.left = tiles0[w] * (c + 1) / workers[w] - x;
+            st.from = x - st.g.before;
         }
+    }
 }
 
 template <int D>
 struct Cfg {
-    static constexpr int kWarps = D > 128 ? 4 : kNarrowWarps;  // of a CTA
+    static constexpr int kWarps = D > 128 ? 6 : kNarrowWarps;  // of a CTA
     static constexpr int kStageBytes = 2 * kStep * D;          // a warp's K and V
     static constexpr int kStages = D == 64 ? 5 : D == 128 ? 3 : 2;
     static constexpr int kWarpBytes = kStages * kStageBytes;
-    static constexpr int kQBytes = D > 128 ? kRows * D * 2 : 0;  // a warp's query fragments
-    static constexpr int kSmem = kWarps * (kWarpBytes + kQBytes);
+    static constexpr int kSmem = kWarps * kWarpBytes;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -224,57 +239,49 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
     griddep_wait();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
-    if (a.Ng == 0 && a.plan->empty > 0) clear_rows<D>(a);
     // this warp's worker, and its head among the worker's
     const int me = blockIdx.x * a.phases + warp / a.heads, hw = warp % a.heads;
-    const int64_t total = a.plan->total[0], workers = a.plan->workers[0];
-    if (warp >= a.phases * a.heads || me >= workers) return;
-    int64_t left = total * (me + 1) / workers - total * me / workers;  // tiles of the range
-    int64_t from = a.starts[me].tiles, at = a.starts[me].at;           // next: in its segment; that one
+    if (warp >= a.phases * a.heads) return;
+    const Start start = a.starts[me];
+    if (a.Ng == 0 && start.empty > 0) clear_rows<D>(a, warp * 32 + lane, a.phases * a.heads * 32);
+    int64_t left = start.left, from = start.from;  // tiles of the range; the next, in its segment
+    int at = start.at, s = start.s;
+    Segment sg = start.g;
     bool first = true;
     const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
-    uint2 *qs = reinterpret_cast<uint2 *>(smem + C::kWarps * C::kWarpBytes + warp * C::kQBytes);  // [KS][2][32]
 
     while (left > 0) {
-        const int s = a.order[at];
-        const Segment sg = a.segs[s];
+        if (from < 0) {  // the next segment
+            s = a.order[++at];
+            sg = a.segs[s];
+            from = 0;
+        }
         const Narrow nw(a, sg);
         const int ktiles = nw.ktiles;
         const int unit = (int)(from / ktiles);
         const int kt0 = (int)(from - (int64_t)unit * ktiles);
         const int kt1 = (int)min((int64_t)ktiles, kt0 + left);
         const int rt = unit / nw.groups, h = (unit - rt * nw.groups) * a.heads + hw;
-        const int64_t nrows = (int64_t)sg.ntok * a.G, row0 = (int64_t)rt * kRows;
-        if (first && a.Ng == 0 && hw == 0 && lane == 0) {
-            // the range begins in the middle of a unit: what the join will need
-            Split sp;
-            sp.rows = 0;
-            const int64_t u0 = sg.before + from - kt0;
-            if (kt0 > 0 && total * (me - 1) / workers <= u0) {
-                const Pieces pc(u0, ktiles, total, workers);
-                sp.token = sg.t0 + row0 / a.G, sp.sub = (int)(row0 % a.G), sp.head = h;
-                sp.rows = (int)min((int64_t)kRows, nrows - row0);
-                sp.n = pc.n, sp.c0 = pc.c0, sp.first = pc.first;
-            }
-            a.splits[me] = sp;
-        }
+        const uint32_t nrows = (uint32_t)sg.ntok * a.G, row0 = (uint32_t)rt * kRows;
+        if (first && a.Ng == 0 && hw == 0 && lane == 0)
+            tell_split(a, false, me, sg, from, kt0, ktiles, sg.t0 + row0 / a.G, (int)(row0 % a.G), h,
+                       (int)min((uint32_t)kRows, nrows - row0));
         left -= kt1 - kt0;
         from += kt1 - kt0;
-        if (from == nw.tiles()) from = 0, ++at;
+        if (from == nw.tiles()) from = -1;
         const bool begins = first;
         first = false;
         if (h >= a.Hk) continue;  // (the last group of heads may be short)
 
-        // queries: rows g and g + 8 of the tile, channels 64 i + 16 j .. + 15
-        uint32_t qf[D <= 128 ? KS : 1][4];
-        float f[2];
+        // the query: row g of the tile, channels 64 i + 16 j .. + 15
+        uint32_t qf[KS][2];
+        float f[2];                // of rows 2 j and 2 j + 1
         int pos[2];                // a row past the unit's last hides no key
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int64_t rr = row0 + g + 8 * r;
+        {
+            const uint32_t rr = row0 + g, tok = rr < nrows ? rr / a.G : 0;
             const bool ok = rr < nrows;
-            const int64_t t = sg.t0 + (ok ? rr / a.G : 0);
-            const int hq = h * a.G + (ok ? (int)(rr % a.G) : 0);
+            const int64_t t = sg.t0 + tok;
+            const int hq = h * a.G + (ok ? (int)(rr - tok * a.G) : 0);
             const uint16_t *src = a.q + t * a.ldq + (int64_t)hq * D + 16 * j;
             uint4 w[2 * H];
             float top = 0.0f;
@@ -290,36 +297,26 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
             }
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const float up = row_power(top);
-            f[r] = a.scale * a.ks[h] * kLog2e * inverse_power(up);
-            pos[r] = 0x7FFFFFFF;
-            if (ok) {
-                int b = s;
-                if (s >= a.B) b = min(sg.r0 + upper(a.off + sg.r0, sg.r1 - sg.r0, t), a.B - 1);
-                pos[r] = position(a, b, t);
+            float up = row_power(top);
+            float mine = a.scale * a.ks[h] * kLog2e * inverse_power(up);
+            if (mine < 0.0f) mine = -mine, up = -up;  // maxima are of the raw scores
+            mine = fmaxf(mine, 0x1p-126f);
+            const int place = ok ? position(a, sg, s, t) : 0x7FFFFFFF;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                f[r] = __shfl_sync(~0u, mine, 4 * (2 * j + r));
+                pos[r] = __shfl_sync(~0u, place, 4 * (2 * j + r));
             }
 #pragma unroll
             for (int i = 0; i < 2 * H; ++i) {
                 const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                uint32_t v[4];
+                // steps 4 (i / 2) + 2 (i % 2) + {0, 1}: channels 4 at a time
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    v[k] = pack_f16(__uint_as_float(u[k] << 16) * up,
-                                    __uint_as_float(u[k] & 0xFFFF0000u) * up);
-                // step 4 (i / 2) + 2 (i % 2) + {0, 1}: channels 4 at a time
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int ks = 4 * (i >> 1) + 2 * (i & 1) + k;
-                    if constexpr (D <= 128) {
-                        qf[ks][r] = v[2 * k];
-                        qf[ks][2 + r] = v[2 * k + 1];
-                    } else {
-                        qs[(ks * 2 + r) * 32 + lane] = make_uint2(v[2 * k], v[2 * k + 1]);
-                    }
-                }
+                    qf[4 * (i >> 1) + 2 * (i & 1) + (k >> 1)][k & 1] =
+                        pack_f16(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xFFFF0000u) * up);
             }
         }
-        if (D > 128) __syncwarp();
         const bool causal = __any_sync(~0u, min(pos[0], pos[1]) < sg.k1 - 1);
 
         const int32_t *tab = a.table + (int64_t)sg.row * a.width;
@@ -327,10 +324,10 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
         auto slot_of = [&](int kt) -> int {
             const int64_t p = (int64_t)sg.k0 + (int64_t)kt * kStep + lane;
             if (kt >= kt1 || p >= sg.k1) return -1;
-            const uint32_t blk = (uint32_t)p / (uint32_t)a.bs;
-            const int64_t id = tab[blk];
+            uint32_t in;
+            const int64_t id = tab[block_of(a, (uint32_t)p, in)];
             if (id < 0) return -1;
-            const int64_t slot = id * a.bs + ((uint32_t)p - blk * (uint32_t)a.bs);
+            const int64_t slot = id * a.bs + in;
             return slot < a.S ? (int)slot : -1;
         };
         auto issue = [&](int kt, int st, int slot) {
@@ -342,17 +339,18 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
                 for (int i = 0; i < KS; ++i) {
                     const int idx = i * 32 + lane, key = idx / KS, c = idx % KS;
                     const int sl = __shfl_sync(~0u, slot, key);
-                    const int64_t from = ((int64_t)(sl < 0 ? 0 : sl) * a.Hk + h) * D + c * 16;
-                    copy16(dst + place<D, false>(key, c), a.kc + from, sl >= 0);
-                    copy16(dst + 32 * D + place<D, true>(key, c), a.vc + from, sl >= 0);
+                    const int64_t at = (int64_t)(sl < 0 ? 0 : sl) * (a.Hk * D) + h * D + c * 16;
+                    copy16(dst + place<D, false>(key, c), a.kc + at, sl >= 0);
+                    copy16(dst + 32 * D + place<D, true>(key, c), a.vc + at, sl >= 0);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
 
-        float o[NT][4];
+        // o[n]: channels 16 (or 8) g + 2 n, + 1 of each 128 (or 64), for rows 2 j, 2 j + 1
+        float o[NT / 2][4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        for (int i = 0; i < NT / 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < ST - 1; ++i) issue(kt0 + i, i, slot_of(kt0 + i));
@@ -370,82 +368,75 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
             const uint32_t kb = ring + use_st * C::kStageBytes, vb = kb + 32 * D;
             const uint32_t mask = sh_mask[warp][use_st];
             if (mask == 0) continue;
-            // scores of keys 8 t + 2 j, + 1 for rows g and g + 8
-            float sc[4][4];
+            // scores of keys 16 t + g (and + 8) for rows 2 j and 2 j + 1: the keys are the
+            // products' rows, so that eight of the sixteen are not wasted on a few queries
+            float sc[2][4] = {};
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+            for (int i = 0; i < H; ++i) {
+                uint32_t u[4][4];
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
+                for (int t = 0; t < 4; ++t) {
                     const uint4 w = lds16(kb + place<D, false>(8 * t + g, 4 * i + j));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int ks = 4 * i + k;
-                        if constexpr (D <= 128) {
-                            mma16816(sc[t], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3],
-                                     codes_f16(u[k]), codes_f16_hi(u[k]));
-                        } else {
-                            const uint2 lo = qs[(ks * 2) * 32 + lane], hi = qs[(ks * 2 + 1) * 32 + lane];
-                            mma16816(sc[t], lo.x, hi.x, lo.y, hi.y, codes_f16(u[k]),
-                                     codes_f16_hi(u[k]));
-                        }
-                    }
+                    u[t][0] = w.x, u[t][1] = w.y, u[t][2] = w.z, u[t][3] = w.w;
                 }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        mma16816(sc[t], codes_f16(u[2 * t][k]), codes_f16(u[2 * t + 1][k]),
+                                 codes_f16_hi(u[2 * t][k]), codes_f16_hi(u[2 * t + 1][k]),
+                                 qf[4 * i + k][0], qf[4 * i + k][1]);
             }
-            float top[2] = {-INFINITY, -INFINITY};
-            // a key of the mask lies below 2^31, and so do its tile's others but for the last few
-            const uint32_t p0 = (uint32_t)sg.k0 + (uint32_t)kt * kStep + 2 * j;
-            const bool all = mask == ~0u && !causal;
+            if (mask != ~0u || causal) {
+                const uint32_t p0 = (uint32_t)sg.k0 + (uint32_t)kt * kStep;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = sc[t][e] * f[e >> 1];
-                    if (!all) {
-                        const int key = 8 * t + 2 * j + (e & 1);
-                        if (!((mask >> key) & 1) || (int64_t)(p0 + 8 * t + (e & 1)) > pos[e >> 1])
-                            v = -INFINITY;
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = 16 * t + 8 * (e >> 1) + g;
+                        // (a key of the mask lies below 2^31)
+                        if (!((mask >> key) & 1) || (int64_t)(p0 + key) > pos[e & 1]) sc[t][e] = -INFINITY;
                     }
-                    sc[t][e] = v;
-                    top[e >> 1] = fmaxf(top[e >> 1], v);
-                }
-            float use[2];
+            }
+            float top[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
-                top[r] = fmaxf(top[r], m[r]);
-                use[r] = top[r] == -INFINITY ? 0.0f : top[r];
+                top[r] = fmaxf(fmaxf(sc[0][r], sc[0][r + 2]), fmaxf(sc[1][r], sc[1][r + 2]));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 4));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 8));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 16));
+                top[r] = fmaxf(top[r] * f[r], m[r]);
             }
             if (__any_sync(~0u, top[0] != m[0] || top[1] != m[1])) {
-                const float c0 = ex2(m[0] - use[0]), c1 = ex2(m[1] - use[1]);
+                const float c0 = ex2(m[0] - (top[0] == -INFINITY ? 0.0f : top[0])),
+                            c1 = ex2(m[1] - (top[1] == -INFINITY ? 0.0f : top[1]));
                 l[0] *= c0;
                 l[1] *= c1;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
+                for (int i = 0; i < NT / 2; ++i) {
                     o[i][0] *= c0;
-                    o[i][1] *= c0;
-                    o[i][2] *= c1;
+                    o[i][1] *= c1;
+                    o[i][2] *= c0;
                     o[i][3] *= c1;
                 }
                 m[0] = top[0];
                 m[1] = top[1];
             }
-            uint32_t pw[4][2];
+            const float n0 = m[0] == -INFINITY ? 0.0f : -m[0], n1 = m[1] == -INFINITY ? 0.0f : -m[1];
+            // weights, turned so that a thread has those of row g and keys 2 j, 2 j + 1 (of
+            // each eight)
+            uint32_t pw[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float e0 = ex2(sc[t][2 * r] - use[r]), e1 = ex2(sc[t][2 * r + 1] - use[r]);
-                    l[r] += e0 + e1;
-                    pw[t][r] = pack_f16(e0, e1);
-                }
-            // values: keys 16 u + {2j, 2j + 1, 2j + 8, 2j + 9}
+            for (int t = 0; t < 4; ++t) {
+                const float e0 = ex2(fmaf(sc[t >> 1][2 * (t & 1)], f[0], n0)),
+                            e1 = ex2(fmaf(sc[t >> 1][2 * (t & 1) + 1], f[1], n1));
+                l[0] += e0;
+                l[1] += e1;
+                asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pw[t]) : "r"(pack_f16(e0, e1)));
+            }
+            // values: keys 16 u + {2j, 2j + 1, 2j + 8, 2j + 9}, channels as the products' rows
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint32_t a0 = pw[2 * u][0], a1 = pw[2 * u][1], a2 = pw[2 * u + 1][0],
-                               a3 = pw[2 * u + 1][1];
                 const int r0 = 16 * u + 2 * j;
                 constexpr int HV = D == 256 ? 2 : 1, NW = D == 64 ? 2 : 4;
 #pragma unroll
@@ -472,50 +463,53 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
                                        l1 = __byte_perm(w[0][c], w[1][c], 0x7362),
                                        h0 = __byte_perm(w[2][c], w[3][c], 0x5140),
                                        h1 = __byte_perm(w[2][c], w[3][c], 0x7362);
-                        const int n = hv * 16 + c * 4;
-                        mma16816(o[n], a0, a1, a2, a3, codes_f16(l0), codes_f16(h0));
-                        mma16816(o[n + 1], a0, a1, a2, a3, codes_f16_hi(l0), codes_f16_hi(h0));
-                        mma16816(o[n + 2], a0, a1, a2, a3, codes_f16(l1), codes_f16(h1));
-                        mma16816(o[n + 3], a0, a1, a2, a3, codes_f16_hi(l1), codes_f16_hi(h1));
+                        const int n = hv * 8 + c * 2;
+                        mma16816(o[n], codes_f16(l0), codes_f16_hi(l0), codes_f16(h0), codes_f16_hi(h0),
+                                 pw[2 * u], pw[2 * u + 1]);
+                        mma16816(o[n + 1], codes_f16(l1), codes_f16_hi(l1), codes_f16(h1), codes_f16_hi(h1),
+                                 pw[2 * u], pw[2 * u + 1]);
                     }
                 }
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         const bool full = kt1 - kt0 == ktiles, direct = full && a.Ng == 0;
-        constexpr int W = D == 64 ? 8 : 16;  // channels of one column of a fragment
+        constexpr int W = D == 64 ? 8 : 16;  // channels of a thread (of each 128)
         float *const po = full ? a.whole : a.part, *const pml = full ? a.whole_ml : a.part_ml;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(~0u, l[r], 1);
-            l[r] += __shfl_xor_sync(~0u, l[r], 2);
-            const int64_t rr = row0 + g + 8 * r;
+            l[r] += __shfl_xor_sync(~0u, l[r], 4);
+            l[r] += __shfl_xor_sync(~0u, l[r], 8);
+            l[r] += __shfl_xor_sync(~0u, l[r], 16);
+            const uint32_t rr = row0 + 2 * j + r;
             if (rr >= nrows) continue;
-            const int64_t t = sg.t0 + rr / a.G;
-            const int hq = h * a.G + (int)(rr % a.G);
+            const uint32_t tok = rr / a.G;
+            const int64_t t = sg.t0 + tok;
+            const int hq = h * a.G + (int)(rr - tok * a.G);
             const int64_t slot = full ? ((s < a.B ? a.T : 0) + t) * a.Hq + hq
-                                      : ((int64_t)(2 * me + (begins ? 0 : 1)) * a.heads + hw) * kRows + g + 8 * r;
+                                      : ((int64_t)(2 * me + (begins ? 0 : 1)) * a.heads + hw) * kRows + 2 * j + r;
             const float inv = l[r] > 0.0f ? a.vs[h] / l[r] : 0.0f;
-            // the thread's channels of a row are 2 W neighbours (of each 128)
 #pragma unroll
-            for (int n = 0; n < NT; n += 4)
+            for (int n = 0; n < NT / 2; n += 4) {
+                const int d = (n / 8) * 128 + W * g + 2 * (n % 8);
+                const float v[8] = {o[n][r], o[n][2 + r], o[n + 1][r], o[n + 1][2 + r],
+                                    o[n + 2][r], o[n + 2][2 + r], o[n + 3][r], o[n + 3][2 + r]};
+                if (direct) {
+                    uint32_t w[4];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int d = (n / W) * 128 + n % W + W * (2 * j + c);
-                    const float v0 = o[n][2 * r + c], v1 = o[n + 1][2 * r + c], v2 = o[n + 2][2 * r + c],
-                                v3 = o[n + 3][2 * r + c];
-                    if (direct) {
-                        const __nv_bfloat162 b0 = __floats2bfloat162_rn(v0 * inv, v1 * inv),
-                                             b1 = __floats2bfloat162_rn(v2 * inv, v3 * inv);
-                        uint2 w;
-                        w.x = *reinterpret_cast<const uint32_t *>(&b0);
-                        w.y = *reinterpret_cast<const uint32_t *>(&b1);
-                        *reinterpret_cast<uint2 *>(a.out + t * a.ldo + (int64_t)hq * D + d) = w;
-                    } else {
-                        *reinterpret_cast<float4 *>(po + slot * D + d) = make_float4(v0, v1, v2, v3);
+                    for (int k = 0; k < 4; ++k) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
+                        w[k] = *reinterpret_cast<const uint32_t *>(&b);
                     }
+                    *reinterpret_cast<uint4 *>(a.out + t * a.ldo + (int64_t)hq * D + d) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(po + slot * D + d);
+                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
                 }
-            if (j == 0) {
+            }
+            if (g == 0) {
                 if (!direct) {
                     pml[slot * 2] = m[r];
                     pml[slot * 2 + 1] = l[r];
@@ -577,12 +571,8 @@ struct Row {
     }
 };
 
-// Without groups: the rows of the units that more than one worker had, each found by
-// the first worker that began in its middle.  A CTA takes the rows r0, r0 + 4, ... of one
-// of them (and one head); a row's pieces are shared by one warp, or by eight where there
-// are many.
-constexpr int kJoinRows = 4;
-
+// Without groups: the rows of the units that more than one worker had.  A warp takes a
+// row; a row of many pieces is shared by a CTA's eight.
 template <int D>
 __global__ void __launch_bounds__(256, 4) attention_join_split_kernel(const Args a) {
     griddep_launch_dependents();
@@ -592,38 +582,40 @@ __global__ void __launch_bounds__(256, 4) attention_join_split_kernel(const Args
     const bool wide = a.wide_own;
     const int heads = wide ? 1 : a.heads, rows = wide ? kWideRows : kRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int worker = blockIdx.x / heads, hw = blockIdx.x % heads;
-    if (worker >= a.plan->workers[wide]) return;
-    const Split sp = a.splits[(wide ? kNarrowWorkers : 0) + worker];
-    const int h = sp.head + hw;
-    if (sp.rows == 0 || h >= a.Hk) return;
+    const int splits = a.plan->splits, many = a.plan->many;
     const float *po = wide ? a.wpart : a.part, *ml = wide ? a.wpart_ml : a.part_ml;
-    const int each = sp.n > 8 ? 8 : 1;  // warps a row
-    for (int r = blockIdx.y + gridDim.y * (warp / each); r < sp.rows; r += gridDim.y * (8 / each)) {
-        auto slot = [&](int i) -> int64_t {
-            return ((i == 0 ? sp.first : 2 * (sp.c0 + i)) * (int64_t)heads + hw) * rows + r;
-        };
-        Row<D> row;
-        const uint32_t rr = sp.sub + r, tok = rr / (uint32_t)a.G;
-        const int64_t t = sp.token + tok;
-        const int hq = h * a.G + (int)(rr - tok * a.G);
-        if (each == 1) {
-            row.add(po, ml, sp.n, slot);
-            row.write(a, t, hq);
-            continue;
-        }
-        const int i0 = sp.n * warp / 8, i1 = sp.n * (warp + 1) / 8;
-        row.add(po, ml, i1 - i0, [&](int i) { return slot(i0 + i); });
+    for (int pass = 0; pass <= many; ++pass) {
+        const int chunks = pass == 0 ? rows / 8 : rows;  // of a unit and head: 8 rows, or one
+        for (int i = blockIdx.x; i < splits * heads * chunks; i += gridDim.x) {
+            const int unit = i / chunks, chunk = i - unit * chunks, hw = unit % heads;
+            const Split sp = a.splits[unit / heads];
+            const int h = sp.head + hw, r = pass == 0 ? chunk * 8 + warp : chunk;
+            if ((sp.n > kManyPieces) != (pass == 1) || h >= a.Hk || r >= sp.rows) continue;
+            auto slot = [&](int k) -> int64_t {
+                return ((k == 0 ? sp.first : 2 * (sp.c0 + k)) * (int64_t)heads + hw) * rows + r;
+            };
+            const uint32_t rr = sp.sub + r, tok = rr / (uint32_t)a.G;
+            const int64_t t = sp.token + tok;
+            const int hq = h * a.G + (int)(rr - tok * a.G);
+            Row<D> row;
+            if (pass == 0) {
+                row.add(po, ml, sp.n, slot);
+                row.write(a, t, hq);
+                continue;
+            }
+            const int k0 = sp.n * warp / 8, k1 = sp.n * (warp + 1) / 8;
+            row.add(po, ml, k1 - k0, [&](int k) { return slot(k0 + k); });
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) sh_o[warp][lane + 32 * e] = row.o[e];
-        if (lane == 0) sh_ml[warp] = make_float2(row.m, row.l);
-        __syncthreads();
-        if (warp == 0) {
-            Row<D> all;
-            all.add(&sh_o[0][0], reinterpret_cast<const float *>(sh_ml), 8, [](int i) { return (int64_t)i; });
-            all.write(a, t, hq);
+            for (int e = 0; e < D / 32; ++e) sh_o[warp][lane + 32 * e] = row.o[e];
+            if (lane == 0) sh_ml[warp] = make_float2(row.m, row.l);
+            __syncthreads();
+            if (warp == 0) {
+                Row<D> all;
+                all.add(&sh_o[0][0], reinterpret_cast<const float *>(sh_ml), 8, [](int k) { return (int64_t)k; });
+                all.write(a, t, hq);
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -667,7 +659,7 @@ __global__ void __launch_bounds__(256, 4) attention_join_kernel(const Args a) {
                 r = (int)((t - g.t0) - (int64_t)rt * w.tokens) * a.G + gi;
             } else {
                 const Narrow w(a, g);
-                const int64_t rr = (t - g.t0) * a.G + gi;
+                const uint32_t rr = (uint32_t)(t - g.t0) * a.G + gi;
                 n = w.ktiles;
                 u0 += (rr / kRows * w.groups + h / a.heads) * n;
                 r = (int)(rr % kRows);
@@ -729,7 +721,7 @@ Layout layout(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B, int64_t N
 
 bool shape_ok(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B, int64_t Ng) {
     if (T < 0 || Hq < 0 || Hk < 0 || B < 0 || Ng < 0) return false;
-    if (Hq > 1024 || T >= (int64_t)1 << 24 || B > 8192 || Ng > B) return false;
+    if (Hq > 1024 || T >= (int64_t)1 << 24 || T * Hq >= (int64_t)1 << 31 || B > 8192 || Ng > B) return false;
     if (Hq > 0 && (Hk == 0 || Hq % Hk != 0)) return false;
     return D == 64 || D == 128 || D == 256;
 }
@@ -762,9 +754,7 @@ jet_status launch(const DeviceInfo &dev, const Args &a, cudaStream_t stream) {
         return launch_pdl(attention_join_kernel<D>, dim3((unsigned)a.B, (unsigned)(want < 1 ? 1 : want > 1024 ? 1024 : want)),
                           dim3(256), 0, stream, a);
     }
-    const int units = a.wide_own ? a.ctas : a.ctas * a.phases * a.heads;
-    return launch_pdl(attention_join_split_kernel<D>, dim3((unsigned)units, a.wide_own ? 8 : kJoinRows), dim3(256),
-                      0, stream, a);
+    return launch_pdl(attention_join_split_kernel<D>, dim3((unsigned)(4 * dev.num_sms)), dim3(256), 0, stream, a);
 }
 
 inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -816,6 +806,9 @@ jet_status jet_kv_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H
     a.q = q, a.ldq = ldq, a.T = T, a.Hq = (int)Hq, a.Hk = (int)Hk, a.G = (int)(Hq / Hk);
     a.kc = k_cache, a.vc = v_cache, a.S = S, a.ks = k_scale, a.vs = v_scale;
     a.table = table, a.width = width, a.bs = block_size, a.off = offsets, a.len = lengths;
+    a.bs_shift = -1;
+    for (int i = 0; i < 30; ++i)
+        if (block_size == (int64_t)1 << i) a.bs_shift = i;
     a.B = (int)B, a.po = prefix_offsets, a.pl = prefix_lengths, a.Ng = (int)n_prefix;
     a.scale = scale, a.out = out, a.ldo = ldo, a.lse = lse;
     // arrays begin at multiples of 256

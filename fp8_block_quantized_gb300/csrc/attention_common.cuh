@@ -11,7 +11,7 @@ namespace attn {
 
 constexpr int kTile = 128;         // keys of a wide tile
 constexpr int kStep = 32;          // keys of a narrow tile
-constexpr int kRows = 16;          // rows of a narrow unit
+constexpr int kRows = 8;           // rows of a narrow unit
 constexpr int kMaxCtas = 160;      // most CTAs of a launch (one on each SM)
 constexpr int kNarrowWarps = 8;    // most of a CTA
 constexpr int kNarrowWorkers = kMaxCtas * kNarrowWarps;
@@ -28,6 +28,7 @@ struct Args {
     const float *ks, *vs;
     const int32_t *table;
     int64_t width, bs;
+    int bs_shift;                  // log2 of bs, or -1
     const int64_t *off;
     const int32_t *len;
     int B;
@@ -50,7 +51,7 @@ struct Args {
     struct Segment *segs;          // [B + Ng]
     int *order;                    // [2][B + Ng] the segments with work (narrow, wide)
     struct Start *starts;          // [kNarrowWorkers + kMaxCtas] of the workers' ranges
-    struct Split *splits;          // the same, of the units that the ranges begin in
+    struct Split *splits;          // [the same], in no order
     struct Plan *plan;
 };
 
@@ -94,34 +95,44 @@ struct Segment {
     int group;         // own part: the request's group, or -1
 };
 
-// Where a worker's range begins: the segment order[at], `tiles` tiles into it.
+// A worker's range: how many tiles, from which one of the segment order[at] = s on;
+// what it needs at first in one read.
 struct Start {
-    int64_t tiles;
-    int64_t at;
+    Segment g;
+    int64_t left, from;
+    int at, s;
+    int empty;         // the plan's
+    int pad;
 };
 
 struct Plan {
     int64_t total[2];  // tiles (narrow, wide)
     int workers[2];    // none of them without a tile
     int empty;         // segments with tokens and no keys
+    int splits;        // units that more than one worker has (without groups)
+    int many;          // whether one of them has more than kManyPieces pieces
 };
+constexpr int kManyPieces = 8;
 
-// The unit that a worker's range begins in the middle of, if that is the unit's first
-// such worker: what is to be joined.
+// A unit that more than one worker has, as the first worker that begins in its middle
+// tells it the join.
 struct Split {
     int64_t token;     // the unit's first row: token and query head within the KV head's group
     int sub;
     int head;          // its first KV head
-    int rows;          // 0: nothing to join
+    int rows;
     int n, c0, first;  // pieces: their number, the first one's worker and slot
 };
 
-// Position of token t of request b.
-__device__ __forceinline__ int position(const Args &a, int b, int64_t t) {
+// Position of token t of segment s.
+__device__ __forceinline__ int position(const Args &a, const Segment &g, int s, int64_t t) {
+    if (g.base >= 0) return g.base + (int)(t - g.t0);
+    int b = s;
+    if (s >= a.B) b = min(g.r0 + upper(a.off + g.r0, g.r1 - g.r0, t), a.B - 1);
     return (int)clamp64((int64_t)a.len[b] - (a.off[b + 1] - t), -1, 0x7FFFFFFF);
 }
 
-// Narrow units: 16 rows of each of `heads` KV heads, whose keys lie side by side.
+// Narrow units: 8 rows of each of `heads` KV heads, whose keys lie side by side.
 struct Narrow {
     int rtiles, groups, ktiles;  // row tiles, groups of heads, key tiles
     __device__ Narrow(const Args &a, const Segment &g) {
@@ -176,6 +187,27 @@ struct Pieces {
     __device__ int64_t slot(int i) const { return i == 0 ? first : 2 * (c0 + i); }
 };
 
+// Adds the unit of `tiles` tiles that worker `me` begins in, `in` tiles from its start, to
+// the splits, if it is the first to.
+__device__ __forceinline__ void tell_split(const Args &a, bool wide, int me, const Segment &g, int64_t from,
+                                           int in, int tiles, int64_t token, int sub, int head, int rows) {
+    const int64_t total = a.plan->total[wide], workers = a.plan->workers[wide], u0 = g.before + from - in;
+    if (in == 0 || total * (me - 1) / workers > u0) return;
+    const Pieces p(u0, tiles, total, workers);
+    Split sp;
+    sp.token = token, sp.sub = sub, sp.head = head, sp.rows = rows;
+    sp.n = p.n, sp.c0 = p.c0, sp.first = p.first;
+    if (p.n > kManyPieces) a.plan->many = 1;
+    a.splits[atomicAdd(&a.plan->splits, 1)] = sp;
+}
+
+// Block of key p and the key's place in it.
+__device__ __forceinline__ uint32_t block_of(const Args &a, uint32_t p, uint32_t &at) {
+    const uint32_t b = a.bs_shift >= 0 ? p >> a.bs_shift : p / (uint32_t)a.bs;
+    at = p - b * (uint32_t)a.bs;
+    return b;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -217,17 +249,17 @@ __device__ __forceinline__ float inverse_power(float v) {
 // The rows of the segments without keys, where no join writes them (without
 // groups).
 template <int D>
-__device__ __forceinline__ void clear_rows(const Args &a) {
+__device__ __forceinline__ void clear_rows(const Args &a, int tid, int threads) {
     for (int s = blockIdx.x; s < a.B; s += gridDim.x) {
         const Segment &g = a.segs[s];
         if (g.k1 > g.k0) continue;
         const int64_t n = (int64_t)g.ntok * a.Hq * (D / 8);
-        for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
+        for (int64_t i = tid; i < n; i += threads) {
             const int64_t t = g.t0 + i / (a.Hq * (D / 8)), c = i % (a.Hq * (D / 8));
             *reinterpret_cast<uint4 *>(a.out + t * a.ldo + c * 8) = make_uint4(0, 0, 0, 0);
         }
         if (a.lse)
-            for (int64_t i = threadIdx.x; i < (int64_t)g.ntok * a.Hq; i += blockDim.x)
+            for (int64_t i = tid; i < (int64_t)g.ntok * a.Hq; i += threads)
                 a.lse[g.t0 * a.Hq + i] = -INFINITY;
     }
 }

@@ -72,6 +72,7 @@ struct Piece {
     int64_t token;     // the unit's first
     int s, r0, r1;     // segment; its requests
     int k0, k1, row;   // keys, table row
+    int base;          // the first token's position, or -1
     int h;
     int kt0, n;        // first tile (or pair of tiles) and their number; n = 0: no more
     int ktiles;        // of the unit
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
     const uint32_t tmem = tmem_sh;
     griddep_launch_dependents();
     griddep_wait();
-    if (a.Ng == 0 && a.plan->empty > 0) clear_rows<D>(a);
+    if (a.Ng == 0 && a.starts[kNarrowWorkers + blockIdx.x].empty > 0) clear_rows<D>(a, tid, kThreads);
 
     // A warp's wait for the n-th phase of a barrier, and its arrival.  One lane does
     // either: every lane's would be one operation on the barrier after another, in
@@ -224,23 +225,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
         reg_dealloc<kRegsControl>();
         if (warp == 18) {
             // ------------------------------------------------------ the walk
-            const int64_t total = a.plan->total[1], workers = a.plan->workers[1];
-            int64_t left = 0, from = 0;  // tiles of the CTA's range; the next one in its segment
-            int64_t at = 0;
-            if (blockIdx.x < workers) {
-                const Start &st = a.starts[kNarrowWorkers + blockIdx.x];
-                left = total * (blockIdx.x + 1) / workers - total * blockIdx.x / workers;
-                from = st.tiles, at = st.at;
-            }
+            const Start &start = a.starts[kNarrowWorkers + blockIdx.x];
+            int64_t left = start.left, from = start.from;  // tiles of the range; the next, in its segment
+            int at = start.at, s = start.s;
+            Segment g = start.g;
             const int *order = a.order + a.B + a.Ng;
             bool more = true, first = true;
             for (uint32_t i = 0; more; ++i) {
                 Piece p;
                 p.n = 0;
                 if (left > 0) {
-                    int s = order[at];
-                    Segment g = a.segs[s];
-                    Wide w(a, g);
+                    if (from < 0) {  // the next segment
+                        s = order[++at];
+                        g = a.segs[s];
+                        from = 0;
+                    }
+                    const Wide w(a, g);
                     // the row tile that holds tile `from`
                     int64_t u = from;
                     int rt = 0;
@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     p.s = s;
                     p.r0 = g.r0, p.r1 = g.r1;
                     p.k0 = g.k0, p.k1 = g.k1, p.row = g.row;
+                    p.base = g.base >= 0 ? g.base + rt * w.tokens : -1;
                     p.ktiles = w.ktiles(g, rt);
                     p.h = (int)((uint32_t)u / (uint32_t)p.ktiles);
                     p.kt0 = (int)((uint32_t)u - (uint32_t)p.h * p.ktiles);
@@ -262,23 +263,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     p.pairs = w.keys != kTile;
                     p.rows = min(w.tokens, g.ntok - rt * w.tokens) * a.G;
                     p.both = p.pairs || p.rows > 128;
-                    if (lane == 0 && first && a.Ng == 0) {
-                        // the range begins in the middle of a unit: what the join will need
-                        Split sp;
-                        sp.rows = 0;
-                        const int64_t u0 = g.before + from - p.kt0;
-                        if (p.kt0 > 0 && total * ((int64_t)blockIdx.x - 1) / workers <= u0) {
-                            const Pieces pc(u0, p.ktiles, total, workers);
-                            sp.token = p.token, sp.sub = 0, sp.head = p.h, sp.rows = p.rows;
-                            sp.n = pc.n, sp.c0 = pc.c0, sp.first = pc.first;
-                        }
-                        a.splits[kNarrowWorkers + blockIdx.x] = sp;
-                    }
+                    if (lane == 0 && first && a.Ng == 0)
+                        tell_split(a, true, blockIdx.x, g, from, p.kt0, p.ktiles, p.token, 0, p.h, p.rows);
                     p.first = first;
                     first = false;
                     left -= p.n;
                     from += p.n;
-                    if (rt == w.rtiles - 1 && p.h == a.Hk - 1 && p.kt0 + p.n == p.ktiles) from = 0, ++at;
+                    if (rt == w.rtiles - 1 && p.h == a.Hk - 1 && p.kt0 + p.n == p.ktiles) from = -1;
                 }
                 more = p.n > 0;
                 if (!wait(&piece_empty[i & 1], (i >> 1) + 1, kSitePiece)) break;
@@ -382,9 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                 const int64_t key = key0 + (int64_t)i * kTile;
                 Entry e = {-1, 0u};
                 if (i < tiles && key < k1) {
-                    const uint32_t blk = (uint32_t)key / (uint32_t)a.bs;
-                    e.at = (uint32_t)key - blk * (uint32_t)a.bs;
-                    e.id = tab[blk];
+                    e.id = tab[block_of(a, (uint32_t)key, e.at)];
                 }
                 return e;
             };
@@ -501,9 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     }
                 }
                 if (row_ok) {
-                    int b = p.r0;
-                    if (p.s >= a.B) b = min(p.r0 + upper(a.off + p.r0, p.r1 - p.r0, t), a.B - 1);
-                    pos = position(a, b, t);
+                    Segment g;
+                    g.t0 = p.token, g.r0 = p.r0, g.r1 = p.r1, g.base = p.base;
+                    pos = position(a, g, p.s, t);
                 }
                 float up = row_power(top);
                 f = a.scale * a.ks[p.h] * kLog2e * inverse_power(up);

@@ -689,7 +689,7 @@ JET_API jet_status jet_sample_unaligned(const void *logits, int dtype, int64_t B
  *   lse [T][Hq] FP32 (out), or NULL.
  *   ws / ws_bytes: at least jet_kv_attention_workspace() bytes of device
  *       memory; scratch, not initialised.
- * 0 <= T < 2^24; Hq <= 1024, a multiple of Hk; D = 64, 128 or 256; B <= 8192;
+ * 0 <= T < 2^24, T*Hq < 2^31; Hq <= 1024, a multiple of Hk; D = 64, 128 or 256; B <= 8192;
  * n_prefix <= B; S, width < 2^31; 1 <= block_size < 2^30; scale > 0; strides
  * >= Hq*D and multiples of 8.
  */
