@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(256, 4) attention_join_kernel(const Args a) {
 
 // Which segments go to the wide kernel, by the rows that a unit has on average:
 // requests' own parts and prefixes.
-constexpr int64_t kWideFrom = 32;
+constexpr int64_t kWideFrom = 48;
 
 struct Layout {
     bool wide_own, wide_prefix;

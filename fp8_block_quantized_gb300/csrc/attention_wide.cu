@@ -9,8 +9,8 @@
 //                   maximum, weights e^(x - max) as FP16 back to TMEM over the
 //                   scores (handed on 64 keys at a time), and at a piece's end its
 //                   output;
-//   warps 8-15      the tiles' codes: read through the block table a tile ahead
-//                   (32 KB in flight), turned to FP16 (exact) and laid out in
+//   warps 8-15      the tiles' codes, four warps a stage: read through the
+//                   block table two tiles ahead (64 KB in flight), turned to FP16 (exact) and laid out in
 //                   shared memory, K and V alike as rows of keys with the 128-byte
 //                   swizzle: K-major for the scores, MN-major for the values;
 //   warps 16, 17    issue the MMAs of A and of B: scores S = Q K^T (both operands in
@@ -45,11 +45,11 @@ using namespace jet::ptx;
 
 constexpr int kThreads = 640;
 constexpr int kLoaders = 8;
-// Registers a thread of each warpgroup after setmaxnreg: 2 x 128 x 128 + 2 x 128 x 80 +
+// Registers a thread of each warpgroup after setmaxnreg: 2 x 128 x 112 + 2 x 128 x 96 +
 // 128 x 64 = 640 x 96, what the block is launched with.
-constexpr uint32_t kRegsRows = 128, kRegsLoad = 80, kRegsControl = 64;
+constexpr uint32_t kRegsRows = 112, kRegsLoad = 96, kRegsControl = 64;
 static_assert(256 * kRegsRows + 256 * kRegsLoad + 128 * kRegsControl <= kThreads * 96, "registers");
-constexpr int kStages = 3;  // of which units of 256 rows use two
+constexpr int kStages = 2;
 // Wait sites in the status word (after those of head.cu).
 constexpr unsigned kSiteLoad = 24, kSiteQuery = 25, kSiteTile = 26, kSiteWeights = 27, kSiteScores = 28,
                    kSiteOutput = 29, kSiteDrain = 30, kSitePiece = 31;
@@ -59,9 +59,7 @@ struct Cfg {
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kKBytes = 128 * D * 2;
     static constexpr int kStageBytes = 2 * kKBytes;
-    // Two queries' tiles and two stages; the third stage's keys are in the place of
-    // the second queries' tile (units of at most 128 rows have one), its values behind.
-    static constexpr int kUsed = 2 * kQBytes + 2 * kStageBytes + kKBytes + 1024;
+    static constexpr int kUsed = 2 * kQBytes + kStages * kStageBytes + 1024;
     // at least half of an SM's, so that no second CTA waits there for TMEM
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -81,23 +79,14 @@ struct Piece {
     int first;         // of this CTA
 };
 
-// The stages of a piece's tiles, in turn from the first one on, and how often each
-// was used before; the same for all roles.
+// How often the stages were used before a piece; its tiles take them in turn from the
+// first one on (where A and B have alternate tiles, each half has its own stage).  The
+// same for all roles.
 struct Ring {
-    uint32_t used[kStages] = {0, 0, 0};
-    // stage of a tile and its use of it
-    __device__ static int stage(bool pairs, int tile) { return pairs ? tile % 3 : tile & 1; }
-    __device__ uint32_t use(bool pairs, int tile) const {
-        const int st = stage(pairs, tile);
-        return (st == 0 ? used[0] : st == 1 ? used[1] : used[2]) + (pairs ? tile / 3 : tile >> 1);
-    }
-    __device__ void end(bool pairs, int tiles) {
-        if (pairs) {
-            used[0] += (tiles + 2) / 3, used[1] += (tiles + 1) / 3, used[2] += tiles / 3;
-        } else {
-            used[0] += (tiles + 1) >> 1, used[1] += tiles >> 1;
-        }
-    }
+    uint32_t used[kStages] = {0, 0};
+    __device__ static int stage(int tile) { return tile & 1; }
+    __device__ uint32_t use(int tile) const { return (tile & 1 ? used[1] : used[0]) + (tile >> 1); }
+    __device__ void end(int tiles) { used[0] += (tiles + 1) >> 1, used[1] += tiles >> 1; }
 };
 
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -148,10 +137,10 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args a, unsigned *status) {
     using C = Cfg<D>;
     extern __shared__ uint8_t dyn[];
-    __shared__ uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2],
+    __shared__ uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2], pv_done[2],
         o_full[2], ml_full, drain_bar, piece_full[2], piece_empty[2];
     __shared__ Piece pieces[2];
-    __shared__ __align__(16) uint16_t sh_mask[kStages][8];
+    __shared__ __align__(16) uint32_t sh_mask[kStages][4];
     __shared__ float sh_m[128], sh_l[128];
     __shared__ uint64_t in_turn[4][2];
     __shared__ uint32_t tmem_sh;
@@ -165,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
         mbar_init(&ml_full, 4);
         mbar_init(&drain_bar, 2);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&kv_full[i], kLoaders);
+            mbar_init(&kv_full[i], kLoaders / 2);
             mbar_init(&kv_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -173,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
             mbar_init(&p_full[i][0], 4);
             mbar_init(&p_full[i][1], 4);
             mbar_init(&o_full[i], 1);
+            mbar_init(&pv_done[i], 1);
             for (int q = 0; q < 4; ++q) mbar_init(&in_turn[q][i], 1);
             mbar_init(&piece_full[i], 1);
             mbar_init(&piece_empty[i], 8 + kLoaders + 2);
@@ -203,12 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
         if (lane == 0) mbar_arrive(bar);
     };
     const uint32_t q_s = smem;
-    auto keys_at = [&](int st) -> uint32_t {
-        return st < 2 ? smem + 2 * C::kQBytes + st * C::kStageBytes : smem + C::kQBytes;
-    };
-    auto values_at = [&](int st) -> uint32_t {
-        return smem + 2 * C::kQBytes + (st < 2 ? st * C::kStageBytes + C::kKBytes : 2 * C::kStageBytes);
-    };
+    auto keys_at = [&](int st) -> uint32_t { return smem + 2 * C::kQBytes + st * C::kStageBytes; };
+    auto values_at = [&](int st) -> uint32_t { return keys_at(st) + C::kKBytes; };
     uint32_t np = 0;  // pieces so far
     Ring ring;
     // The next piece (a warp's calls): waited for, and given back when done with.  It
@@ -303,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                 done();
                 const uint64_t qa = kKMajor + ((q_s + (pairs ? 0 : hf) * C::kQBytes) >> 4);
                 auto scores = [&](int i) -> bool {
-                    const int tile = i * each + (pairs ? hf : 0), st = Ring::stage(pairs, tile);
-                    if (!wait(&kv_full[st], ring.use(pairs, tile), kSiteTile)) return false;
+                    const int tile = i * each + (pairs ? hf : 0), st = Ring::stage(tile);
+                    if (!wait(&kv_full[st], ring.use(tile), kSiteTile)) return false;
                     tc_fence_after();
                     const uint64_t kb = kKMajor + (keys_at(st) >> 4);
 #pragma unroll
@@ -317,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                 };
                 if (n > 0) ok = scores(0);
                 for (int i = 0; ok && i < n; ++i, ++nt) {
-                    const int st = Ring::stage(pairs, i * each + (pairs ? hf : 0));
+                    const int st = Ring::stage(i * each + (pairs ? hf : 0));
                     const uint64_t vb = kMnMajor + (values_at(st) >> 4);
                     // values, 64 keys at a time, the later ones first
 #pragma unroll
@@ -329,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                         for (int ks = 0; ks < 4; ++ks)
                             mma_16bit_ta_if(lead, o_t, s_t + 64 + b * 32 + ks * 8, vb + (b * 8192 + ks * 2048) / 16, kO,
                                             i > 0 || b == 0 || ks > 0);
+                        if (b == 1) commit_if(lead, &pv_done[hf]);
                     }
                     if (!ok) break;
                     commit_if(lead, &kv_empty[st]);
@@ -336,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     if (i + 1 == n) commit_if(lead, &o_full[hf]);
                     else ok = scores(i + 1);
                 }
-                ring.end(pairs, all * each);
+                ring.end(all * each);
             }
             commit_if(lead, &drain_bar);
             __syncwarp();
@@ -347,21 +334,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
         reg_dealloc<kRegsLoad>();
         constexpr int CH = D / 16;          // 16-byte chunks of a key's codes
         constexpr int RW = 32 / CH;         // rows a warp reads at once
-        constexpr int KW = kTile / kLoaders;  // rows of a warp
+        constexpr int KW = 2 * kTile / kLoaders;  // rows of a warp
         constexpr int NI = KW / RW;
-        const int w = warp - 8;
-        uint32_t no = 0;                    // outputs of B so far
-        bool ok = true, queries = false;    // the last piece had queries in B's place
+        const int w = warp & 3, set = (warp - 8) >> 2;  // the two sets have a stage each
+        bool ok = true;
         while (ok && next()) {
             const Piece &p = pieces[np & 1];
             const bool pairs = p.pairs;
             const int64_t key0 = (int64_t)p.k0 + (int64_t)p.kt0 * (pairs ? 2 : 1) * kTile + KW * w + lane;
-            const int k1 = lane < KW ? p.k1 : 0, tiles = p.n * (pairs ? 2 : 1);
+            const int k1 = p.k1, tiles = p.n * (pairs ? 2 : 1);
             const int64_t head = (int64_t)p.h * D;
-            // the third stage takes their place once the last piece's products are done
-            if (pairs && queries && !wait(&o_full[1], no - 1, kSiteLoad)) break;
-            queries = p.both && !pairs;
-            no += p.both;
             const int32_t *tab = a.table + (int64_t)p.row * a.width;
             // the block of key KW w + lane of tile i (the table's entry, or -1) and the
             // key's place in it
@@ -412,18 +394,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
             };
             // Loads come back in order: the entry of a tile is asked for before the
             // codes of the tile before it, and used behind them.
-            Entry nxt = entry_of(1);
-            int cur = slot_of(entry_of(0));
-            load(cur);
-            for (int i = 0; i < tiles; ++i) {
-                const int st = Ring::stage(pairs, i);
-                if (!wait(&kv_empty[st], ring.use(pairs, i) + 1, kSiteLoad)) {
+            Entry nxt = entry_of(set + 2);
+            int cur = slot_of(entry_of(set));
+            if (set < tiles) load(cur);
+            for (int i = set; i < tiles; i += 2) {
+                const int st = set;
+                if (!wait(&kv_empty[st], ring.use(i) + 1, kSiteLoad)) {
                     ok = false;
                     break;
                 }
                 const uint32_t mask = __ballot_sync(~0u, cur >= 0);
-                if (lane == 0) sh_mask[st][w] = (uint16_t)mask;
-                if (mask != (1u << KW) - 1u) {
+                if (lane == 0) sh_mask[st][w] = mask;
+                if (mask != ~0u) {
 #pragma unroll
                     for (int j = 0; j < NI; ++j)
                         if (!((mask >> (RW * j + rq)) & 1u)) vr[j] = make_uint4(0, 0, 0, 0);
@@ -433,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                 fence_proxy_async();
                 arrive(&kv_full[st]);
                 cur = slot_of(nxt);
-                nxt = entry_of(i + 2);
-                if (i + 1 < tiles) load(cur);
+                nxt = entry_of(i + 4);
+                if (i + 2 < tiles) load(cur);
             }
-            ring.end(pairs, tiles);
+            ring.end(tiles);
             done();
         }
     } else {
@@ -453,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
             const bool pairs = p.pairs, active = hf == 0 || p.both;
             const int n = active ? p.n : 0;
             const int lr = r + (pairs ? 0 : 128 * hf);
-            const bool row_ok = lr < p.rows;
+            const bool row_ok = lr < p.rows, idle = !__any_sync(~0u, row_ok);
             // token and query head of the row
             auto place_of = [&](int64_t &t, int &hq) {
                 const uint32_t row = row_ok ? lr : 0, tok = row / (uint32_t)a.G;
@@ -523,17 +505,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
             const int64_t key0 = (int64_t)p.k0 + (int64_t)p.kt0 * each * kTile;
             if (!active && !wait(&q_full, no[0], kSiteQuery)) break;  // its next arrival is the next piece's
             for (int i = 0; i < n; ++i, ++nt) {
-                const int tile = i * each + (pairs ? hf : 0), st = Ring::stage(pairs, tile);
-                if (!wait(&s_full[hf], nt, kSiteScores) || !wait(&kv_full[st], ring.use(pairs, tile), kSiteScores)) {
+                const int tile = i * each + (pairs ? hf : 0), st = Ring::stage(tile);
+                if (!wait(&s_full[hf], nt, kSiteScores) || !wait(&kv_full[st], ring.use(tile), kSiteScores)) {
                     ok = false;
                     break;
                 }
                 // (the two halves' warps of an SM sub-partition compute in turn)
-                if (p.both && !wait(&in_turn[warp & 3][hf], turns + 1 - hf, kSiteScores)) {
-                    ok = false;
-                    break;
-                }
                 tc_fence_after();
+                if (idle) {  // no row of the warp's is the unit's: nobody reads its weights' products
+                    arrive(&p_full[hf][1]);
+                    arrive(&p_full[hf][0]);
+                    continue;
+                }
                 // the keys that the row sees, where some are hidden
                 const int64_t left = pos - (key0 + (int64_t)tile * kTile);
                 const uint4 there = *reinterpret_cast<const uint4 *>(&sh_mask[st][0]);
@@ -562,82 +545,74 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                         }
                     }
                 };
-                float top = -INFINITY, top1 = -INFINITY;
-                auto largest = [&](const uint32_t (&v)[32]) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        top = max3(top, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                        top1 = max3(top1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-                    }
-                };
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    read(h);
-                    largest(v0);
-                    largest(v1);
-                }
-                top = fmaxf(top, top1) * f;
-                const bool grown = i > 0 && top > ref + 8.0f;
-                if (i == 0) ref = top;
-                if (__any_sync(~0u, grown)) {
-                    // (the products of the last weights are in the output: they were issued
-                    // before these scores, whose arrival was waited for)
-                    const float c = grown ? ex2(ref - top) : 1.0f;
-                    if (grown) ref = top;
-                    l *= c;
-#pragma unroll 1
-                    for (int ch = 0; ch < D / 16; ++ch) {
-                        uint32_t o[16];
-                        tmem_ld16(o_t + ch * 16, o);
-                        tmem_ld_wait(o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * c);
-                        tmem_st16(o_t + ch * 16, o);
-                    }
-                }
                 const float2 f2 = make_float2(f, f);
-                const float nm = ref == -INFINITY ? 0.0f : -ref;
-                const float2 nm2 = make_float2(nm, nm);
-                float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-                // weights (hidden keys' scores are -inf) of 32 keys, to 16 columns over the
-                // upper half of the scores: the later 64 keys, in registers, first; the
-                // others' scores are read again
-                auto weigh = [&](const uint32_t (&v)[32], int col) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 x = __ffma2_rn(
-                            make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), f2, nm2);
-                        const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                        if (k & 1) s1 = __fadd2_rn(s1, e); else s0 = __fadd2_rn(s0, e);
-                        w[k] = pack_f16(e.x, e.y);
-                    }
-                    __syncwarp();
-                    tmem_st16(s_t + 64 + col, w);
-                };
+                // 64 keys at a time, the later ones first: their maximum, the reference raised
+                // where it has grown too far, their weights (hidden keys' scores are -inf) to
+                // 32 columns over the upper half of the scores
 #pragma unroll
                 for (int h = 1; h >= 0; --h) {
-                    if (h == 0) read(0);
+                    read(h);
+                    float top = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        top = max3(top, __uint_as_float(v0[k]), __uint_as_float(v0[k + 1]));
+                        top1 = max3(top1, __uint_as_float(v1[k]), __uint_as_float(v1[k + 1]));
+                    }
+                    top = fmaxf(top, top1) * f;
+                    const bool start = i == 0 && h == 1, grown = !start && top > ref + 8.0f;
+                    if (start) ref = top;
+                    if (__any_sync(~0u, grown)) {
+                        // the output so far: the products of the last tile were issued before these
+                        // scores, whose arrival was waited for; those of this tile's later keys
+                        if (h == 0 && !wait(&pv_done[hf], nt, kSiteOutput)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const float c = grown ? ex2(ref - top) : 1.0f;
+                        if (grown) ref = top;
+                        l *= c;
+#pragma unroll 1
+                        for (int ch = 0; ch < D / 16; ++ch) {
+                            uint32_t o[16];
+                            tmem_ld16(o_t + ch * 16, o);
+                            tmem_ld_wait(o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * c);
+                            tmem_st16(o_t + ch * 16, o);
+                        }
+                    }
+                    const float nm = ref == -INFINITY ? 0.0f : -ref;
+                    const float2 nm2 = make_float2(nm, nm);
+                    float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+                    auto weigh = [&](const uint32_t (&v)[32], int col) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 x = __ffma2_rn(
+                                make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), f2, nm2);
+                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            if (k & 1) s1 = __fadd2_rn(s1, e); else s0 = __fadd2_rn(s0, e);
+                            w[k] = pack_f16(e.x, e.y);
+                        }
+                        __syncwarp();
+                        tmem_st16(s_t + 64 + col, w);
+                    };
                     weigh(v0, 32 * h);
                     weigh(v1, 32 * h + 16);
+                    l += (s0.x + s0.y) + (s1.x + s1.y);
                     tmem_st_wait();
                     tc_fence_before();
                     arrive(&p_full[hf][h]);
                 }
-                l += (s0.x + s0.y) + (s1.x + s1.y);
-                if (p.both) {
-                    arrive(&in_turn[warp & 3][1 - hf]);
-                    ++turns;
-                }
+                if (!ok) break;
             }
-            ring.end(pairs, p.n * each);
+            ring.end(p.n * each);
             if (!ok) break;
             // the output
             if (active) {
                 if (!wait(&o_full[hf], no[hf], kSiteOutput)) break;
                 if (pairs && hf == 1) {
-                    // (A's products too, before the next piece's queries take the third stage's place)
-                    if (!wait(&o_full[0], no[0], kSiteOutput)) break;
                     sh_m[r] = ref;
                     sh_l[r] = l;
                     arrive(&ml_full);
