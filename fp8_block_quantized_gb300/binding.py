@@ -5,8 +5,8 @@ their dtype/shape/device, and forwards the raw device pointers, sizes and the
 current CUDA stream to the C entry point of the same name.  All quantization,
 GEMM and reduction work happens in the library's kernels.  There is no CPU
 fallback: if the library is missing or fails to load, ``load()`` raises.  The
-operators that a decoding step calls many times (residual norms, rotary
-positions, slot maps, attention, sampling) are marshalled by a compiled module,
+operators that a step calls many times (residual norms, rotary positions, slot
+maps, attention, sampling, the head and the gated activation's backward) are marshalled by a compiled module,
 ``pysrc/marshal.cpp``, with the same checks.
 """
 from __future__ import annotations
@@ -117,7 +117,8 @@ def load(build_if_missing: bool = True):
 # The C functions the compiled module calls, in the order it takes them.
 MARSHALLED = ("jet_add_rmsnorm_quant_1x128", "jet_add_rmsnorm_bwd", "jet_rope",
               "jet_rope_kv_cache_write", "jet_kv_slot_map", "jet_sample_unaligned",
-              "jet_workspace_bytes", "jet_kv_attention", "jet_kv_attention_workspace")
+              "jet_workspace_bytes", "jet_kv_attention", "jet_kv_attention_workspace",
+              "jet_head_logp", "jet_head_logp_bwd", "jet_swiglu_bwd_quant_1x128")
 
 
 def _compiled():
@@ -274,30 +275,6 @@ def jet_swiglu_quant_1x128(gate, up, q, s, stream=None):
     _need(s, torch.float32, (F // 128, M), "s")
     _check("jet_swiglu_quant_1x128", load().jet_swiglu_quant_1x128(
         _ptr(gate), _ptr(up), ld, M, F, _ptr(q), _ptr(s), _stream(stream)))
-
-
-def jet_swiglu_bwd_quant_1x128(gate, up, dh, qg, sg, qu, su, stream=None):
-    """The gradients of gate and up (views as in jet_swiglu_quant_1x128) from
-    dh [M, F] of the activation, in the 1x128 form: codes qg, qu [M, F],
-    scales sg, su [F/128, M]."""
-    import torch
-    M, F = gate.shape
-    for t, name in ((gate, "gate"), (up, "up")):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (M, F):
-            raise ValueError(f"{name}: expected bfloat16 [{M}, {F}]")
-        if t.numel() and (not t.is_cuda or t.stride(1) != 1):
-            raise ValueError(f"{name}: must be a CUDA tensor with contiguous rows")
-    ld = gate.stride(0) if M > 1 else F
-    if M > 1 and up.stride(0) != ld:
-        raise ValueError("gate and up must have the same row stride")
-    _need(dh, torch.bfloat16, (M, F), "dh")
-    for t, name in ((qg, "qg"), (qu, "qu")):
-        _need(t, torch.uint8, (M, F), name)
-    for t, name in ((sg, "sg"), (su, "su")):
-        _need(t, torch.float32, (F // 128, M), name)
-    _check("jet_swiglu_bwd_quant_1x128", load().jet_swiglu_bwd_quant_1x128(
-        _ptr(gate), _ptr(up), ld, _ptr(dh), M, F, _ptr(qg), _ptr(sg), _ptr(qu), _ptr(su),
-        _stream(stream)))
 
 
 def jet_rmsnorm_quant_1x128(x, g, eps, q, s, stream=None):
@@ -801,6 +778,13 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stre
     return token, logp, logp_all, kept
 
 
+def jet_swiglu_bwd_quant_1x128(gate, up, dh, qg, sg, qu, su, stream=None):
+    """The gradients of gate and up (views as in jet_swiglu_quant_1x128) from
+    dh [M, F] of the activation, in the 1x128 form: codes qg, qu [M, F],
+    scales sg, su [F/128, M]."""
+    (_marshal or _compiled()).swiglu_bwd_quant_1x128(gate, up, dh, qg, sg, qu, su, stream)
+
+
 def swiglu_bwd_quant_1x128(gate, up, dh, stream=None):
     """(qg, sg, qu, su): the 1x128 forms of the gradients of gate and up."""
     import torch
@@ -855,39 +839,23 @@ def kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, block_size, offse
 # The head's log-probabilities and their gradient
 # --------------------------------------------------------------------------
 
-def _head_args(x, w, target):
+def _ws_on(op, M, N, K, device, stream):
+    """A workspace that belongs to the stream given; None for the current one, for
+    which the compiled part allocates."""
     import torch
-    T, K = x.shape
-    V = w.shape[0]
-    _need(x, torch.bfloat16, (T, K), "x")
-    _need(w, torch.bfloat16, (V, K), "w")
-    _need(target, torch.int64, (T,), "target")
-    for t in (x, w, target):
-        if t.numel() and t.device.index != torch.cuda.current_device():
-            raise ValueError("the tensors must be on the current device")
-    return T, K, V
-
-
-def _head_ws(op, T, V, K, ws, device, stream):
-    import torch
-    if ws is None:
-        with _allocating_on(stream):
-            ws = torch.empty((workspace_bytes(op, T, V, K),), dtype=torch.uint8, device=device)
-    return ws
+    if stream is None:
+        return None
+    with _allocating_on(stream):
+        return torch.empty((workspace_bytes(op, M, N, K),), dtype=torch.uint8, device=device)
 
 
 def jet_head_logp(x, w, target, scale, logp, lse, ws=None, stream=None):
     """logp and lse [T] of the tokens target [T] (int64) under the head w [V, K]
     for x [T, K]: the logits scale * x w^T are not kept; a target outside
     [0, V) is ignored (logp 0)."""
-    import torch
-    T, K, V = _head_args(x, w, target)
-    _need(logp, torch.float32, (T,), "logp")
-    _need(lse, torch.float32, (T,), "lse")
-    ws = _head_ws("head_logp", T, V, K, ws, x.device, stream)
-    _check("jet_head_logp", load().jet_head_logp(
-        _ptr(x), _ptr(w), T, K, V, _ptr(target), float(scale), _ptr(logp), _ptr(lse), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)))
+    if ws is None:
+        ws = _ws_on("head_logp", x.shape[0], w.shape[0], w.shape[1], x.device, stream)
+    (_marshal or _compiled()).head_logp(x, w, target, scale, logp, lse, ws, stream)
 
 
 def head_logp(x, w, target, scale=1.0, stream=None):
@@ -902,18 +870,9 @@ def head_logp(x, w, target, scale=1.0, stream=None):
 def jet_head_logp_bwd(x, w, target, lse, dlogp, scale, dx, dw, ws=None, stream=None):
     """dx [T, K] and dw [V, K] (BF16; either may be None) of sum(dlogp * logp)
     from jet_head_logp's lse."""
-    import torch
-    T, K, V = _head_args(x, w, target)
-    _need(lse, torch.float32, (T,), "lse")
-    _need(dlogp, torch.float32, (T,), "dlogp")
-    if dx is not None:
-        _need(dx, torch.bfloat16, (T, K), "dx")
-    if dw is not None:
-        _need(dw, torch.bfloat16, (V, K), "dw")
-    ws = _head_ws("head_logp_bwd", T, V, K, ws, x.device, stream)
-    _check("jet_head_logp_bwd", load().jet_head_logp_bwd(
-        _ptr(x), _ptr(w), T, K, V, _ptr(target), _ptr(lse), _ptr(dlogp), float(scale), _ptr(dx),
-        _ptr(dw), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    if ws is None:
+        ws = _ws_on("head_logp_bwd", x.shape[0], w.shape[0], w.shape[1], x.device, stream)
+    (_marshal or _compiled()).head_logp_bwd(x, w, target, lse, dlogp, scale, dx, dw, ws, stream)
 
 
 def head_logp_bwd(x, w, target, lse, dlogp, scale=1.0, stream=None):

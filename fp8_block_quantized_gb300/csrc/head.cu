@@ -6,8 +6,11 @@
 //   d_tv = scale g_t ([v = target] - e^(z_tv - lse_t)),  dx = d w,  dw = d^T x.
 // All four products (z twice, dx, dw) are BF16 products on the 5th-generation
 // tensor core with binary32 accumulators, one kernel template:
-//   kLse   z tiles; the epilogue keeps each row's maximum and sum of a tile,
-//          joined over the tiles by head_join_kernel;
+//   kLse   z tiles; the epilogue keeps each row's maximum and sum of a tile's half,
+//          joined over the tiles by head_join_kernel.  The tensor core cuts
+//          off its sums (2^-24 of the sum a step): over 4096 products that is 2e-5 of
+//          a logit, so after every 1024 the sum is taken over into registers and
+//          added up there, rounded to nearest;
 //   kGrad  z tiles of a piece of the vocabulary again; the epilogue writes d in
 //          BF16 (the type that the next two products read: 2^-9 relative a
 //          value, below the outputs' own rounding in the sums);
@@ -20,7 +23,7 @@
 //
 // The kernel is persistent: warp 0 loads operand slices of 64 along the
 // contraction by TMA into a ring of stages (128-byte swizzle), warp 1 issues the
-// MMAs into one of two TMEM accumulators, warps 4-7 drain the other one.  Large
+// MMAs into one of two TMEM accumulators, warps 4-7 (kLse: 4-11) drain the other one.  Large
 // products run as CTA pairs on 256 x 256 tiles, few rows on single CTAs with 128 x
 // 128.  Every wait is bounded (jet_common.cuh); a role that gives up sets the
 // CTA's abort flag, copies and MMAs in flight are awaited, TMEM is freed.
@@ -43,8 +46,12 @@ enum Product { kLse = 0, kGrad = 1, kDx = 2, kDw = 3 };
 constexpr unsigned kSiteProducer = 16, kSiteMma = 17, kSiteMmaTmem = 18, kSiteEpilogue = 19,
                    kSiteDrain = 20;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kLseThreads = 384;
 constexpr int BM = 128, BK = 64;
+constexpr int kChunk = 16;  // kLse: slices that the tensor core adds up by itself
+// kLse's registers a thread after setmaxnreg: 128 x 72 + 256 x 216 = 384 x 168.
+constexpr uint32_t kRegsControl = 72, kRegsEpilogue = 216;
+static_assert(128 * kRegsControl + 256 * kRegsEpilogue <= kLseThreads * 168, "registers");
 constexpr int kStages = 6;
 constexpr int kABytes = BM * BK * 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -64,7 +71,7 @@ struct Epilogue {
     const float *lse, *dlogp;
     float scale;
     int V, v0;               // vocabulary, and the first entry of the piece
-    float2 *part;            // kLse: [column tiles][T] (maximum, sum) in powers of two
+    float2 *part;            // kLse: [2 column tiles][T] (maximum, sum) in powers of two
     float *zt;               // kLse: [T] the target's logit, in powers of two
     uint16_t *d;             // kGrad: [T][ldd]
     int64_t ldd;
@@ -85,7 +92,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // rows R, columns C, contraction D in elements; `splits` ranges of the contraction.
 template <int P, int CL>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(P == kLse ? kLseThreads : kThreads, 1)
 head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, int R,
             int C, int D, int splits, const Epilogue ep, unsigned *status) {
     using CF = Cfg<CL>;
@@ -108,7 +115,7 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], 4 * CL);
+            mbar_init(&tempty_bar[b], (P == kLse ? 8 : 4) * CL);
         }
         mbar_init(&drain_bar, 1);
         abort_sh = 0;
@@ -159,6 +166,8 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
     auto wait = [&](uint64_t *bar, uint32_t parity, unsigned site) -> bool {
         return __all_sync(~0u, mbar_wait(bar, parity, abort, status, site));
     };
+    if constexpr (P == kLse)
+        if (warp < 4) reg_dealloc<kRegsControl>();
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
@@ -210,16 +219,18 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             return mn ? smem_desc(a + ks * 2048, 8192, 1024, kSwizzle128B)
                       : smem_desc(a + ks * 32, 16, 1024, kSwizzle128B);
         };
-        uint32_t it = 0, tiles = 0;
+        uint32_t it = 0, sums = 0;  // slices, and sums (a tile's, or a chunk's of it) so far
         bool ok = true;
-        for (int t = unit0; ok && t < total; t += step, ++tiles) {
+        for (int t = unit0; ok && t < total; t += step) {
             int m0, n0, k0, k1, sp;
             coords(t, m0, n0, k0, k1, sp);
-            const uint32_t buf = tiles & 1u;
-            if (!wait(&tempty_bar[buf], ((tiles >> 1) & 1u) ^ 1u, kSiteMmaTmem)) break;
             for (int kb = k0; kb < k1; ++kb, ++it) {
+                const bool begins = P == kLse ? (kb - k0) % kChunk == 0 : kb == k0;
+                const bool ends = kb + 1 == k1 || (P == kLse && (kb + 1 - k0) % kChunk == 0);
+                const uint32_t buf = sums & 1u;
                 const int s = it % S;
-                if (!wait(&full_bar[s], (it / S) & 1u, kSiteMma)) {
+                if ((begins && !wait(&tempty_bar[buf], ((sums >> 1) & 1u) ^ 1u, kSiteMmaTmem)) ||
+                    !wait(&full_bar[s], (it / S) & 1u, kSiteMma)) {
                     ok = false;
                     break;
                 }
@@ -229,20 +240,20 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
 #pragma unroll
                     for (int ks = 0; ks < BK / 16; ++ks) {
                         const uint64_t da = desc(as, kAMn, ks), db = desc(bs, kBMn, ks);
-                        const uint32_t more = kb > k0 || ks > 0;
+                        const uint32_t more = !begins || ks > 0;
                         if (kPair) mma_16bit_pair(tmem + buf * BN, da, db, kIdesc, more);
                         else mma_16bit(tmem + buf * BN, da, db, kIdesc, more);
                     }
                     if (kPair) mma_commit_pair_mc(&empty_bar[s], 0x3);
                     else mma_commit(&empty_bar[s]);
+                    if (ends) {
+                        if (kPair) mma_commit_pair_mc(&tfull_bar[buf], 0x3);
+                        else mma_commit(&tfull_bar[buf]);
+                    }
                 }
+                sums += ends;
                 __syncwarp();
             }
-            if (ok && lane == 0) {
-                if (kPair) mma_commit_pair_mc(&tfull_bar[buf], 0x3);
-                else mma_commit(&tfull_bar[buf]);
-            }
-            __syncwarp();
         }
         if (lane == 0) {
             if (kPair) mma_commit_pair_mc(&drain_bar, 0x1);
@@ -250,7 +261,80 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
         }
         __syncwarp();
         mbar_wait(&drain_bar, 0, nullptr, status, kSiteDrain);
-    } else if (warp >= 4) {
+    } else if (P == kLse && warp >= 4) {
+        if constexpr (P == kLse) {
+            reg_alloc<kRegsEpilogue>();
+            constexpr int H = BN / 2;  // columns of a thread
+            const int quad = warp & 3, half = (warp - 4) >> 2;
+            uint32_t release[2] = {0u, 0u};
+            if (kPair) {
+                release[0] = map_to_cta(&tempty_bar[0], 0);
+                release[1] = map_to_cta(&tempty_bar[1], 0);
+            }
+            const float c = ep.scale * kLog2e;
+            uint32_t sums = 0;
+            bool ok = true;
+            for (int t = unit0; ok && t < total; t += step) {
+                int m0, n0, k0, k1, sp;
+                coords(t, m0, n0, k0, k1, sp);
+                const int row = m0 + quad * 32 + lane, col0 = n0 + half * H;
+                float2 acc[H / 2];
+#pragma unroll
+                for (int i = 0; i < H / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+                for (int kb = k0; kb < k1; kb += kChunk, ++sums) {
+                    const uint32_t buf = sums & 1u;
+                    if (!wait(&tfull_bar[buf], (sums >> 1) & 1u, kSiteEpilogue)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + half * H;
+#pragma unroll
+                    for (int ch = 0; ch < H / 16; ++ch) {
+                        uint32_t r[16];
+                        tmem_ld16(from + ch * 16, r);
+                        tmem_ld_wait(r);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[ch * 8 + i] = __fadd2_rn(
+                                acc[ch * 8 + i],
+                                make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (kPair) mbar_arrive_cluster_relaxed(release[buf]);
+                        else mbar_arrive(&tempty_bar[buf]);
+                    }
+                }
+                if (!ok) break;
+                if (row >= R) continue;
+                // the target's column, if it is one of these
+                const int64_t token = ep.target[row];
+                const int want = token >= 0 && token < ep.V ? (int)token - col0 : -1;
+                float top = -INFINITY, zt = 0.0f;
+#pragma unroll
+                for (int i = 0; i < H / 2; ++i) {
+                    float2 x = __fmul2_rn(acc[i], make_float2(c, c));
+                    if (col0 + 2 * i >= C) x.x = -INFINITY;
+                    if (col0 + 2 * i + 1 >= C) x.y = -INFINITY;
+                    if (want == 2 * i) zt = x.x;
+                    if (want == 2 * i + 1) zt = x.y;
+                    acc[i] = x;
+                    top = fmaxf(top, fmaxf(x.x, x.y));
+                }
+                if (want >= 0 && want < H) ep.zt[row] = zt;
+                const float2 use = make_float2(top == -INFINITY ? 0.0f : -top, top == -INFINITY ? 0.0f : -top);
+                float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < H / 2; ++i) {
+                    const float2 d = __fadd2_rn(acc[i], use);
+                    sum = __fadd2_rn(sum, make_float2(ex2(d.x), ex2(d.y)));
+                }
+                ep.part[(int64_t)(2 * (n0 / BN) + half) * R + row] = make_float2(top, sum.x + sum.y);
+            }
+        }
+    } else if (P != kLse && warp >= 4) {
         const int quad = warp & 3;
         uint32_t release[2] = {0u, 0u};
         if (kPair) {
@@ -265,21 +349,20 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             const int row = m0 + quad * 32 + lane;
             const bool row_ok = row < R;
             const uint32_t buf = tiles & 1u;
-            // kLse, kGrad: the target's column of the piece (none: out of any tile)
+            // kGrad: the target's column of the piece (none: out of any tile)
             int want = -1;
             float lse2 = 0.0f, g = 0.0f;
-            if ((P == kLse || P == kGrad) && row_ok) {
+            if (P == kGrad && row_ok) {
                 const int64_t token = ep.target[row];
                 if (token >= 0 && token < ep.V) {
                     want = (int)token - ep.v0;
-                    if (P == kGrad) g = ep.dlogp[row] * ep.scale;
+                    g = ep.dlogp[row] * ep.scale;
                 }
-                if (P == kGrad) lse2 = ep.lse[row] * kLog2e;
+                lse2 = ep.lse[row] * kLog2e;
             }
             if (!wait(&tfull_bar[buf], (tiles >> 1) & 1u, kSiteEpilogue)) break;
             tc_fence_after();
             const uint32_t acc0 = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
-            float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
             for (int ch = 0; ch < BN / 32; ++ch) {
                 uint32_t r[32];
@@ -287,30 +370,7 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                 tmem_ld32(acc0 + ch * 32, r);
                 tmem_wait32(r);
                 const int col = n0 + ch * 32;
-                if constexpr (P == kLse) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float x = __uint_as_float(r[i]) * c;
-                        if (col + i >= C) x = -INFINITY;
-                        r[i] = __float_as_uint(x);
-                        mx = fmaxf(mx, x);
-                    }
-                    if (want >= col && want < col + 32) {
-                        float x = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (want - col == i) x = __uint_as_float(r[i]);
-                        ep.zt[row] = x;
-                    }
-                    if (mx > top) {
-                        sum *= ex2(top - mx);
-                        top = mx;
-                    }
-                    const float use = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) sum += ex2(__uint_as_float(r[i]) - use);
-                } else if constexpr (P == kGrad) {
+                if constexpr (P == kGrad) {
                     uint16_t *dst = ep.d + (int64_t)row * ep.ldd + col;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
@@ -355,7 +415,6 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                 if (kPair) mbar_arrive_cluster_relaxed(release[buf]);
                 else mbar_arrive(&tempty_bar[buf]);
             }
-            if (P == kLse && row_ok) ep.part[(int64_t)(n0 / BN) * R + row] = make_float2(top, sum);
         }
     }
     tc_fence_before();
@@ -438,7 +497,7 @@ constexpr int64_t kPieceBytes = 512ll << 20;
 Plan plan(int64_t T, int64_t V, int64_t K) {
     Plan p;
     p.cl_z = p.cl_dx = T <= BM ? 1 : 2;
-    p.tiles_z = ceil_div(V, p.cl_z == 2 ? 256 : 128);
+    p.tiles_z = 2 * ceil_div(V, p.cl_z == 2 ? 256 : 128);  // halves of tiles
     p.fwd_bytes = up256((size_t)(p.tiles_z * T) * sizeof(float2)) + up256((size_t)T * 4);
     // pieces of equal size whose d takes at most kPieceBytes, 4096 entries at least
     int64_t most = kPieceBytes / (2 * (T > 0 ? T : 1));
@@ -482,7 +541,7 @@ jet_status product(const DeviceInfo &dev, const CUtensorMap &ta, const CUtensorM
     static int at_once[64] = {};
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(P == kLse ? kLseThreads : kThreads);
     cfg.dynamicSmemBytes = CF::kSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;

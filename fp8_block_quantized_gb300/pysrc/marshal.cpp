@@ -30,6 +30,9 @@ decltype(&jet_sample_unaligned) f_sample;
 decltype(&jet_workspace_bytes) f_workspace;
 decltype(&jet_kv_attention) f_attention;
 decltype(&jet_kv_attention_workspace) f_attention_workspace;
+decltype(&jet_head_logp) f_head;
+decltype(&jet_head_logp_bwd) f_head_bwd;
+decltype(&jet_swiglu_bwd_quant_1x128) f_swiglu_bwd;
 PyObject *jet_error;
 
 // Thrown once a Python exception is set.
@@ -134,6 +137,26 @@ Heads heads(PyObject *o, const char *name, int64_t T, int64_t D) {
 }
 
 int64_t numel(PyObject *o, const char *name) { return tensor(o, name).numel(); }
+
+// None, or a tensor of the current device (whose stream the call runs on).
+void on_this_device(PyObject *o) {
+    if (o == Py_None) return;
+    const at::Tensor &t = tensor(o, "argument");
+    if (t.numel() && t.is_cuda() && t.get_device() != c10::cuda::current_device()) {
+        PyErr_SetString(PyExc_ValueError, "the tensors must be on the current device");
+        throw Raised();
+    }
+}
+
+// The workspace given, or `need` bytes allocated beside `like` on the current stream.
+at::Tensor workspace(PyObject *o, const at::Tensor &like, size_t need) {
+    if (o != Py_None) {
+        const at::Tensor &t = tensor(o, "ws");
+        arg<void>(o, "ws", t.scalar_type(), {t.numel()});
+        return t;
+    }
+    return need ? at::empty({(int64_t)need}, like.options().dtype(at::kByte)) : at::Tensor();
+}
 
 // The stream to run on: None is the current one; else a stream object or its handle.
 void *stream_of(PyObject *o) {
@@ -346,13 +369,7 @@ void attention(PyObject *const *a) {  // q, k_cache, v_cache, k_scale, v_scale, 
         throw Raised();
     }
     for (int i = 0; i < 13; ++i)
-        if (i != 6 && a[i] != Py_None) {
-            const at::Tensor &x = tensor(a[i], "argument");
-            if (x.numel() && x.is_cuda() && x.get_device() != c10::cuda::current_device()) {
-                PyErr_SetString(PyExc_ValueError, "the tensors must be on the current device");
-                throw Raised();
-            }
-        }
+        if (i != 6) on_this_device(a[i]);
     const auto *kc = arg<uint8_t>(a[1], "k_cache", at::kByte, {S, Hk, D});
     const auto *vc = arg<uint8_t>(a[2], "v_cache", at::kByte, {S, Hk, D});
     const auto *ks = arg<float>(a[3], "k_scale", at::kFloat, {Hk});
@@ -371,14 +388,7 @@ void attention(PyObject *const *a) {  // q, k_cache, v_cache, k_scale, v_scale, 
     const auto *po = arg<int64_t>(a[11], "prefix_offsets", at::kLong, {Ng + 1});
     const auto *pl = arg<int32_t>(a[12], "prefix_lengths", at::kInt, {Ng});
     const float scale = a[13] == Py_None ? 1.0f / std::sqrt((float)(D > 0 ? D : 1)) : (float)number(a[13]);
-    at::Tensor ws;  // given, or allocated on the current stream
-    if (a[14] == Py_None) {
-        const size_t need = f_attention_workspace(T, q.H, Hk, D, B, Ng);
-        if (need) ws = at::empty({(int64_t)need}, t.options().dtype(at::kByte));
-    } else {
-        ws = tensor(a[14], "ws");
-        arg<void>(a[14], "ws", ws.scalar_type(), {ws.numel()});
-    }
+    const at::Tensor ws = workspace(a[14], t, f_attention_workspace(T, q.H, Hk, D, B, Ng));
     void *room = ws.defined() ? address(ws) : nullptr, *stream = stream_of(a[15]);
     const size_t bytes = ws.defined() ? ws.nbytes() : 0;
     call("jet_kv_attention", [&] {
@@ -386,6 +396,78 @@ void attention(PyObject *const *a) {  // q, k_cache, v_cache, k_scale, v_scale, 
                            offsets, lengths, B, po, pl, Ng, scale, out.p, out.ld, lse, room, bytes,
                            stream);
     });
+}
+
+void head(PyObject *const *a) {  // x, w, target, scale, logp, lse, ws, stream
+    const auto size = matrix(a[0], "x");
+    const int64_t T = size.first, K = size.second, V = matrix(a[1], "w").first;
+    const auto *x = arg<uint16_t>(a[0], "x", at::kBFloat16, {T, K});
+    const auto *w = arg<uint16_t>(a[1], "w", at::kBFloat16, {V, K});
+    const auto *target = arg<int64_t>(a[2], "target", at::kLong, {T});
+    const float scale = (float)number(a[3]);
+    auto *logp = arg<float>(a[4], "logp", at::kFloat, {T});
+    auto *lse = arg<float>(a[5], "lse", at::kFloat, {T});
+    for (int i : {0, 1, 2, 4, 5}) on_this_device(a[i]);
+    const at::Tensor ws = workspace(a[6], tensor(a[0], "x"), f_workspace(JET_OP_HEAD_LOGP, T, V, K));
+    void *room = ws.defined() ? address(ws) : nullptr, *stream = stream_of(a[7]);
+    const size_t bytes = ws.defined() ? ws.nbytes() : 0;
+    call("jet_head_logp",
+         [&] { return f_head(x, w, T, K, V, target, scale, logp, lse, room, bytes, stream); });
+}
+
+void head_bwd(PyObject *const *a) {  // x, w, target, lse, dlogp, scale, dx, dw, ws, stream
+    const auto size = matrix(a[0], "x");
+    const int64_t T = size.first, K = size.second, V = matrix(a[1], "w").first;
+    const auto *x = arg<uint16_t>(a[0], "x", at::kBFloat16, {T, K});
+    const auto *w = arg<uint16_t>(a[1], "w", at::kBFloat16, {V, K});
+    const auto *target = arg<int64_t>(a[2], "target", at::kLong, {T});
+    const auto *lse = arg<float>(a[3], "lse", at::kFloat, {T});
+    const auto *dlogp = arg<float>(a[4], "dlogp", at::kFloat, {T});
+    const float scale = (float)number(a[5]);
+    auto *dx = arg<uint16_t>(a[6], "dx", at::kBFloat16, {T, K});
+    auto *dw = arg<uint16_t>(a[7], "dw", at::kBFloat16, {V, K});
+    for (int i : {0, 1, 2, 3, 4, 6, 7}) on_this_device(a[i]);
+    const at::Tensor ws = workspace(a[8], tensor(a[0], "x"), f_workspace(JET_OP_HEAD_LOGP_BWD, T, V, K));
+    void *room = ws.defined() ? address(ws) : nullptr, *stream = stream_of(a[9]);
+    const size_t bytes = ws.defined() ? ws.nbytes() : 0;
+    call("jet_head_logp_bwd", [&] {
+        return f_head_bwd(x, w, T, K, V, target, lse, dlogp, scale, dx, dw, room, bytes, stream);
+    });
+}
+
+// [M, F] BF16 rows, which may be strided; its row stride.
+uint16_t *rows(PyObject *o, const char *name, int64_t M, int64_t F, int64_t &ld) {
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != at::kBFloat16 || t.dim() != 2 || t.size(0) != M || t.size(1) != F) {
+        PyErr_Format(PyExc_ValueError, "%s: expected bfloat16 [%lld, %lld]", name, (long long)M, (long long)F);
+        throw Raised();
+    }
+    if (t.numel() && (!t.is_cuda() || (F > 1 && t.stride(1) != 1))) {
+        PyErr_Format(PyExc_ValueError, "%s: must be a CUDA tensor with contiguous rows", name);
+        throw Raised();
+    }
+    ld = M > 1 ? t.stride(0) : F;
+    return static_cast<uint16_t *>(address(t));
+}
+
+void swiglu_bwd(PyObject *const *a) {  // gate, up, dh, qg, sg, qu, su, stream
+    const auto size = matrix(a[0], "gate");
+    const int64_t M = size.first, F = size.second;
+    int64_t ld = F, ldu = F;
+    const uint16_t *gate = rows(a[0], "gate", M, F, ld), *up = rows(a[1], "up", M, F, ldu);
+    if (ld != ldu) {
+        PyErr_SetString(PyExc_ValueError, "gate and up must have the same row stride");
+        throw Raised();
+    }
+    const auto *dh = arg<uint16_t>(a[2], "dh", at::kBFloat16, {M, F});
+    auto *qg = arg<uint8_t>(a[3], "qg", at::kByte, {M, F});
+    auto *sg = arg<float>(a[4], "sg", at::kFloat, {F / 128, M});
+    auto *qu = arg<uint8_t>(a[5], "qu", at::kByte, {M, F});
+    auto *su = arg<float>(a[6], "su", at::kFloat, {F / 128, M});
+    for (int i = 0; i < 7; ++i) on_this_device(a[i]);
+    void *stream = stream_of(a[7]);
+    call("jet_swiglu_bwd_quant_1x128",
+         [&] { return f_swiglu_bwd(gate, up, ld, dh, M, F, qg, sg, qu, su, stream); });
 }
 
 // ------------------------------------------------------------------ the module
@@ -408,14 +490,14 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-// bind(JetError, the addresses of the nine C functions in the order above)
+// bind(JetError, the addresses of the twelve C functions in the order above)
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (n != 10) {
-        PyErr_SetString(PyExc_TypeError, "bind: expected the error class and nine addresses");
+    if (n != 13) {
+        PyErr_SetString(PyExc_TypeError, "bind: expected the error class and twelve addresses");
         return nullptr;
     }
-    void *p[9];
-    for (int i = 0; i < 9; ++i) {
+    void *p[12];
+    for (int i = 0; i < 12; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i + 1]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -428,6 +510,9 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     f_workspace = reinterpret_cast<decltype(f_workspace)>(p[6]);
     f_attention = reinterpret_cast<decltype(f_attention)>(p[7]);
     f_attention_workspace = reinterpret_cast<decltype(f_attention_workspace)>(p[8]);
+    f_head = reinterpret_cast<decltype(f_head)>(p[9]);
+    f_head_bwd = reinterpret_cast<decltype(f_head_bwd)>(p[10]);
+    f_swiglu_bwd = reinterpret_cast<decltype(f_swiglu_bwd)>(p[11]);
     Py_XSETREF(jet_error, Py_NewRef(args[0]));
     Py_RETURN_NONE;
 }
@@ -440,6 +525,9 @@ PyMethodDef methods[] = {ENTRY("add_rmsnorm_quant_1x128", norm, 9),
                          ENTRY("kv_slot_map", slots, 12),
                          ENTRY("sample", sample, 11),
                          ENTRY("kv_attention", attention, 16),
+                         ENTRY("head_logp", head, 8),
+                         ENTRY("head_logp_bwd", head_bwd, 10),
+                         ENTRY("swiglu_bwd_quant_1x128", swiglu_bwd, 8),
                          {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
