@@ -7,9 +7,10 @@ layer.
     python examples/rl_step.py
 
 The linear layers, the norms with their residual additions, the rotary
-positions, the cache writes and slot maps, and the sampling are the library's
-calls.  Embedding, attention and the loss are plain torch, as they would be
-another library's in a real program.
+positions, the cache writes and slot maps, the rollout's attention over the cache,
+the sampling, the drawn tokens' log-probabilities with their gradient, and the
+gated activation's backward are the library's calls.  Embedding and the training
+attention are plain torch, as they would be another library's in a real program.
 """
 import os
 import sys
@@ -46,9 +47,10 @@ class Model:
                     for l in self.layers]
         self.fp8_head = jet.quant_w_128x128(self.head)
 
-    def forward(self, tokens, attend, save=None):
-        """Logits [T, VOCAB] of the tokens; attend(layer, q, k, v) is the attention
-        over [T, heads, D].  `save` (a dict) takes what the last layer's backward needs."""
+    def hidden(self, tokens, attend, save=None):
+        """The 1x128 form of the tokens' hidden states behind the last norm;
+        attend(layer, q, k, v) is the attention over [T, heads, D].  `save` (a dict)
+        takes what the last layer's backward needs."""
         T = tokens.numel()
         x, d = self.embed[tokens], torch.zeros((T, HIDDEN), dtype=BF16, device=tokens.device)
         for i, (p, w) in enumerate(zip(self.layers, self.fp8)):
@@ -64,7 +66,10 @@ class Model:
         x, n, s, r = jet.add_rmsnorm_quant_1x128(x, d, self.norm, EPS, with_rstd=True)
         if save is not None:
             save.update(xf=x, rf=r)
-        return jet.gemm_fp8_fwd(n, s, *self.fp8_head)
+        return n, s
+
+    def logits(self, tokens, attend):
+        return jet.gemm_fp8_fwd(*self.hidden(tokens, attend), *self.fp8_head)
 
 
 def attention(q, k, v, q_pos, k_pos):
@@ -92,7 +97,6 @@ class PagedCache:
         offsets, pos, slots, rows, self.next = jet.kv_slot_map(
             self.length, added, BLOCK, self.table, self.free, self.next[:1], capacity)
         self.length += added
-        start, length = offsets.tolist(), self.length.tolist()
 
         def attend(i, q, k, v):
             if self.scale[i] is None:    # calibrated on the prompts after the weight sync
@@ -103,17 +107,10 @@ class PagedCache:
             qr = torch.empty_like(q)
             jet.jet_rope_kv_cache_write(q, k, v, model.inv_freq, pos, ks, vs, slots, qr, self.k[i],
                                         self.v[i], mscale=model.mscale)
-            out = []
-            for b, n in enumerate(length):
-                at = torch.arange(n, device=q.device)
-                at_slot = self.table[b, at // BLOCK].long() * BLOCK + at % BLOCK
-                kk, vv = (c[at_slot].view(torch.float8_e4m3fn).float() * s[:, None]
-                          for c, s in ((self.k[i], ks), (self.v[i], vs)))
-                lo, hi = start[b], start[b + 1]
-                out.append(attention(qr[lo:hi], kk, vv, pos[lo:hi], at))
-            return torch.cat(out).flatten(1).to(BF16)
+            return jet.kv_attention(qr, self.k[i], self.v[i], ks, vs, self.table, BLOCK, offsets,
+                                    self.length).flatten(1)
 
-        return model.forward(tokens, attend), start
+        return model.logits(tokens, attend), offsets
 
 
 def rollout(model, prompts, steps, seed=1):
@@ -128,8 +125,8 @@ def rollout(model, prompts, steps, seed=1):
     added = torch.tensor([p.numel() for p in prompts], dtype=torch.int32, device=dev)
     drawn, logps = [], []
     for _ in range(steps):
-        logits, start = cache.step(model, tokens, added, tokens.numel())
-        last = logits[torch.tensor(start[1:], device=dev) - 1].contiguous()
+        logits, offsets = cache.step(model, tokens, added, tokens.numel())
+        last = logits[offsets[1:] - 1].contiguous()
         u = torch.rand((B,), generator=g, device=dev)
         token, _, logp, _ = jet.sample(last, u, **settings)
         drawn.append(token)
@@ -140,8 +137,8 @@ def rollout(model, prompts, steps, seed=1):
 
 
 def train_forward(model, sequences, save=None):
-    """Logits of the concatenated sequences with BF16 keys and values, and the
-    sequences' ranges."""
+    """Hidden states (BF16) of the concatenated sequences with BF16 keys and values,
+    and the sequences' ranges."""
     ends = torch.tensor([s.numel() for s in sequences]).cumsum(0).tolist()
     ranges = list(zip([0] + ends[:-1], ends))
     pos = torch.cat([torch.arange(s.numel(), device=s.device) for s in sequences])
@@ -153,24 +150,25 @@ def train_forward(model, sequences, save=None):
         return torch.cat([attention(qr[a:b], kr[a:b], v[a:b], pos[a:b], pos[a:b])
                           for a, b in ranges]).flatten(1).to(BF16)
 
-    return model.forward(torch.cat(sequences), attend, save), ranges
+    codes, scales = model.hidden(torch.cat(sequences), attend, save)
+    x = codes.view(torch.float8_e4m3fn).float() * scales.t().repeat_interleave(128, 1)
+    return x.to(BF16), ranges
 
 
-def backward_last_layer(model, save, dlogits):
+def backward_last_layer(model, save, dx):
     """Gradients of the last layer's norms and of its input from those of the
-    logits: DGrads in FP8, the norms' and the rotation's backward, attention and
-    SwiGLU by autograd."""
+    hidden states: DGrads in FP8, the norms', the rotation's and the gated
+    activation's backward, attention by autograd."""
     p, w = model.layers[-1], model.fp8[-1]
 
     def dgrad(dy, weight):
         return jet.gemm_fp8_dgrad(*jet.quant_act_1x128(dy.contiguous()), *weight)
 
-    dx, dnorm = jet.add_rmsnorm_bwd(save["xf"], model.norm, save["rf"], [dgrad(dlogits, model.fp8_head)])
-    gate, up = (save[n].float().requires_grad_() for n in ("gate", "up"))
-    h = torch.nn.functional.silu(gate) * up
-    dgate, dup = (t.to(BF16) for t in torch.autograd.grad(h, (gate, up), dgrad(dx, w["down"]).float()))
+    dx, dnorm = jet.add_rmsnorm_bwd(save["xf"], model.norm, save["rf"], [dx])
+    qg, sg, qu, su = jet.swiglu_bwd_quant_1x128(save["gate"], save["up"], dgrad(dx, w["down"]))
     dx, dnorm2 = jet.add_rmsnorm_bwd(save["x2"], p["norm2"], save["r2"],
-                                     [dgrad(dgate, w["gate"]), dgrad(dup, w["up"])], dx)
+                                     [jet.gemm_fp8_dgrad(qg, sg, *w["gate"]),
+                                      jet.gemm_fp8_dgrad(qu, su, *w["up"])], dx)
     da = dgrad(dx, w["o"]).float().unflatten(1, (HQ, D))
     q, k, v = (save[n].float().requires_grad_() for n in ("qr", "kr", "v"))
     a = torch.cat([attention(q[s:e], k[s:e], v[s:e], save["pos"][s:e], save["pos"][s:e])
@@ -191,20 +189,22 @@ def rl_step(requests=8, steps=24, seed=0):
                for n in torch.randint(1, 40, (requests,), generator=g)]
     sequences, logp_rollout = rollout(model, prompts, steps, seed + 2)
     save = {}
-    logits, ranges = train_forward(model, sequences, save)
-    # the drawn tokens' log-probabilities under the training forward
+    x, ranges = train_forward(model, sequences, save)
+    # the drawn tokens' log-probabilities under the training forward: a token is the target
+    # of the position before it, the prompts' are ignored
+    target = torch.full((x.shape[0],), -100, device="cuda")
     at = torch.cat([torch.arange(e - steps - 1, e - 1) for _, e in ranges]).cuda()
-    tokens = torch.cat([s[-steps:] for s in sequences])
-    logp = torch.log_softmax(logits[at].float(), -1)
-    logp_train = logp.gather(1, tokens[:, None])[:, 0]
+    target[at] = torch.cat([s[-steps:] for s in sequences])
+    logp, lse = jet.head_logp(x, model.head, target)
+    logp_train = logp[at]
     metric, count, weight = jet.token_mismatch_masked(logp_train.contiguous(),
                                                       logp_rollout.flatten().contiguous(), cap=2.0)
     # policy gradient of -sum(weight * logp) with unit advantages
-    dlogits = torch.zeros_like(logits)
-    grad = torch.exp(logp)
-    grad[torch.arange(at.numel(), device="cuda"), tokens] -= 1.0
-    dlogits[at] = (grad * (weight / count)[:, None]).to(BF16)
-    grads = backward_last_layer(model, save, dlogits)
+    dlogp = torch.zeros_like(logp)
+    dlogp[at] = -weight / count
+    dx, dhead = jet.head_logp_bwd(x, model.head, target, lse, dlogp)
+    grads = backward_last_layer(model, save, dx)
+    grads["head"] = dhead
     torch.cuda.synchronize()
     code, word = jet.device_status()
     assert code == 0, f"device status {code} ({word:#x})"
