@@ -397,6 +397,31 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
                         // (a key of the mask lies below 2^31)
                         if (!((mask >> key) & 1) || (int64_t)(p0 + key) > pos[e & 1]) sc[t][e] = -INFINITY;
                     }
+                // A NaN among the values of a key that some row does not see (weight 0) would
+                // reach that row: taken out, and given to the rows that see the key.
+                if (causal && __any_sync(~0u, (int64_t)p0 + (kStep - 1) > min(pos[0], pos[1]))) {
+                    uint32_t bad = 0;
+#pragma unroll 1
+                    for (int i = lane; i < kStep * KS; i += 32) {
+                        const uint32_t at = vb + place<D, true>(i / KS, i % KS);
+                        if (nan_bits(lds16(at))) {
+                            bad |= 1u << (i / KS);
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                        }
+                    }
+                    bad = __reduce_or_sync(~0u, bad);
+                    if (bad != 0) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int64_t last = (int64_t)pos[r] - p0;  // the last key that the row sees
+                            const uint32_t see = last < 0 ? 0u : last >= 31 ? ~0u : (2u << (int)last) - 1u;
+                            if ((bad & mask & see) == 0) continue;
+#pragma unroll
+                            for (int n = 0; n < NT / 2; ++n) o[n][r] = o[n][2 + r] = __uint_as_float(0x7FFFFFFFu);
+                        }
+                        __syncwarp();
+                    }
+                }
             }
             float top[2];
 #pragma unroll
@@ -488,7 +513,7 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
             const int hq = h * a.G + (int)(rr - tok * a.G);
             const int64_t slot = full ? ((s < a.B ? a.T : 0) + t) * a.Hq + hq
                                       : ((int64_t)(2 * me + (begins ? 0 : 1)) * a.heads + hw) * kRows + 2 * j + r;
-            const float inv = l[r] > 0.0f ? a.vs[h] / l[r] : 0.0f;
+            const float inv = row_factor(a.vs[h], l[r]);
 #pragma unroll
             for (int n = 0; n < NT / 2; n += 4) {
                 const int d = (n / 8) * 128 + W * g + 2 * (n % 8);
@@ -514,7 +539,7 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
                     pml[slot * 2] = m[r];
                     pml[slot * 2 + 1] = l[r];
                 } else if (a.lse) {
-                    a.lse[t * a.Hq + hq] = l[r] > 0.0f ? kLn2 * (m[r] + log2f(l[r])) : -INFINITY;
+                    a.lse[t * a.Hq + hq] = row_lse(m[r], l[r]);
                 }
             }
         }
@@ -534,10 +559,15 @@ struct Row {
         const int lane = threadIdx.x & 31;
         for (int b = 0; b < n; b += 32) {
             float mi = -INFINITY, li = 0.0f;
+            bool bad = false;  // a sum below 0: the row saw a value that is NaN
             if (b + lane < n) {
                 const float2 v = *reinterpret_cast<const float2 *>(ml + 2 * piece(b + lane));
-                mi = v.x, li = v.y;
+                mi = v.x, li = fabsf(v.y);
+                bad = v.y < 0.0f;
             }
+            if (__any_sync(~0u, bad))
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = __uint_as_float(0x7FFFFFFFu);
             float top = fmaxf(m, mi);
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
@@ -561,13 +591,13 @@ struct Row {
     }
     __device__ void write(const Args &a, int64_t t, int hq) const {
         const int lane = threadIdx.x & 31;
-        const float inv = l > 0.0f ? a.vs[hq / a.G] / l : 0.0f;
+        const float inv = row_factor(a.vs[hq / a.G], l);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const __nv_bfloat16 v = __float2bfloat16_rn(o[e] * inv);
             a.out[t * a.ldo + (int64_t)hq * D + lane + 32 * e] = *reinterpret_cast<const uint16_t *>(&v);
         }
-        if (a.lse && lane == 0) a.lse[t * a.Hq + hq] = l > 0.0f ? kLn2 * (m + log2f(l)) : -INFINITY;
+        if (a.lse && lane == 0) a.lse[t * a.Hq + hq] = row_lse(m, l);
     }
 };
 

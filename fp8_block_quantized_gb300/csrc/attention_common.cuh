@@ -234,6 +234,19 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
+// Bits 0x80 where one of the four times four codes is NaN (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_bits(uint4 v) {
+    auto top = [](uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; };
+    return (top(v.x) | top(v.y) | top(v.z) | top(v.w)) & 0x80808080u;
+}
+
+// lse in natural units and the factor of an output from a row's reference and sum: no
+// key, no weight.
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l == 0.0f ? -INFINITY : kLn2 * (m + log2f(l));
+}
+__device__ __forceinline__ float row_factor(float vs, float l) { return l == 0.0f ? 0.0f : vs / l; }
+
 // The power of two that brings a row's largest channel to [2^14, 2^15).
 __device__ __forceinline__ float row_power(float top) {
     const int e = min(254, 268 - (int)(__float_as_uint(top) >> 23));

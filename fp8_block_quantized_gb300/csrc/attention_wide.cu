@@ -9,14 +9,13 @@
 //                   maximum, weights e^(x - max) as FP16 back to TMEM over the
 //                   scores (handed on 64 keys at a time), and at a piece's end its
 //                   output;
-//   warps 8-15      the tiles' codes, four warps a stage: read through the
-//                   block table two tiles ahead (64 KB in flight), turned to FP16 (exact) and laid out in
-//                   shared memory, K and V alike as rows of keys with the 128-byte
-//                   swizzle: K-major for the scores, MN-major for the values;
+//   warps 8-15      the tiles' codes, four warps a stage: read through the block table
+//                   into registers two tiles ahead (64 KB in flight), turned to FP16
+//                   (exact) and laid out in shared memory, K and V alike as rows of
+//                   keys with the 128-byte swizzle: K-major for the scores, MN-major
+//                   for the values;
 //   warps 16, 17    issue the MMAs of A and of B: scores S = Q K^T (both operands in
-//                   shared memory) and O += P V (P in TMEM); one thread for both
-//                   could not issue them fast enough beside the others' instructions
-//                   (5300 cycles a tile against 4000);
+//                   shared memory) and O += P V (P in TMEM);
 //   warp 18         walks the CTA's range and tells the others its pieces.
 // In a wide unit A and B are the two halves of 256 rows at the same keys; a unit
 // of at most 128 rows has them at alternate tiles of the same rows, whose results
@@ -65,7 +64,7 @@ struct Cfg {
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// One stretch of a unit in a CTA's range, as warp 17 tells it the others.
+// One stretch of a unit in a CTA's range, as warp 18 tells it the others.
 struct Piece {
     int64_t token;     // the unit's first
     int s, r0, r1;     // segment; its requests
@@ -115,22 +114,36 @@ __device__ __forceinline__ void stg32(void *p, uint32_t a, uint32_t b, uint32_t 
                  : "memory");
 }
 
+// Tensor core instructions under a predicate, for a warp whose lanes all run the loop
+// around them: `lead` is 1 in the lane that issues them.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void mma_16bit_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+__device__ __forceinline__ void mma_16bit_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
 }
-__device__ __forceinline__ void mma_16bit_ta_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+// A in TMEM: its rows are lanes, two 16-bit values a column.
+__device__ __forceinline__ void mma_16bit_ta_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
 }
 
 template <int D>
@@ -140,9 +153,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
     __shared__ uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2], pv_done[2],
         o_full[2], ml_full, drain_bar, piece_full[2], piece_empty[2];
     __shared__ Piece pieces[2];
-    __shared__ __align__(16) uint32_t sh_mask[kStages][4];
+    // of a stage's keys: those that are there; those with a NaN among their values (and
+    // then not in the first), where some row does not see all keys
+    __shared__ __align__(16) uint32_t sh_mask[kStages][4], sh_nan[kStages][4];
     __shared__ float sh_m[128], sh_l[128];
-    __shared__ uint64_t in_turn[4][2];
+    __shared__ bool sh_bad[2][128];  // the row sees a value that is NaN
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -163,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
             mbar_init(&p_full[i][1], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&pv_done[i], 1);
-            for (int q = 0; q < 4; ++q) mbar_init(&in_turn[q][i], 1);
             mbar_init(&piece_full[i], 1);
             mbar_init(&piece_empty[i], 8 + kLoaders + 2);
         }
@@ -182,9 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
     griddep_wait();
     if (a.Ng == 0 && a.starts[kNarrowWorkers + blockIdx.x].empty > 0) clear_rows<D>(a, tid, kThreads);
 
-    // A warp's wait for the n-th phase of a barrier, and its arrival.  One lane does
-    // either: every lane's would be one operation on the barrier after another, in
-    // shared memory's way (a tile took 4700 cycles so, 3200 with one lane).
+    // A warp's wait for the n-th phase of a barrier (every lane asks: one lane's answer
+    // passed on by a shuffle took a fifth longer), and its arrival, by one lane.
     auto wait = [&](uint64_t *bar, uint32_t n, unsigned site) -> bool {
         return __all_sync(~0u, mbar_wait(bar, n & 1u, abort, status, site));
     };
@@ -363,6 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                 const int64_t slot = (int64_t)e.id * a.bs + e.at;
                 return e.id >= 0 && slot < a.S ? (int)slot : -1;
             };
+            // the first key from which on a tile may begin that not all rows see whole
+            const int whole = (int)max(p.base - (key0 - lane - KW * w) - (kTile - 2), (int64_t)-1);
             uint4 kr[NI] = {}, vr[NI] = {};
             const int c = lane % CH, rq = lane / CH;
             // (a missing key reads slot 0: its score is left out, its value zeroed)
@@ -399,18 +414,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
             if (set < tiles) load(cur);
             for (int i = set; i < tiles; i += 2) {
                 const int st = set;
+                // A NaN among the values of a key that some row does not see (weight 0) would
+                // reach that row: taken out below, and given to the rows that see the key.
+                bool some = false;
+                if (i * kTile >= whole) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) some = some || nan_bits(vr[j]) != 0;
+                }
                 if (!wait(&kv_empty[st], ring.use(i) + 1, kSiteLoad)) {
                     ok = false;
                     break;
                 }
                 const uint32_t mask = __ballot_sync(~0u, cur >= 0);
-                if (lane == 0) sh_mask[st][w] = mask;
+                if (lane == 0) sh_mask[st][w] = mask, sh_nan[st][w] = 0u;
+                __syncwarp();
                 if (mask != ~0u) {
 #pragma unroll
                     for (int j = 0; j < NI; ++j)
                         if (!((mask >> (RW * j + rq)) & 1u)) vr[j] = make_uint4(0, 0, 0, 0);
                 }
                 store(keys_at(st), kr);
+                if (some) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) {
+                        if (nan_bits(vr[j]) == 0) continue;
+                        atomicOr(&sh_nan[st][w], 1u << (RW * j + rq));
+                        atomicAnd(&sh_mask[st][w], ~(1u << (RW * j + rq)));
+                        vr[j] = make_uint4(0, 0, 0, 0);
+                    }
+                }
                 store(values_at(st), vr);
                 fence_proxy_async();
                 arrive(&kv_full[st]);
@@ -428,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_t = lanes + hf * 128, o_t = lanes + 256 + hf * D;
         const bool wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.ldo % 16 == 0;
-        uint32_t turns = 0, nt = 0, no[2] = {0, 0}, nml = 0;  // the half's tiles, outputs, merges so far
+        uint32_t nt = 0, no[2] = {0, 0}, nml = 0;  // the half's tiles, outputs, merges so far
         bool ok = true;
         while (ok && next()) {
             const Piece &p = pieces[np & 1];
@@ -499,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     fence_proxy_async();
                 }
             }
+            sh_bad[hf][r] = false;
             tc_fence_before();  // the last piece's reads of TMEM
             arrive(&q_full);
             const int each = pairs ? 2 : 1;
@@ -510,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     ok = false;
                     break;
                 }
-                // (the two halves' warps of an SM sub-partition compute in turn)
                 tc_fence_after();
                 if (idle) {  // no row of the warp's is the unit's: nobody reads its weights' products
                     arrive(&p_full[hf][1]);
@@ -532,12 +564,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     tmem_wait32(v0);
                     tmem_wait32(v1);
                     if (hidden) {
-                        uint32_t see[2] = {h ? there.z : there.x, h ? there.w : there.y};
+                        const uint32_t nan[2] = {sh_nan[st][2 * h], sh_nan[st][2 * h + 1]};
+                        uint32_t see[2] = {(h ? there.z : there.x) | nan[0], (h ? there.w : there.y) | nan[1]};
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const int64_t l = left - 64 * h - 32 * c;
                             if (l < 31) see[c] &= l < 0 ? 0u : (2u << (int)l) - 1u;
                         }
+                        if ((see[0] & nan[0]) | (see[1] & nan[1])) sh_bad[hf][r] = true;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             if (!((see[0] >> k) & 1u)) v0[k] = __float_as_uint(-INFINITY);
@@ -637,7 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     const int64_t slot = full ? ((p.s < a.B ? a.T : 0) + t) * a.Hq + hq
                                               : (int64_t)(2 * blockIdx.x + (p.first ? 0 : 1)) * kWideRows + lr;
                     float *po = (full ? a.whole : a.wpart) + slot * D;
-                    const float inv = l > 0.0f ? a.vs[p.h] / l : 0.0f;
+                    const bool bad = sh_bad[hf][r] || (pairs && sh_bad[1][r]);
+                    const float inv = bad ? __uint_as_float(0x7FFFFFFFu) : row_factor(a.vs[p.h], l);
                     uint16_t *out = a.out + t * a.ldo + (int64_t)hq * D;
 #pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
@@ -686,9 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                         if (!direct) {
                             float *ml = (full ? a.whole_ml : a.wpart_ml) + slot * 2;
                             ml[0] = ref;
-                            ml[1] = l;
+                            ml[1] = bad ? -l : l;
                         } else if (a.lse) {
-                            a.lse[t * a.Hq + hq] = l > 0.0f ? kLn2 * (ref + log2f(l)) : -INFINITY;
+                            a.lse[t * a.Hq + hq] = row_lse(ref, l);
                         }
                     }
                 }

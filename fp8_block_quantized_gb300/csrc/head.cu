@@ -12,8 +12,8 @@
 //          a logit, so after every 1024 the sum is taken over into registers and
 //          added up there, rounded to nearest;
 //   kGrad  z tiles of a piece of the vocabulary again; the epilogue writes d in
-//          BF16 (the type that the next two products read: 2^-9 relative a
-//          value, below the outputs' own rounding in the sums);
+//          BF16 (the type that the next two products read: up to 2^-8 of each
+//          value, whose errors mostly cancel in the sums);
 //   kDx    d w over the piece (w read MN-major as it lies), binary32 results of
 //          one or more ranges of the contraction, added up by head_sum_kernel;
 //   kDw    d^T x (both read MN-major as they lie), BF16.

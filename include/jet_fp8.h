@@ -670,7 +670,8 @@ JET_API jet_status jet_sample_unaligned(const void *logits, int dtype, int64_t B
  * k_p, v_p the codes in slot table[b][p / block_size] * block_size +
  * p % block_size.  A key without a slot (a negative table entry, a slot >= S, a
  * position past the table's width) is left out; a query that sees no key gets
- * out 0 and lse -inf.  Products of the queries with the codes are exact to 2^-38
+ * out 0 and lse -inf.  What a key that a query does not see holds does not matter
+ * to it, NaN codes included.  Products of the queries with the codes are exact to 2^-38
  * of the query's largest channel, sums in binary32, weights rounded to 11 bits,
  * one rounding to BF16; the result is the same for the same call, whatever ran
  * before.
@@ -752,7 +753,7 @@ JET_API jet_status jet_head_logp(const uint16_t *x, const uint16_t *w, int64_t T
  *   d_tv = scale dlogp_t ([v = target[t]] - e^(z_tv - lse_t)), 0 for ignored rows,
  *   dx = d w,  dw = d^T x.
  * The logits are computed again, a piece of the vocabulary at a time (at most
- * 512 MB of d, 4096 entries at least); d is rounded to BF16 (2^-9 relative a
+ * 512 MB of d, 4096 entries at least); d is rounded to BF16 (2^-8 of each
  * value), sums are binary32, dx and dw rounded once to BF16.
  *   x, w, target, scale, lse: as in and from jet_head_logp.  dlogp [T] FP32 (in;
  *       not read for ignored rows).

@@ -282,6 +282,36 @@ def test_nan_behind_the_length_does_not_show_in_many_rows(jet):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,length", [(9, 77), (300, 300), (70, 333), (33, 4000)])
+@pytest.mark.parametrize("prefix", [0, 1, 2])  # no group, a prefix before the key, one with it
+def test_nan_in_a_later_key(jet, D, n, length, prefix):
+    """NaN codes of a token in the middle of a chunk reach the queries from it on, none before,
+    and another request's only where they are its prefix too."""
+    at = length - n // 2 - 1                    # the position of the chunk's token n - n // 2 - 1
+    shared = [None, min(length // 3, at), at + 3][prefix]
+    b = Batch([(n, length), (2, length + 5)], 8, 2, D, 16, seed=41, groups=[(0, 2, shared)] if prefix else ())
+    want, want_lse = b.call(jet)
+    slot = int(b.table[0, at // b.bs]) * b.bs + at % b.bs
+    before = n - n // 2 - 1
+    for cache, code, sees in ((b.v, 0x7F, "value"), (b.k, 0xFF, "key")):
+        kept = cache[slot].clone()
+        cache[slot, 1, 17] = code
+        got, lse = b.call(jet)
+        assert torch.equal(got[:before], want[:before]) and torch.equal(lse[:before], want_lse[:before])
+        if prefix < 2:
+            assert torch.equal(got[n:], want[n:]) and torch.equal(lse[n:], want_lse[n:])
+        else:
+            assert torch.equal(got[n:, :4], want[n:, :4]) and got[n:, 4:, 17].isnan().all()
+        assert torch.equal(got[before:n, :4], want[before:n, :4])           # the other head's
+        assert got[before:n, 4:, 17].isnan().all()
+        if sees == "key":
+            assert lse[before:n, 4:].isnan().all() and got[before:n, 4:].isnan().all()
+        else:
+            assert torch.equal(lse[before:n], want_lse[before:n])
+        cache[slot] = kept
+
+
 def test_long_context(jet):
     """Many pieces of one unit."""
     g = torch.Generator().manual_seed(1)
