@@ -3,11 +3,10 @@
 // projections' DGrads, without BF16 gradients in between.  With s = 1 / (1 +
 // e^-g):
 //   dup = dh g s,   dgate = dh up s (1 + g (1 - s)).
-// Both s and 1 - s come from t = e^-|g| in (0, 1]: r = 1 / (1 + t) is the larger
-// of them and t r the smaller, so neither overflows nor cancels.  t is one
-// exp2 of a binary32 product (relative error 2^-22 + |g| 2^-24), r a reciprocal
-// approximation with one Newton step (its error below 2^-23); then the 1x128
-// group rule of quant_rule.cuh on the binary32 values.
+// With t = e^-g, s = 1 / (1 + t) and 1 - s = t s, so neither cancels; t is one exp2 of
+// a binary32 product (relative error 2^-22 + |g| 2^-24) held below 2^127, the
+// reciprocal approximation's error 2^-23; where s would be below 2^-126 it is 0.  Then
+// the 1x128 group rule of quant_rule.cuh on the binary32 values.
 //
 // Work is split as in the forward's quantizer: half a warp takes a group of 128
 // (8 elements a lane, one 16-byte load of each tensor), a warp two neighbouring
@@ -27,18 +26,24 @@ constexpr int kCtasPerSm = 4;
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// -dgate and -dup of one element, for the division routine
-__device__ __forceinline__ void neg_gradients(float g, float u, float d, float &ng, float &nu) {
-    const float t = exp2f(-1.4426950408889634f * fabsf(g));
-    const float q = 1.0f + t;
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(q));  // q in [1, 2]
-    r = fmaf(fmaf(-q, r, 1.0f), r, r);
-    const float tr = t * r;
-    const float s = g >= 0.0f ? r : tr, c = g >= 0.0f ? tr : r;  // s and 1 - s
-    const float nd = -d * s;
-    nu = nd * g;
-    ng = nd * u * fmaf(g, c, 1.0f);
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 unpack(uint32_t w) { return make_float2(lo(w), hi(w)); }
+
+// -dgate and -dup of two elements, for the division routine, in packed arithmetic
+__device__ __forceinline__ void neg_gradients(uint32_t g, uint32_t u, uint32_t d, float *ng, float *nu) {
+    const float2 m = unpack(g ^ 0x80008000u), dh = unpack(d);  // m = -g
+    const float2 x = __fmul2_rn(m, both(1.4426950408889634f));
+    float2 t, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(fminf(x.x, 127.0f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(fminf(x.y, 127.0f)));
+    const float2 q = __fadd2_rn(t, both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(q.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(q.y));
+    const float2 ds = __fmul2_rn(dh, s);
+    const float2 a = __fmul2_rn(ds, m);
+    const float2 f = __ffma2_rn(m, __fmul2_rn(t, s), both(-1.0f));  // -(1 + g (1 - s))
+    const float2 b = __fmul2_rn(__fmul2_rn(ds, unpack(u)), f);
+    nu[0] = a.x, nu[1] = a.y, ng[0] = b.x, ng[1] = b.y;
 }
 
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
@@ -80,26 +85,26 @@ swiglu_bwd_kernel(const uint16_t *__restrict__ gate, const uint16_t *__restrict_
         float ng[8], nu[8], ag = 0.0f, au = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            neg_gradients(lo(g[i]), lo(u[i]), lo(d[i]), ng[2 * i], nu[2 * i]);
-            neg_gradients(hi(g[i]), hi(u[i]), hi(d[i]), ng[2 * i + 1], nu[2 * i + 1]);
+            neg_gradients(g[i], u[i], d[i], ng + 2 * i, nu + 2 * i);
             ag = max_abs2(ag, ng[2 * i], ng[2 * i + 1]);
             au = max_abs2(au, nu[2 * i], nu[2 * i + 1]);
         }
+        // the first eight lanes of a group take dgate's maximum, scale and reciprocal, the
+        // others dup's
+        const bool second = j >= 8;
+        float amax = fmaxf(second ? au : ag, __shfl_xor_sync(~0u, second ? ag : au, 8));
 #pragma unroll
-        for (int off = 8; off >= 1; off >>= 1) {
-            ag = fmaxf(ag, __shfl_xor_sync(~0u, ag, off));
-            au = fmaxf(au, __shfl_xor_sync(~0u, au, off));
-        }
+        for (int off = 4; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, off));
+        const Divisor mine = make_divisor(group_scale(amax));
+        Divisor d0, d1;
+        d0.s = __shfl_sync(~0u, mine.s, 0, 16), d1.s = __shfl_sync(~0u, mine.s, 8, 16);
+        d0.ny = __shfl_sync(~0u, mine.ny, 0, 16), d1.ny = __shfl_sync(~0u, mine.ny, 8, 16);
+        d0.fast = d0.ny != 0.0f, d1.fast = d1.ny != 0.0f;
         if (fb < nfb) {
             const int64_t at = m * F + fb * 128 + 8 * j;
-            const float s0 = group_scale(ag), s1 = group_scale(au);
-            const Divisor d0 = make_divisor(s0), d1 = make_divisor(s1);
             *reinterpret_cast<uint2 *>(qg + at) = make_uint2(encode4(ng, d0), encode4(ng + 4, d0));
             *reinterpret_cast<uint2 *>(qu + at) = make_uint2(encode4(nu, d1), encode4(nu + 4, d1));
-            if (j == 0) {
-                sg[fb * M + m] = s0;
-                su[fb * M + m] = s1;
-            }
+            if ((j & 7) == 0) (second ? su : sg)[fb * M + m] = mine.s;
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i) cur[i] = nxt[i];

@@ -713,7 +713,7 @@ JET_API size_t jet_kv_attention_workspace(int64_t T, int64_t Hq, int64_t Hk, int
  * gradients straight through), its two gradients quantized for the DGrads of the
  * gate and up projections.  With s = 1 / (1 + e^-gate) in binary32:
  *   dup = dh gate s,  dgate = dh up s (1 + gate (1 - s)),
- * within a few 2^-22 relative; the 1x128 group rule applies to the binary32
+ * within a few 2^-22 relative (s below 2^-126 counts as 0); the 1x128 group rule applies to the binary32
  * values.  The 128x1 forms for the WGrads come from jet_requant_128x1, as for
  * every other operand.
  *   gate, up [M][F] BF16 bits (in) with row stride ld (two halves of a gate_up
