@@ -69,27 +69,6 @@ struct Cfg {
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// How many ranges dx's contraction is cut into, at most `most`, by the kept rows: it has
-// few tiles and a long contraction, so the ranges that make the shortest time of
-// whole waves (a slice of 64 takes about 800 cycles on a pair, 400 on one CTA; a range 12
-// slices of start-up) and of their results' way through memory (about 3500 bytes a
-// cycle, written and read).  By the sizes alone, not the device's: the order of the
-// sums is the same everywhere.
-constexpr int kClusters = 76;  // pairs of 152 SMs
-__host__ __device__ inline int dx_splits(uint32_t rows, uint32_t K, uint32_t nk, int cl, int most) {
-    const uint32_t bm = BM * cl, bn = cl == 2 ? 256 : 128, tiles = (rows + bm - 1) / bm * ((K + bn - 1) / bn);
-    const uint32_t at_once = cl == 2 ? kClusters : 2 * kClusters, cycles = cl == 2 ? 800 : 400;
-    const uint64_t memory = (uint64_t)rows * K / 437;
-    uint64_t best = ~0ull;
-    int found = 1;
-    for (uint32_t s = 1; s <= (uint32_t)most && s <= nk; ++s) {
-        const uint64_t cost = (uint64_t)((tiles * s + at_once - 1) / at_once) * (((nk + s - 1) / s + 12) * cycles) +
-                              s * memory;
-        if (cost < best) best = cost, found = (int)s;
-    }
-    return found;
-}
-
 struct Epilogue {
     const int64_t *target;   // kLse: [T]
     float scale;
@@ -118,8 +97,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// rows R, columns C, contraction D in elements; `splits` ranges of the contraction
-// (kDx: at most).
+// rows R, columns C, contraction D in elements; `splits` ranges of the contraction.
 template <int P, int CL>
 __global__ void __launch_bounds__(P == kLse ? kLseThreads : kThreads, 1)
 head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, int R,
@@ -172,7 +150,6 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
     if (P == kDw) D = *ep.count;
     const int tm = (R + BM * CL - 1) / (BM * CL), tn = (C + BN - 1) / BN;
     const int nk = (D + BK - 1) / BK;
-    if (P == kDx) splits = dx_splits(R, C, nk, CL, splits);
     const int total = tm * tn * splits;
     const int unit0 = blockIdx.x / CL, step = gridDim.x / CL;
     // Unit t: the operand of fewer tiles is walked fastest, so that it stays in
@@ -561,13 +538,12 @@ head_gather_kernel(const uint4 *__restrict__ x, int64_t chunks, const int *__res
 // dx = BF16(sum of the ranges' results, in order, after the pieces before), zeros for
 // the rows that were not kept.
 __global__ void __launch_bounds__(256)
-head_sum_kernel(const float4 *__restrict__ acc, int most, int64_t nk, int cl, int64_t T, int64_t chunks,
+head_sum_kernel(const float4 *__restrict__ acc, int splits, int64_t T, int64_t chunks,
                 const int *__restrict__ count, const int *__restrict__ to,
                 const float4 *__restrict__ before, float4 *__restrict__ run, uint2 *__restrict__ dx) {
     griddep_launch_dependents();
     griddep_wait();
     const int64_t each = *count * chunks;
-    const int splits = dx_splits(*count, chunks * 4, nk, cl, most);
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < T * chunks; i += gridDim.x * 256ll) {
         const int64_t t = i / chunks;
         const int r = to[t];
@@ -595,11 +571,12 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 struct Plan {
     int cl_z, cl_dx, cl_dw;   // CTAs a tile
     int64_t piece;            // vocabulary entries of a piece (backward)
-    int splits;               // most ranges of dx's contraction in a piece
+    int splits;               // ranges of dx's contraction in a piece
     int64_t tiles_z;          // column tiles of the forward
     size_t fwd_bytes, d_bytes, acc_bytes, run_bytes, x_bytes, row_bytes, bwd_bytes;
 };
 
+constexpr int64_t kClusters = 76;        // what the plan counts with: pairs of 152 SMs
 constexpr int64_t kPieceBytes = 512ll << 20;
 
 Plan plan(int64_t T, int64_t V, int64_t K) {
@@ -613,9 +590,20 @@ Plan plan(int64_t T, int64_t V, int64_t K) {
     const int64_t pieces = ceil_div(V, most);
     p.piece = ceil_div(ceil_div(V, pieces), 256) * 256;
     p.cl_dw = p.piece <= BM ? 1 : 2;
-    // the most ranges whose results take 256 MB
+    // dx has few tiles and a long contraction: the ranges that make the shortest
+    // time of whole waves (a slice of 64 takes about 540 cycles on a pair, 270 on
+    // one CTA; a range 12 slices of start-up) and of its results' way through
+    // memory (about 3500 bytes a cycle, written and read)
+    const int64_t tiles = ceil_div(T, BM * p.cl_dx) * ceil_div(K, p.cl_dx == 2 ? 256 : 128);
+    const int64_t at_once = p.cl_dx == 2 ? kClusters : 2 * kClusters, nk = ceil_div(p.piece, BK);
+    const int64_t cycles = p.cl_dx == 2 ? 540 : 270;
+    int64_t best = -1;
     p.splits = 1;
-    while (p.splits < 16 && (p.splits + 1) * T * K * 4 <= (256ll << 20)) ++p.splits;
+    for (int64_t s = 1; s <= 16 && s <= nk; ++s) {
+        if (s > 1 && s * T * K * 4 > (512ll << 20)) break;
+        const int64_t cost = ceil_div(tiles * s, at_once) * (ceil_div(nk, s) + 12) * cycles + s * T * K * 8 / 3500;
+        if (best < 0 || cost < best) best = cost, p.splits = (int)s;
+    }
     const int64_t rows = ceil_div(T, 64) * 64;
     p.d_bytes = up256((size_t)(rows * p.piece) * 2);
     p.acc_bytes = up256((size_t)(p.splits * T * K) * 4);
@@ -806,8 +794,7 @@ jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, in
             if (st != JET_OK) return st;
             const bool last = v0 + nv == V;
             st = launch_pdl(head_sum_kernel, blocks(T * K / 4), dim3(256), 0, s,
-                            reinterpret_cast<const float4 *>(ep.acc), splits, nk, p.cl_dx, T, K / 4,
-                            (const int *)count,
+                            reinterpret_cast<const float4 *>(ep.acc), splits, T, K / 4, (const int *)count,
                             (const int *)to,
                             v0 > 0 ? reinterpret_cast<const float4 *>(run) : (const float4 *)nullptr,
                             reinterpret_cast<float4 *>(run),
