@@ -17,9 +17,6 @@
 //   kDx    d w over the piece (w read MN-major as it lies), binary32 results of
 //          one or more ranges of the contraction, added up by head_sum_kernel;
 //   kDw    d^T x (both read MN-major as they lie), BF16.
-// The backward begins by dropping the rows whose gradient is zero (ignored targets,
-// dlogp = 0): the kept rows of x are copied side by side, all products work on
-// them, and how many they are stays on the device.
 // Forward: bound by the tensor core for many tokens (2 T K V operations), by the
 // read of w for few.  Backward: 8 T K V operations, a quarter of them the logits
 // again; d passes through memory once per piece.
@@ -70,19 +67,15 @@ struct Cfg {
 };
 
 struct Epilogue {
-    const int64_t *target;   // kLse: [T]
+    const int64_t *target;
+    const float *lse, *dlogp;
     float scale;
     int V, v0;               // vocabulary, and the first entry of the piece
-    // backward: how many rows are kept; their target, lse (in powers of two) and
-    // gradient times scale, up to the next multiple of 64 (there none, 0, 0)
-    const int *count;
-    const int *token;
-    const float *lse2, *grad;
     float2 *part;            // kLse: [2 column tiles][T] (maximum, sum) in powers of two
     float *zt;               // kLse: [T] the target's logit, in powers of two
     uint16_t *d;             // kGrad: [T][ldd]
     int64_t ldd;
-    float *acc;              // kDx: [splits][rows][K]
+    float *acc;              // kDx: [splits][T][K]
     uint16_t *dw;            // kDw: [V][K]
 };
 
@@ -146,8 +139,6 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
     griddep_launch_dependents();
     griddep_wait();
 
-    if (P == kGrad || P == kDx) R = *ep.count;
-    if (P == kDw) D = *ep.count;
     const int tm = (R + BM * CL - 1) / (BM * CL), tn = (C + BN - 1) / BN;
     const int nk = (D + BK - 1) / BK;
     const int total = tm * tn * splits;
@@ -358,31 +349,26 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             const int row = m0 + quad * 32 + lane;
             const bool row_ok = row < R;
             const uint32_t buf = tiles & 1u;
-            // kGrad: the target's column of the piece (none: out of any tile); rows up to the
-            // next multiple of 64 are written too, as zeros: kDw reads 64 at a time
-            const bool pad_ok = P == kGrad && row < (R + 63) / 64 * 64;
+            // kGrad: the target's column of the piece (none: out of any tile)
             int want = -1;
             float lse2 = 0.0f, g = 0.0f;
-            if (pad_ok) {
-                want = ep.token[row] - ep.v0;
-                lse2 = ep.lse2[row];
-                g = ep.grad[row];
+            if (P == kGrad && row_ok) {
+                const int64_t token = ep.target[row];
+                if (token >= 0 && token < ep.V) {
+                    want = (int)token - ep.v0;
+                    g = ep.dlogp[row] * ep.scale;
+                }
+                lse2 = ep.lse[row] * kLog2e;
             }
-            const bool empty = k0 == k1;  // kDw without rows: zeros
-            if (!empty && !wait(&tfull_bar[buf], (tiles >> 1) & 1u, kSiteEpilogue)) break;
+            if (!wait(&tfull_bar[buf], (tiles >> 1) & 1u, kSiteEpilogue)) break;
             tc_fence_after();
             const uint32_t acc0 = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
 #pragma unroll 1
             for (int ch = 0; ch < BN / 32; ++ch) {
                 uint32_t r[32];
                 __syncwarp();
-                if (P == kDw && empty) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0u;
-                } else {
-                    tmem_ld32(acc0 + ch * 32, r);
-                    tmem_wait32(r);
-                }
+                tmem_ld32(acc0 + ch * 32, r);
+                tmem_wait32(r);
                 const int col = n0 + ch * 32;
                 if constexpr (P == kGrad) {
                     uint16_t *dst = ep.d + (int64_t)row * ep.ldd + col;
@@ -397,11 +383,11 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                                 const int at = i + 2 * k + e;
                                 const float p = ex2(fmaf(__uint_as_float(r[at]), c, -lse2));
                                 v[e] = g * ((want == col + at ? 1.0f : 0.0f) - p);
-                                if (g == 0.0f) v[e] = 0.0f;  // the rows up to a multiple of 64
+                                if (g == 0.0f) v[e] = 0.0f;  // whatever lse is there
                             }
                             w[k] = pack2(v[0], v[1]);
                         }
-                        if (pad_ok && col + i < C)  // (up to the padded row end past the piece's last)
+                        if (row_ok && col + i < C)  // (up to the padded row end past the piece's last)
                             *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else if constexpr (P == kDx) {
@@ -425,7 +411,7 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && !empty) {
+            if (lane == 0) {
                 if (kPair) mbar_arrive_cluster_relaxed(release[buf]);
                 else mbar_arrive(&tempty_bar[buf]);
             }
@@ -473,91 +459,20 @@ head_join_kernel(const float2 *__restrict__ part, const float *__restrict__ zt,
     logp[row] = token >= 0 && token < V ? kLn2 * ((zt[row] - m) - l) : 0.0f;
 }
 
-// The rows with a gradient, in order: where each came from (`from`) and went to
-// (`to`, -1 for the others), its token, lse and gradient.  One CTA.
-__global__ void __launch_bounds__(1024)
-head_pick_kernel(const int64_t *__restrict__ target, const float *__restrict__ lse,
-                 const float *__restrict__ dlogp, int T, int V, float scale, int *__restrict__ count,
-                 int *__restrict__ from, int *__restrict__ to, int *__restrict__ token,
-                 float *__restrict__ lse2, float *__restrict__ grad) {
-    griddep_launch_dependents();
-    griddep_wait();
-    __shared__ int sh[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int n = 0;  // kept so far
-    for (int t0 = 0; t0 < T; t0 += 1024) {
-        const int t = t0 + tid;
-        const int64_t tk = t < T ? target[t] : -1;
-        const bool real = tk >= 0 && tk < V;
-        const float g = real ? dlogp[t] * scale : 0.0f;
-        const bool keep = real && g != 0.0f;
-        const unsigned votes = __ballot_sync(~0u, keep);
-        if (lane == 0) sh[warp] = __popc(votes);
-        __syncthreads();
-        int v = sh[lane];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(~0u, v, d);
-            if (lane >= d) v += u;
-        }
-        const int before = __shfl_sync(~0u, v, warp > 0 ? warp - 1 : 0);
-        const int at = n + (warp > 0 ? before : 0) + __popc(votes & ((1u << lane) - 1u));
-        n += __shfl_sync(~0u, v, 31);
-        if (t < T) to[t] = keep ? at : -1;
-        if (keep) {
-            from[at] = t;
-            token[at] = (int)tk;
-            lse2[at] = lse[t] * kLog2e;
-            grad[at] = g;
-        }
-        __syncthreads();
-    }
-    const int end = (n + 63) / 64 * 64;
-    if (n + tid < end) {
-        from[n + tid] = -1;
-        token[n + tid] = -1;
-        lse2[n + tid] = grad[n + tid] = 0.0f;
-    }
-    if (tid == 0) *count = n;
-}
-
-// The kept rows of x side by side, and zeros up to a multiple of 64.
+// dx = BF16(sum of the ranges' results, in order, after the pieces before).
 __global__ void __launch_bounds__(256)
-head_gather_kernel(const uint4 *__restrict__ x, int64_t chunks, const int *__restrict__ count,
-                   const int *__restrict__ from, uint4 *__restrict__ out) {
+head_sum_kernel(const float4 *__restrict__ acc, int splits, int64_t n4, const float4 *__restrict__ before,
+                float4 *__restrict__ run, uint2 *__restrict__ dx) {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t n = (*count + 63) / 64 * 64 * chunks;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        const int64_t r = i / chunks;
-        const int t = from[r];
-        out[i] = t >= 0 ? x[t * chunks + (i - r * chunks)] : make_uint4(0, 0, 0, 0);
-    }
-}
-
-// dx = BF16(sum of the ranges' results, in order, after the pieces before), zeros for
-// the rows that were not kept.
-__global__ void __launch_bounds__(256)
-head_sum_kernel(const float4 *__restrict__ acc, int splits, int64_t T, int64_t chunks,
-                const int *__restrict__ count, const int *__restrict__ to,
-                const float4 *__restrict__ before, float4 *__restrict__ run, uint2 *__restrict__ dx) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const int64_t each = *count * chunks;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < T * chunks; i += gridDim.x * 256ll) {
-        const int64_t t = i / chunks;
-        const int r = to[t];
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r >= 0) {
-            const int64_t at = r * chunks + (i - t * chunks);
-            if (before) a = before[at];
-            for (int s = 0; s < splits; ++s) {
-                const float4 b = acc[s * each + at];
-                a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
-            }
-            if (!dx) run[at] = a;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += gridDim.x * 256ll) {
+        float4 a = before ? before[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s = 0; s < splits; ++s) {
+            const float4 b = acc[s * n4 + i];
+            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
         }
         if (dx) dx[i] = make_uint2(pack2(a.x, a.y), pack2(a.z, a.w));
+        else run[i] = a;
     }
 }
 
@@ -573,7 +488,7 @@ struct Plan {
     int64_t piece;            // vocabulary entries of a piece (backward)
     int splits;               // ranges of dx's contraction in a piece
     int64_t tiles_z;          // column tiles of the forward
-    size_t fwd_bytes, d_bytes, acc_bytes, run_bytes, x_bytes, row_bytes, bwd_bytes;
+    size_t fwd_bytes, d_bytes, acc_bytes, run_bytes;
 };
 
 constexpr int64_t kClusters = 76;        // what the plan counts with: pairs of 152 SMs
@@ -604,13 +519,9 @@ Plan plan(int64_t T, int64_t V, int64_t K) {
         const int64_t cost = ceil_div(tiles * s, at_once) * (ceil_div(nk, s) + 12) * cycles + s * T * K * 8 / 3500;
         if (best < 0 || cost < best) best = cost, p.splits = (int)s;
     }
-    const int64_t rows = ceil_div(T, 64) * 64;
-    p.d_bytes = up256((size_t)(rows * p.piece) * 2);
+    p.d_bytes = up256((size_t)(T * p.piece) * 2);
     p.acc_bytes = up256((size_t)(p.splits * T * K) * 4);
     p.run_bytes = p.piece < V ? up256((size_t)(T * K) * 4) : 0;
-    p.x_bytes = up256((size_t)(rows * K) * 2);
-    p.row_bytes = up256((size_t)rows * 4);  // five arrays of one value a row, and the count
-    p.bwd_bytes = p.d_bytes + p.acc_bytes + p.run_bytes + p.x_bytes + 5 * p.row_bytes + 256;
     return p;
 }
 
@@ -688,7 +599,7 @@ inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<ui
 size_t jet_head_workspace(int op, int64_t T, int64_t V, int64_t K) {
     if (!shape_ok(T, K, V) || T == 0) return 0;
     const Plan p = plan(T, V, K);
-    return op == JET_OP_HEAD_LOGP ? p.fwd_bytes : p.bwd_bytes;
+    return op == JET_OP_HEAD_LOGP ? p.fwd_bytes : p.d_bytes + p.acc_bytes + p.run_bytes;
 }
 
 jet_status jet_head_logp(const uint16_t *x, const uint16_t *w, int64_t T, int64_t K, int64_t V,
@@ -732,7 +643,7 @@ jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, in
                     aligned_to(target, 8) && aligned_to(lse, 4) && aligned_to(dlogp, 4),
                 JET_ERR_ALIGN);
     const Plan p = plan(T, V, K);
-    JET_REQUIRE(T == 0 || (ws && ws_bytes >= p.bwd_bytes), JET_ERR_WORKSPACE);
+    JET_REQUIRE(T == 0 || (ws && ws_bytes >= p.d_bytes + p.acc_bytes + p.run_bytes), JET_ERR_WORKSPACE);
     DeviceInfo dev;
     jet_status st = current_device(&dev);
     if (st != JET_OK) return st;
@@ -746,43 +657,22 @@ jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, in
     }
     uint8_t *base = static_cast<uint8_t *>(ws);
     Epilogue ep = {};
-    ep.scale = scale, ep.V = (int)V;
+    ep.target = target, ep.lse = lse, ep.dlogp = dlogp, ep.scale = scale, ep.V = (int)V;
     ep.d = reinterpret_cast<uint16_t *>(base), ep.ldd = p.piece;
     ep.acc = reinterpret_cast<float *>(base + p.d_bytes);
     ep.dw = dw;
     float *run = reinterpret_cast<float *>(base + p.d_bytes + p.acc_bytes);
-    uint8_t *rest = base + p.d_bytes + p.acc_bytes + p.run_bytes;
-    uint16_t *xk = reinterpret_cast<uint16_t *>(rest);  // the kept rows of x
-    rest += p.x_bytes;
-    int *from = reinterpret_cast<int *>(rest), *to = reinterpret_cast<int *>(rest + p.row_bytes);
-    int *token = reinterpret_cast<int *>(rest + 2 * p.row_bytes);
-    float *lse2 = reinterpret_cast<float *>(rest + 3 * p.row_bytes),
-          *grad = reinterpret_cast<float *>(rest + 4 * p.row_bytes);
-    int *count = reinterpret_cast<int *>(rest + 5 * p.row_bytes);
-    ep.count = count, ep.token = token, ep.lse2 = lse2, ep.grad = grad;
-    const int64_t rows = ceil_div(T, 64) * 64;
-    st = launch_pdl(head_pick_kernel, dim3(1), dim3(1024), 0, s, target, lse, dlogp, (int)T, (int)V, scale,
-                    count, from, to, token, lse2, grad);
-    if (st != JET_OK) return st;
-    auto blocks = [&](int64_t items) {
-        const int64_t want = ceil_div(items, 256), cap = (int64_t)dev.num_sms * 8;
-        return dim3((unsigned)(want < cap ? want : cap));
-    };
-    st = launch_pdl(head_gather_kernel, blocks(rows * K / 8), dim3(256), 0, s,
-                    reinterpret_cast<const uint4 *>(x), K / 8, (const int *)count, (const int *)from,
-                    reinterpret_cast<uint4 *>(xk));
-    if (st != JET_OK) return st;
     CUtensorMap tx, tx64;
-    if (!map_rows16(&tx, xk, (uint64_t)K, (uint64_t)rows, (uint64_t)K, BM) ||
-        !map_rows16(&tx64, xk, (uint64_t)K, (uint64_t)rows, (uint64_t)K, BK))
+    if (!map_rows16(&tx, x, (uint64_t)K, (uint64_t)T, (uint64_t)K, BM) ||
+        !map_rows16(&tx64, x, (uint64_t)K, (uint64_t)T, (uint64_t)K, BK))
         return JET_ERR_CUDA;
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         const int64_t nv = V - v0 < p.piece ? V - v0 : p.piece;
         CUtensorMap tw, tw64, td, td64;
         if (!map_rows16(&tw, w + v0 * K, (uint64_t)K, (uint64_t)nv, (uint64_t)K, BM) ||
             !map_rows16(&tw64, w + v0 * K, (uint64_t)K, (uint64_t)nv, (uint64_t)K, BK) ||
-            !map_rows16(&td, ep.d, (uint64_t)nv, (uint64_t)rows, (uint64_t)p.piece, BM) ||
-            !map_rows16(&td64, ep.d, (uint64_t)nv, (uint64_t)rows, (uint64_t)p.piece, BK))
+            !map_rows16(&td, ep.d, (uint64_t)nv, (uint64_t)T, (uint64_t)p.piece, BM) ||
+            !map_rows16(&td64, ep.d, (uint64_t)nv, (uint64_t)T, (uint64_t)p.piece, BK))
             return JET_ERR_CUDA;
         ep.v0 = (int)v0;
         st = product<kGrad>(p.cl_z, dev, tx, tw, T, nv, K, 1, ep, s);
@@ -793,9 +683,9 @@ jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, in
             st = product<kDx>(p.cl_dx, dev, td, tw64, T, K, nv, splits, ep, s);
             if (st != JET_OK) return st;
             const bool last = v0 + nv == V;
-            st = launch_pdl(head_sum_kernel, blocks(T * K / 4), dim3(256), 0, s,
-                            reinterpret_cast<const float4 *>(ep.acc), splits, T, K / 4, (const int *)count,
-                            (const int *)to,
+            const int64_t n4 = T * K / 4, want = ceil_div(n4, 256), cap = (int64_t)dev.num_sms * 8;
+            st = launch_pdl(head_sum_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0,
+                            s, reinterpret_cast<const float4 *>(ep.acc), splits, n4,
                             v0 > 0 ? reinterpret_cast<const float4 *>(run) : (const float4 *)nullptr,
                             reinterpret_cast<float4 *>(run),
                             last ? reinterpret_cast<uint2 *>(dx) : (uint2 *)nullptr);

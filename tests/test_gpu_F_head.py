@@ -126,24 +126,6 @@ def test_ignored_rows_are_exactly_zero(jet):
     assert not dx.any() and not dw.any()
 
 
-def test_few_rows_with_a_gradient(jet):
-    """The rows without one are left out of the products: first, last, single and no rows kept."""
-    x, w, target, dlogp = make(700, 128, 1000, 12)
-    _, lse = jet.head_logp(x, w, target)
-    for keep in ([0], [699], [5, 63, 64, 65, 300], list(range(64)), list(range(100, 229)), []):
-        some = torch.zeros((700,), dtype=torch.bool, device="cuda")
-        some[keep] = True
-        for how in ("target", "dlogp"):
-            t2, d2 = target.clone(), dlogp.clone()
-            if how == "target":
-                t2[~some] = -100
-            else:
-                d2[~some] = 0.0
-            dx, dw = jet.head_logp_bwd(x, w, t2, lse, d2)
-            assert not dx[~some].any()
-            check_bwd(x, w, t2, d2, 1.0, lse, dx, dw)
-
-
 def test_no_tokens(jet):
     x, w, target, dlogp = make(1, 64, 50, 6)
     e = torch.empty((0,), device="cuda")
