@@ -126,6 +126,40 @@ def test_ignored_rows_are_exactly_zero(jet):
     assert not dx.any() and not dw.any()
 
 
+def test_few_rows_with_a_gradient(jet):
+    """The rows without one get exact zeros and add nothing: first, last, single and no rows with one."""
+    x, w, target, dlogp = make(700, 128, 1000, 12)
+    _, lse = jet.head_logp(x, w, target)
+    for keep in ([0], [699], [5, 63, 64, 65, 300], list(range(64)), list(range(100, 229)), []):
+        some = torch.zeros((700,), dtype=torch.bool, device="cuda")
+        some[keep] = True
+        for how in ("target", "dlogp"):
+            t2, d2 = target.clone(), dlogp.clone()
+            if how == "target":
+                t2[~some] = -100
+            else:
+                d2[~some] = 0.0
+            dx, dw = jet.head_logp_bwd(x, w, t2, lse, d2)
+            assert not dx[~some].any()
+            check_bwd(x, w, t2, d2, 1.0, lse, dx, dw)
+
+
+def test_one_row_with_a_gradient_many_calls(jet):
+    """Few rows of a long contraction and a large vocabulary, calls one behind another."""
+    x, w, target, dlogp = make(129, 4096, 32000, 13)
+    _, lse = jet.head_logp(x, w, target)
+    for keep in (0, 1, 16, 100, 128, 129):
+        t2 = target.clone()
+        t2[keep:] = -1
+        first = jet.head_logp_bwd(x, w, t2, lse, dlogp)
+        for _ in range(10):
+            dx, dw = jet.head_logp_bwd(x, w, t2, lse, dlogp)
+        torch.cuda.synchronize()
+        assert jet.device_status()[0] == 0
+        assert torch.equal(dx, first[0]) and torch.equal(dw, first[1]) and not dx[keep:].any()
+    check_bwd(x, w, target, dlogp, 1.0, lse, dx, dw)
+
+
 def test_no_tokens(jet):
     x, w, target, dlogp = make(1, 64, 50, 6)
     e = torch.empty((0,), device="cuda")
