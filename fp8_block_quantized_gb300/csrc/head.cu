@@ -13,7 +13,9 @@
 //          added up there, rounded to nearest;
 //   kGrad  z tiles of a piece of the vocabulary again; the epilogue writes d in
 //          BF16 (the type that the next two products read: up to 2^-8 of each
-//          value, whose errors mostly cancel in the sums);
+//          value, whose errors mostly cancel in the sums of many tokens; up to 128
+//          tokens have a second array with what the first left over, 2^-16, and
+//          both products go over the two);
 //   kDx    d w over the piece (w read MN-major as it lies), binary32 results of
 //          one or more ranges of the contraction, added up by head_sum_kernel;
 //   kDw    d^T x (both read MN-major as they lie), BF16.
@@ -22,7 +24,7 @@
 // again; d passes through memory once per piece.  4096 tokens, K = 4096, V = 128256:
 // forward 2.81 ms (1534 TFLOP/s), backward 8.5 ms (1515), 65 to 70% of the tensor
 // core's cycles: the operands' feed by TMA is the limit (42 bytes a cycle and SM).  1537
-// tokens, K = 5120, V = 50257: backward 1.72 ms.  48 tokens, K = 512, V = 2048: forward
+// tokens, K = 5120, V = 50257: backward 1.75 ms.  48 tokens, K = 512, V = 2048: forward
 // 12.3 us, two launches of dependent loads.
 //
 // The kernel is persistent: warp 0 loads operand slices of 64 along the
@@ -79,7 +81,8 @@ struct Epilogue {
     float *zt;               // kLse: [T] the target's logit, in powers of two
     uint16_t *d;             // kGrad: [T][ldd]
     int64_t ldd;
-    float *acc;              // kDx: [splits][T][K]
+    int second;              // kGrad, kDw: the first row of d's second part, or 0
+    float *acc;              // kDx: [splits][rows of d][K]
     uint16_t *dw;            // kDw: [V][K]
 };
 
@@ -203,7 +206,8 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                     if (kBMn) {
 #pragma unroll
                         for (int i = 0; i < CF::kBRows / 64; ++i)
-                            load(bs + i * 8192, &tb, b0 + 64 * i, kb * BK);
+                            load(bs + i * 8192, &tb, b0 + 64 * i,
+                                 P == kDw && kb * BK >= ep.second ? kb * BK - ep.second : kb * BK);
                     } else {
                         load(bs, &tb, kb * BK, b0);
                     }
@@ -378,7 +382,7 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                     uint16_t *dst = ep.d + (int64_t)row * ep.ldd + col;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
-                        uint32_t w[4];
+                        uint32_t w[4], left[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             float v[2];
@@ -390,9 +394,14 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                                 if (g == 0.0f) v[e] = 0.0f;  // whatever lse is there
                             }
                             w[k] = pack2(v[0], v[1]);
+                            left[k] = pack2(v[0] - __uint_as_float(w[k] << 16),
+                                            v[1] - __uint_as_float(w[k] & 0xFFFF0000u));
                         }
-                        if (row_ok && col + i < C)  // (up to the padded row end past the piece's last)
+                        if ((row_ok || row < ep.second) && col + i < C)  // (up to the padded row end past the piece's last)
                             *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (row < ep.second && col + i < C)
+                            *reinterpret_cast<uint4 *>(dst + ep.second * ep.ldd + i) =
+                                make_uint4(left[0], left[1], left[2], left[3]);
                     }
                 } else if constexpr (P == kDx) {
                     float *dst = ep.acc + ((int64_t)sp * R + row) * C + col;
@@ -463,16 +472,22 @@ head_join_kernel(const float2 *__restrict__ part, const float *__restrict__ zt,
     logp[row] = token >= 0 && token < V ? kLn2 * ((zt[row] - m) - l) : 0.0f;
 }
 
-// dx = BF16(sum of the ranges' results, in order, after the pieces before).
+// dx = BF16(sum of the ranges' results, in order, after the pieces before); a range has
+// `each` values, the second part of d's from `second` on (or 0: none).
 __global__ void __launch_bounds__(256)
-head_sum_kernel(const float4 *__restrict__ acc, int splits, int64_t n4, const float4 *__restrict__ before,
+head_sum_kernel(const float4 *__restrict__ acc, int splits, int64_t n4, int64_t each, int64_t second,
+                const float4 *__restrict__ before,
                 float4 *__restrict__ run, uint2 *__restrict__ dx) {
     griddep_launch_dependents();
     griddep_wait();
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += gridDim.x * 256ll) {
         float4 a = before ? before[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int s = 0; s < splits; ++s) {
-            const float4 b = acc[s * n4 + i];
+            float4 b = acc[s * each + i];
+            if (second > 0) {
+                const float4 c = acc[s * each + second + i];
+                b.x += c.x, b.y += c.y, b.z += c.z, b.w += c.w;
+            }
             a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
         }
         if (dx) dx[i] = make_uint2(pack2(a.x, a.y), pack2(a.z, a.w));
@@ -492,6 +507,7 @@ struct Plan {
     int64_t piece;            // vocabulary entries of a piece (backward)
     int splits;               // ranges of dx's contraction in a piece
     int64_t tiles_z;          // column tiles of the forward
+    int64_t second, rows;     // where d's second part begins (0: none); rows of d
     size_t fwd_bytes, d_bytes, acc_bytes, run_bytes;
 };
 
@@ -500,9 +516,9 @@ constexpr int64_t kPieceBytes = 512ll << 20;
 
 Plan plan(int64_t T, int64_t V, int64_t K) {
     Plan p;
-    // up to 128 rows a pair would have half a tile idle (dx of 128 rows, K = 4096, V = 32000:
-    // 124 us on single CTAs); above, single CTAs read w once for each 128 rows (256 rows 216 us
-    // against 137 on pairs, 1024 rows 736)
+    // up to 128 rows a pair would have half a tile idle; above, single CTAs read w once for
+    // each 128 rows (forward, K = 4096, V = 32000: 128 rows 59.3 us on single CTAs and 61.1 on
+    // pairs, 256 rows 106.6 and 61.9)
     p.cl_z = p.cl_dx = T <= BM ? 1 : 2;
     p.tiles_z = 2 * ceil_div(V, p.cl_z == 2 ? 256 : 128);  // halves of tiles
     p.fwd_bytes = up256((size_t)(p.tiles_z * T) * sizeof(float2)) + up256((size_t)T * 4);
@@ -516,18 +532,23 @@ Plan plan(int64_t T, int64_t V, int64_t K) {
     // time of whole waves (a slice of 64 takes about 540 cycles on a pair, 270 on
     // one CTA; a range 12 slices of start-up) and of its results' way through
     // memory (about 3500 bytes a cycle, written and read)
-    const int64_t tiles = ceil_div(T, BM * p.cl_dx) * ceil_div(K, p.cl_dx == 2 ? 256 : 128);
+    // d in two parts for the few rows of one tile: one gradient's rounding can be all of an
+    // output's error there (0.0031 of its norm against 0.0017), and the products are bound by
+    // w; a small call of 177 us takes 194
+    p.second = T <= BM ? ceil_div(T, BK) * BK : 0;
+    p.rows = p.second > 0 ? 2 * p.second : T;
+    const int64_t tiles = ceil_div(p.rows, BM * p.cl_dx) * ceil_div(K, p.cl_dx == 2 ? 256 : 128);
     const int64_t at_once = p.cl_dx == 2 ? kClusters : 2 * kClusters, nk = ceil_div(p.piece, BK);
     const int64_t cycles = p.cl_dx == 2 ? 540 : 270;
     int64_t best = -1;
     p.splits = 1;
     for (int64_t s = 1; s <= 16 && s <= nk; ++s) {
-        if (s > 1 && s * T * K * 4 > (512ll << 20)) break;
-        const int64_t cost = ceil_div(tiles * s, at_once) * (ceil_div(nk, s) + 12) * cycles + s * T * K * 8 / 3500;
+        if (s > 1 && s * p.rows * K * 4 > (512ll << 20)) break;
+        const int64_t cost = ceil_div(tiles * s, at_once) * (ceil_div(nk, s) + 12) * cycles + s * p.rows * K * 8 / 3500;
         if (best < 0 || cost < best) best = cost, p.splits = (int)s;
     }
-    p.d_bytes = up256((size_t)(T * p.piece) * 2);
-    p.acc_bytes = up256((size_t)(p.splits * T * K) * 4);
+    p.d_bytes = up256((size_t)(p.rows * p.piece) * 2);
+    p.acc_bytes = up256((size_t)(p.splits * p.rows * K) * 4);
     p.run_bytes = p.piece < V ? up256((size_t)(T * K) * 4) : 0;
     return p;
 }
@@ -665,7 +686,7 @@ jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, in
     uint8_t *base = static_cast<uint8_t *>(ws);
     Epilogue ep = {};
     ep.target = target, ep.lse = lse, ep.dlogp = dlogp, ep.scale = scale, ep.V = (int)V;
-    ep.d = reinterpret_cast<uint16_t *>(base), ep.ldd = p.piece;
+    ep.d = reinterpret_cast<uint16_t *>(base), ep.ldd = p.piece, ep.second = (int)p.second;
     ep.acc = reinterpret_cast<float *>(base + p.d_bytes);
     ep.dw = dw;
     float *run = reinterpret_cast<float *>(base + p.d_bytes + p.acc_bytes);
@@ -678,8 +699,8 @@ jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, in
         CUtensorMap tw, tw64, td, td64;
         if (!map_rows16(&tw, w + v0 * K, (uint64_t)K, (uint64_t)nv, (uint64_t)K, BM) ||
             !map_rows16(&tw64, w + v0 * K, (uint64_t)K, (uint64_t)nv, (uint64_t)K, BK) ||
-            !map_rows16(&td, ep.d, (uint64_t)nv, (uint64_t)T, (uint64_t)p.piece, BM) ||
-            !map_rows16(&td64, ep.d, (uint64_t)nv, (uint64_t)T, (uint64_t)p.piece, BK))
+            !map_rows16(&td, ep.d, (uint64_t)nv, (uint64_t)p.rows, (uint64_t)p.piece, BM) ||
+            !map_rows16(&td64, ep.d, (uint64_t)nv, (uint64_t)p.rows, (uint64_t)p.piece, BK))
             return JET_ERR_CUDA;
         ep.v0 = (int)v0;
         st = product<kGrad>(p.cl_z, dev, tx, tw, T, nv, K, 1, ep, s);
@@ -687,19 +708,19 @@ jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, in
         if (dx) {
             const int64_t nk = ceil_div(nv, BK);
             const int splits = (int)(p.splits < nk ? p.splits : nk);
-            st = product<kDx>(p.cl_dx, dev, td, tw64, T, K, nv, splits, ep, s);
+            st = product<kDx>(p.cl_dx, dev, td, tw64, p.rows, K, nv, splits, ep, s);
             if (st != JET_OK) return st;
             const bool last = v0 + nv == V;
             const int64_t n4 = T * K / 4, want = ceil_div(n4, 256), cap = (int64_t)dev.num_sms * 8;
             st = launch_pdl(head_sum_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0,
-                            s, reinterpret_cast<const float4 *>(ep.acc), splits, n4,
+                            s, reinterpret_cast<const float4 *>(ep.acc), splits, n4, p.rows * K / 4, p.second * K / 4,
                             v0 > 0 ? reinterpret_cast<const float4 *>(run) : (const float4 *)nullptr,
                             reinterpret_cast<float4 *>(run),
                             last ? reinterpret_cast<uint2 *>(dx) : (uint2 *)nullptr);
             if (st != JET_OK) return st;
         }
         if (dw) {
-            st = product<kDw>(p.cl_dw, dev, td64, tx64, nv, K, T, 1, ep, s);
+            st = product<kDw>(p.cl_dw, dev, td64, tx64, nv, K, p.rows, 1, ep, s);
             if (st != JET_OK) return st;
         }
     }

@@ -69,7 +69,7 @@ def check_bwd(x, w, target, dlogp, scale, lse, dx, dw):
     d = torch.where(real[:, None], up[:, None] * (hot - p), 0.0)
     # e^(z - lse): the logit's error, lse's and the argument's roundings; d once more to BF16 (2^-8)
     off = up.abs()[:, None] * p * (2 * dz[:, None] + (z.abs() + lse.double().abs()[:, None] + 8) * 2.0 ** -22)
-    off = torch.where(real[:, None], off, 0.0) + 2.0 ** -8 * d.abs()
+    off = torch.where(real[:, None], off, 0.0) + 2.0 ** (-16 if len(x) <= 128 else -8) * d.abs()
     for got, ref, bound, n in ((dx, d @ w.double(), off @ w.double().abs(), V),
                                (dw, d.t() @ x.double(), off.t() @ x.double().abs(), x.shape[0])):
         if got is None:
