@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Args
     if (tid == 0) sh_empty = 0;
     __syncthreads();
     const int64_t *po = held ? sh_po : a.po;
-    int64_t tiles0[2] = {0, 0};  // before this round's segments
+    int64_t tiles0[2] = {0, 0};  // before the segments of this pass
     int count0[2] = {0, 0};
     int *order[2] = {a.order, a.order + nseg};
     for (int s0 = 0; s0 < nseg; s0 += kPlanThreads) {
