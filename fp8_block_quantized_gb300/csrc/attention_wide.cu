@@ -162,7 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
     // then not in the first), where some row does not see all keys
     __shared__ __align__(16) uint32_t sh_mask[kStages][4], sh_nan[kStages][4];
     __shared__ float sh_m[128], sh_l[128];
-    __shared__ bool sh_bad[2][128];  // the row sees a value that is NaN
+    // Whether the row sees a value that is NaN, by the piece's parity: B clears its flags for
+    // the next piece while A may still have to read the last one's.
+    __shared__ bool sh_bad[2][2][128];
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     fence_proxy_async();
                 }
             }
-            sh_bad[hf][r] = false;
+            sh_bad[np & 1][hf][r] = false;
             tc_fence_before();  // the last piece's reads of TMEM
             arrive(&q_full);
             const int each = pairs ? 2 : 1;
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                             const int64_t l = left - 64 * h - 32 * c;
                             if (l < 31) see[c] &= l < 0 ? 0u : (2u << (int)l) - 1u;
                         }
-                        if ((see[0] & nan[0]) | (see[1] & nan[1])) sh_bad[hf][r] = true;
+                        if ((see[0] & nan[0]) | (see[1] & nan[1])) sh_bad[np & 1][hf][r] = true;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             if (!((see[0] >> k) & 1u)) v0[k] = __float_as_uint(-INFINITY);
@@ -676,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                     const int64_t slot = full ? ((p.s < a.B ? a.T : 0) + t) * a.Hq + hq
                                               : (int64_t)(2 * blockIdx.x + (p.first ? 0 : 1)) * kWideRows + lr;
                     float *po = (full ? a.whole : a.wpart) + slot * D;
-                    const bool bad = sh_bad[hf][r] || (pairs && sh_bad[1][r]);
+                    const bool bad = sh_bad[np & 1][hf][r] || (pairs && sh_bad[np & 1][1][r]);
                     const float inv = bad ? __uint_as_float(0x7FFFFFFFu) : row_factor(a.vs[p.h], l);
                     uint16_t *out = a.out + t * a.ldo + (int64_t)hq * D;
 #pragma unroll 1

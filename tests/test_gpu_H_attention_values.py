@@ -1,0 +1,68 @@
+"""GPU tests of the attention over the paged cache where single values decide:
+NaN codes and scales, weights far below a row's largest, indexes past 32 bits."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF16, F8, F32, F64, I32, I64, U8 = (torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.float64,
+                                    torch.int32, torch.int64, torch.uint8)
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def jet(torch_cuda):
+    import fp8_block_quantized_gb300 as j
+    j.load()
+    return j
+
+
+def codes(x):
+    return x.clamp(-448, 448).to(F8).view(U8).cuda()
+
+
+def call(jet, q, k, v, table, bs, new, lengths, ks=None, vs=None, groups=None, scale=1.0):
+    """(out, lse) of requests with new[b] tokens each; groups: (offsets, lengths)."""
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    one = torch.ones((Hk,), device="cuda")
+    out = torch.full((T, Hq, D), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((T, Hq), 7.0, device="cuda")
+    po, pl = (None, None) if groups is None else (torch.tensor(groups[0]).cuda(),
+                                                  torch.tensor(groups[1], dtype=I32).cuda())
+    jet.jet_kv_attention(q, k, v, one if ks is None else ks, one if vs is None else vs, table, bs,
+                         torch.tensor([0] + new).cumsum(0).cuda(), torch.tensor(lengths, dtype=I32).cuda(),
+                         out, lse, po, pl, scale=scale)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_value_in_units_one_behind_another(jet, D):
+    """Units of one pair of tiles, some ten for each CTA; the NaN lies in the second tile, which
+    all requests share and L2 holds.  The first tiles come from memory and their maxima grow, so
+    that their half ends later."""
+    Hq, Hk, bs, n, B = 4, 1, 128, 16, 1600
+    g = torch.Generator(device="cuda").manual_seed(D)
+    k = torch.randn(((B + 1) * bs, Hk, D), generator=g, device="cuda")
+    at = torch.arange(bs, device="cuda")
+    # 64 keys at a time, the later ones of a tile are weighed first
+    k.view(B + 1, bs, D)[:B, :, 0] = torch.where(at < 64, 200.0, -200.0)
+    k.view(B + 1, bs, D)[B, :, 0] = -200.0
+    v = torch.randn(((B + 1) * bs, Hk, D), generator=g, device="cuda") * 90
+    q = torch.randn((B * n, Hq, D), generator=g, device="cuda").to(BF16)
+    q[:, :, 0] = 0.25
+    table = torch.stack([torch.randperm(B, generator=g, device="cuda"), torch.full((B,), B, device="cuda")], 1)
+    args = dict(table=table.to(I32), bs=bs, new=[n] * B, lengths=[2 * bs] * B)
+    kc, vc = codes(k), codes(v)
+    want, lse = call(jet, q, kc, vc, **args)
+    assert torch.isfinite(want.float()).all()
+    vc[B * bs + 50, 0, 17] = 0x7F      # every query sees it
+    flush = torch.empty((1 << 28,), device="cuda")
+    for _ in range(10):
+        flush.zero_()
+        q.amax(), kc[B * bs:].amax(), vc[B * bs:].amax()
+        got, l2 = call(jet, q, kc, vc, **args)
+        assert got[:, :, 17].isnan().all(), int((~got[:, :, 17].isnan()).sum())
+        assert torch.equal(l2, lse)
