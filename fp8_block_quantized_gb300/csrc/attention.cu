@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
             const int hq = h * a.G + (int)(rr - tok * a.G);
             const int64_t slot = full ? ((s < a.B ? a.T : 0) + t) * a.Hq + hq
                                       : ((int64_t)(2 * me + (begins ? 0 : 1)) * a.heads + hw) * kRows + 2 * j + r;
-            const float inv = row_factor(a.vs[h], l[r]);
+            const float inv = row_factor(a.vs[h], l[r], a.ks[h]);
 #pragma unroll
             for (int n = 0; n < NT / 2; n += 4) {
                 const int d = (n / 8) * 128 + W * g + 2 * (n % 8);
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
                     pml[slot * 2] = m[r];
                     pml[slot * 2 + 1] = l[r];
                 } else if (a.lse) {
-                    a.lse[t * a.Hq + hq] = row_lse(m[r], l[r]);
+                    a.lse[t * a.Hq + hq] = row_lse(m[r], l[r], a.ks[h]);
                 }
             }
         }
@@ -597,13 +597,13 @@ struct Row {
     }
     __device__ void write(const Args &a, int64_t t, int hq) const {
         const int lane = threadIdx.x & 31;
-        const float inv = row_factor(a.vs[hq / a.G], l);
+        const float ks = a.ks[hq / a.G], inv = row_factor(a.vs[hq / a.G], l, ks);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const __nv_bfloat16 v = __float2bfloat16_rn(o[e] * inv);
             a.out[t * a.ldo + (int64_t)hq * D + lane + 32 * e] = *reinterpret_cast<const uint16_t *>(&v);
         }
-        if (a.lse && lane == 0) a.lse[t * a.Hq + hq] = row_lse(m, l);
+        if (a.lse && lane == 0) a.lse[t * a.Hq + hq] = row_lse(m, l, ks);
     }
 };
 

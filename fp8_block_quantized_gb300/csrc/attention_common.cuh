@@ -243,11 +243,15 @@ __device__ __forceinline__ uint32_t nan_bits(uint4 v) {
 }
 
 // lse in natural units and the factor of an output from a row's reference and sum: no
-// key, no weight.
-__device__ __forceinline__ float row_lse(float m, float l) {
-    return l == 0.0f ? -INFINITY : kLn2 * (m + log2f(l));
+// key, no weight.  A NaN scale of the keys comes in here: the scores' factors are held
+// above 2^-126, which leaves a NaN out.
+__device__ __forceinline__ float nan_or_zero(float ks) { return ks == ks ? 0.0f : ks; }
+__device__ __forceinline__ float row_lse(float m, float l, float ks) {
+    return l == 0.0f ? -INFINITY : kLn2 * (m + log2f(l)) + nan_or_zero(ks);
 }
-__device__ __forceinline__ float row_factor(float vs, float l) { return l == 0.0f ? 0.0f : vs / l; }
+__device__ __forceinline__ float row_factor(float vs, float l, float ks) {
+    return l == 0.0f ? 0.0f : vs / l + nan_or_zero(ks);
+}
 
 // The power of two that brings a row's largest channel to [2^14, 2^15).
 __device__ __forceinline__ float row_power(float top) {

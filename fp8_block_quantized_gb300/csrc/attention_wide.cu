@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                                               : (int64_t)(2 * blockIdx.x + (p.first ? 0 : 1)) * kWideRows + lr;
                     float *po = (full ? a.whole : a.wpart) + slot * D;
                     const bool bad = sh_bad[np & 1][hf][r] || (pairs && sh_bad[np & 1][1][r]);
-                    const float inv = bad ? __uint_as_float(0x7FFFFFFFu) : row_factor(a.vs[p.h], l);
+                    const float inv = bad ? __uint_as_float(0x7FFFFFFFu) : row_factor(a.vs[p.h], l, a.ks[p.h]);
                     uint16_t *out = a.out + t * a.ldo + (int64_t)hq * D;
 #pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                             ml[0] = ref;
                             ml[1] = bad ? -l : l;
                         } else if (a.lse) {
-                            a.lse[t * a.Hq + hq] = row_lse(ref, l);
+                            a.lse[t * a.Hq + hq] = row_lse(ref, l, a.ks[p.h]);
                         }
                     }
                 }

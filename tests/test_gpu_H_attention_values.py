@@ -66,3 +66,38 @@ def test_nan_value_in_units_one_behind_another(jet, D):
         got, l2 = call(jet, q, kc, vc, **args)
         assert got[:, :, 17].isnan().all(), int((~got[:, :, 17].isnan()).sum())
         assert torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 40, 300])       # tokens of a request: few rows a unit, and many
+@pytest.mark.parametrize("groups", [None, ([0, 3], [50])])
+def test_scales_of_the_keys(jet, D, n, groups):
+    """NaN: all queries of the head that see a key, none of another's; zero: the values' mean."""
+    Hq, Hk, bs, L = 8, 2, 16, 333
+    g = torch.Generator().manual_seed(n)
+    S = (L + bs) // bs * bs
+    kc, vc = (codes(torch.randn((S, Hk, D), generator=g) * 90) for _ in range(2))
+    q = torch.randn((3 * n, Hq, D), generator=g).to(BF16).cuda()
+    table = torch.arange(S // bs, dtype=I32).repeat(3, 1).cuda()
+    args = dict(table=table, bs=bs, new=[n] * 3, lengths=[L, 0, L], groups=groups, scale=D ** -0.5)
+    ks = torch.tensor([0.01, 0.01], device="cuda")
+    want, lse = call(jet, q, kc, vc, ks=ks, **args)
+    ks[1] = float("nan")
+    got, l2 = call(jet, q, kc, vc, ks=ks, **args)
+    assert torch.equal(got[:, :4], want[:, :4]) and torch.equal(l2[:, :4], lse[:, :4])
+    sees = torch.ones((3 * n,), dtype=torch.bool)
+    sees[n:2 * n] = False
+    assert got[sees, 4:].isnan().all() and l2[sees, 4:].isnan().all()
+    assert not got[~sees].any() and (l2[~sees] == -INF).all()
+    ks[1] = 0.0
+    got, l2 = call(jet, q, kc, vc, ks=ks, **args)
+    v = vc.view(F8).double()[:, 1]
+    mean = v.cumsum(0) / torch.arange(1, S + 1, device="cuda")[:, None]
+    size = v.abs().cumsum(0) / torch.arange(1, S + 1, device="cuda")[:, None]
+    for t in list(range(n)) + list(range(2 * n, 3 * n)):
+        seen = L - n + t % n + 1
+        # weights of 1 up to the factor's floor (2^-126 of a raw score: nothing); sums of `seen` terms in
+        # binary32, and the output's rounding
+        bound = 2.0 ** -8 * mean[seen - 1].abs() + 2 * (seen + 8) * 2.0 ** -24 * size[seen - 1]
+        assert ((got[t, 4:].double() - mean[seen - 1]).abs() <= bound).all()
+        assert ((l2[t, 4:].double() - math.log(seen)).abs() <= (seen + 16) * 2.0 ** -24).all()
