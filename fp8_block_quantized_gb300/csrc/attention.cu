@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(256, 4) attention_join_kernel(const Args a) {
                 const Narrow w(a, g);
                 const uint32_t rr = (uint32_t)(t - g.t0) * a.G + gi;
                 n = w.ktiles;
-                u0 += (rr / kRows * w.groups + h / a.heads) * n;
+                u0 += ((int64_t)(rr / kRows) * w.groups + h / a.heads) * n;
                 r = (int)(rr % kRows);
             }
             const Pieces p(u0, n, plan.total[wide], plan.workers[wide]);

@@ -101,3 +101,31 @@ def test_scales_of_the_keys(jet, D, n, groups):
         bound = 2.0 ** -8 * mean[seen - 1].abs() + 2 * (seen + 8) * 2.0 ** -24 * size[seen - 1]
         assert ((got[t, 4:].double() - mean[seen - 1]).abs() <= bound).all()
         assert ((l2[t, 4:].double() - math.log(seen)).abs() <= (seen + 16) * 2.0 ** -24).all()
+
+
+def test_more_tiles_than_32_bits_count(jet):
+    """A group of more than 2^32 tiles of 8 rows and 32 keys, of which all but the first few have
+    no slot."""
+    Hq, Hk, D, bs, T, width = 256, 1, 64, 1 << 16, 1040, 64
+    assert T * Hq // 8 * (width * bs // 32) > 2 ** 32
+    g = torch.Generator().manual_seed(5)
+    kc, vc = (codes(torch.randn((100, Hk, D), generator=g) * 90) for _ in range(2))
+    q = torch.randn((T, Hq, D), generator=g).to(BF16).cuda()
+    table = torch.full((1, width), -1, dtype=I32, device="cuda")
+    table[0, 0] = 0                                # keys 0 .. 99; slots behind them are not there
+    ks = torch.full((Hk,), 0.01, device="cuda")
+    args = dict(table=table, bs=bs, new=[T], ks=ks, scale=D ** -0.5)
+    out, lse = call(jet, q, kc, vc, lengths=[width * bs], groups=([0, 1], [width * bs - T]), **args)
+    k, v = kc.view(F8).double()[:, 0] * ks.double(), vc.view(F8).double()[:, 0]
+    x = q.double() @ k.t() * D ** -0.5                                       # [T, Hq, 100]
+    w = torch.softmax(x, 2)
+    ref = w @ v
+    # a score: D products summed in binary32 and the factor's roundings, e^x to 2^-22; a weight: that twice
+    # and FP16's 2^-11 (or 2^-25 of the largest); sums of 100 terms and the joins' in binary32; BF16's 2^-8.
+    # (Another split of the keys among workers gives other roundings: no call is bit for bit another's.)
+    dx = (D + 8) * 2.0 ** -24 * (q.double().abs() @ k.abs().t()).amax(2) * D ** -0.5 + 2.0 ** -22 * x.abs().amax(2)
+    rel = 2.0 ** -11 + 2 * dx + 2.0 ** -21 + 300 * 2.0 ** -24
+    bound = 2.0 ** -8 * ref.abs() + rel[..., None] * (w @ v.abs()) + 2.0 ** -25 * v.abs().sum(0) * w.amax(2)[..., None]
+    assert ((out.double() - ref).abs() <= bound).all()
+    rl = torch.logsumexp(x, 2)
+    assert ((lse.double() - rl).abs() <= dx + 2.0 ** -21 + 300 * 2.0 ** -24 + 2.0 ** -22 * rl.abs()).all()
