@@ -21,8 +21,10 @@
 // of at most 128 rows has them at alternate tiles of the same rows, whose results
 // are added at the end.  While one half's weights are computed the tensor core
 // works for the other.  A row's output is rescaled in TMEM only when its maximum
-// has grown by more than 2^8 since the last time: weights then reach 2^8 at most,
-// within FP16, and are summed in binary32.
+// has grown by more than 2^8 since the last time.  The weights' reference lies 2^7 below
+// the maximum at that time: weights reach 2^15 at most, within FP16, those below 2^-21
+// of the row's largest are off by 2^-32 of it (the others by 2^-11 of themselves), and
+// they are summed in binary32.
 //
 // What bounds it: a 256 x 128 tile is 2048 cycles of MMAs and takes about 4300, a half's
 // chain of scores (1950 cycles from its last weights on, behind the other half's
@@ -103,6 +105,12 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
 __device__ __forceinline__ uint32_t place(int r, int c) {
     return (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
+
+// The weights' reference at a maximum, and how far maxima may be before it is set again.
+// Where a score's own rounding comes near a power of two (2^20 and above: 2^-4), neither
+// has slack.
+__device__ __forceinline__ float reference(float top) { return fabsf(top) < 0x1p20f ? top - 7.0f : top; }
+__device__ __forceinline__ float limit(float ref) { return fabsf(ref) < 0x1p20f ? ref + 15.0f : ref; }
 
 // max(a, b, c) in one instruction.
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -483,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
             };
             // the query
             float f, ref = -INFINITY, l = 0.0f;  // factor of the scores; the weights' reference
-                                                 // (a power of two) and sum
+                                                 // (an exponent of two) and sum
             int pos = 0x7FFFFFFF;                // a row past the unit's last hides no key
             {
                 int64_t t;
@@ -600,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                         top1 = max3(top1, __uint_as_float(v1[k]), __uint_as_float(v1[k + 1]));
                     }
                     top = fmaxf(top, top1) * f;
-                    const bool start = i == 0 && h == 1, grown = !start && top > ref + 8.0f;
-                    if (start) ref = top;
+                    const bool start = i == 0 && h == 1, grown = !start && top > limit(ref);
+                    if (start) ref = reference(top);
                     if (__any_sync(~0u, grown)) {
                         // the output so far: the products of the last tile were issued before these
                         // scores, whose arrival was waited for; those of this tile's later keys
@@ -610,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_wide_kernel(const Args 
                             break;
                         }
                         tc_fence_after();
-                        const float c = grown ? ex2(ref - top) : 1.0f;
-                        if (grown) ref = top;
+                        const float now = grown ? reference(top) : ref, c = grown ? ex2(ref - now) : 1.0f;
+                        ref = now;
                         l *= c;
 #pragma unroll 1
                         for (int ch = 0; ch < D / 16; ++ch) {

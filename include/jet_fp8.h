@@ -672,8 +672,8 @@ JET_API jet_status jet_sample_unaligned(const void *logits, int dtype, int64_t B
  * position past the table's width) is left out; a query that sees no key gets
  * out 0 and lse -inf.  What a key that a query does not see holds does not matter
  * to it, NaN codes included.  Products of the queries with the codes are exact to 2^-38
- * of the query's largest channel, sums in binary32, weights rounded to 11 bits,
- * one rounding to BF16; the result is the same for the same call, whatever ran
+ * of the query's largest channel, sums in binary32, weights rounded to 11 bits
+ * (those below 2^-21 of the row's largest to within 2^-32 of it), one rounding to BF16; the result is the same for the same call, whatever ran
  * before.
  * Groups: group i is the requests prefix_offsets[i] .. prefix_offsets[i+1]-1,
  * whose first prefix_lengths[i] keys are the same; they are read through the

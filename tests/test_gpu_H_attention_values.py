@@ -129,3 +129,73 @@ def test_more_tiles_than_32_bits_count(jet):
     assert ((out.double() - ref).abs() <= bound).all()
     rl = torch.logsumexp(x, 2)
     assert ((lse.double() - rl).abs() <= dx + 2.0 ** -21 + 300 * 2.0 ** -24 + 2.0 ** -22 * rl.abs()).all()
+
+
+def sink(n, G, D, gap, L, seed):
+    """(q, k, v, k_scale): L keys of score 0, and key 100 of score `gap`, whose values are zero."""
+    g = torch.Generator().manual_seed(seed)
+    k = torch.zeros((L, 1, D))
+    k[100, 0, 0] = 448
+    kc = codes(k)
+    v = torch.rand((L, 1, D), generator=g) * 400 + 40
+    v[100] = 0
+    vc = codes(v)
+    q = torch.randn((n, G, D), generator=g).to(BF16).cuda()
+    q[:, :, 0] = 1.0
+    return q, kc, vc, torch.tensor([gap / 448], device="cuda")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,n,B", [(4, 1, 2048), (8, 16, 304), (4, 64, 304)])   # rows of a unit: 4, 128, 256
+@pytest.mark.parametrize("gap", [15.0, 17.0, 18.0, 20.0])
+def test_keys_far_below_the_largest(jet, D, G, n, B, gap):
+    """One key without values far above 8191 others, all in one piece: they are the output."""
+    L = 8192
+    q, kc, vc, ks = sink(n, G, D, gap, L, int(gap) + n)
+    table = torch.arange(L // 64, dtype=I32).repeat(B, 1).cuda()
+    out, lse = call(jet, q.repeat(B, 1, 1), kc, vc, table, 64, [n] * B, [L] * B, ks=ks)
+    x = float(ks) * 448
+    v = vc.view(F8).double()[:, 0]
+    seen = torch.arange(L - n, L, device="cuda") + 1
+    total = v.cumsum(0)[seen - 1]                                             # [n, D]
+    e = math.exp(-x)
+    z = 1 + (seen - 1) * e
+    ref = (e * total / z[:, None])[:, None]                                   # [n, 1, D]
+    # scores are exact but for the factor's roundings and the argument's (2^-22 x in all); a weight: that,
+    # e^x to 2^-22, FP16's 2^-11, and 2^-32 of the largest near its smallest; sums of L terms, cut off or
+    # rounded 16 at a time; BF16's 2^-8
+    rel = 2.0 ** -8 + 2.0 ** -11 + 2 * (2.0 ** -22 * x + 2.0 ** -22) + 2 * L * 2.0 ** -24
+    bound = rel * ref + 2.0 ** -32 * total[:, None] / z[:, None, None]
+    got = out.view(B, n, G, D).double()
+    assert ((got - ref).abs() <= bound).all(), ((got - ref).abs() / ref).max()
+    rl = x + torch.log(z)
+    assert ((lse.view(B, n, G).double() - rl[:, None]).abs() <= 2.0 ** -20 + 2.0 ** -22 * x + L * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,n", [(4, 1), (8, 16), (4, 64)])
+@pytest.mark.parametrize("power", [10, 17, 19, 20, 21, 24, 26])
+def test_large_scores(jet, D, G, n, power):
+    """Scores whose own rounding is up to four powers of two: the largest one's value alone."""
+    B, L = 3, 1500
+    for gap in (1.1 * 2 ** power, 1.37 * 2 ** power, -1.77 * 2 ** power):
+        q, kc, vc, ks = sink(n, G, D, abs(gap), L, power)
+        if gap < 0:                          # all others share the largest score, 0
+            kc[100, 0, 0] |= 0x80
+        else:
+            vc[100] = vc[99]
+        table = torch.arange((L + 63) // 64, dtype=I32).repeat(B, 1).cuda()
+        pad = 64 * table.shape[1] - L
+        kc, vc = (torch.cat([c, c[:pad]]) for c in (kc, vc))
+        out, lse = call(jet, q.repeat(B, 1, 1), kc, vc, table, 64, [n] * B, [L] * B, ks=ks)
+        v = vc.view(F8).double()[:, 0]
+        seen = torch.arange(L - n, L, device="cuda") + 1
+        x = float(ks) * 448
+        if gap > 0:
+            ref, rl = v[100].expand(n, D), torch.full((n,), x, dtype=F64, device="cuda")
+        else:
+            ref, rl = v.cumsum(0)[seen - 1] / (seen - 1)[:, None], torch.log((seen - 1).double())
+        # weights that are equal are rounded alike (2^-11), sums of L terms, BF16
+        got = out.view(B, n, G, D).double()
+        assert ((got - ref[:, None]).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2 * L * 2.0 ** -24) * ref[:, None]).all()
+        assert ((lse.view(B, n, G).double() - rl[:, None]).abs() <= 2.0 ** -22 * rl[:, None] + 2.0 ** -20 + L * 2.0 ** -24).all()
