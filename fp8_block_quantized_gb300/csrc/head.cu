@@ -506,7 +506,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // How a call is cut; by the sizes alone, so that the workspace and the order of
 // the sums do not depend on the device.
 struct Plan {
-    int cl_z, cl_dx, cl_dw;   // CTAs a tile
+    int cl_z, cl_dx;          // CTAs a tile (dw: by the piece)
     int64_t piece;            // vocabulary entries of a piece (backward)
     int splits;               // ranges of dx's contraction in a piece
     int64_t tiles_z;          // column tiles of the forward
@@ -530,7 +530,6 @@ Plan plan(int64_t T, int64_t V, int64_t K) {
     if (most < 4096) most = 4096;
     const int64_t pieces = ceil_div(V, most);
     p.piece = ceil_div(ceil_div(V, pieces), 256) * 256;
-    p.cl_dw = p.piece <= BM ? 1 : 2;
     // dx has few tiles and a long contraction: the ranges that make the shortest
     // time of whole waves (a slice of 64 takes about 540 cycles on a pair, 270 on
     // one CTA; a range 12 slices of start-up) and of its results' way through
@@ -723,7 +722,8 @@ jet_status jet_head_logp_bwd(const uint16_t *x, const uint16_t *w, int64_t T, in
             if (st != JET_OK) return st;
         }
         if (dw) {
-            st = product<kDw>(p.cl_dw, dev, td64, tx64, nv, K, p.rows, 1, ep, s);
+            // (a last piece of up to 128 entries has no rows for a pair's second CTA)
+            st = product<kDw>(nv <= BM ? 1 : 2, dev, td64, tx64, nv, K, p.rows, 1, ep, s);
             if (st != JET_OK) return st;
         }
     }
