@@ -11,7 +11,8 @@
 //          off its sums (2^-24 of the sum a step): over 4096 products that is 2e-5 of
 //          a logit, so after every 1024 the sum is taken over into registers and
 //          added up there, rounded to nearest;
-//   kGrad  z tiles of a piece of the vocabulary again; the epilogue writes d in
+//   kGrad  z tiles of a piece of the vocabulary again, with the same sums, so that
+//          e^(z - lse) is of the forward's own logits; the epilogue writes d in
 //          BF16 (the type that the next two products read: up to 2^-8 of each
 //          value, whose errors mostly cancel in the sums of many tokens; up to 128
 //          tokens have a second array with what the first left over, 2^-16, and
@@ -29,7 +30,7 @@
 //
 // The kernel is persistent: warp 0 loads operand slices of 64 along the
 // contraction by TMA into a ring of stages (128-byte swizzle), warp 1 issues the
-// MMAs into one of two TMEM accumulators, warps 4-7 (kLse: 4-11) drain the other one.  Large
+// MMAs into one of two TMEM accumulators, warps 4-7 (kLse, kGrad: 4-11) drain the other one.  Large
 // products run as CTA pairs on 256 x 256 tiles, few rows on single CTAs with 128 x
 // 128.  Every wait is bounded (jet_common.cuh); a role that gives up sets the
 // CTA's abort flag, copies and MMAs in flight are awaited, TMEM is freed.
@@ -52,12 +53,13 @@ enum Product { kLse = 0, kGrad = 1, kDx = 2, kDw = 3 };
 constexpr unsigned kSiteProducer = 16, kSiteMma = 17, kSiteMmaTmem = 18, kSiteEpilogue = 19,
                    kSiteDrain = 20;
 
-constexpr int kThreads = 256, kLseThreads = 384;
 constexpr int BM = 128, BK = 64;
-constexpr int kChunk = 16;  // kLse: slices that the tensor core adds up by itself
-// kLse's registers a thread after setmaxnreg: 128 x 72 + 256 x 216 = 384 x 168.
+constexpr int kChunk = 16;  // kLse, kGrad: slices that the tensor core adds up by itself
+__host__ __device__ constexpr bool sums_chunks(int product) { return product == kLse || product == kGrad; }
+__host__ __device__ constexpr int threads_of(int product) { return sums_chunks(product) ? 384 : 256; }
+// Their registers a thread after setmaxnreg: 128 x 72 + 256 x 216 = 384 x 168.
 constexpr uint32_t kRegsControl = 72, kRegsEpilogue = 216;
-static_assert(128 * kRegsControl + 256 * kRegsEpilogue <= kLseThreads * 168, "registers");
+static_assert(128 * kRegsControl + 256 * kRegsEpilogue <= 384 * 168, "registers");
 constexpr int kStages = 6;
 constexpr int kABytes = BM * BK * 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -99,12 +101,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // rows R, columns C, contraction D in elements; `splits` ranges of the contraction.
 template <int P, int CL>
-__global__ void __launch_bounds__(P == kLse ? kLseThreads : kThreads, 1)
+__global__ void __launch_bounds__(threads_of(P), 1)
 head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, int R,
             int C, int D, int splits, const Epilogue ep, unsigned *status) {
     using CF = Cfg<CL>;
     constexpr int S = kStages, BN = CF::BN;
-    constexpr bool kPair = CL == 2, kAMn = P == kDw, kBMn = P == kDx || P == kDw;
+    constexpr bool kPair = CL == 2, kAMn = P == kDw, kBMn = P == kDx || P == kDw, kChunks = sums_chunks(P);
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t full_bar[S], empty_bar[S], tfull_bar[2], tempty_bar[2], drain_bar;
     __shared__ uint32_t tmem_sh;
@@ -122,7 +124,7 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], (P == kLse ? 8 : 4) * CL);
+            mbar_init(&tempty_bar[b], (kChunks ? 8 : 4) * CL);
         }
         mbar_init(&drain_bar, 1);
         abort_sh = 0;
@@ -173,7 +175,7 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
     auto wait = [&](uint64_t *bar, uint32_t parity, unsigned site) -> bool {
         return __all_sync(~0u, mbar_wait(bar, parity, abort, status, site));
     };
-    if constexpr (P == kLse)
+    if constexpr (kChunks)
         if (warp < 4) reg_dealloc<kRegsControl>();
     if (warp == 0) {
         if (lane == 0) {
@@ -236,8 +238,8 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             int m0, n0, k0, k1, sp;
             coords(t, m0, n0, k0, k1, sp);
             for (int kb = k0; kb < k1; ++kb, ++it) {
-                const bool begins = P == kLse ? (kb - k0) % kChunk == 0 : kb == k0;
-                const bool ends = kb + 1 == k1 || (P == kLse && (kb + 1 - k0) % kChunk == 0);
+                const bool begins = kChunks ? (kb - k0) % kChunk == 0 : kb == k0;
+                const bool ends = kb + 1 == k1 || (kChunks && (kb + 1 - k0) % kChunk == 0);
                 const uint32_t buf = sums & 1u;
                 const int s = it % S;
                 if ((begins && !wait(&tempty_bar[buf], ((sums >> 1) & 1u) ^ 1u, kSiteMmaTmem)) ||
@@ -272,8 +274,8 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
         }
         __syncwarp();
         mbar_wait(&drain_bar, 0, nullptr, status, kSiteDrain);
-    } else if (P == kLse && warp >= 4) {
-        if constexpr (P == kLse) {
+    } else if (kChunks && warp >= 4) {
+        if constexpr (kChunks) {
             reg_alloc<kRegsEpilogue>();
             constexpr int H = BN / 2;  // columns of a thread
             const int quad = warp & 3, half = (warp - 4) >> 2;
@@ -319,40 +321,68 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                     }
                 }
                 if (!ok) break;
-                if (row >= R) continue;
-                // the target's column, if it is one of these
-                const int64_t token = ep.target[row];
-                const int want = token >= 0 && token < ep.V ? (int)token - col0 : -1;
-                float top = -INFINITY, zt = 0.0f;
+                if (row >= (P == kGrad ? max(R, ep.second) : R)) continue;
+                // the target's column, if it is one of these (kGrad: rows from R on are zeros)
+                const int64_t token = P == kLse || row < R ? ep.target[row] : -1;
+                const bool real = token >= 0 && token < ep.V;
+                const int want = real ? (int)token - (P == kGrad ? ep.v0 : 0) - col0 : -1;
+                if constexpr (P == kLse) {
+                    float top = -INFINITY, zt = 0.0f;
 #pragma unroll
-                for (int i = 0; i < H / 2; ++i) {
-                    float2 x = __fmul2_rn(acc[i], make_float2(c, c));
-                    if (col0 + 2 * i >= C) x.x = -INFINITY;
-                    if (col0 + 2 * i + 1 >= C) x.y = -INFINITY;
-                    if (want == 2 * i) zt = x.x;
-                    if (want == 2 * i + 1) zt = x.y;
-                    acc[i] = x;
-                    top = fmaxf(top, fmaxf(x.x, x.y));
-                }
-                if (want >= 0 && want < H) ep.zt[row] = zt;
-                const float2 use = make_float2(top == -INFINITY ? 0.0f : -top, top == -INFINITY ? 0.0f : -top);
-                float2 sum = make_float2(0.0f, 0.0f);
+                    for (int i = 0; i < H / 2; ++i) {
+                        float2 x = __fmul2_rn(acc[i], make_float2(c, c));
+                        if (col0 + 2 * i >= C) x.x = -INFINITY;
+                        if (col0 + 2 * i + 1 >= C) x.y = -INFINITY;
+                        if (want == 2 * i) zt = x.x;
+                        if (want == 2 * i + 1) zt = x.y;
+                        acc[i] = x;
+                        top = fmaxf(top, fmaxf(x.x, x.y));
+                    }
+                    if (want >= 0 && want < H) ep.zt[row] = zt;
+                    const float2 use = make_float2(top == -INFINITY ? 0.0f : -top, top == -INFINITY ? 0.0f : -top);
+                    float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int i = 0; i < H / 2; ++i) {
-                    const float2 d = __fadd2_rn(acc[i], use);
-                    sum = __fadd2_rn(sum, make_float2(ex2(d.x), ex2(d.y)));
+                    for (int i = 0; i < H / 2; ++i) {
+                        const float2 d = __fadd2_rn(acc[i], use);
+                        sum = __fadd2_rn(sum, make_float2(ex2(d.x), ex2(d.y)));
+                    }
+                    ep.part[(int64_t)(2 * (n0 / BN) + half) * R + row] = make_float2(top, sum.x + sum.y);
+                } else {
+                    const float g = real ? ep.dlogp[row] * ep.scale : 0.0f, neg = real ? -ep.lse[row] * kLog2e : 0.0f;
+                    uint16_t *dst = ep.d + (int64_t)row * ep.ldd + col0;
+#pragma unroll
+                    for (int i = 0; i < H / 2; i += 4) {
+                        if (col0 + 2 * i >= C) break;  // (up to the padded row end past the piece's last)
+#pragma unroll
+                        for (int k = i; k < i + 4; ++k) {
+                            const float2 x = __ffma2_rn(acc[k], make_float2(c, c), make_float2(neg, neg));
+                            acc[k].x = g * ((want == 2 * k ? 1.0f : 0.0f) - ex2(x.x));
+                            acc[k].y = g * ((want == 2 * k + 1 ? 1.0f : 0.0f) - ex2(x.y));
+                            if (g == 0.0f) acc[k] = make_float2(0.0f, 0.0f);  // whatever lse is there
+                        }
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) w[k] = pack2(acc[i + k].x, acc[i + k].y);
+                        *reinterpret_cast<uint4 *>(dst + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (ep.second > 0) {  // what is left over
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack2(acc[i + k].x - __uint_as_float(w[k] << 16),
+                                             acc[i + k].y - __uint_as_float(w[k] & 0xFFFF0000u));
+                            *reinterpret_cast<uint4 *>(dst + ep.second * ep.ldd + 2 * i) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
                 }
-                ep.part[(int64_t)(2 * (n0 / BN) + half) * R + row] = make_float2(top, sum.x + sum.y);
             }
         }
-    } else if (P != kLse && warp >= 4) {
+    } else if (!kChunks && warp >= 4) {
         const int quad = warp & 3;
         uint32_t release[2] = {0u, 0u};
         if (kPair) {
             release[0] = map_to_cta(&tempty_bar[0], 0);
             release[1] = map_to_cta(&tempty_bar[1], 0);
         }
-        const float c = ep.scale * kLog2e;
         uint32_t tiles = 0;
         for (int t = unit0; t < total; t += step, ++tiles) {
             int m0, n0, k0, k1, sp;
@@ -360,17 +390,6 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             const int row = m0 + quad * 32 + lane;
             const bool row_ok = row < R;
             const uint32_t buf = tiles & 1u;
-            // kGrad: the target's column of the piece (none: out of any tile)
-            int want = -1;
-            float lse2 = 0.0f, g = 0.0f;
-            if (P == kGrad && row_ok) {
-                const int64_t token = ep.target[row];
-                if (token >= 0 && token < ep.V) {
-                    want = (int)token - ep.v0;
-                    g = ep.dlogp[row] * ep.scale;
-                }
-                lse2 = ep.lse[row] * kLog2e;
-            }
             if (!wait(&tfull_bar[buf], (tiles >> 1) & 1u, kSiteEpilogue)) break;
             tc_fence_after();
             const uint32_t acc0 = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
@@ -381,32 +400,7 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
                 tmem_ld32(acc0 + ch * 32, r);
                 tmem_wait32(r);
                 const int col = n0 + ch * 32;
-                if constexpr (P == kGrad) {
-                    uint16_t *dst = ep.d + (int64_t)row * ep.ldd + col;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t w[4], left[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float v[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int at = i + 2 * k + e;
-                                const float p = ex2(fmaf(__uint_as_float(r[at]), c, -lse2));
-                                v[e] = g * ((want == col + at ? 1.0f : 0.0f) - p);
-                                if (g == 0.0f) v[e] = 0.0f;  // whatever lse is there
-                            }
-                            w[k] = pack2(v[0], v[1]);
-                            left[k] = pack2(v[0] - __uint_as_float(w[k] << 16),
-                                            v[1] - __uint_as_float(w[k] & 0xFFFF0000u));
-                        }
-                        if ((row_ok || row < ep.second) && col + i < C)  // (up to the padded row end past the piece's last)
-                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                        if (row < ep.second && col + i < C)
-                            *reinterpret_cast<uint4 *>(dst + ep.second * ep.ldd + i) =
-                                make_uint4(left[0], left[1], left[2], left[3]);
-                    }
-                } else if constexpr (P == kDx) {
+                if constexpr (P == kDx) {
                     float *dst = ep.acc + ((int64_t)sp * R + row) * C + col;
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
@@ -571,7 +565,7 @@ jet_status product(const DeviceInfo &dev, const CUtensorMap &ta, const CUtensorM
     static int at_once[64] = {};
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.blockDim = dim3(P == kLse ? kLseThreads : kThreads);
+    cfg.blockDim = dim3(threads_of(P));
     cfg.dynamicSmemBytes = CF::kSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -752,8 +752,8 @@ JET_API jet_status jet_head_logp(const uint16_t *x, const uint16_t *w, int64_t T
  * dlogp: -1/T for the mean cross entropy):
  *   d_tv = scale dlogp_t ([v = target[t]] - e^(z_tv - lse_t)), 0 for ignored rows,
  *   dx = d w,  dw = d^T x.
- * The logits are computed again, a piece of the vocabulary at a time (at most
- * 512 MB of d, 4096 entries at least); d is rounded to BF16 (2^-8 of each
+ * The logits are computed again, by the same sums as in jet_head_logp and a piece
+ * of the vocabulary at a time (at most 512 MB of d, 4096 entries at least); d is rounded to BF16 (2^-8 of each
  * value; in two parts, 2^-16, for up to 128 tokens), sums are binary32, dx and dw rounded once to BF16.
  *   x, w, target, scale, lse: as in and from jet_head_logp.  dlogp [T] FP32 (in;
  *       not read for ignored rows).

@@ -59,3 +59,38 @@ def test_a_short_last_piece(jet):
     bound = off.t() @ x.double().abs() + 2.0 ** -8 * ref.abs() + (T / 16 + 20) * 2.0 ** -22 * (d.abs().t() @ x.double().abs())
     assert ((dw[v0:].double() - ref).abs() <= bound).all()
     assert not (dw == 7.0).all(1).any()
+
+
+@pytest.mark.parametrize("T", [32, 200])
+@pytest.mark.parametrize("K", [4096, 16384])
+def test_gradients_of_confident_tokens(jet, T, K):
+    """Logits of 20 to 100 whose products all have one sign; the target's probability is about 0.95.
+    Against the gradient by the formula, not by the lse that the forward gave."""
+    V = 600
+    x, w, target, _ = make(T, K, V, K + T, std=0.1)
+    target = torch.randperm(V // 2, device="cuda")[:T]
+    z = torch.linspace(20, 100, T, device="cuda")
+    unit = x.float() / x.float().square().sum(1, keepdim=True)
+    w[target] = (unit * z[:, None]).to(BF16)
+    w[target + V // 2] = (unit * (z - 3)[:, None]).to(BF16)
+    dlogp = torch.where(torch.arange(T, device="cuda") % 2 == 0, 1.0, -0.5)
+    _, lse = jet.head_logp(x, w, target)
+    dx, dw = jet.head_logp_bwd(x, w, target, lse, dlogp)
+    x64, w64 = x.double(), w.double()
+    z64 = x64 @ w64.t()
+    p = torch.softmax(z64, 1)
+    hot = torch.zeros_like(p).scatter_(1, target[:, None], 1.0)
+    up = dlogp.double()[:, None]
+    d = up * (hot - p)
+    at = torch.arange(T, device="cuda")
+    assert (d[at, target].abs() < 0.1 * up.abs()[:, 0]).all()
+    # a logit: 64 sums of 16 products at a time into binary32, each off by a unit of 2^-22 of what was added up,
+    # then the chunks'; alike in both calls, so that a probability is off by p (1 - p) times two of that;
+    # and the roundings of lse, of its product and the exponential's argument
+    dz = (x64.abs() @ w64.abs().t()).amax(1, keepdim=True) * (66 + K / 1024) * 2.0 ** -22
+    top = z64.abs().amax(1, keepdim=True)
+    off = up.abs() * p * ((1 - p) * 2 * dz + (2 * top + 8) * 2.0 ** -22) + 2.0 ** (-16 if T <= 128 else -8) * d.abs()
+    for got, ref, bound, mag, n in ((dx, d @ w64, off @ w64.abs(), d.abs() @ w64.abs(), V),
+                                    (dw, d.t() @ x64, off.t() @ x64.abs(), d.abs().t() @ x64.abs(), T)):
+        bound = bound + 2.0 ** -8 * ref.abs() + mag * (n / 16 + 20) * 2.0 ** -22 + 1e-38
+        assert ((got.double() - ref).abs() <= bound).all(), ((got.double() - ref).abs() / bound).max()
