@@ -519,8 +519,13 @@ Plan plan(int64_t T, int64_t V, int64_t K) {
     p.cl_z = p.cl_dx = T <= BM ? 1 : 2;
     p.tiles_z = 2 * ceil_div(V, p.cl_z == 2 ? 256 : 128);  // halves of tiles
     p.fwd_bytes = up256((size_t)(p.tiles_z * T) * sizeof(float2)) + up256((size_t)T * 4);
+    // d in two parts for the few rows of one tile: one gradient's rounding can be all of an
+    // output's error there (0.0031 of its norm against 0.0017), and the products are bound by
+    // w; a small call of 177 us takes 194
+    p.second = T <= BM ? ceil_div(T, BK) * BK : 0;
+    p.rows = p.second > 0 ? 2 * p.second : T;
     // pieces of equal size whose d takes at most kPieceBytes, 4096 entries at least
-    int64_t most = kPieceBytes / (2 * (T > 0 ? T : 1));
+    int64_t most = kPieceBytes / (2 * (p.rows > 0 ? p.rows : 1)) / 256 * 256;
     if (most < 4096) most = 4096;
     const int64_t pieces = ceil_div(V, most);
     p.piece = ceil_div(ceil_div(V, pieces), 256) * 256;
@@ -528,11 +533,6 @@ Plan plan(int64_t T, int64_t V, int64_t K) {
     // time of whole waves (a slice of 64 takes about 540 cycles on a pair, 270 on
     // one CTA; a range 12 slices of start-up) and of its results' way through
     // memory (about 3500 bytes a cycle, written and read)
-    // d in two parts for the few rows of one tile: one gradient's rounding can be all of an
-    // output's error there (0.0031 of its norm against 0.0017), and the products are bound by
-    // w; a small call of 177 us takes 194
-    p.second = T <= BM ? ceil_div(T, BK) * BK : 0;
-    p.rows = p.second > 0 ? 2 * p.second : T;
     const int64_t tiles = ceil_div(p.rows, BM * p.cl_dx) * ceil_div(K, p.cl_dx == 2 ? 256 : 128);
     const int64_t at_once = p.cl_dx == 2 ? kClusters : 2 * kClusters, nk = ceil_div(p.piece, BK);
     const int64_t cycles = p.cl_dx == 2 ? 540 : 270;

@@ -94,3 +94,25 @@ def test_gradients_of_confident_tokens(jet, T, K):
                                     (dw, d.t() @ x64, off.t() @ x64.abs(), d.abs().t() @ x64.abs(), T)):
         bound = bound + 2.0 ** -8 * ref.abs() + mag * (n / 16 + 20) * 2.0 ** -22 + 1e-38
         assert ((got.double() - ref).abs() <= bound).all(), ((got.double() - ref).abs() / bound).max()
+
+
+def test_few_tokens_of_a_vocabulary_in_pieces(jet):
+    """Up to 128 tokens, whose d has two parts: pieces of the vocabulary and dx added up over them."""
+    T, K, V = 3, 64, 2200000
+    x, w, target, dlogp = make(T, K, V, 2)
+    target[0] = V - 1
+    _, lse = jet.head_logp(x, w, target)
+    dx, dw = jet.head_logp_bwd(x, w, target, lse, dlogp)
+    x64, w64 = x.double(), w.double()
+    z = x64 @ w64.t()
+    p = torch.exp(z - lse.double()[:, None])
+    up = dlogp.double()[:, None]
+    d = (-up * p).scatter_add_(1, target[:, None], up)
+    # a logit: sums of 16 products into binary32; lse's rounding and the argument's; d in two parts; sums of V or
+    # T terms, the outputs' rounding
+    dz = (x64.abs() @ w64.abs().t()) * (K / 16 + 2) * 2.0 ** -22
+    off = up.abs() * p * (2 * dz + (z.abs() + lse.double().abs()[:, None] + 8) * 2.0 ** -22) + 2.0 ** -16 * d.abs()
+    for got, ref, bound, mag, n in ((dx, d @ w64, off @ w64.abs(), d.abs() @ w64.abs(), V),
+                                    (dw, d.t() @ x64, off.t() @ x64.abs(), d.abs().t() @ x64.abs(), T)):
+        bound = bound + 2.0 ** -8 * ref.abs() + mag * (n / 16 + 20) * 2.0 ** -22 + 1e-38
+        assert ((got.double() - ref).abs() <= bound).all()
