@@ -152,6 +152,7 @@ void on_this_device(PyObject *o) {
 at::Tensor workspace(PyObject *o, const at::Tensor &like, size_t need) {
     if (o != Py_None) {
         const at::Tensor &t = tensor(o, "ws");
+        on_this_device(o);
         arg<void>(o, "ws", t.scalar_type(), {t.numel()});
         return t;
     }
