@@ -218,10 +218,13 @@ head_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUte
             // every load has landed before the CTA may exit (a pair's are the leader's)
             // and, in a pair's other CTA, what the leader's commits still have to say to its
             // barriers: its memory may be another CTA's when they arrive, and the leader's own
-            // drain does not say that they have
+            // drain does not say that they have (where one stays out the leader has given up,
+            // and so do the others)
             for (uint32_t i = it > (uint32_t)S ? it - S : 0u; i < it; ++i)
-                mbar_wait(leader ? &full_bar[i % S] : &empty_bar[i % S], (i / S) & 1u, nullptr, status,
-                          kSiteDrain);
+                if (!mbar_wait(leader ? &full_bar[i % S] : &empty_bar[i % S], (i / S) & 1u, nullptr, status,
+                               kSiteDrain) &&
+                    !leader)
+                    break;
         }
         __syncwarp();
     } else if (warp == 1 && leader) {
