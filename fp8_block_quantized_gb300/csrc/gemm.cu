@@ -491,10 +491,18 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
             }
             // Every issued load must have landed before the CTA can exit (the
-            // pair's loads are tracked by the leader's barriers).
-            if (!kPair || leader)
+            // pair's loads are tracked by the leader's barriers).  Its other CTA
+            // waits for the leader's last commits on its own barriers: its memory
+            // may be another CTA's when they arrive, and the leader's drain does
+            // not say that they have (where one stays out the leader has given
+            // up, and so do the others).
+            if (!kPair || leader) {
                 for (uint32_t j = it > (uint32_t)S ? it - S : 0u; j < it; ++j)
                     mbar_wait(&full_bar[j % S], (j / S) & 1u, nullptr, status, SITE_GEMM_DRAIN);
+            } else {
+                for (uint32_t j = it > (uint32_t)S ? it - S : 0u; j < it; ++j)
+                    if (!mbar_wait(&empty_bar[j % S], (j / S) & 1u, nullptr, status, SITE_GEMM_DRAIN)) break;
+            }
             for (uint32_t j = it > (uint32_t)SS ? it - SS : 0u; j < it; ++j)
                 mbar_wait(&sfull_bar[j % SS], (j / SS) & 1u, nullptr, status, SITE_GEMM_DRAIN);
         } else if ((warp == 1 || (warp == 2 && kIssuers == 2)) && leader) {
