@@ -32,9 +32,9 @@
 // are in binary32, and the 2^15 is taken out at a piece's end.
 //
 // What bounds it: the read of the cache.  64 requests of 17 to 8192 tokens, 32 query and
-// 8 KV heads of 128 channels: 538 MB in 90 us (6.0 TB/s; a copy runs at 6.8), 103 us with
+// 8 KV heads of 128 channels: 538 MB in 91 us (5.9 TB/s; a copy runs at 6.8), 100 us with
 // the plan and the join; two requests of 100000 to 131072 tokens with 64 query heads: 449
-// MB in 76, with both 87.  A single request of 4001 tokens, 20.5 us, is three launches of
+// MB in 77, with both 86.  A single request of 4001 tokens, 17 us, is three launches of
 // dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -30,8 +30,8 @@
 // chain of scores (1950 cycles from its last weights on, behind the other half's
 // products) and of two times 64 keys' weights (1200 each).  A unit's start (queries, first
 // keys) and end (output) add 10000 to 25000.  Eight requests of up to 1024 new tokens
-// behind 1024 to 4096 keys, 32 query and 8 KV heads of 128: 210 us of 234 with the plan and the
-// join, 587 TFLOP/s; a prefix of 32768 keys with 128 responses of 64 query heads: 117 us.
+// behind 1024 to 4096 keys, 32 query and 8 KV heads of 128: 215 us of 238 with the plan and the
+// join, 566 TFLOP/s; a prefix of 32768 keys with 128 responses of 64 query heads: 120 us.
 //
 // Every wait is bounded (jet_common.cuh); a role that gives up sets the CTA's abort
 // flag, MMAs in flight are awaited and TMEM is freed.

@@ -23,17 +23,20 @@
 // Forward: bound by the tensor core for many tokens (2 T K V operations), by the
 // read of w for few.  Backward: 8 T K V operations, a quarter of them the logits
 // again; d passes through memory once per piece.  4096 tokens, K = 4096, V = 128256:
-// forward 2.81 ms (1534 TFLOP/s), backward 8.5 ms (1515), 65 to 70% of the tensor
-// core's cycles: the operands' feed by TMA is the limit (42 bytes a cycle and SM).  1537
-// tokens, K = 5120, V = 50257: backward 1.75 ms.  48 tokens, K = 512, V = 2048: forward
-// 12.3 us, two launches of dependent loads.
+// forward 2.76 ms (1562 TFLOP/s; 2.58 ms before its sums were taken over every 1024
+// products), backward 8.45 ms (2040 TFLOP/s of the 8 T K V, above the library
+// product's rate: what is left there is the logits' second product).  1537 tokens, K =
+// 5120, V = 50257: backward 1.74 ms.  48 tokens, K = 512, V = 2048: forward 8.5 us, two
+// launches of dependent loads.
 //
 // The kernel is persistent: warp 0 loads operand slices of 64 along the
 // contraction by TMA into a ring of stages (128-byte swizzle), warp 1 issues the
 // MMAs into one of two TMEM accumulators, warps 4-7 (kLse, kGrad: 4-11) drain the other one.  Large
 // products run as CTA pairs on 256 x 256 tiles, few rows on single CTAs with 128 x
-// 128.  Every wait is bounded (jet_common.cuh); a role that gives up sets the
-// CTA's abort flag, copies and MMAs in flight are awaited, TMEM is freed.
+// 128.  Every mbarrier wait is bounded (jet_common.cuh); a role that gives up sets
+// the CTA's abort flag, copies and MMAs in flight are awaited, TMEM is freed.  (A pair's
+// other CTA learns of it through its own waits; the two then meet at the last cluster
+// barrier.)
 #include <cuda_bf16.h>
 
 #include <mutex>
@@ -524,7 +527,8 @@ Plan plan(int64_t T, int64_t V, int64_t K) {
     p.fwd_bytes = up256((size_t)(p.tiles_z * T) * sizeof(float2)) + up256((size_t)T * 4);
     // d in two parts for the few rows of one tile: one gradient's rounding can be all of an
     // output's error there (0.0031 of its norm against 0.0017), and the products are bound by
-    // w; a small call of 177 us takes 194
+    // w (K = 4096, V = 32000, cold caches: 64 tokens 220 us, 128 tokens 270; 129 in one part
+    // on pairs 230)
     p.second = T <= BM ? ceil_div(T, BK) * BK : 0;
     p.rows = p.second > 0 ? 2 * p.second : T;
     // pieces of equal size whose d takes at most kPieceBytes, 4096 entries at least

@@ -671,7 +671,8 @@ JET_API jet_status jet_sample_unaligned(const void *logits, int dtype, int64_t B
  * p % block_size.  A key without a slot (a negative table entry, a slot >= S, a
  * position past the table's width) is left out; a query that sees no key gets
  * out 0 and lse -inf.  What a key that a query does not see holds does not matter
- * to it, NaN codes included.  Products of the queries with the codes are exact to 2^-38
+ * to it, NaN codes included; a NaN among the values of one that it sees makes that
+ * channel of its output NaN, and can make the head's others NaN too.  Products of the queries with the codes are exact to 2^-38
  * of the query's largest channel, sums in binary32, weights rounded to 11 bits
  * (those below 2^-21 of the row's largest to within 2^-32 of it), one rounding to BF16; the result is the same for the same call, whatever ran
  * before.
@@ -754,7 +755,9 @@ JET_API jet_status jet_head_logp(const uint16_t *x, const uint16_t *w, int64_t T
  *   dx = d w,  dw = d^T x.
  * The logits are computed again, by the same sums as in jet_head_logp and a piece
  * of the vocabulary at a time (at most 512 MB of d, 4096 entries at least); d is rounded to BF16 (2^-8 of each
- * value; in two parts, 2^-16, for up to 128 tokens), sums are binary32, dx and dw rounded once to BF16.
+ * value; in two parts, 2^-16, for up to 128 tokens), sums are binary32 (the tensor
+ * core's, which cuts off up to 2^-23 of a sum every 16 terms: dw over T tokens, dx
+ * over a range of the vocabulary), dx and dw rounded once to BF16.
  *   x, w, target, scale, lse: as in and from jet_head_logp.  dlogp [T] FP32 (in;
  *       not read for ignored rows).
  *   dx [T][K], dw [V][K] BF16 bits (out); either may be NULL.  dw is zeros for
