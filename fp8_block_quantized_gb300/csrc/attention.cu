@@ -438,10 +438,11 @@ __global__ void __launch_bounds__(32 * Cfg<D>::kWarps, 1) attention_kernel(const
                 top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 4));
                 top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 8));
                 top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 16));
-                // A new reference is the next value above the maximum, so that no weight,
-                // whose score is not rounded, is above 1 (and FP16 holds it times 2^15).
+                // A reference is the next value above any maximum so far (-inf and inf are their
+                // own), so that no weight, whose score is not rounded, is above 1 (and FP16
+                // holds it times 2^15).
                 top[r] *= f[r];
-                top[r] = top[r] > m[r] ? fmaf(fabsf(top[r]), 0x1.2p-24f, top[r]) : m[r];
+                top[r] = top[r] >= m[r] ? fmaf(fminf(fabsf(top[r]), 0x1.fffffep127f), 0x1.2p-24f, top[r]) : m[r];
             }
             if (__any_sync(~0u, top[0] != m[0] || top[1] != m[1])) {
                 const float c0 = ex2(m[0] - (top[0] == -INFINITY ? 0.0f : top[0])),

@@ -199,3 +199,29 @@ def test_large_scores(jet, D, G, n, power):
         got = out.view(B, n, G, D).double()
         assert ((got - ref[:, None]).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2 * L * 2.0 ** -24) * ref[:, None]).all()
         assert ((lse.view(B, n, G).double() - rl[:, None]).abs() <= 2.0 ** -22 * rl[:, None] + 2.0 ** -20 + L * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,n,B", [(4, 1, 2048), (8, 16, 304), (4, 64, 304)])   # a unit in one piece
+@pytest.mark.parametrize("power", [20, 25, 26])
+def test_large_scores_beside_each_other(jet, D, G, n, B, power):
+    """Two keys whose scores are the same value or neighbouring ones, in one tile and the next, and
+    whose values are the same: their order and distance do not show."""
+    L = 900
+    for step, gap in [(s, 1.37 + j / 64) for s in (0, 2, 4) for j in range(12)]:
+        q, kc, vc, ks = sink(n, G, D, gap * 2 ** power, L, step)
+        q[:, :, 1] = 2.0 ** -22                     # a unit of key 500's second channel: 2^-22 of the first's
+        kc[500] = kc[100]
+        kc[500, 0, 1] = codes(torch.tensor([64.0 * step]))[0]
+        vc[100] = vc[99]
+        vc[500] = vc[99]
+        table = torch.arange((L + 63) // 64, dtype=I32).repeat(B, 1).cuda()
+        pad = 64 * table.shape[1] - L
+        kc, vc = (torch.cat([c, c[:pad]]) for c in (kc, vc))
+        for swap in (False, True):
+            if swap:
+                kc[[100, 500]] = kc[[500, 100]]
+            out, _ = call(jet, q.repeat(B, 1, 1), kc, vc, table, 64, [n] * B, [L] * B, ks=ks)
+            v = vc.view(F8).double()[99, 0]
+            # the others' weights are zero; two weights of any sizes, each rounded to 2^-11, BF16
+            assert ((out.double() - v).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -21) * v).all()
