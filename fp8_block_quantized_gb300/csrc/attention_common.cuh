@@ -113,7 +113,7 @@ struct Plan {
     int many;          // whether one of them has more than kManyPieces pieces
 };
 // A row of more pieces than this is joined by the eight warps of a CTA, not by one (one
-// request of 4001 keys: 20.5 us, with one warp 39.0; two of 100000 to 131072: 87 and 101).
+// request of 4001 keys: 17.1 us, with one warp 36.2; two of 100000 to 131072: 87 and 102).
 constexpr int kManyPieces = 8;
 
 // A unit that more than one worker has, as the first worker that begins in its middle
